@@ -319,6 +319,132 @@ DION3_API dion3_status dion3_symm_f16(const uint16_t* A, const uint16_t* B, cons
                             int32_t batch, int64_t s, int64_t ld, float alpha, float beta,
                             float gamma, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Operators of the layers whose weights the step updates: the norm before a
+ * linear layer, the layer's product with its epilogue, both gradients, and
+ * activations held in 8 bits between the forward and the backward pass.  The
+ * weight gradient is summed in fp32 and may be added straight into the
+ * momentum buffer M, which the step then takes as it is (dion3_step: no G).
+ *
+ * T tokens; matrices are row-major with a row stride (ld) of their own.
+ * 16-bit data (`dtype`: DION3_BF16 or DION3_F16) is passed as void*; every
+ * pointer is aligned to its element size (8-bit data: 16 bytes).  Any side
+ * from 1 and any row stride that holds the row is taken; rows that are
+ * 16-byte aligned with sides that are multiples of 8 are fastest (the
+ * products copy an operand that is not into the workspace first).  T = 0 is
+ * valid: nothing is written, except that gradients over no tokens are zero.
+ * Statistics, products and column sums are held in fp32 and added in an order
+ * fixed by the sizes, strides and alignment alone; every output is rounded
+ * once.  Outputs must not overlap inputs or each other except where said.
+ * NaN and infinities propagate as in the formulas.
+ * DION3_ERR_ARG: a null required pointer, a negative T, a side below 1, a
+ * row stride below the row, an unknown type or activation, an unaligned
+ * pointer.  DION3_ERR_UNSUPPORTED: T above DION3_MAX_TOKENS, a side above
+ * DION3_MAX_DIM, a row stride above 2^21 or more than 2^42 elements.
+ * DION3_ERR_WORKSPACE: as elsewhere; a call whose workspace size is 0 takes
+ * ws = NULL. */
+#define DION3_F32 0
+#define DION3_BF16 1
+#define DION3_F16 2
+
+#define DION3_ACT_NONE 0
+#define DION3_ACT_RELU 1
+#define DION3_ACT_GELU 2        /* z (1 + erf(z / sqrt 2)) / 2 */
+#define DION3_ACT_GELU_TANH 3   /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2 */
+#define DION3_ACT_SILU 4        /* z / (1 + exp(-z)) */
+
+#define DION3_MAX_TOKENS (1 << 24)
+
+/* The 8-bit format.  Columns are padded with zeros to mp = m rounded up to
+ * DION3_F8_BLOCK; Q holds T x mp bytes of e4m3 (contiguous), S one scale byte
+ * per block of DION3_F8_BLOCK columns (T x mp / DION3_F8_BLOCK, contiguous).
+ * A value is q * 2^(s - 127).  The scale is the smallest power of two
+ * that brings the block's largest finite magnitude to 448 or below (at least
+ * 2^-127), so that nothing saturates, and q is rounded to nearest even.
+ * Infinities and NaN become NaN and leave the scale alone.  In a block whose
+ * scale is the type's last (2^120; 2^8 for fp16) magnitudes end at 240
+ * scales, so that every value fits its type again. */
+#define DION3_F8_BLOCK 32
+
+/* h = X + R, rstd = 1 / sqrt(mean_j h_j^2 + eps), Y = h * rstd * w per row.
+ * H receives h rounded to dtype, and the statistics and Y are those of the
+ * rounded h.  R and H are both given, or both NULL (then h = X); H may be X
+ * or R.  w has m entries of wtype (DION3_F32 or dtype).  Outputs: Y and / or
+ * Q and S (the packed form of Y's rounded values), and rstd (T floats)
+ * unless NULL. */
+DION3_API dion3_status dion3_add_rms_norm(const void* X, int64_t ldx, const void* R, int64_t ldr,
+                                          const void* w, int32_t wtype, void* H, int64_t ldh,
+                                          void* Y, int64_t ldy, uint8_t* Q, uint8_t* S, float* rstd,
+                                          int64_t T, int64_t m, float eps, int32_t dtype,
+                                          void* stream);
+
+/* Its gradient, from h and rstd as the forward pass left them.  With a = w dY
+ * and u = h rstd: dX = rstd (a - u mean_j(a_j u_j)) + dH, the gradient of both
+ * X and R (dH: the gradient that reaches h past the norm, or NULL), and
+ * dw = sum over tokens of dY u.  dX and dw may each be NULL, not both; dX may
+ * be dY or dH. */
+DION3_API dion3_status dion3_add_rms_norm_grad_workspace_size(int64_t T, int64_t m, size_t* bytes);
+DION3_API dion3_status dion3_add_rms_norm_grad(const void* dY, int64_t lddy, const void* H,
+                                               int64_t ldh, const float* rstd, const void* w,
+                                               int32_t wtype, const void* dH, int64_t lddh, void* dX,
+                                               int64_t lddx, float* dw, int64_t T, int64_t m,
+                                               int32_t dtype, void* ws, size_t ws_bytes,
+                                               void* stream);
+
+/* X (dtype, or DION3_F32) into the 8-bit format, and its values back. */
+DION3_API dion3_status dion3_pack_f8(const void* X, int64_t ldx, uint8_t* Q, uint8_t* S, int64_t T,
+                                     int64_t m, int32_t dtype, void* stream);
+DION3_API dion3_status dion3_unpack_f8(const uint8_t* Q, const uint8_t* S, void* Y, int64_t ldy,
+                                       int64_t T, int64_t m, int32_t dtype, void* stream);
+
+/* z = X W^T + bias, Y = act(z) + R, with X: T x m, W: n x m, Y: T x n.  bias
+ * (n entries of bias_type, DION3_F32 or dtype), R (T x n) and Z may be NULL;
+ * Z receives z rounded to dtype (act reads it unrounded).  Y may be R.  The
+ * workspace depends on the pointers' alignment only, not on their contents. */
+DION3_API dion3_status dion3_linear_workspace_size(const void* X, int64_t ldx, const void* W,
+                                                   int64_t ldw, int64_t T, int64_t n, int64_t m,
+                                                   size_t* bytes);
+DION3_API dion3_status dion3_linear(const void* X, int64_t ldx, const void* W, int64_t ldw,
+                                    const void* bias, int32_t bias_type, const void* R, int64_t ldr,
+                                    void* Y, int64_t ldy, void* Z, int64_t ldz, int64_t T, int64_t n,
+                                    int64_t m, int32_t act, int32_t dtype, void* ws, size_t ws_bytes,
+                                    void* stream);
+
+/* dZ = dY act'(z) and db = sum over tokens of dY act'(z) (fp32, n entries,
+ * summed before dZ's rounding).  z comes from Z, or from its 8-bit form ZQ,
+ * ZS; neither is read for DION3_ACT_NONE.  dZ and db may each be NULL, not
+ * both; dZ may be dY or Z.  The workspace is used for db only. */
+DION3_API dion3_status dion3_act_grad_workspace_size(int64_t T, int64_t n, size_t* bytes);
+DION3_API dion3_status dion3_act_grad(const void* dY, int64_t lddy, const void* Z, int64_t ldz,
+                                      const uint8_t* ZQ, const uint8_t* ZS, void* dZ, int64_t lddz,
+                                      float* db, int64_t T, int64_t n, int32_t act, int32_t dtype,
+                                      void* ws, size_t ws_bytes, void* stream);
+
+/* dX = dZ W (+ R, T x m, or NULL), with dZ: T x n, W: n x m.  dX may be R. */
+DION3_API dion3_status dion3_linear_grad_input_workspace_size(const void* dZ, int64_t lddz,
+                                                              const void* W, int64_t ldw, int64_t T,
+                                                              int64_t n, int64_t m, size_t* bytes);
+DION3_API dion3_status dion3_linear_grad_input(const void* dZ, int64_t lddz, const void* W,
+                                               int64_t ldw, const void* R, int64_t ldr, void* dX,
+                                               int64_t lddx, int64_t T, int64_t n, int64_t m,
+                                               int32_t dtype, void* ws, size_t ws_bytes,
+                                               void* stream);
+
+/* G = dZ^T X, or with accumulate != 0 G <- G + dZ^T X, in fp32: dZ: T x n,
+ * G: n x m.  X is T x m of dtype when S is NULL; otherwise X and S are an
+ * 8-bit checkpoint (ldx is not read), whose values enter the product rounded
+ * to dtype (exact unless they leave its range).  G may be the momentum M of
+ * dion3_step. */
+DION3_API dion3_status dion3_linear_grad_weight_workspace_size(const void* dZ, int64_t lddz,
+                                                               const void* X, int64_t ldx,
+                                                               const uint8_t* S, int64_t T,
+                                                               int64_t n, int64_t m, size_t* bytes);
+DION3_API dion3_status dion3_linear_grad_weight(const void* dZ, int64_t lddz, const void* X,
+                                                int64_t ldx, const uint8_t* S, float* G, int64_t ldg,
+                                                int32_t accumulate, int64_t T, int64_t n, int64_t m,
+                                                int32_t dtype, void* ws, size_t ws_bytes,
+                                                void* stream);
+
 /* Kernel timing trace, for benchmarks.  dion3_trace_enable(capacity > 0)
  * creates 2 * capacity HIP events (no device memory) and starts recording:
  * each kernel the library then launches is timed by events on the caller's

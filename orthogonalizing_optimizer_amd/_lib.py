@@ -96,6 +96,27 @@ def _declare(lib):
                                                    c.POINTER(NsCfg), vp, vp, vp]),
         "dion3_syrk_f16": (c.c_int, [vp, vp, i32, i64, i64, i64, i64, vp]),
         "dion3_symm_f16": (c.c_int, [vp, vp, vp, vp, i32, i64, i64, f32, f32, f32, vp]),
+        "dion3_add_rms_norm": (c.c_int, [vp, i64, vp, i64, vp, i32, vp, i64, vp, i64, vp, vp, vp,
+                                         i64, i64, f32, i32, vp]),
+        "dion3_add_rms_norm_grad_workspace_size": (c.c_int, [i64, i64, c.POINTER(sz)]),
+        "dion3_add_rms_norm_grad": (c.c_int, [vp, i64, vp, i64, vp, vp, i32, vp, i64, vp, i64, vp,
+                                              i64, i64, i32, vp, sz, vp]),
+        "dion3_pack_f8": (c.c_int, [vp, i64, vp, vp, i64, i64, i32, vp]),
+        "dion3_unpack_f8": (c.c_int, [vp, vp, vp, i64, i64, i64, i32, vp]),
+        "dion3_linear_workspace_size": (c.c_int, [vp, i64, vp, i64, i64, i64, i64, c.POINTER(sz)]),
+        "dion3_linear": (c.c_int, [vp, i64, vp, i64, vp, i32, vp, i64, vp, i64, vp, i64, i64, i64,
+                                   i64, i32, i32, vp, sz, vp]),
+        "dion3_act_grad_workspace_size": (c.c_int, [i64, i64, c.POINTER(sz)]),
+        "dion3_act_grad": (c.c_int, [vp, i64, vp, i64, vp, vp, vp, i64, vp, i64, i64, i32, i32, vp,
+                                     sz, vp]),
+        "dion3_linear_grad_input_workspace_size": (c.c_int, [vp, i64, vp, i64, i64, i64, i64,
+                                                             c.POINTER(sz)]),
+        "dion3_linear_grad_input": (c.c_int, [vp, i64, vp, i64, vp, i64, vp, i64, i64, i64, i64,
+                                              i32, vp, sz, vp]),
+        "dion3_linear_grad_weight_workspace_size": (c.c_int, [vp, i64, vp, i64, vp, i64, i64, i64,
+                                                              c.POINTER(sz)]),
+        "dion3_linear_grad_weight": (c.c_int, [vp, i64, vp, i64, vp, vp, i64, i32, i64, i64, i64,
+                                               i32, vp, sz, vp]),
         "dion3_trace_enable": (c.c_int, [i32]),
         "dion3_trace_count": (i32, []),
         "dion3_trace_reset": (None, []),
@@ -116,7 +137,13 @@ EXPORTED = ("dion3_version", "dion3_ns_cfg_size", "dion3_ns_cfg_default", "dion3
             "dion3_step_megabatch", "dion3_step_accum", "dion3_step_megabatch_accum",
             "dion3_step_megabatch_norm", "dion3_group_size", "dion3_workspace_size_groups",
             "dion3_step_groups", "dion3_step_megabatch_noalloc",
-            "dion3_syrk_f16", "dion3_symm_f16", "dion3_trace_enable",
+            "dion3_syrk_f16", "dion3_symm_f16", "dion3_add_rms_norm",
+            "dion3_add_rms_norm_grad_workspace_size", "dion3_add_rms_norm_grad", "dion3_pack_f8",
+            "dion3_unpack_f8", "dion3_linear_workspace_size", "dion3_linear",
+            "dion3_act_grad_workspace_size", "dion3_act_grad",
+            "dion3_linear_grad_input_workspace_size", "dion3_linear_grad_input",
+            "dion3_linear_grad_weight_workspace_size", "dion3_linear_grad_weight",
+            "dion3_trace_enable",
             "dion3_trace_count", "dion3_trace_reset", "dion3_trace_record", "dion3_status_string",
             "dion3_last_hip_error")
 

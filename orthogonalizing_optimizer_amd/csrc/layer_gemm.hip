@@ -1,0 +1,762 @@
+// The products of a linear layer for gfx950: Y = act(X W^T + b) + R, its
+// input gradient dX = dZ W (+ R) and its weight gradient G (+)= dZ^T X with X
+// in 16 bits or in the 8-bit checkpoint format.  bf16 or fp16 operands on
+// the matrix cores (v_mfma_f32_32x32x16), fp32 accumulation, one rounding at
+// the end.
+//
+// One kernel computes C = A B^T by tiles, K 64 at a time through two LDS
+// buffers, for every layout the three products need.  An operand is staged
+// in one of three ways:
+//   * K-contiguous rows (X and W of the forward product, dZ of the input
+//     gradient): rows of 64 + 8 halves in LDS, fragments by 16-byte reads;
+//   * K as rows (W of the input gradient, dZ and X of the weight gradient):
+//     64 rows of R + 32 halves, fragments by transposing reads
+//     (ds_read_b64_tr_b16), so that no transposed copy is ever made;
+//   * K as rows in 8 bits: the same, decoded between the global load and the
+//     LDS store, two values an instruction (the scale is the instruction's
+//     operand), so the checkpoint crosses HBM and the caches at half the size.
+// Two tiles: 256 x 256 (8 waves of 128 x 64, one workgroup a CU) and 128 x
+// 128 (4 waves of 64 x 64, two workgroups a CU).  Each slice of 16 K issues
+// the next slice's LDS reads ahead of its MFMAs, the first one also the next
+// tile's LDS stores and the global loads of the tile after that.
+// Few tiles are split over K: each part leaves an fp32 tile in the scratch,
+// which k_lin_join adds up in order and finishes.
+// The epilogue passes the fp32 accumulators through LDS so that bias,
+// residual, outputs and the accumulated G move as 16-byte pieces of rows.
+#include "layer_internal.h"
+
+namespace dion3 {
+namespace {
+
+constexpr int BK = 64;
+constexpr int LDSK = BK + 8;      // halves per K-contiguous LDS row
+constexpr int kPadN = 32;         // halves of padding of a [K][R] LDS row
+
+typedef short short4v __attribute__((ext_vector_type(4)));
+typedef short short8 __attribute__((ext_vector_type(8)));
+typedef f16 half8 __attribute__((ext_vector_type(8)));
+typedef bf16 bfloat8 __attribute__((ext_vector_type(8)));
+typedef float floatx16 __attribute__((ext_vector_type(16)));
+typedef float floatx4 __attribute__((ext_vector_type(4)));
+typedef int int4v __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) short4v lds_short4;
+
+__device__ __forceinline__ floatx16 mfma32(f16, short8 a, short8 b, floatx16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8, a),
+                                                __builtin_bit_cast(half8, b), c, 0, 0, 0);
+}
+__device__ __forceinline__ floatx16 mfma32(bf16, short8 a, short8 b, floatx16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bfloat8, a),
+                                                 __builtin_bit_cast(bfloat8, b), c, 0, 0, 0);
+}
+__device__ __forceinline__ floatx4 mfma16(f16, short8 a, short8 b, floatx4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8, a),
+                                                __builtin_bit_cast(half8, b), c, 0, 0, 0);
+}
+__device__ __forceinline__ floatx4 mfma16(bf16, short8 a, short8 b, floatx4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bfloat8, a),
+                                                 __builtin_bit_cast(bfloat8, b), c, 0, 0, 0);
+}
+
+// Raw buffer over `bytes` bytes: loads past them return zero.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* base, int bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc((void*)base, (short)0, bytes, 0x00020000);
+}
+constexpr int kOut = (int)0x80000000;    // an offset past every buffer
+
+// What becomes of C.
+struct Finish {
+  void* Y; void* Z; const void* R; const void* bias;
+  float* G;
+  long long ldy, ldz, ldr, ldg;
+  int bias_f32, act, accumulate;
+  int N;
+};
+
+// Columns c .. c + 7 of output row r.
+template <class E, bool F32>
+__device__ __forceinline__ void finish8(const Finish& f, long long r, int c, float (&v)[8]) {
+  if constexpr (F32) {
+    float* g = f.G + r * f.ldg;
+    const bool vec = rows_aligned(f.G, f.ldg);
+    if (f.accumulate) {
+      float o[8];
+      load8((const float*)g, c, f.N, vec, o);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] += o[e];
+    }
+    store8(g, c, f.N, vec, v);
+  } else {
+    if (f.bias) {
+      float b[8];
+      if (f.bias_f32) load8((const float*)f.bias, c, f.N, rows_aligned((const float*)f.bias, 8), b);
+      else load8((const E*)f.bias, c, f.N, rows_aligned((const E*)f.bias, 8), b);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] += b[e];
+    }
+    if (f.Z) store8((E*)f.Z + r * f.ldz, c, f.N, rows_aligned((const E*)f.Z, f.ldz), v);
+    if (f.act != DION3_ACT_NONE) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = activate(f.act, v[e]);
+    }
+    if (f.R) {
+      float o[8];
+      load8((const E*)f.R + r * f.ldr, c, f.N, rows_aligned((const E*)f.R, f.ldr), o);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] += o[e];
+    }
+    store8((E*)f.Y + r * f.ldy, c, f.N, rows_aligned((const E*)f.Y, f.ldy), v);
+  }
+}
+
+struct LinP {
+  const void* A; const void* B; const unsigned char* bs;
+  long long lda, ldb;
+  long long M, K;
+  int N;
+  int tilesM, tilesN, splits, steps;   // steps: K steps of one split
+  long long total;                     // workgroups
+  float* part; long long part_stride;  // splits > 1: fp32 [split][M][ldp]
+  int ldp;
+  Finish f;
+};
+
+template <int BM_, int WAVES_M, int WAVES_N>
+struct Cfg {
+  static constexpr int BM = BM_, BN = BM_;
+  static constexpr int NT = 64 * WAVES_M * WAVES_N;
+  static constexpr int WTM = BM / WAVES_M, WTN = BN / WAVES_N;
+  static constexpr int FM = WTM / 32, FN = WTN / 32;
+  static constexpr int PART = (BM * LDSK > BK * (BM + kPadN)) ? BM * LDSK : BK * (BM + kPadN);
+  static constexpr int STAGE = 2 * PART;                     // halves
+  // epilogue staging: rows of BN + 8 floats; the 4 rows between a wave's two
+  // halves then lie 32 banks apart
+  static constexpr int EP = BN + 8;
+  static constexpr int EROWS = BM > 128 ? 128 : BM;          // rows staged at a time
+  static constexpr int EBYTES = EROWS * EP * 4;
+  static constexpr int BYTES = 2 * STAGE * 2 > EBYTES ? 2 * STAGE * 2 : EBYTES;
+};
+typedef Cfg<256, 2, 4> CfgL;
+typedef Cfg<128, 2, 2> CfgS;
+
+enum Kind { kRowsK = 0, kColsK = 1, kColsF8 = 2 };
+
+// One operand of R output rows: its registers, LDS part and fragments.
+template <class E, int R, int NT, int KIND>
+struct Operand {
+  static constexpr int RS = R + kPadN;                                 // [K][R] LDS row
+  static constexpr int CH = KIND == kColsF8 ? R * BK / 16 / NT : R * BK / 8 / NT;
+  static constexpr int LOADS = KIND == kColsF8 ? 2 * CH : CH;          // global loads a step
+  static constexpr int STORES = KIND == kColsF8 ? 2 * CH : CH;         // LDS stores a step
+  static constexpr int READS = KIND == kRowsK ? 1 : 2;                 // LDS reads a fragment
+  const char* base;      // kRowsK: the tile's first row; else column r0 of row 0
+  const unsigned char* sbase;
+  long long ld;          // bytes
+  long long K;
+  int bytes;             // kRowsK: of the tile's rows
+  int cols;              // else: bytes of a row that may be read
+  int scols;
+  int voff;
+  int4v reg[CH];
+  unsigned sreg[KIND == kColsF8 ? CH : 1];
+
+  __device__ __forceinline__ void init(const void* p, const unsigned char* sc, long long ldp,
+                                       long long rows, long long k, long long r0, int tid) {
+    K = k;
+    if constexpr (KIND == kRowsK) {
+      K = (k + 7) & ~7LL;        // rows end in whole chunks (zeros past K: see in_place)
+      ld = ldp * 2;
+      base = (const char*)p + r0 * ld;
+      const int n = (int)(rows - r0 < R ? rows - r0 : R);
+      bytes = (int)((n - 1) * ld + K * 2);
+      voff = (int)((tid >> 3) * ld) + (tid & 7) * 16;
+    } else if constexpr (KIND == kColsK) {
+      constexpr int CPR = R / 8;
+      ld = ldp * 2;
+      base = (const char*)p + r0 * 2;
+      cols = (int)(rows - r0 < R ? (rows - r0 + 7) & ~7LL : R) * 2;
+      voff = (int)((tid / CPR) * ld) + (tid % CPR) * 16;
+    } else {
+      constexpr int CPR = R / 16;
+      ld = ldp;
+      base = (const char*)p + r0;
+      sbase = sc + r0 / kF8Block;
+      cols = (int)(ldp - r0 < R ? ldp - r0 : R);        // (the pitch is whole blocks)
+      scols = cols / kF8Block;
+      voff = (int)((tid / CPR) * ld) + (tid % CPR) * 16;
+    }
+  }
+
+  // The tile's K rows / columns k0 .. k0 + 63 into registers (zero past K).
+  __device__ __forceinline__ void load(long long k0, int tid) {
+    if constexpr (KIND == kRowsK) {
+      const __amdgpu_buffer_rsrc_t rs = rsrc(base, bytes);
+      constexpr int STEP = NT / 8;
+      const int v = k0 + (tid & 7) * 8 < K ? voff + (int)k0 * 2 : kOut;
+#pragma unroll
+      for (int i = 0; i < CH; ++i)
+        reg[i] = __builtin_amdgcn_raw_buffer_load_b128(rs, v + i * STEP * (int)ld, 0, 0);
+    } else {
+      constexpr int CPR = KIND == kColsK ? R / 8 : R / 16;
+      constexpr int STEP = NT / CPR;
+      const long long left = K - k0;
+      const int n = left <= 0 ? 0 : left < BK ? (int)left : BK;        // valid rows
+      const __amdgpu_buffer_rsrc_t rs = rsrc(base + k0 * ld, n > 0 ? (int)((n - 1) * ld) + cols : 0);
+#pragma unroll
+      for (int i = 0; i < CH; ++i)
+        reg[i] = __builtin_amdgcn_raw_buffer_load_b128(rs, voff + i * STEP * (int)ld, 0, 0);
+      if constexpr (KIND == kColsF8) {
+        const int lds = (int)(ld / kF8Block);
+        const __amdgpu_buffer_rsrc_t ss =
+            rsrc(sbase + k0 * lds, n > 0 ? (n - 1) * lds + scols : 0);
+#pragma unroll
+        for (int i = 0; i < CH; ++i)
+          sreg[i] = (unsigned char)__builtin_amdgcn_raw_buffer_load_b8(
+              ss, (tid / CPR + i * STEP) * lds + (tid % CPR) / 2, 0, 0);
+      }
+    }
+  }
+
+  __device__ __forceinline__ void store(short* __restrict__ s, int tid) const {
+    if constexpr (KIND == kRowsK) {
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        const int c = tid + NT * i;
+        *(int4v*)(s + (c >> 3) * LDSK + (c & 7) * 8) = reg[i];
+      }
+    } else if constexpr (KIND == kColsK) {
+      constexpr int CPR = R / 8;
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        const int c = tid + NT * i;
+        *(int4v*)(s + (c / CPR) * RS + (c % CPR) * 8) = reg[i];
+      }
+    } else {
+      constexpr int CPR = R / 16;
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        const int c = tid + NT * i;
+        const float sc = f8_scale_float(sreg[i]);
+        short* d = s + (c / CPR) * RS + (c % CPR) * 16;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          int4v o;
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            const unsigned u = (unsigned)reg[i][2 * h + w];
+            o[2 * w] = __builtin_bit_cast(int, f8_decode2<false>(E(), u, sc));
+            o[2 * w + 1] = __builtin_bit_cast(int, f8_decode2<true>(E(), u, sc));
+          }
+          *(int4v*)(d + 8 * h) = o;
+        }
+      }
+    }
+  }
+
+  // This lane's offset into the part for the wave's rows w0 .., and the
+  // fragment (8 consecutive K of row lane % 32, from K = 8 (lane / 32)) of
+  // block i and slice kk.  Transposing reads: in each group of 16 lanes, lane
+  // 4 e + u points at row e, columns 4 u .. 4 u + 3 of a 4 x 16 block and
+  // receives that block's column lane % 16.
+  static __device__ __forceinline__ int frag_off(int w0, int lane) {
+    if constexpr (KIND == kRowsK) return (w0 + (lane & 31)) * LDSK + (lane >> 5) * 8;
+    return ((lane >> 5) * 8 + ((lane & 15) >> 2)) * RS + w0 + ((lane >> 4) & 1) * 16 + (lane & 3) * 4;
+  }
+  static __device__ __forceinline__ short8 frag(const short* p, int i, int kk) {
+    if constexpr (KIND == kRowsK) return *(const short8*)(p + i * 32 * LDSK + kk * 16);
+    const short* q = p + i * 32 + kk * 16 * RS;
+    const short4v lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4*)q);
+    const short4v hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4*)(q + 4 * RS));
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  }
+};
+
+// Scheduling-group masks of __builtin_amdgcn_sched_group_barrier.
+constexpr int kSgMfma = 0x008, kSgVmemRead = 0x020, kSgDsRead = 0x100, kSgDsWrite = 0x200;
+
+// Slice 0's order: MFMA q, then its share of the LDS stores and global loads.
+template <int NM, int NS, int NL, int Q>
+__device__ __forceinline__ void slice0_order() {
+  if constexpr (Q < NM) {
+    constexpr int w = ((Q + 1) * NS + NM - 1) / NM - (Q * NS + NM - 1) / NM;
+    constexpr int l = ((Q + 1) * NL + NM - 1) / NM - (Q * NL + NM - 1) / NM;
+    __builtin_amdgcn_sched_group_barrier(kSgMfma, 1, 0);
+    if constexpr (w > 0) __builtin_amdgcn_sched_group_barrier(kSgDsWrite, w, 0);
+    if constexpr (l > 0) __builtin_amdgcn_sched_group_barrier(kSgVmemRead, l, 0);
+    slice0_order<NM, NS, NL, Q + 1>();
+  }
+}
+
+template <class E, class C, int KA, int KB, bool STORE, bool LOAD, bool NEXT>
+__device__ __forceinline__ void k_step(const short* __restrict__ st, short* __restrict__ nxt,
+                                       Operand<E, C::BM, C::NT, KA>& A,
+                                       Operand<E, C::BN, C::NT, KB>& B, long long k_next, int tid,
+                                       int aoff, int boff, short8 (&fa0)[C::FM],
+                                       short8 (&fb0)[C::FN], floatx16 (&acc)[C::FM][C::FN]) {
+  typedef Operand<E, C::BM, C::NT, KA> OA;
+  typedef Operand<E, C::BN, C::NT, KB> OB;
+  constexpr int NS = BK / 16, NM = C::FM * C::FN;
+  constexpr int NR = OA::READS * C::FM + OB::READS * C::FN;
+  constexpr int NP = NM < NR ? NM : NR;
+  short8 af[2][C::FM], bf[2][C::FN];
+#pragma unroll
+  for (int i = 0; i < C::FM; ++i) af[0][i] = fa0[i];
+#pragma unroll
+  for (int j = 0; j < C::FN; ++j) bf[0][j] = fb0[j];
+#pragma unroll
+  for (int kk = 0; kk < NS; ++kk) {
+    const int cb = kk & 1;
+    if (kk + 1 < NS) {
+#pragma unroll
+      for (int i = 0; i < C::FM; ++i) af[cb ^ 1][i] = OA::frag(st + aoff, i, kk + 1);
+#pragma unroll
+      for (int j = 0; j < C::FN; ++j) bf[cb ^ 1][j] = OB::frag(st + C::PART + boff, j, kk + 1);
+    } else {
+      __syncthreads();
+      if (NEXT) {
+#pragma unroll
+        for (int i = 0; i < C::FM; ++i) fa0[i] = OA::frag(nxt + aoff, i, 0);
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j) fb0[j] = OB::frag(nxt + C::PART + boff, j, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (kk == 0 && STORE) {
+      A.store(nxt, tid);
+      B.store(nxt + C::PART, tid);
+    }
+    if (kk == 0 && LOAD) {
+      A.load(k_next, tid);
+      B.load(k_next, tid);
+    }
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+      for (int j = 0; j < C::FN; ++j) acc[i][j] = mfma32(E(), af[cb][i], bf[cb][j], acc[i][j]);
+    if (kk == 0) {
+      __builtin_amdgcn_sched_group_barrier(kSgDsRead, NR, 0);
+      slice0_order<NM, OA::STORES + OB::STORES, OA::LOADS + OB::LOADS, 0>();
+    } else if (kk + 1 < NS) {
+#pragma unroll
+      for (int q = 0; q < NP; ++q) {
+        __builtin_amdgcn_sched_group_barrier(kSgDsRead, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(kSgMfma, 1, 0);
+      }
+      if constexpr (NM > NP) __builtin_amdgcn_sched_group_barrier(kSgMfma, NM - NP, 0);
+      if constexpr (NR > NP) __builtin_amdgcn_sched_group_barrier(kSgDsRead, NR - NP, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
+// F32: C goes to G; PART: to the scratch (splits); else to Y.
+template <class E, class C, int KA, int KB, bool F32, bool PART>
+__global__ __launch_bounds__(C::NT, (C::BM == 256 ? 1 : 2)) void k_lin(LinP p) {
+  __shared__ __attribute__((aligned(16))) char lds_raw[C::BYTES];
+  short* lds = (short*)lds_raw;
+
+  // Workgroups go round-robin over the 8 XCDs; renumbered so that each XCD
+  // takes a contiguous run of tiles.  Within a split: groups of 8 tile rows,
+  // columns first, so that consecutive tiles share panels in that XCD's L2.
+  const int total = (int)p.total;
+  const int w = blockIdx.x, q = total >> 3, rem = total & 7, xcd = w & 7;
+  const int lid = xcd * q + min(xcd, rem) + (w >> 3);
+  const int tiles = p.tilesM * p.tilesN;
+  const int split = PART ? lid / tiles : 0;
+  const int t = lid - split * tiles;
+  constexpr int GR = 8;
+  const int g0 = (t / (GR * p.tilesN)) * GR;
+  const int gsz = min(p.tilesM - g0, GR);
+  const int r = t - g0 * p.tilesN;
+  const int bi = g0 + r % gsz, bj = r / gsz;
+  const long long m0 = (long long)bi * C::BM;
+  const int n0 = bj * C::BN;
+
+  const int tid = threadIdx.x, lane = tid & 63, wid = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wid / (C::BN / C::WTN), wn = wid % (C::BN / C::WTN);
+
+  floatx16 acc[C::FM][C::FN];
+#pragma unroll
+  for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+
+  {
+    const long long k0 = (long long)split * p.steps * BK;
+    long long k1 = k0 + (long long)p.steps * BK;
+    if (k1 > p.K) k1 = p.K;
+    const int nk = (int)((k1 - k0 + BK - 1) / BK);          // >= 1
+    typedef Operand<E, C::BM, C::NT, KA> OA;
+    typedef Operand<E, C::BN, C::NT, KB> OB;
+    OA A;
+    OB B;
+    A.init(p.A, nullptr, p.lda, p.M, p.K, m0, tid);
+    B.init(p.B, p.bs, p.ldb, p.N, p.K, n0, tid);
+    const int aoff = OA::frag_off(wm * C::WTM, lane), boff = OB::frag_off(wn * C::WTN, lane);
+    A.load(k0, tid);
+    B.load(k0, tid);
+    A.store(lds, tid);
+    B.store(lds + C::PART, tid);
+    if (nk > 1) {
+      A.load(k0 + BK, tid);
+      B.load(k0 + BK, tid);
+    }
+    __syncthreads();
+    short8 fa0[C::FM], fb0[C::FN];
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i) fa0[i] = OA::frag(lds + aoff, i, 0);
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j) fb0[j] = OB::frag(lds + C::PART + boff, j, 0);
+    int kt = 0;
+    for (; kt + 2 < nk; ++kt)
+      k_step<E, C, KA, KB, true, true, true>(lds + (kt & 1) * C::STAGE, lds + ((kt + 1) & 1) * C::STAGE,
+                                             A, B, k0 + (long long)(kt + 2) * BK, tid, aoff, boff,
+                                             fa0, fb0, acc);
+    if (kt + 1 < nk) {
+      k_step<E, C, KA, KB, true, false, true>(lds + (kt & 1) * C::STAGE, lds + ((kt + 1) & 1) * C::STAGE,
+                                              A, B, 0, tid, aoff, boff, fa0, fb0, acc);
+      ++kt;
+    }
+    // the last step's barrier also frees the LDS for the epilogue
+    k_step<E, C, KA, KB, false, false, false>(lds + (kt & 1) * C::STAGE, lds + ((kt + 1) & 1) * C::STAGE,
+                                              A, B, 0, tid, aoff, boff, fa0, fb0, acc);
+  }
+
+  // Accumulators of a 32 x 32 block: lane l, value v holds row 8 (v / 4) +
+  // 4 (l / 32) + v % 4, column l % 32.
+  float* S = (float*)lds_raw;
+  constexpr int CPR = C::BN / 8, RPP = C::NT / CPR;      // chunks a row, rows a pass
+#pragma unroll
+  for (int h = 0; h < C::BM / C::EROWS; ++h) {
+    if (h > 0) __syncthreads();
+    if (C::EROWS == C::BM || wm == h) {
+      const int rb = C::EROWS == C::BM ? wm * C::WTM : 0;
+#pragma unroll
+      for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+          for (int v = 0; v < 16; ++v)
+            S[(rb + i * 32 + 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3)) * C::EP + wn * C::WTN + j * 32 +
+              (lane & 31)] = acc[i][j][v];
+    }
+    __syncthreads();
+    const int c = (tid % CPR) * 8;
+    if (n0 + c < p.N) {
+#pragma unroll 4
+      for (int rr = tid / CPR; rr < C::EROWS; rr += RPP) {
+        const long long row = m0 + h * C::EROWS + rr;
+        if (row >= p.M) break;
+        float v[8];
+        const float4 a = *(const float4*)(S + rr * C::EP + c), b = *(const float4*)(S + rr * C::EP + c + 4);
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+        if constexpr (PART)
+          store8(p.part + split * p.part_stride + row * p.ldp, n0 + c, p.ldp, true, v);
+        else
+          finish8<E, F32>(p.f, row, n0 + c, v);
+      }
+    }
+  }
+}
+
+// The splits' tiles added in order, then the epilogue.  One chunk of 8
+// columns a thread, the scratch's rows numbered through.
+template <class E, bool F32>
+__global__ __launch_bounds__(256) void k_lin_join(const float* __restrict__ part, long long stride,
+                                                  int splits, long long M, unsigned nch, Finish f) {
+  const long long base = (long long)blockIdx.x * 256;
+  if (base + threadIdx.x >= M * nch) return;
+  const long long row0 = base / nch;
+  const unsigned c0 = (unsigned)(base - row0 * nch) + threadIdx.x;
+  const unsigned dr = c0 / nch;
+  const float* s = part + (base + threadIdx.x) * 8;
+  float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll 4
+  for (int i = 0; i < splits; ++i) {
+    const float4 a = *(const float4*)(s + i * stride), b = *(const float4*)(s + i * stride + 4);
+    v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
+    v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+  }
+  finish8<E, F32>(f, row0 + dr, (int)(c0 - dr * nch) * 8, v);
+}
+
+// No K at all (a gradient over no tokens): C = 0.
+template <class E, bool F32>
+__global__ __launch_bounds__(256) void k_lin_zero(long long M, unsigned nch, Finish f) {
+  const long long e = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (e >= M * nch) return;
+  float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  finish8<E, F32>(f, e / nch, (int)(e % nch) * 8, v);
+}
+
+// An operand that the kernel cannot read in place (rows not 16-byte aligned,
+// or a contiguous side that is no multiple of 8) copied into rows of a whole
+// number of chunks, zeros at their ends.  The copy moves the operand twice
+// more, a small part of the product's time except at few tokens.
+__global__ __launch_bounds__(256) void k_lin_copy(const unsigned short* __restrict__ src,
+                                                  long long ld, long long rows, int cols,
+                                                  unsigned nch, unsigned short* __restrict__ dst) {
+  const long long base = (long long)blockIdx.x * 256;
+  if (base + threadIdx.x >= rows * nch) return;
+  const long long row0 = base / nch;
+  const unsigned c0 = (unsigned)(base - row0 * nch) + threadIdx.x;
+  const unsigned dr = c0 / nch;
+  const int c = (int)(c0 - dr * nch) * 8;
+  const unsigned short* s = src + (row0 + dr) * ld;
+  unsigned short v[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = c + e < cols ? s[c + e] : 0;
+  int4v o;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) o[e] = (int)(v[2 * e] | (unsigned)v[2 * e + 1] << 16);
+  *(int4v*)(dst + (base + threadIdx.x) * 8) = o;
+}
+
+// ------------------------------------------------------------- few tokens
+
+// Y for at most 16 tokens: bound by reading W once.  A workgroup takes 16
+// rows of W, its 8 waves the K axis in turns of 128; a lane reads 64
+// contiguous bytes of one W row (four chunks, one per MFMA: the order of K
+// inside the product is free as long as both operands agree) and the same
+// columns of its token.  The waves' 16 x 16 sums join in LDS in wave order.
+// VEC: both operands readable in 16-byte chunks; else element by element.
+struct ThinP {
+  const void* X; const void* W;
+  long long ldx, ldw, N;
+  int T, K;
+  Finish f;
+};
+
+template <class E, bool VEC>
+__device__ __forceinline__ short8 thin_chunk(__amdgpu_buffer_rsrc_t rs, int row_off, int k, int K) {
+  if constexpr (VEC) {
+    const int4v v = __builtin_amdgcn_raw_buffer_load_b128(rs, k < K ? row_off + k * 2 : kOut, 0, 0);
+    return __builtin_bit_cast(short8, v);
+  } else {
+    short8 o;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      o[e] = (short)__builtin_amdgcn_raw_buffer_load_b16(rs, k + e < K ? row_off + (k + e) * 2 : kOut, 0, 0);
+    return o;
+  }
+}
+
+template <class E, bool VEC>
+__global__ __launch_bounds__(512) void k_lin_thin(ThinP p) {
+  constexpr int NW = 8, U = VEC ? 2 : 1;
+  __shared__ float sh[NW][16][17];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const long long n0 = (long long)blockIdx.x * 16;
+  const int nrows = (int)(p.N - n0 < 16 ? p.N - n0 : 16);
+  const __amdgpu_buffer_rsrc_t rw =
+      rsrc((const E*)p.W + n0 * p.ldw, (int)((nrows - 1) * p.ldw + p.K) * 2);
+  const __amdgpu_buffer_rsrc_t rx = rsrc(p.X, (int)((p.T - 1) * p.ldx + p.K) * 2);
+  const int r = lane & 15, g = lane >> 4;
+  const int wo = r < nrows ? (int)(r * p.ldw) * 2 : 0, xo = r < p.T ? (int)(r * p.ldx) * 2 : 0;
+  const int wK = r < nrows ? p.K : 0, xK = r < p.T ? p.K : 0;
+  floatx4 acc = {0, 0, 0, 0};
+  for (int k0 = wave * 128; k0 < p.K; k0 += NW * 128 * U) {
+    short8 a[U][4], b[U][4];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int k = k0 + u * NW * 128 + g * 32 + i * 8;
+        a[u][i] = thin_chunk<E, VEC>(rw, wo, k, wK);
+        b[u][i] = thin_chunk<E, VEC>(rx, xo, k, xK);
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc = mfma16(E(), a[u][i], b[u][i], acc);
+  }
+  // lane l, value v: W row 4 (l / 16) + v, token l % 16
+#pragma unroll
+  for (int v = 0; v < 4; ++v) sh[wave][r][g * 4 + v] = acc[v];
+  __syncthreads();
+  // thread: token t, 8 of the 16 rows
+  const int t = threadIdx.x >> 1, c = (threadIdx.x & 1) * 8;
+  if (t < p.T && n0 + c < p.N) {
+    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    for (int w = 0; w < NW; ++w)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] += sh[w][t][c + e];
+    finish8<E, false>(p.f, t, (int)n0 + c, v);
+  }
+}
+
+constexpr int kThinTokens = 16;
+
+// ------------------------------------------------------------- host side
+
+// Rows of an operand as the kernel reads it.
+bool in_place(const void* p, long long ld, long long contiguous) {
+  return ((uintptr_t)p & 15) == 0 && ld % 8 == 0 && contiguous % 8 == 0;
+}
+
+struct LinPlan {
+  bool thin, large;
+  int splits, steps;
+  bool copyA, copyB;
+  long long rowsA, colsA, rowsB, colsB;     // as stored
+  size_t oA, oB, oP, total;
+  int ldp;
+};
+
+long long up8(long long x) { return pad_to(x, 8); }
+
+// Tile and splits by an estimate of the time: rounds of workgroups over the
+// 256 CUs (one large tile or two small ones a CU) times the K steps of one,
+// plus each workgroup's fixed part, plus the join's traffic.
+void choose_tile(LinPlan& q, long long M, long long N, long long K) {
+  const long long nk = (K + BK - 1) / BK;
+  double best = 1e30;
+  for (int large = 0; large < 2; ++large) {
+    const int b = large ? 256 : 128;
+    const long long tiles = ((M + b - 1) / b) * ((N + b - 1) / b);
+    const double step = large ? 1.9 : 1.3, fixed = large ? 14.0 : 8.0;
+    const long long slots = large ? 256 : 512;
+    for (long long sp = 1; sp <= 64 && sp <= nk; ++sp) {
+      if (sp > 1 && tiles * sp > 8 * slots) break;
+      const long long steps = (nk + sp - 1) / sp;
+      if ((nk + steps - 1) / steps != sp) continue;           // the same steps as fewer splits
+      const double rounds = (double)((tiles * sp + slots - 1) / slots);
+      double us = rounds * (steps * step + fixed);
+      if (sp > 1) us += 4.0 + 8.0 * (double)sp * M * N / 4.0e6;
+      if (us < best) {
+        best = us;
+        q.large = large;
+        q.splits = (int)sp;
+        q.steps = (int)steps;
+      }
+    }
+  }
+}
+
+LinPlan lin_plan(const LinDesc& d) {
+  LinPlan q = {};
+  if (d.M == 0 || d.K == 0) return q;
+  q.rowsA = d.a_km ? d.K : d.M; q.colsA = d.a_km ? d.M : d.K;
+  q.rowsB = d.b_kn ? d.K : d.N; q.colsB = d.b_kn ? d.N : d.K;
+  // (the thin kernel addresses its 16 rows by 32-bit offsets: see lin_fits)
+  q.thin = !d.a_km && !d.b_kn && !d.G && d.M <= kThinTokens;
+  if (q.thin) return q;
+  q.copyA = !in_place(d.A, d.lda, q.colsA);
+  q.copyB = !d.bs && !in_place(d.B, d.ldb, q.colsB);
+  choose_tile(q, d.M, d.N, d.K);
+  size_t off = 0;
+  auto take = [&](size_t b) { const size_t o = off; off = (off + b + 255) & ~(size_t)255; return o; };
+  if (q.copyA) q.oA = take((size_t)q.rowsA * up8(q.colsA) * 2);
+  if (q.copyB) q.oB = take((size_t)q.rowsB * up8(q.colsB) * 2);
+  q.ldp = (int)up8(d.N);
+  if (q.splits > 1) q.oP = take((size_t)q.splits * d.M * q.ldp * 4);
+  q.total = off;
+  return q;
+}
+
+template <class E, class C, int KA, int KB, bool F32>
+hipError_t launch_tiles(const LinP& p, hipStream_t s) {
+  if (p.splits > 1)
+    hipLaunchKernelGGL((k_lin<E, C, KA, KB, F32, true>), dim3((unsigned)p.total), dim3(C::NT), 0, s, p);
+  else
+    hipLaunchKernelGGL((k_lin<E, C, KA, KB, F32, false>), dim3((unsigned)p.total), dim3(C::NT), 0, s, p);
+  return hipGetLastError();
+}
+
+template <class E, int KA, int KB, bool F32>
+hipError_t launch_cfg(LinP p, bool large, hipStream_t s) {
+  const int b = large ? 256 : 128;
+  p.tilesM = (int)((p.M + b - 1) / b);
+  p.tilesN = (p.N + b - 1) / b;
+  p.total = (long long)p.tilesM * p.tilesN * p.splits;
+  if (p.total > 0x7fffffffLL) return hipErrorInvalidValue;
+  return large ? launch_tiles<E, CfgL, KA, KB, F32>(p, s) : launch_tiles<E, CfgS, KA, KB, F32>(p, s);
+}
+
+template <class E>
+hipError_t launch_lin_t(const LinDesc& d, void* ws, hipStream_t s) {
+  const LinPlan q = lin_plan(d);
+  Finish f = {d.Y, d.Z, d.R, d.bias, d.G, d.ldy, d.ldz, d.ldr, d.ldg,
+              d.bias_type == DION3_F32, d.act, d.accumulate, (int)d.N};
+  const unsigned nch = (unsigned)(up8(d.N) / 8);
+  if (d.M == 0) return hipSuccess;
+  if (d.K == 0) {
+    if (d.accumulate) return hipSuccess;
+    const dim3 grid((unsigned)((d.M * nch + 255) / 256));
+    hipLaunchKernelGGL((k_lin_zero<E, true>), grid, dim3(256), 0, s, d.M, nch, f);
+    return hipGetLastError();
+  }
+  const double flops = 2.0 * (double)d.M * d.N * d.K;
+  if (q.thin) {
+    const ThinP p = {d.A, d.B, d.lda, d.ldb, d.N, (int)d.M, (int)d.K, f};
+    TraceScope ts("linear_thin", flops, 2.0 * (double)d.N * d.K, s);
+    const dim3 grid((unsigned)((d.N + 15) / 16));
+    if (in_place(d.A, d.lda, d.K) && in_place(d.B, d.ldb, d.K))
+      hipLaunchKernelGGL((k_lin_thin<E, true>), grid, dim3(512), 0, s, p);
+    else
+      hipLaunchKernelGGL((k_lin_thin<E, false>), grid, dim3(512), 0, s, p);
+    return hipGetLastError();
+  }
+  LinP p = {};
+  p.A = d.A; p.B = d.B; p.bs = d.bs; p.lda = d.lda; p.ldb = d.ldb;
+  auto copy = [&](const void* src, long long ld, long long rows, long long cols, size_t o) {
+    const unsigned n = (unsigned)(up8(cols) / 8);
+    unsigned short* dst = (unsigned short*)((char*)ws + o);
+    TraceScope ts("linear_copy", 0.0, 4.0 * (double)rows * cols, s);
+    hipLaunchKernelGGL(k_lin_copy, dim3((unsigned)((rows * n + 255) / 256)), dim3(256), 0, s,
+                       (const unsigned short*)src, ld, rows, (int)cols, n, dst);
+    return hipGetLastError();
+  };
+  // (A and B may be one array read two ways: each takes its own copy)
+  if (q.copyA) {
+    const hipError_t e = copy(d.A, d.lda, q.rowsA, q.colsA, q.oA);
+    if (e != hipSuccess) return e;
+    p.A = (char*)ws + q.oA;
+    p.lda = up8(q.colsA);
+  }
+  if (q.copyB) {
+    const hipError_t e = copy(d.B, d.ldb, q.rowsB, q.colsB, q.oB);
+    if (e != hipSuccess) return e;
+    p.B = (char*)ws + q.oB;
+    p.ldb = up8(q.colsB);
+  }
+  // K-contiguous operands end in whole chunks: a copy's are zero past K, and
+  // a K of the other operand's rows past the true K reads zeros either way
+  p.M = d.M; p.N = (int)d.N; p.K = d.K;
+  p.splits = q.splits; p.steps = q.steps;
+  p.part = (float*)((char*)ws + q.oP);
+  p.part_stride = d.M * q.ldp;
+  p.ldp = q.ldp;
+  p.f = f;
+  hipError_t e;
+  {
+    TraceScope ts(d.name, flops, 0.0, s);
+    if (d.bs) e = launch_cfg<E, kColsK, kColsF8, true>(p, q.large, s);
+    else if (d.G) e = launch_cfg<E, kColsK, kColsK, true>(p, q.large, s);
+    else if (d.b_kn) e = launch_cfg<E, kRowsK, kColsK, false>(p, q.large, s);
+    else e = launch_cfg<E, kRowsK, kRowsK, false>(p, q.large, s);
+  }
+  if (e != hipSuccess || q.splits == 1) return e;
+  TraceScope ts("linear_join", 0.0, 4.0 * (double)q.splits * d.M * d.N, s);
+  const dim3 grid((unsigned)((d.M * nch + 255) / 256));
+  if (d.G)
+    hipLaunchKernelGGL((k_lin_join<E, true>), grid, dim3(256), 0, s, p.part, p.part_stride, q.splits,
+                       d.M, nch, f);
+  else
+    hipLaunchKernelGGL((k_lin_join<E, false>), grid, dim3(256), 0, s, p.part, p.part_stride, q.splits,
+                       d.M, nch, f);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t lin_scratch(const LinDesc& d) { return lin_plan(d).total; }
+
+hipError_t launch_lin(const LinDesc& d, void* ws, hipStream_t s) {
+  return d.dtype == DION3_BF16 ? launch_lin_t<bf16>(d, ws, s) : launch_lin_t<f16>(d, ws, s);
+}
+
+}  // namespace dion3

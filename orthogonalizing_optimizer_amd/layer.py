@@ -1,0 +1,369 @@
+"""Operators of the layers whose weights the optimizer steps.
+
+The norm before a linear layer with the residual's addition
+(``add_rms_norm``), the layer's product with bias, activation and residual in
+its epilogue (``linear``), their gradients, and activations kept in 8 bits
+between the forward and the backward pass (``pack_f8``, ``PackedF8``).  Every
+function is one call of libdion3.so (include/dion3.h states the formulas);
+nothing here computes, and there is no fallback.
+
+Tensors are [..., features] on one GPU, bf16 or fp16, with contiguous
+features; leading dimensions that share one stride (any row stride) are
+flattened without a copy.  Calls run on torch's current stream of the
+tensors' device.  Workspaces come from torch's allocator per call, so calls
+on several streams or inside several captured graphs never share one; pass
+``ws`` to manage the memory yourself.
+
+``rms_norm_residual`` and ``linear_layer`` are the differentiable forms; the
+latter can keep its inputs in 8 bits and sum its weight gradient straight
+into the momentum of ``Dion3`` (see there).
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional
+
+import torch
+
+from . import _lib
+
+F8_BLOCK = 32
+_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+
+
+# ------------------------------------------------------------------ arguments
+
+def _t16(t, name):
+    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+        raise TypeError(f"{name} must be a CUDA (HIP) tensor")
+    if t.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"{name} must be bfloat16 or float16")
+
+
+def _same(t, like, name, shape=None):
+    """t shares like's device and type (and has `shape`)."""
+    if not isinstance(t, torch.Tensor) or t.device != like.device:
+        raise TypeError(f"{name} must be a tensor on {like.device}")
+    if t.dtype != like.dtype:
+        raise TypeError(f"{name} must be {like.dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+
+
+def _vector(v, n, like, name):
+    if not isinstance(v, torch.Tensor) or v.device != like.device:
+        raise TypeError(f"{name} must be a tensor on {like.device}")
+    if v.dtype not in (torch.float32, like.dtype):
+        raise TypeError(f"{name} must be float32 or {like.dtype}")
+    if v.dim() != 1 or v.shape[0] != n or (n > 1 and v.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous vector of {n} entries")
+
+
+def _rows(t, name):
+    """(rows, features, row stride) of a [..., features] tensor."""
+    if t.dim() < 1:
+        raise ValueError(f"{name} must have at least one dimension")
+    m = t.shape[-1]
+    if m < 1:
+        raise ValueError(f"{name} needs at least one feature")
+    if m > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must have contiguous features")
+    rows, ld = 1, None
+    for size, stride in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if size == 1:
+            continue
+        if ld is None:
+            ld = stride
+        elif size > 0 and rows > 0 and stride != ld * rows:
+            raise ValueError(f"{name}: its leading dimensions do not share one stride")
+        rows *= size
+    if rows <= 1:
+        ld = max(m, 1) if ld is None or ld < m else ld
+    elif ld < m:
+        raise ValueError(f"{name}: its rows overlap")
+    return rows, m, ld
+
+
+def _act(act):
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {', '.join(ACTIVATIONS)}")
+    return ACTIVATIONS[act]
+
+
+def _ptr(t):
+    return None if t is None or t.numel() == 0 else t.data_ptr()
+
+
+def _scratch(ws, nbytes, device):
+    """(pointer, bytes, what keeps it alive)."""
+    if nbytes == 0:
+        return None, 0, None
+    if ws is not None:
+        p, n = ws.get(nbytes, device)
+        return p, n, ws
+    buf = torch.empty(nbytes + 256, dtype=torch.uint8, device=device)
+    off = (-buf.data_ptr()) % 256
+    return buf.data_ptr() + off, nbytes, buf
+
+
+def _size(fn, *args):
+    out = ctypes.c_size_t(0)
+    _lib._check(getattr(_lib.lib(), fn)(*args, ctypes.byref(out)), fn)
+    return int(out.value)
+
+
+def _call(fn, device, *args):
+    with torch.cuda.device(device):
+        _lib._check(getattr(_lib.lib(), fn)(*args, _lib._stream(device)), fn)
+
+
+# --------------------------------------------------------- the 8-bit format
+
+class PackedF8:
+    """An activation held in 8 bits: ``q`` (e4m3, [rows, cols rounded up to
+    32]) and ``scale`` (uint8, one exponent byte per 32 columns of a row);
+    a value is q * 2^(scale - 127).  ``shape`` is the shape of the tensor it
+    stands for (default: [rows, cols])."""
+
+    def __init__(self, q, scale, cols: int, shape=None):
+        cp = -(-int(cols) // F8_BLOCK) * F8_BLOCK
+        if not isinstance(q, torch.Tensor) or q.device.type != "cuda":
+            raise TypeError("q must be a CUDA (HIP) tensor")
+        if q.dtype != torch.float8_e4m3fn:
+            raise TypeError("q must be float8_e4m3fn")
+        if not isinstance(scale, torch.Tensor) or scale.device != q.device:
+            raise TypeError(f"scale must be a tensor on {q.device}")
+        if scale.dtype != torch.uint8:
+            raise TypeError("scale must be uint8")
+        if cols < 1 or q.dim() != 2 or q.shape[1] != cp or not q.is_contiguous():
+            raise ValueError(f"q must be contiguous [rows, {cp}]")
+        if tuple(scale.shape) != (q.shape[0], cp // F8_BLOCK) or not scale.is_contiguous():
+            raise ValueError(f"scale must be contiguous [{q.shape[0]}, {cp // F8_BLOCK}]")
+        if q.numel() and q.data_ptr() % 16:
+            raise ValueError("q must be 16-byte aligned")
+        self.q, self.scale, self.rows, self.cols = q, scale, q.shape[0], int(cols)
+        self.shape = torch.Size(shape) if shape is not None else torch.Size((self.rows, self.cols))
+        if self.shape[-1] != self.cols or self.shape.numel() != self.rows * self.cols:
+            raise ValueError("shape does not hold these rows and columns")
+
+    @property
+    def device(self):
+        return self.q.device
+
+    @property
+    def nbytes(self) -> int:
+        return self.q.numel() + self.scale.numel()
+
+
+def _empty_packed(rows, cols, shape, device):
+    cp = -(-cols // F8_BLOCK) * F8_BLOCK
+    return PackedF8(torch.empty((rows, cp), dtype=torch.float8_e4m3fn, device=device),
+                    torch.empty((rows, cp // F8_BLOCK), dtype=torch.uint8, device=device),
+                    cols, shape)
+
+
+def pack_f8(x) -> PackedF8:
+    """x ([..., features], bf16, fp16 or fp32) in the 8-bit format."""
+    if not isinstance(x, torch.Tensor) or x.device.type != "cuda":
+        raise TypeError("x must be a CUDA (HIP) tensor")
+    if x.dtype not in _DTYPES:
+        raise TypeError("x must be bfloat16, float16 or float32")
+    T, m, ld = _rows(x, "x")
+    p = _empty_packed(T, m, x.shape, x.device)
+    _call("dion3_pack_f8", x.device, _ptr(x), ld, _ptr(p.q), _ptr(p.scale), T, m, _DTYPES[x.dtype])
+    return p
+
+
+def unpack_f8(p: PackedF8, dtype=torch.bfloat16):
+    """The values that ``p`` stands for, in bf16, fp16 or fp32."""
+    if not isinstance(p, PackedF8):
+        raise TypeError("p must be a PackedF8")
+    if dtype not in _DTYPES:
+        raise TypeError("dtype must be bfloat16, float16 or float32")
+    y = torch.empty(p.shape, dtype=dtype, device=p.device)
+    _call("dion3_unpack_f8", p.device, _ptr(p.q), _ptr(p.scale), _ptr(y), p.cols, p.rows, p.cols,
+          _DTYPES[dtype])
+    return y
+
+
+# ------------------------------------------------------------------- the norm
+
+def add_rms_norm(x, weight, residual=None, eps: float = 1e-6, pack: bool = False,
+                 return_y: bool = True):
+    """(y, h, rstd, packed): h = x + residual rounded to x's type (x itself
+    without a residual), rstd = 1 / sqrt(mean h^2 + eps) per row (fp32),
+    y = h rstd weight, and with ``pack`` the 8-bit form of y.  ``weight`` is
+    fp32 or of x's type.  ``return_y=False`` leaves y out (None)."""
+    _t16(x, "x")
+    T, m, ldx = _rows(x, "x")
+    _vector(weight, m, x, "weight")
+    h, ldr, ldh = x, 0, 0
+    if residual is not None:
+        _same(residual, x, "residual", x.shape)
+        _, _, ldr = _rows(residual, "residual")
+        h, ldh = torch.empty(x.shape, dtype=x.dtype, device=x.device), m
+    if not return_y and not pack:
+        raise ValueError("ask for y, its 8-bit form or both")
+    y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if return_y else None
+    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    p = _empty_packed(T, m, x.shape, x.device) if pack else None
+    _call("dion3_add_rms_norm", x.device, _ptr(x), ldx, _ptr(residual), ldr, weight.data_ptr(),
+          _DTYPES[weight.dtype], None if residual is None else _ptr(h), ldh, _ptr(y), m,
+          _ptr(p.q) if p else None, _ptr(p.scale) if p else None, _ptr(rstd), T, m, float(eps),
+          _DTYPES[x.dtype])
+    return y, h, rstd, p
+
+
+def add_rms_norm_grad(dy, h, rstd, weight, dh=None, need_dx: bool = True, need_dw: bool = True,
+                      ws: Optional[_lib.Workspace] = None):
+    """(dx, dweight) of ``add_rms_norm``: dx, the gradient of both x and the
+    residual, includes ``dh``, the gradient that reaches h past the norm;
+    dweight is fp32.  What is not needed comes back as None."""
+    _t16(dy, "dy")
+    T, m, ldy = _rows(dy, "dy")
+    _same(h, dy, "h", dy.shape)
+    _, _, ldh = _rows(h, "h")
+    _vector(weight, m, dy, "weight")
+    if (not isinstance(rstd, torch.Tensor) or rstd.device != dy.device
+            or rstd.dtype != torch.float32):
+        raise TypeError(f"rstd must be a float32 tensor on {dy.device}")
+    if tuple(rstd.shape) != tuple(dy.shape[:-1]) or not rstd.is_contiguous():
+        raise ValueError("rstd must be contiguous, one entry per row")
+    lddh = 0
+    if dh is not None:
+        _same(dh, dy, "dh", dy.shape)
+        _, _, lddh = _rows(dh, "dh")
+    if not need_dx and not need_dw:
+        return None, None
+    dx = torch.empty(dy.shape, dtype=dy.dtype, device=dy.device) if need_dx else None
+    dw = torch.empty(m, dtype=torch.float32, device=dy.device) if need_dw else None
+    p, nb, keep = _scratch(ws, _size("dion3_add_rms_norm_grad_workspace_size", T, m), dy.device)
+    _call("dion3_add_rms_norm_grad", dy.device, _ptr(dy), ldy, _ptr(h), ldh, _ptr(rstd),
+          weight.data_ptr(), _DTYPES[weight.dtype], _ptr(dh), lddh, _ptr(dx), m, _ptr(dw), T, m,
+          _DTYPES[dy.dtype], p, nb)
+    return dx, dw
+
+
+# ------------------------------------------------------------ linear products
+
+def _matrix(w, like, name):
+    _same(w, like, name)
+    if w.dim() != 2:
+        raise ValueError(f"{name} must be [n, m]")
+    n, m, ld = _rows(w, name)
+    if n < 1:
+        raise ValueError(f"{name} needs at least one row")
+    return n, m, ld
+
+
+def linear(x, w, bias=None, act: str = "none", residual=None, return_preact: bool = False,
+           ws: Optional[_lib.Workspace] = None):
+    """(y, z): z = x w^T + bias and y = act(z) + residual, with w [n, m] of
+    x's type, ``bias`` fp32 or of x's type.  z comes back rounded with
+    ``return_preact`` (for ``act_grad``), else as None."""
+    _t16(x, "x")
+    T, m, ldx = _rows(x, "x")
+    n, wm, ldw = _matrix(w, x, "w")
+    if wm != m:
+        raise ValueError(f"w must have {m} columns")
+    a = _act(act)
+    shape = x.shape[:-1] + (n,)
+    if bias is not None:
+        _vector(bias, n, x, "bias")
+    ldr = 0
+    if residual is not None:
+        _same(residual, x, "residual", shape)
+        _, _, ldr = _rows(residual, "residual")
+    y = torch.empty(shape, dtype=x.dtype, device=x.device)
+    z = torch.empty(shape, dtype=x.dtype, device=x.device) if return_preact else None
+    p, nb, keep = _scratch(ws, _size("dion3_linear_workspace_size", _ptr(x), ldx, w.data_ptr(), ldw,
+                                     T, n, m), x.device)
+    _call("dion3_linear", x.device, _ptr(x), ldx, w.data_ptr(), ldw, _ptr(bias),
+          _DTYPES[bias.dtype] if bias is not None else 0, _ptr(residual), ldr, _ptr(y), n, _ptr(z),
+          n, T, n, m, a, _DTYPES[x.dtype], p, nb)
+    return y, z
+
+
+def act_grad(dy, z, act: str, bias: bool = False, ws: Optional[_lib.Workspace] = None):
+    """(dz, db): dz = dy act'(z) and with ``bias`` the sum of its rows (fp32,
+    before rounding; else None).  z is the preactivation or its PackedF8, and
+    may be None for "none", where dz is dy itself."""
+    _t16(dy, "dy")
+    T, n, ldy = _rows(dy, "dy")
+    a = _act(act)
+    zp = zq = zs = None
+    ldz = 0
+    if act != "none":
+        if isinstance(z, PackedF8):
+            if z.device != dy.device or tuple(z.shape) != tuple(dy.shape):
+                raise ValueError(f"z must have shape {tuple(dy.shape)} on {dy.device}")
+            zq, zs = _ptr(z.q), _ptr(z.scale)
+        else:
+            _same(z, dy, "z", dy.shape)
+            _, _, ldz = _rows(z, "z")
+            zp = _ptr(z)
+    dz = torch.empty(dy.shape, dtype=dy.dtype, device=dy.device) if act != "none" else None
+    db = torch.empty(n, dtype=torch.float32, device=dy.device) if bias else None
+    if dz is not None or db is not None:
+        p, nb, keep = _scratch(ws, _size("dion3_act_grad_workspace_size", T, n) if bias else 0,
+                               dy.device)
+        _call("dion3_act_grad", dy.device, _ptr(dy), ldy, zp, ldz, zq, zs, _ptr(dz), n, _ptr(db), T,
+              n, a, _DTYPES[dy.dtype], p, nb)
+    return (dz if dz is not None else dy), db
+
+
+def linear_grad_input(dz, w, residual=None, ws: Optional[_lib.Workspace] = None):
+    """dx = dz w (+ residual, another branch's gradient of the same x)."""
+    _t16(dz, "dz")
+    T, n, lddz = _rows(dz, "dz")
+    wn, m, ldw = _matrix(w, dz, "w")
+    if wn != n:
+        raise ValueError(f"w must have {n} rows")
+    shape = dz.shape[:-1] + (m,)
+    ldr = 0
+    if residual is not None:
+        _same(residual, dz, "residual", shape)
+        _, _, ldr = _rows(residual, "residual")
+    dx = torch.empty(shape, dtype=dz.dtype, device=dz.device)
+    p, nb, keep = _scratch(ws, _size("dion3_linear_grad_input_workspace_size", _ptr(dz), lddz,
+                                     w.data_ptr(), ldw, T, n, m), dz.device)
+    _call("dion3_linear_grad_input", dz.device, _ptr(dz), lddz, w.data_ptr(), ldw, _ptr(residual),
+          ldr, _ptr(dx), m, T, n, m, _DTYPES[dz.dtype], p, nb)
+    return dx
+
+
+def linear_grad_weight(dz, x, out=None, accumulate: bool = False,
+                       ws: Optional[_lib.Workspace] = None):
+    """dz^T x in fp32 ([n, m]); x is the layer's input or its PackedF8.  With
+    ``out`` (fp32, contiguous rows) it is written there, and with
+    ``accumulate`` added to it: ``out`` may be the optimizer's momentum."""
+    _t16(dz, "dz")
+    T, n, lddz = _rows(dz, "dz")
+    lead = tuple(dz.shape[:-1])
+    if isinstance(x, PackedF8):
+        if x.device != dz.device:
+            raise TypeError(f"x must be on {dz.device}")
+        if x.rows != T or (tuple(x.shape[:-1]) != lead and len(lead) != 1):
+            raise ValueError("x must have dz's rows")
+        m, ldx, xp, sp = x.cols, x.cols, _ptr(x.q), _ptr(x.scale)
+    else:
+        _same(x, dz, "x")
+        if tuple(x.shape[:-1]) != lead:
+            raise ValueError("x must have dz's rows")
+        _, m, ldx = _rows(x, "x")
+        xp, sp = _ptr(x), None
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs out")
+        out = torch.empty((n, m), dtype=torch.float32, device=dz.device)
+    if not isinstance(out, torch.Tensor) or out.device != dz.device or out.dtype != torch.float32:
+        raise TypeError(f"out must be a float32 tensor on {dz.device}")
+    if tuple(out.shape) != (n, m):
+        raise ValueError(f"out must have shape {(n, m)}")
+    _, _, ldg = _rows(out, "out")
+    p, nb, keep = _scratch(ws, _size("dion3_linear_grad_weight_workspace_size", _ptr(dz), lddz, xp,
+                                     ldx, sp, T, n, m), dz.device)
+    _call("dion3_linear_grad_weight", dz.device, _ptr(dz), lddz, xp, ldx, sp, out.data_ptr(), ldg,
+          int(bool(accumulate)), T, n, m, _DTYPES[dz.dtype], p, nb)
+    return out
