@@ -23,6 +23,8 @@
 // which k_lin_join adds up in order and finishes.
 // The epilogue passes the fp32 accumulators through LDS so that bias,
 // residual, outputs and the accumulated G move as 16-byte pieces of rows.
+#include <math.h>
+
 #include "layer_internal.h"
 
 namespace dion3 {
@@ -73,39 +75,57 @@ struct Finish {
   int N;
 };
 
-// Columns c .. c + 7 of output row r.
+// The epilogue of columns c .. c + 7: the bias is read once a thread, what a
+// row adds (the residual, or the G it is summed into) ahead of the row's turn.
 template <class E, bool F32>
-__device__ __forceinline__ void finish8(const Finish& f, long long r, int c, float (&v)[8]) {
-  if constexpr (F32) {
-    float* g = f.G + r * f.ldg;
-    const bool vec = rows_aligned(f.G, f.ldg);
-    if (f.accumulate) {
-      float o[8];
-      load8((const float*)g, c, f.N, vec, o);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] += o[e];
-    }
-    store8(g, c, f.N, vec, v);
-  } else {
-    if (f.bias) {
-      float b[8];
+struct Chunk {
+  float b[8];
+  __device__ __forceinline__ void init(const Finish& f, int c) {
+    if constexpr (!F32) {
+      if (!f.bias) return;
       if (f.bias_f32) load8((const float*)f.bias, c, f.N, rows_aligned((const float*)f.bias, 8), b);
       else load8((const E*)f.bias, c, f.N, rows_aligned((const E*)f.bias, 8), b);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] += b[e];
     }
-    if (f.Z) store8((E*)f.Z + r * f.ldz, c, f.N, rows_aligned((const E*)f.Z, f.ldz), v);
-    if (f.act != DION3_ACT_NONE) {
+  }
+  static __device__ __forceinline__ void addend(const Finish& f, long long r, int c, float (&o)[8]) {
+    if constexpr (F32) load8((const float*)f.G + r * f.ldg, c, f.N, rows_aligned(f.G, f.ldg), o);
+    else load8((const E*)f.R + r * f.ldr, c, f.N, rows_aligned((const E*)f.R, f.ldr), o);
+  }
+  template <bool ADD>
+  __device__ __forceinline__ void put(const Finish& f, long long r, int c, float (&v)[8],
+                                      const float (&o)[8]) const {
+    if constexpr (F32) {
+      if constexpr (ADD) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = activate(f.act, v[e]);
-    }
-    if (f.R) {
-      float o[8];
-      load8((const E*)f.R + r * f.ldr, c, f.N, rows_aligned((const E*)f.R, f.ldr), o);
+        for (int e = 0; e < 8; ++e) v[e] += o[e];
+      }
+      store8(f.G + r * f.ldg, c, f.N, rows_aligned(f.G, f.ldg), v);
+    } else {
+      if (f.bias) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] += o[e];
+        for (int e = 0; e < 8; ++e) v[e] += b[e];
+      }
+      if (f.Z) store8((E*)f.Z + r * f.ldz, c, f.N, rows_aligned((const E*)f.Z, f.ldz), v);
+      if (f.act != DION3_ACT_NONE) activate8(f.act, v);
+      if constexpr (ADD) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += o[e];
+      }
+      store8((E*)f.Y + r * f.ldy, c, f.N, rows_aligned((const E*)f.Y, f.ldy), v);
     }
-    store8((E*)f.Y + r * f.ldy, c, f.N, rows_aligned((const E*)f.Y, f.ldy), v);
+  }
+};
+
+template <class E, bool F32>
+__device__ __forceinline__ void finish8(const Finish& f, long long r, int c, float (&v)[8]) {
+  Chunk<E, F32> k;
+  float o[8];
+  k.init(f, c);
+  if (F32 ? f.accumulate != 0 : f.R != nullptr) {
+    k.addend(f, r, c, o);
+    k.template put<true>(f, r, c, v, o);
+  } else {
+    k.template put<false>(f, r, c, v, o);
   }
 }
 
@@ -121,23 +141,30 @@ struct LinP {
   Finish f;
 };
 
-template <int BM_, int WAVES_M, int WAVES_N>
+template <int I>
+struct Int { static constexpr int value = I; };
+
+template <int BM_, int BN_, int WAVES_M, int WAVES_N, int SPREAD_>
 struct Cfg {
-  static constexpr int BM = BM_, BN = BM_;
+  static constexpr int SPREAD = SPREAD_;   // slices of a K step that share the staging
+  static constexpr int BM = BM_, BN = BN_;
   static constexpr int NT = 64 * WAVES_M * WAVES_N;
   static constexpr int WTM = BM / WAVES_M, WTN = BN / WAVES_N;
   static constexpr int FM = WTM / 32, FN = WTN / 32;
-  static constexpr int PART = (BM * LDSK > BK * (BM + kPadN)) ? BM * LDSK : BK * (BM + kPadN);
-  static constexpr int STAGE = 2 * PART;                     // halves
+  static constexpr int part(int r) { return r * LDSK > BK * (r + kPadN) ? r * LDSK : BK * (r + kPadN); }
+  static constexpr int PART = part(BM), STAGE = PART + part(BN);      // halves
   // epilogue staging: rows of BN + 8 floats; the 4 rows between a wave's two
   // halves then lie 32 banks apart
   static constexpr int EP = BN + 8;
-  static constexpr int EROWS = BM > 128 ? 128 : BM;          // rows staged at a time
+  static constexpr int EROWS = BN > 128 ? WTM : BM;          // rows staged at a time
   static constexpr int EBYTES = EROWS * EP * 4;
   static constexpr int BYTES = 2 * STAGE * 2 > EBYTES ? 2 * STAGE * 2 : EBYTES;
+  static constexpr int PER_CU = BYTES > 81920 ? 1 : 2;       // workgroups of a CU
 };
-typedef Cfg<256, 2, 4> CfgL;
-typedef Cfg<128, 2, 2> CfgS;
+typedef Cfg<256, 256, 2, 4, 3> CfgL;
+typedef Cfg<192, 256, 2, 4, 3> CfgM;
+typedef Cfg<128, 256, 2, 4, 3> CfgW;
+typedef Cfg<128, 128, 2, 2, 1> CfgS;
 
 enum Kind { kRowsK = 0, kColsK = 1, kColsF8 = 2 };
 
@@ -146,8 +173,8 @@ template <class E, int R, int NT, int KIND>
 struct Operand {
   static constexpr int RS = R + kPadN;                                 // [K][R] LDS row
   static constexpr int CH = KIND == kColsF8 ? R * BK / 16 / NT : R * BK / 8 / NT;
-  static constexpr int LOADS = KIND == kColsF8 ? 2 * CH : CH;          // global loads a step
-  static constexpr int STORES = KIND == kColsF8 ? 2 * CH : CH;         // LDS stores a step
+  static constexpr int CPR = KIND == kRowsK ? BK / 8 : KIND == kColsK ? R / 8 : R / 16;  // chunks a row
+  static constexpr int OPS = KIND == kColsF8 ? 2 : 1;                  // loads (and stores) a chunk
   static constexpr int READS = KIND == kRowsK ? 1 : 2;                 // LDS reads a fragment
   const char* base;      // kRowsK: the tile's first row; else column r0 of row 0
   const unsigned char* sbase;
@@ -156,7 +183,8 @@ struct Operand {
   int bytes;             // kRowsK: of the tile's rows
   int cols;              // else: bytes of a row that may be read
   int scols;
-  int voff;
+  static constexpr bool FIXED = NT % CPR == 0;    // a thread's chunks share their column
+  int voff[FIXED ? 1 : CH];
   int4v reg[CH];
   unsigned sreg[KIND == kColsF8 ? CH : 1];
 
@@ -169,88 +197,86 @@ struct Operand {
       base = (const char*)p + r0 * ld;
       const int n = (int)(rows - r0 < R ? rows - r0 : R);
       bytes = (int)((n - 1) * ld + K * 2);
-      voff = (int)((tid >> 3) * ld) + (tid & 7) * 16;
     } else if constexpr (KIND == kColsK) {
-      constexpr int CPR = R / 8;
       ld = ldp * 2;
       base = (const char*)p + r0 * 2;
       cols = (int)(rows - r0 < R ? (rows - r0 + 7) & ~7LL : R) * 2;
-      voff = (int)((tid / CPR) * ld) + (tid % CPR) * 16;
     } else {
-      constexpr int CPR = R / 16;
       ld = ldp;
       base = (const char*)p + r0;
       sbase = sc + r0 / kF8Block;
-      cols = (int)(ldp - r0 < R ? ldp - r0 : R);        // (the pitch is whole blocks)
+      cols = (int)(rows - r0 < R ? (rows - r0 + kF8Block - 1) / kF8Block * kF8Block : R);
       scols = cols / kF8Block;
-      voff = (int)((tid / CPR) * ld) + (tid % CPR) * 16;
     }
+#pragma unroll
+    for (int i = 0; i < (FIXED ? 1 : CH); ++i)
+      voff[i] = (int)(((tid + NT * i) / CPR) * ld) + (tid + NT * i) % CPR * 16;
   }
 
-  // The tile's K rows / columns k0 .. k0 + 63 into registers (zero past K).
-  __device__ __forceinline__ void load(long long k0, int tid) {
+  // Buffers over the tile's K rows / columns k0 .. k0 + 63 (loads past K give
+  // zero), and the offset of this thread's first chunk in them.
+  struct Src {
+    __amdgpu_buffer_rsrc_t rs, ss;
+    int v;
+  };
+  __device__ __forceinline__ Src source(long long k0, int tid) const {
     if constexpr (KIND == kRowsK) {
       const __amdgpu_buffer_rsrc_t rs = rsrc(base, bytes);
-      constexpr int STEP = NT / 8;
-      const int v = k0 + (tid & 7) * 8 < K ? voff + (int)k0 * 2 : kOut;
-#pragma unroll
-      for (int i = 0; i < CH; ++i)
-        reg[i] = __builtin_amdgcn_raw_buffer_load_b128(rs, v + i * STEP * (int)ld, 0, 0);
+      return {rs, rs, k0 + (tid & 7) * 8 < K ? voff[0] + (int)k0 * 2 : kOut};
     } else {
-      constexpr int CPR = KIND == kColsK ? R / 8 : R / 16;
-      constexpr int STEP = NT / CPR;
       const long long left = K - k0;
       const int n = left <= 0 ? 0 : left < BK ? (int)left : BK;        // valid rows
       const __amdgpu_buffer_rsrc_t rs = rsrc(base + k0 * ld, n > 0 ? (int)((n - 1) * ld) + cols : 0);
-#pragma unroll
-      for (int i = 0; i < CH; ++i)
-        reg[i] = __builtin_amdgcn_raw_buffer_load_b128(rs, voff + i * STEP * (int)ld, 0, 0);
       if constexpr (KIND == kColsF8) {
         const int lds = (int)(ld / kF8Block);
-        const __amdgpu_buffer_rsrc_t ss =
-            rsrc(sbase + k0 * lds, n > 0 ? (n - 1) * lds + scols : 0);
-#pragma unroll
-        for (int i = 0; i < CH; ++i)
-          sreg[i] = (unsigned char)__builtin_amdgcn_raw_buffer_load_b8(
-              ss, (tid / CPR + i * STEP) * lds + (tid % CPR) / 2, 0, 0);
+        return {rs, rsrc(sbase + k0 * lds, n > 0 ? (n - 1) * lds + scols : 0), voff[0]};
       }
+      return {rs, rs, voff[0]};
     }
   }
 
-  __device__ __forceinline__ void store(short* __restrict__ s, int tid) const {
+  // Chunk i of the tile into this thread's registers.
+  __device__ __forceinline__ void load(const Src& s, int i, int tid) {
+    constexpr int STEP = NT / CPR;
+    static_assert(FIXED || KIND == kColsK, "other operands' chunks share their column");
+    const int v = FIXED ? s.v + i * STEP * (int)ld : voff[FIXED ? 0 : i];
+    reg[i] = __builtin_amdgcn_raw_buffer_load_b128(s.rs, v, 0, 0);
+    if constexpr (KIND == kColsF8)
+      sreg[i] = (unsigned char)__builtin_amdgcn_raw_buffer_load_b8(
+          s.ss, (tid / CPR + i * STEP) * (int)(ld / kF8Block) + (tid % CPR) / 2, 0, 0);
+  }
+  __device__ __forceinline__ void load_all(long long k0, int tid) {
+    const Src s = source(k0, tid);
+#pragma unroll
+    for (int i = 0; i < CH; ++i) load(s, i, tid);
+  }
+
+  // Chunk i from the registers into the LDS part s.
+  __device__ __forceinline__ void store(short* __restrict__ s, int i, int tid) const {
+    const int c = tid + NT * i;
     if constexpr (KIND == kRowsK) {
-#pragma unroll
-      for (int i = 0; i < CH; ++i) {
-        const int c = tid + NT * i;
-        *(int4v*)(s + (c >> 3) * LDSK + (c & 7) * 8) = reg[i];
-      }
+      *(int4v*)(s + (c / CPR) * LDSK + (c % CPR) * 8) = reg[i];
     } else if constexpr (KIND == kColsK) {
-      constexpr int CPR = R / 8;
-#pragma unroll
-      for (int i = 0; i < CH; ++i) {
-        const int c = tid + NT * i;
-        *(int4v*)(s + (c / CPR) * RS + (c % CPR) * 8) = reg[i];
-      }
+      *(int4v*)(s + (c / CPR) * RS + (c % CPR) * 8) = reg[i];
     } else {
-      constexpr int CPR = R / 16;
+      const float sc = f8_scale_float(sreg[i]);
+      short* d = s + (c / CPR) * RS + (c % CPR) * 16;
 #pragma unroll
-      for (int i = 0; i < CH; ++i) {
-        const int c = tid + NT * i;
-        const float sc = f8_scale_float(sreg[i]);
-        short* d = s + (c / CPR) * RS + (c % CPR) * 16;
+      for (int h = 0; h < 2; ++h) {
+        int4v o;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          int4v o;
-#pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            const unsigned u = (unsigned)reg[i][2 * h + w];
-            o[2 * w] = __builtin_bit_cast(int, f8_decode2<false>(E(), u, sc));
-            o[2 * w + 1] = __builtin_bit_cast(int, f8_decode2<true>(E(), u, sc));
-          }
-          *(int4v*)(d + 8 * h) = o;
+        for (int w = 0; w < 2; ++w) {
+          const unsigned u = (unsigned)reg[i][2 * h + w];
+          o[2 * w] = __builtin_bit_cast(int, f8_decode2<false>(E(), u, sc));
+          o[2 * w + 1] = __builtin_bit_cast(int, f8_decode2<true>(E(), u, sc));
         }
+        *(int4v*)(d + 8 * h) = o;
       }
     }
+  }
+  __device__ __forceinline__ void store_all(short* __restrict__ s, int tid) const {
+#pragma unroll
+    for (int i = 0; i < CH; ++i) store(s, i, tid);
   }
 
   // This lane's offset into the part for the wave's rows w0 .., and the
@@ -274,16 +300,19 @@ struct Operand {
 // Scheduling-group masks of __builtin_amdgcn_sched_group_barrier.
 constexpr int kSgMfma = 0x008, kSgVmemRead = 0x020, kSgDsRead = 0x100, kSgDsWrite = 0x200;
 
-// Slice 0's order: MFMA q, then its share of the LDS stores and global loads.
-template <int NM, int NS, int NL, int Q>
-__device__ __forceinline__ void slice0_order() {
+// The order of a slice: its NM MFMAs, each followed by its share of the NR LDS
+// reads, NS LDS stores and NL global loads.
+template <int NM, int NR, int NS, int NL, int Q>
+__device__ __forceinline__ void slice_order() {
   if constexpr (Q < NM) {
+    constexpr int r = ((Q + 1) * NR + NM - 1) / NM - (Q * NR + NM - 1) / NM;
     constexpr int w = ((Q + 1) * NS + NM - 1) / NM - (Q * NS + NM - 1) / NM;
     constexpr int l = ((Q + 1) * NL + NM - 1) / NM - (Q * NL + NM - 1) / NM;
+    if constexpr (r > 0) __builtin_amdgcn_sched_group_barrier(kSgDsRead, r, 0);
     __builtin_amdgcn_sched_group_barrier(kSgMfma, 1, 0);
     if constexpr (w > 0) __builtin_amdgcn_sched_group_barrier(kSgDsWrite, w, 0);
     if constexpr (l > 0) __builtin_amdgcn_sched_group_barrier(kSgVmemRead, l, 0);
-    slice0_order<NM, NS, NL, Q + 1>();
+    slice_order<NM, NR, NS, NL, Q + 1>();
   }
 }
 
@@ -297,23 +326,29 @@ __device__ __forceinline__ void k_step(const short* __restrict__ st, short* __re
   typedef Operand<E, C::BN, C::NT, KB> OB;
   constexpr int NS = BK / 16, NM = C::FM * C::FN;
   constexpr int NR = OA::READS * C::FM + OB::READS * C::FN;
-  constexpr int NP = NM < NR ? NM : NR;
+  constexpr int SPREAD = C::SPREAD;                      // slices that share the staging
+  constexpr int CHT = OA::CH + OB::CH;
   short8 af[2][C::FM], bf[2][C::FN];
 #pragma unroll
   for (int i = 0; i < C::FM; ++i) af[0][i] = fa0[i];
 #pragma unroll
   for (int j = 0; j < C::FN; ++j) bf[0][j] = fb0[j];
-#pragma unroll
-  for (int kk = 0; kk < NS; ++kk) {
-    const int cb = kk & 1;
-    if (kk + 1 < NS) {
+  const typename OA::Src sa = A.source(k_next, tid);
+  const typename OB::Src sb = B.source(k_next, tid);
+  auto slice = [&](auto KK) {
+    constexpr int kk = KK.value;
+    constexpr int cb = kk & 1;
+    constexpr int c0 = kk < SPREAD ? kk * CHT / SPREAD : CHT, c1 = kk < SPREAD ? (kk + 1) * CHT / SPREAD : CHT;
+    constexpr int na = (c1 < OA::CH ? c1 : OA::CH) - (c0 < OA::CH ? c0 : OA::CH), nb = c1 - c0 - na;
+    constexpr int ops = na * OA::OPS + nb * OB::OPS;
+    if constexpr (kk + 1 < NS) {
 #pragma unroll
       for (int i = 0; i < C::FM; ++i) af[cb ^ 1][i] = OA::frag(st + aoff, i, kk + 1);
 #pragma unroll
       for (int j = 0; j < C::FN; ++j) bf[cb ^ 1][j] = OB::frag(st + C::PART + boff, j, kk + 1);
     } else {
       __syncthreads();
-      if (NEXT) {
+      if constexpr (NEXT) {
 #pragma unroll
         for (int i = 0; i < C::FM; ++i) fa0[i] = OA::frag(nxt + aoff, i, 0);
 #pragma unroll
@@ -321,37 +356,41 @@ __device__ __forceinline__ void k_step(const short* __restrict__ st, short* __re
       }
       __builtin_amdgcn_sched_barrier(0);
     }
-    if (kk == 0 && STORE) {
-      A.store(nxt, tid);
-      B.store(nxt + C::PART, tid);
-    }
-    if (kk == 0 && LOAD) {
-      A.load(k_next, tid);
-      B.load(k_next, tid);
+    if constexpr (STORE) {
+#pragma unroll
+      for (int c = c0; c < c1; ++c) {
+        if (c < OA::CH) {
+          A.store(nxt, c, tid);
+          if (LOAD) A.load(sa, c, tid);
+        } else {
+          B.store(nxt + C::PART, c - OA::CH, tid);
+          if (LOAD) B.load(sb, c - OA::CH, tid);
+        }
+      }
     }
 #pragma unroll
     for (int i = 0; i < C::FM; ++i)
 #pragma unroll
       for (int j = 0; j < C::FN; ++j) acc[i][j] = mfma32(E(), af[cb][i], bf[cb][j], acc[i][j]);
-    if (kk == 0) {
+    if constexpr (kk + 1 == NS) {
+      // (the reads are already ahead of the MFMAs)
+    } else if constexpr (kk == 0 && SPREAD == 1) {
       __builtin_amdgcn_sched_group_barrier(kSgDsRead, NR, 0);
-      slice0_order<NM, OA::STORES + OB::STORES, OA::LOADS + OB::LOADS, 0>();
-    } else if (kk + 1 < NS) {
-#pragma unroll
-      for (int q = 0; q < NP; ++q) {
-        __builtin_amdgcn_sched_group_barrier(kSgDsRead, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(kSgMfma, 1, 0);
-      }
-      if constexpr (NM > NP) __builtin_amdgcn_sched_group_barrier(kSgMfma, NM - NP, 0);
-      if constexpr (NR > NP) __builtin_amdgcn_sched_group_barrier(kSgDsRead, NR - NP, 0);
+      slice_order<NM, 0, STORE ? ops : 0, LOAD ? ops : 0, 0>();
+    } else {
+      slice_order<NM, NR, STORE ? ops : 0, LOAD ? ops : 0, 0>();
     }
     __builtin_amdgcn_sched_barrier(0);
-  }
+  };
+  slice(Int<0>());
+  slice(Int<1>());
+  slice(Int<2>());
+  slice(Int<3>());
 }
 
 // F32: C goes to G; PART: to the scratch (splits); else to Y.
 template <class E, class C, int KA, int KB, bool F32, bool PART>
-__global__ __launch_bounds__(C::NT, (C::BM == 256 ? 1 : 2)) void k_lin(LinP p) {
+__global__ __launch_bounds__(C::NT, C::PER_CU) void k_lin(LinP p) {
   __shared__ __attribute__((aligned(16))) char lds_raw[C::BYTES];
   short* lds = (short*)lds_raw;
 
@@ -395,13 +434,13 @@ __global__ __launch_bounds__(C::NT, (C::BM == 256 ? 1 : 2)) void k_lin(LinP p) {
     A.init(p.A, nullptr, p.lda, p.M, p.K, m0, tid);
     B.init(p.B, p.bs, p.ldb, p.N, p.K, n0, tid);
     const int aoff = OA::frag_off(wm * C::WTM, lane), boff = OB::frag_off(wn * C::WTN, lane);
-    A.load(k0, tid);
-    B.load(k0, tid);
-    A.store(lds, tid);
-    B.store(lds + C::PART, tid);
+    A.load_all(k0, tid);
+    B.load_all(k0, tid);
+    A.store_all(lds, tid);
+    B.store_all(lds + C::PART, tid);
     if (nk > 1) {
-      A.load(k0 + BK, tid);
-      B.load(k0 + BK, tid);
+      A.load_all(k0 + BK, tid);
+      B.load_all(k0 + BK, tid);
     }
     __syncthreads();
     short8 fa0[C::FM], fb0[C::FN];
@@ -428,6 +467,11 @@ __global__ __launch_bounds__(C::NT, (C::BM == 256 ? 1 : 2)) void k_lin(LinP p) {
   // 4 (l / 32) + v % 4, column l % 32.
   float* S = (float*)lds_raw;
   constexpr int CPR = C::BN / 8, RPP = C::NT / CPR;      // chunks a row, rows a pass
+  static_assert(C::EROWS % (RPP * 2) == 0, "whole batches");
+  const int c = (tid % CPR) * 8;
+  const bool in = n0 + c < p.N;
+  Chunk<E, F32> ch;
+  if (!PART && in) ch.init(p.f, n0 + c);
 #pragma unroll
   for (int h = 0; h < C::BM / C::EROWS; ++h) {
     if (h > 0) __syncthreads();
@@ -443,21 +487,42 @@ __global__ __launch_bounds__(C::NT, (C::BM == 256 ? 1 : 2)) void k_lin(LinP p) {
               (lane & 31)] = acc[i][j][v];
     }
     __syncthreads();
-    const int c = (tid % CPR) * 8;
-    if (n0 + c < p.N) {
-#pragma unroll 4
-      for (int rr = tid / CPR; rr < C::EROWS; rr += RPP) {
-        const long long row = m0 + h * C::EROWS + rr;
-        if (row >= p.M) break;
-        float v[8];
-        const float4 a = *(const float4*)(S + rr * C::EP + c), b = *(const float4*)(S + rr * C::EP + c + 4);
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-        if constexpr (PART)
-          store8(p.part + split * p.part_stride + row * p.ldp, n0 + c, p.ldp, true, v);
-        else
-          finish8<E, F32>(p.f, row, n0 + c, v);
+    if (!in) continue;
+    const long long r0 = m0 + h * C::EROWS + tid / CPR;
+    const float* s0 = S + tid / CPR * C::EP + c;
+    // (the choices are the whole launch's, so each is made once a tile)
+    auto rows = [&](auto FULL, auto ADD) {
+      // rows in flight (4 with an activation's code spill registers)
+      constexpr int U = (F32 || PART) && C::EROWS % (RPP * 4) == 0 ? 4 : 2;
+      for (int b = 0; b < C::EROWS / RPP; b += U) {
+        float v[U][8], o[U][8];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (ADD.value && (FULL.value || r0 + (b + u) * RPP < p.M))
+            Chunk<E, F32>::addend(p.f, r0 + (b + u) * RPP, n0 + c, o[u]);
+          const float* s = s0 + (b + u) * RPP * C::EP;
+          const float4 x = *(const float4*)s, y = *(const float4*)(s + 4);
+          v[u][0] = x.x; v[u][1] = x.y; v[u][2] = x.z; v[u][3] = x.w;
+          v[u][4] = y.x; v[u][5] = y.y; v[u][6] = y.z; v[u][7] = y.w;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const long long row = r0 + (b + u) * RPP;
+          if (!FULL.value && row >= p.M) continue;
+          if constexpr (PART)
+            store8(p.part + split * p.part_stride + row * p.ldp, n0 + c, p.ldp, true, v[u]);
+          else
+            ch.template put<ADD.value>(p.f, row, n0 + c, v[u], o[u]);
+        }
       }
+    };
+    const bool add = !PART && (F32 ? p.f.accumulate != 0 : p.f.R != nullptr);
+    if (m0 + (h + 1) * C::EROWS <= p.M) {
+      if (add) rows(Int<1>(), Int<1>());
+      else rows(Int<1>(), Int<0>());
+    } else {
+      if (add) rows(Int<0>(), Int<1>());
+      else rows(Int<0>(), Int<0>());
     }
   }
 }
@@ -597,40 +662,86 @@ bool in_place(const void* p, long long ld, long long contiguous) {
   return ((uintptr_t)p & 15) == 0 && ld % 8 == 0 && contiguous % 8 == 0;
 }
 
+// A rectangle of the output by one tile shape, its K axis in `splits` parts of
+// `steps` K steps.
+struct LinPart {
+  long long m0, n0, M, N;
+  int tile, splits, steps;
+};
 struct LinPlan {
-  bool thin, large;
-  int splits, steps;
+  bool thin;
   bool copyA, copyB;
   long long rowsA, colsA, rowsB, colsB;     // as stored
   size_t oA, oB, oP, total;
-  int ldp;
+  int nparts;
+  LinPart part[2];
 };
 
 long long up8(long long x) { return pad_to(x, 8); }
 
-// Tile and splits by an estimate of the time: rounds of workgroups over the
-// 256 CUs (one large tile or two small ones a CU) times the K steps of one,
-// plus each workgroup's fixed part, plus the join's traffic.
-void choose_tile(LinPlan& q, long long M, long long N, long long K) {
+// Tile shapes with their time model, fitted to whole rounds at K = 64 .. 4096
+// (8192 x 4096 x 4096 class sizes): microseconds of one K step and of the
+// fixed part (first loads, epilogue) of one round of workgroups.
+struct Tile { int bm, bn, slots; double step, fixed; };
+constexpr Tile kTiles[4] = {{256, 256, 256, 1.53, 11.0},
+                            {192, 256, 256, 1.24, 8.5},
+                            {128, 256, 256, 0.89, 6.5},
+                            {128, 128, 512, 1.05, 6.5}};
+
+// The cheapest tile shape and split of one rectangle: rounds of workgroups
+// over the 256 CUs, and for splits the join's launch and its traffic.
+double choose_tile(LinPart& q, long long K) {
+  static const int kSplits[] = {1, 2, 3, 4, 5, 6, 7, 8, 10, 12, 14, 16, 20, 24, 28, 32, 40, 48, 64};
   const long long nk = (K + BK - 1) / BK;
   double best = 1e30;
-  for (int large = 0; large < 2; ++large) {
-    const int b = large ? 256 : 128;
-    const long long tiles = ((M + b - 1) / b) * ((N + b - 1) / b);
-    const double step = large ? 1.9 : 1.3, fixed = large ? 14.0 : 8.0;
-    const long long slots = large ? 256 : 512;
-    for (long long sp = 1; sp <= 64 && sp <= nk; ++sp) {
-      if (sp > 1 && tiles * sp > 8 * slots) break;
-      const long long steps = (nk + sp - 1) / sp;
-      if ((nk + steps - 1) / steps != sp) continue;           // the same steps as fewer splits
-      const double rounds = (double)((tiles * sp + slots - 1) / slots);
-      double us = rounds * (steps * step + fixed);
-      if (sp > 1) us += 4.0 + 8.0 * (double)sp * M * N / 4.0e6;
+  for (int i = 0; i < 4; ++i) {
+    const Tile& t = kTiles[i];
+    const long long tiles = ((q.M + t.bm - 1) / t.bm) * ((q.N + t.bn - 1) / t.bn);
+    for (const int sp : kSplits) {
+      if (sp > 1 && (sp > nk || tiles * sp > 4 * t.slots)) break;
+      const int steps = (int)((nk + sp - 1) / sp);
+      const double rounds = ceil((double)(tiles * sp) / t.slots);
+      double us = rounds * (steps * t.step + t.fixed);
+      if (sp > 1) us += 4.0 + 8.0 * sp * (double)q.M * q.N / 5.0e6;
       if (us < best) {
         best = us;
-        q.large = large;
-        q.splits = (int)sp;
-        q.steps = (int)steps;
+        q.tile = i;
+        q.splits = (int)((nk + steps - 1) / steps);      // (without parts that would be empty)
+        q.steps = steps;
+      }
+    }
+  }
+  return best;
+}
+
+// More tiles than one round: the rows or columns of tiles that fill whole
+// rounds, and what is left as a rectangle of its own with its own tile shape
+// (8192 x 11008 outputs are 5.4 rounds of the large tile: 5 rounds and 768
+// columns in one round of 128 x 256 tiles instead of 6).
+void choose_parts(LinPlan& q, long long M, long long N, long long K) {
+  LinPart whole = {0, 0, M, N, 0, 1, 0};
+  double best = choose_tile(whole, K);
+  q.nparts = 1;
+  q.part[0] = whole;
+  const int nk = (int)((K + BK - 1) / BK);
+  for (int i = 0; i < 4; ++i) {
+    const Tile& t = kTiles[i];
+    const long long tm = (M + t.bm - 1) / t.bm, tn = (N + t.bn - 1) / t.bn;
+    const long long full = tm * tn / t.slots;
+    if (full < 1) continue;
+    const double us = (double)full * (nk * t.step + t.fixed) + 3.0;
+    for (int side = 0; side < 2; ++side) {
+      const long long cut = side ? full * t.slots / tn : full * t.slots / tm;   // tile rows / columns
+      if (cut < 1 || cut >= (side ? tm : tn)) continue;
+      const LinPart a = {0, 0, side ? cut * t.bm : M, side ? N : cut * t.bn, i, 1, nk};
+      LinPart b = {side ? cut * t.bm : 0, side ? 0 : cut * t.bn, side ? M - cut * t.bm : M,
+                   side ? N : N - cut * t.bn, 0, 1, 0};
+      const double both = us + choose_tile(b, K);
+      if (both < best) {
+        best = both;
+        q.nparts = 2;
+        q.part[0] = a;
+        q.part[1] = b;
       }
     }
   }
@@ -641,18 +752,24 @@ LinPlan lin_plan(const LinDesc& d) {
   if (d.M == 0 || d.K == 0) return q;
   q.rowsA = d.a_km ? d.K : d.M; q.colsA = d.a_km ? d.M : d.K;
   q.rowsB = d.b_kn ? d.K : d.N; q.colsB = d.b_kn ? d.N : d.K;
-  // (the thin kernel addresses its 16 rows by 32-bit offsets: see lin_fits)
   q.thin = !d.a_km && !d.b_kn && !d.G && d.M <= kThinTokens;
   if (q.thin) return q;
   q.copyA = !in_place(d.A, d.lda, q.colsA);
   q.copyB = !d.bs && !in_place(d.B, d.ldb, q.colsB);
-  choose_tile(q, d.M, d.N, d.K);
+  choose_parts(q, d.M, d.N, d.K);
   size_t off = 0;
   auto take = [&](size_t b) { const size_t o = off; off = (off + b + 255) & ~(size_t)255; return o; };
   if (q.copyA) q.oA = take((size_t)q.rowsA * up8(q.colsA) * 2);
   if (q.copyB) q.oB = take((size_t)q.rowsB * up8(q.colsB) * 2);
-  q.ldp = (int)up8(d.N);
-  if (q.splits > 1) q.oP = take((size_t)q.splits * d.M * q.ldp * 4);
+  size_t parts = 0;      // one after the other: they share the scratch of the splits
+  for (int i = 0; i < q.nparts; ++i) {
+    const LinPart& t = q.part[i];
+    if (t.splits > 1) {
+      const size_t b = (size_t)t.splits * t.M * up8(t.N) * 4;
+      parts = b > parts ? b : parts;
+    }
+  }
+  if (parts) q.oP = take(parts);
   q.total = off;
   return q;
 }
@@ -667,13 +784,18 @@ hipError_t launch_tiles(const LinP& p, hipStream_t s) {
 }
 
 template <class E, int KA, int KB, bool F32>
-hipError_t launch_cfg(LinP p, bool large, hipStream_t s) {
-  const int b = large ? 256 : 128;
-  p.tilesM = (int)((p.M + b - 1) / b);
-  p.tilesN = (p.N + b - 1) / b;
+hipError_t launch_cfg(LinP p, int tile, hipStream_t s) {
+  const Tile& t = kTiles[tile];
+  p.tilesM = (int)((p.M + t.bm - 1) / t.bm);
+  p.tilesN = (p.N + t.bn - 1) / t.bn;
   p.total = (long long)p.tilesM * p.tilesN * p.splits;
   if (p.total > 0x7fffffffLL) return hipErrorInvalidValue;
-  return large ? launch_tiles<E, CfgL, KA, KB, F32>(p, s) : launch_tiles<E, CfgS, KA, KB, F32>(p, s);
+  switch (tile) {
+    case 0: return launch_tiles<E, CfgL, KA, KB, F32>(p, s);
+    case 1: return launch_tiles<E, CfgM, KA, KB, F32>(p, s);
+    case 2: return launch_tiles<E, CfgW, KA, KB, F32>(p, s);
+  }
+  return launch_tiles<E, CfgS, KA, KB, F32>(p, s);
 }
 
 template <class E>
@@ -725,30 +847,52 @@ hipError_t launch_lin_t(const LinDesc& d, void* ws, hipStream_t s) {
   }
   // K-contiguous operands end in whole chunks: a copy's are zero past K, and
   // a K of the other operand's rows past the true K reads zeros either way
-  p.M = d.M; p.N = (int)d.N; p.K = d.K;
-  p.splits = q.splits; p.steps = q.steps;
-  p.part = (float*)((char*)ws + q.oP);
-  p.part_stride = d.M * q.ldp;
-  p.ldp = q.ldp;
-  p.f = f;
-  hipError_t e;
-  {
-    TraceScope ts(d.name, flops, 0.0, s);
-    if (d.bs) e = launch_cfg<E, kColsK, kColsF8, true>(p, q.large, s);
-    else if (d.G) e = launch_cfg<E, kColsK, kColsK, true>(p, q.large, s);
-    else if (d.b_kn) e = launch_cfg<E, kRowsK, kColsK, false>(p, q.large, s);
-    else e = launch_cfg<E, kRowsK, kRowsK, false>(p, q.large, s);
+  const LinP whole = p;
+  for (int i = 0; i < q.nparts; ++i) {
+    const LinPart& t = q.part[i];
+    p = whole;
+    p.A = (const char*)p.A + 2 * (d.a_km ? t.m0 : t.m0 * p.lda);
+    if (d.bs) {
+      p.B = (const char*)p.B + t.n0;
+      p.bs = p.bs + t.n0 / kF8Block;
+    } else {
+      p.B = (const char*)p.B + 2 * (d.b_kn ? t.n0 : t.n0 * p.ldb);
+    }
+    p.M = t.M; p.N = (int)t.N; p.K = d.K;
+    p.splits = t.splits; p.steps = t.steps;
+    p.part = (float*)((char*)ws + q.oP);
+    p.ldp = (int)up8(t.N);
+    p.part_stride = t.M * p.ldp;
+    p.f = f;
+    p.f.N = (int)t.N;
+    if (f.Y) p.f.Y = (char*)f.Y + 2 * (t.m0 * f.ldy + t.n0);
+    if (f.Z) p.f.Z = (char*)f.Z + 2 * (t.m0 * f.ldz + t.n0);
+    if (f.R) p.f.R = (const char*)f.R + 2 * (t.m0 * f.ldr + t.n0);
+    if (f.G) p.f.G = f.G + t.m0 * f.ldg + t.n0;
+    if (f.bias) p.f.bias = (const char*)f.bias + (f.bias_f32 ? 4 : 2) * t.n0;
+    hipError_t e;
+    {
+      TraceScope ts(d.name, 2.0 * (double)t.M * t.N * d.K, 0.0, s);
+      if (d.bs) e = launch_cfg<E, kColsK, kColsF8, true>(p, t.tile, s);
+      else if (d.G) e = launch_cfg<E, kColsK, kColsK, true>(p, t.tile, s);
+      else if (d.b_kn) e = launch_cfg<E, kRowsK, kColsK, false>(p, t.tile, s);
+      else e = launch_cfg<E, kRowsK, kRowsK, false>(p, t.tile, s);
+    }
+    if (e != hipSuccess) return e;
+    if (t.splits == 1) continue;
+    TraceScope ts("linear_join", 0.0, 4.0 * (double)t.splits * t.M * t.N, s);
+    const unsigned nch = (unsigned)(p.ldp / 8);
+    const dim3 grid((unsigned)((t.M * nch + 255) / 256));
+    if (d.G)
+      hipLaunchKernelGGL((k_lin_join<E, true>), grid, dim3(256), 0, s, p.part, p.part_stride,
+                         t.splits, t.M, nch, p.f);
+    else
+      hipLaunchKernelGGL((k_lin_join<E, false>), grid, dim3(256), 0, s, p.part, p.part_stride,
+                         t.splits, t.M, nch, p.f);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
   }
-  if (e != hipSuccess || q.splits == 1) return e;
-  TraceScope ts("linear_join", 0.0, 4.0 * (double)q.splits * d.M * d.N, s);
-  const dim3 grid((unsigned)((d.M * nch + 255) / 256));
-  if (d.G)
-    hipLaunchKernelGGL((k_lin_join<E, true>), grid, dim3(256), 0, s, p.part, p.part_stride, q.splits,
-                       d.M, nch, f);
-  else
-    hipLaunchKernelGGL((k_lin_join<E, false>), grid, dim3(256), 0, s, p.part, p.part_stride, q.splits,
-                       d.M, nch, f);
-  return hipGetLastError();
+  return hipSuccess;
 }
 
 }  // namespace

@@ -75,7 +75,12 @@ __device__ __forceinline__ void store8(E* __restrict__ row, int c, int m, bool v
 
 // -------------------------------------------------------------- activations
 
-__device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + __expf(-x)); }
+// 1 / (1 + exp(-x)) by the hardware's exponential and reciprocal (each within
+// one step of fp32): a divide rounded to the last bit costs ten instructions
+// more for every output element, and the outputs are 16-bit.
+__device__ __forceinline__ float sigmoid(float x) {
+  return __builtin_amdgcn_rcpf(1.0f + __expf(-x));
+}
 
 constexpr float kGeluC = 0.7978845608028654f;    // sqrt(2 / pi)
 constexpr float kGeluA = 0.044715f;
@@ -94,6 +99,22 @@ __device__ __forceinline__ float activate(int act, float z) {
     case DION3_ACT_SILU: return z * sigmoid(z);
   }
   return z;
+}
+
+// act(z) of 8 values, the choice made once for all of them.
+__device__ __forceinline__ void activate8(int act, float (&v)[8]) {
+#define DION3_ACT8(A)                                    \
+  case A: {                                              \
+    _Pragma("unroll") for (int e = 0; e < 8; ++e) v[e] = activate(A, v[e]); \
+    return;                                              \
+  }
+  switch (act) {
+    DION3_ACT8(DION3_ACT_RELU)
+    DION3_ACT8(DION3_ACT_GELU)
+    DION3_ACT8(DION3_ACT_GELU_TANH)
+    DION3_ACT8(DION3_ACT_SILU)
+  }
+#undef DION3_ACT8
 }
 
 // act'(z)

@@ -67,6 +67,8 @@ def _rows(t, name):
     m = t.shape[-1]
     if m < 1:
         raise ValueError(f"{name} needs at least one feature")
+    if t.is_contiguous():
+        return t.numel() // m, m, m
     if m > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name} must have contiguous features")
     rows, ld = 1, None
@@ -79,8 +81,8 @@ def _rows(t, name):
             raise ValueError(f"{name}: its leading dimensions do not share one stride")
         rows *= size
     if rows <= 1:
-        ld = max(m, 1) if ld is None or ld < m else ld
-    elif ld < m:
+        return rows, m, m
+    if ld < m:
         raise ValueError(f"{name}: its rows overlap")
     return rows, m, ld
 
@@ -92,7 +94,11 @@ def _act(act):
 
 
 def _ptr(t):
-    return None if t is None or t.numel() == 0 else t.data_ptr()
+    return None if t is None else t.data_ptr() or None     # (no tokens: no storage)
+
+
+def _like(t):
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
 def _scratch(ws, nbytes, device):
@@ -103,19 +109,29 @@ def _scratch(ws, nbytes, device):
         p, n = ws.get(nbytes, device)
         return p, n, ws
     buf = torch.empty(nbytes + 256, dtype=torch.uint8, device=device)
-    off = (-buf.data_ptr()) % 256
-    return buf.data_ptr() + off, nbytes, buf
+    p = buf.data_ptr()
+    return p + (-p) % 256, nbytes, buf
 
 
 def _size(fn, *args):
     out = ctypes.c_size_t(0)
     _lib._check(getattr(_lib.lib(), fn)(*args, ctypes.byref(out)), fn)
-    return int(out.value)
+    return out.value
+
+
+# The stream's handle without a torch.cuda.Stream around it (about 2 us a
+# call, as much as a small kernel), where torch offers it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _call(fn, device, *args):
-    with torch.cuda.device(device):
-        _lib._check(getattr(_lib.lib(), fn)(*args, _lib._stream(device)), fn)
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _lib._check(getattr(_lib.lib(), fn)(*args, _lib._stream(device)), fn)
+    stream = _raw_stream(device.index) if _raw_stream is not None else _lib._stream(device)
+    status = getattr(_lib.lib(), fn)(*args, stream)
+    if status:
+        _lib._check(status, fn)
 
 
 # --------------------------------------------------------- the 8-bit format
@@ -156,11 +172,14 @@ class PackedF8:
         return self.q.numel() + self.scale.numel()
 
 
-def _empty_packed(rows, cols, shape, device):
+def _empty_packed(like, rows, cols):
+    """A PackedF8 to be filled, for `like`, whose rows and columns these are."""
     cp = -(-cols // F8_BLOCK) * F8_BLOCK
-    return PackedF8(torch.empty((rows, cp), dtype=torch.float8_e4m3fn, device=device),
-                    torch.empty((rows, cp // F8_BLOCK), dtype=torch.uint8, device=device),
-                    cols, shape)
+    p = PackedF8.__new__(PackedF8)
+    p.q = like.new_empty((rows, cp), dtype=torch.float8_e4m3fn)
+    p.scale = like.new_empty((rows, cp // F8_BLOCK), dtype=torch.uint8)
+    p.rows, p.cols, p.shape = rows, cols, like.shape
+    return p
 
 
 def pack_f8(x) -> PackedF8:
@@ -170,7 +189,7 @@ def pack_f8(x) -> PackedF8:
     if x.dtype not in _DTYPES:
         raise TypeError("x must be bfloat16, float16 or float32")
     T, m, ld = _rows(x, "x")
-    p = _empty_packed(T, m, x.shape, x.device)
+    p = _empty_packed(x, T, m)
     _call("dion3_pack_f8", x.device, _ptr(x), ld, _ptr(p.q), _ptr(p.scale), T, m, _DTYPES[x.dtype])
     return p
 
@@ -202,12 +221,12 @@ def add_rms_norm(x, weight, residual=None, eps: float = 1e-6, pack: bool = False
     if residual is not None:
         _same(residual, x, "residual", x.shape)
         _, _, ldr = _rows(residual, "residual")
-        h, ldh = torch.empty(x.shape, dtype=x.dtype, device=x.device), m
+        h, ldh = _like(x), m
     if not return_y and not pack:
         raise ValueError("ask for y, its 8-bit form or both")
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if return_y else None
-    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-    p = _empty_packed(T, m, x.shape, x.device) if pack else None
+    y = _like(x) if return_y else None
+    rstd = x.new_empty(x.shape[:-1], dtype=torch.float32)
+    p = _empty_packed(x, T, m) if pack else None
     _call("dion3_add_rms_norm", x.device, _ptr(x), ldx, _ptr(residual), ldr, weight.data_ptr(),
           _DTYPES[weight.dtype], None if residual is None else _ptr(h), ldh, _ptr(y), m,
           _ptr(p.q) if p else None, _ptr(p.scale) if p else None, _ptr(rstd), T, m, float(eps),
@@ -236,8 +255,8 @@ def add_rms_norm_grad(dy, h, rstd, weight, dh=None, need_dx: bool = True, need_d
         _, _, lddh = _rows(dh, "dh")
     if not need_dx and not need_dw:
         return None, None
-    dx = torch.empty(dy.shape, dtype=dy.dtype, device=dy.device) if need_dx else None
-    dw = torch.empty(m, dtype=torch.float32, device=dy.device) if need_dw else None
+    dx = _like(dy) if need_dx else None
+    dw = dy.new_empty(m, dtype=torch.float32) if need_dw else None
     p, nb, keep = _scratch(ws, _size("dion3_add_rms_norm_grad_workspace_size", T, m), dy.device)
     _call("dion3_add_rms_norm_grad", dy.device, _ptr(dy), ldy, _ptr(h), ldh, _ptr(rstd),
           weight.data_ptr(), _DTYPES[weight.dtype], _ptr(dh), lddh, _ptr(dx), m, _ptr(dw), T, m,
@@ -275,8 +294,8 @@ def linear(x, w, bias=None, act: str = "none", residual=None, return_preact: boo
     if residual is not None:
         _same(residual, x, "residual", shape)
         _, _, ldr = _rows(residual, "residual")
-    y = torch.empty(shape, dtype=x.dtype, device=x.device)
-    z = torch.empty(shape, dtype=x.dtype, device=x.device) if return_preact else None
+    y = x.new_empty(shape)
+    z = x.new_empty(shape) if return_preact else None
     p, nb, keep = _scratch(ws, _size("dion3_linear_workspace_size", _ptr(x), ldx, w.data_ptr(), ldw,
                                      T, n, m), x.device)
     _call("dion3_linear", x.device, _ptr(x), ldx, w.data_ptr(), ldw, _ptr(bias),
@@ -303,8 +322,8 @@ def act_grad(dy, z, act: str, bias: bool = False, ws: Optional[_lib.Workspace] =
             _same(z, dy, "z", dy.shape)
             _, _, ldz = _rows(z, "z")
             zp = _ptr(z)
-    dz = torch.empty(dy.shape, dtype=dy.dtype, device=dy.device) if act != "none" else None
-    db = torch.empty(n, dtype=torch.float32, device=dy.device) if bias else None
+    dz = _like(dy) if act != "none" else None
+    db = dy.new_empty(n, dtype=torch.float32) if bias else None
     if dz is not None or db is not None:
         p, nb, keep = _scratch(ws, _size("dion3_act_grad_workspace_size", T, n) if bias else 0,
                                dy.device)
@@ -325,7 +344,7 @@ def linear_grad_input(dz, w, residual=None, ws: Optional[_lib.Workspace] = None)
     if residual is not None:
         _same(residual, dz, "residual", shape)
         _, _, ldr = _rows(residual, "residual")
-    dx = torch.empty(shape, dtype=dz.dtype, device=dz.device)
+    dx = dz.new_empty(shape)
     p, nb, keep = _scratch(ws, _size("dion3_linear_grad_input_workspace_size", _ptr(dz), lddz,
                                      w.data_ptr(), ldw, T, n, m), dz.device)
     _call("dion3_linear_grad_input", dz.device, _ptr(dz), lddz, w.data_ptr(), ldw, _ptr(residual),
@@ -356,7 +375,7 @@ def linear_grad_weight(dz, x, out=None, accumulate: bool = False,
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
-        out = torch.empty((n, m), dtype=torch.float32, device=dz.device)
+        out = dz.new_empty((n, m), dtype=torch.float32)
     if not isinstance(out, torch.Tensor) or out.device != dz.device or out.dtype != torch.float32:
         raise TypeError(f"out must be a float32 tensor on {dz.device}")
     if tuple(out.shape) != (n, m):

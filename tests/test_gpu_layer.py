@@ -282,6 +282,15 @@ def test_products_exact(T, n, m, dtype):
     assert torch.equal(d(d3.linear_grad_weight(dz.cuda(), p, out=out, accumulate=True)), 2 * gw)
 
 
+@pytest.mark.parametrize("T,n,m", [(2100, 4100, 72), (4100, 2120, 40), (2100, 72, 4100),
+                                   (4200, 40, 2100), (72, 2100, 4100), (40, 4200, 2150),
+                                   (3000, 6300, 64)])
+def test_products_of_many_tiles(T, n, m):
+    """More tiles than one round of workgroups, with a remainder: the output is
+    cut in two rectangles, by rows or by columns, each exact."""
+    test_products_exact(T, n, m, BF)
+
+
 @pytest.mark.parametrize("how", ["wide", "odd", "off"])
 @pytest.mark.parametrize("T,n,m", [(3, 40, 72), (5, 33, 101), (150, 264, 136), (141, 131, 203),
                                    (300, 257, 520)])
