@@ -15,10 +15,14 @@
 //   * K as rows in 8 bits: the same, decoded between the global load and the
 //     LDS store, two values an instruction (the scale is the instruction's
 //     operand), so the checkpoint crosses HBM and the caches at half the size.
-// Two tiles: 256 x 256 (8 waves of 128 x 64, one workgroup a CU) and 128 x
-// 128 (4 waves of 64 x 64, two workgroups a CU).  Each slice of 16 K issues
-// the next slice's LDS reads ahead of its MFMAs, the first one also the next
-// tile's LDS stores and the global loads of the tile after that.
+// Tiles: 256 x 256, 192 x 256 and 128 x 256 (8 waves, one workgroup a CU; the
+// first has the best rate, 1.2-1.25 PFLOP/s on 8192 x 4096 x 4096, the others
+// fill the last round of workgroups better), 128 x 128 and 64 x 64 (4 waves,
+// for few tokens).  Each slice of 16 K issues the next slice's LDS reads ahead
+// of its MFMAs; the next tile's LDS stores and the global loads of a later one
+// are spread over the step's first slices.  The time of a step is shared by
+// MFMA issue (2048 cycles of the large tile) and LDS traffic (192 KB read,
+// 64 KB written), at a clock that power limits.
 // Few tiles are split over K: each part leaves an fp32 tile in the scratch,
 // which k_lin_join adds up in order and finishes.
 // The epilogue passes the fp32 accumulators through LDS so that bias,
@@ -144,8 +148,9 @@ struct LinP {
 template <int I>
 struct Int { static constexpr int value = I; };
 
-template <int BM_, int BN_, int WAVES_M, int WAVES_N, int SPREAD_>
+template <int BM_, int BN_, int WAVES_M, int WAVES_N, int SPREAD_, int PF_>
 struct Cfg {
+  static constexpr int PF = PF_;           // K steps of register prefetch
   static constexpr int SPREAD = SPREAD_;   // slices of a K step that share the staging
   static constexpr int BM = BM_, BN = BN_;
   static constexpr int NT = 64 * WAVES_M * WAVES_N;
@@ -159,17 +164,18 @@ struct Cfg {
   static constexpr int EROWS = BN > 128 ? WTM : BM;          // rows staged at a time
   static constexpr int EBYTES = EROWS * EP * 4;
   static constexpr int BYTES = 2 * STAGE * 2 > EBYTES ? 2 * STAGE * 2 : EBYTES;
-  static constexpr int PER_CU = BYTES > 81920 ? 1 : 2;       // workgroups of a CU
+  static constexpr int PER_CU = BYTES > 81920 ? 1 : BYTES > 54608 ? 2 : 3;   // workgroups of a CU
 };
-typedef Cfg<256, 256, 2, 4, 3> CfgL;
-typedef Cfg<192, 256, 2, 4, 3> CfgM;
-typedef Cfg<128, 256, 2, 4, 3> CfgW;
-typedef Cfg<128, 128, 2, 2, 1> CfgS;
+typedef Cfg<256, 256, 2, 4, 3, 1> CfgL;
+typedef Cfg<192, 256, 2, 4, 3, 2> CfgM;
+typedef Cfg<128, 256, 2, 4, 3, 1> CfgW;
+typedef Cfg<128, 128, 2, 2, 1, 1> CfgS;
+typedef Cfg<64, 64, 2, 2, 1, 2> CfgT;
 
 enum Kind { kRowsK = 0, kColsK = 1, kColsF8 = 2 };
 
 // One operand of R output rows: its registers, LDS part and fragments.
-template <class E, int R, int NT, int KIND>
+template <class E, int R, int NT, int KIND, int PF>
 struct Operand {
   static constexpr int RS = R + kPadN;                                 // [K][R] LDS row
   static constexpr int CH = KIND == kColsF8 ? R * BK / 16 / NT : R * BK / 8 / NT;
@@ -185,8 +191,8 @@ struct Operand {
   int scols;
   static constexpr bool FIXED = NT % CPR == 0;    // a thread's chunks share their column
   int voff[FIXED ? 1 : CH];
-  int4v reg[CH];
-  unsigned sreg[KIND == kColsF8 ? CH : 1];
+  int4v reg[PF][CH];
+  unsigned sreg[PF][KIND == kColsF8 ? CH : 1];
 
   __device__ __forceinline__ void init(const void* p, const unsigned char* sc, long long ldp,
                                        long long rows, long long k, long long r0, int tid) {
@@ -235,38 +241,41 @@ struct Operand {
     }
   }
 
-  // Chunk i of the tile into this thread's registers.
+  // Chunk i of the tile into this thread's register set P.
+  template <int P>
   __device__ __forceinline__ void load(const Src& s, int i, int tid) {
     constexpr int STEP = NT / CPR;
     static_assert(FIXED || KIND == kColsK, "other operands' chunks share their column");
     const int v = FIXED ? s.v + i * STEP * (int)ld : voff[FIXED ? 0 : i];
-    reg[i] = __builtin_amdgcn_raw_buffer_load_b128(s.rs, v, 0, 0);
+    reg[P][i] = __builtin_amdgcn_raw_buffer_load_b128(s.rs, v, 0, 0);
     if constexpr (KIND == kColsF8)
-      sreg[i] = (unsigned char)__builtin_amdgcn_raw_buffer_load_b8(
+      sreg[P][i] = (unsigned char)__builtin_amdgcn_raw_buffer_load_b8(
           s.ss, (tid / CPR + i * STEP) * (int)(ld / kF8Block) + (tid % CPR) / 2, 0, 0);
   }
+  template <int P>
   __device__ __forceinline__ void load_all(long long k0, int tid) {
     const Src s = source(k0, tid);
 #pragma unroll
-    for (int i = 0; i < CH; ++i) load(s, i, tid);
+    for (int i = 0; i < CH; ++i) load<P>(s, i, tid);
   }
 
   // Chunk i from the registers into the LDS part s.
+  template <int P>
   __device__ __forceinline__ void store(short* __restrict__ s, int i, int tid) const {
     const int c = tid + NT * i;
     if constexpr (KIND == kRowsK) {
-      *(int4v*)(s + (c / CPR) * LDSK + (c % CPR) * 8) = reg[i];
+      *(int4v*)(s + (c / CPR) * LDSK + (c % CPR) * 8) = reg[P][i];
     } else if constexpr (KIND == kColsK) {
-      *(int4v*)(s + (c / CPR) * RS + (c % CPR) * 8) = reg[i];
+      *(int4v*)(s + (c / CPR) * RS + (c % CPR) * 8) = reg[P][i];
     } else {
-      const float sc = f8_scale_float(sreg[i]);
+      const float sc = f8_scale_float(sreg[P][i]);
       short* d = s + (c / CPR) * RS + (c % CPR) * 16;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         int4v o;
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
-          const unsigned u = (unsigned)reg[i][2 * h + w];
+          const unsigned u = (unsigned)reg[P][i][2 * h + w];
           o[2 * w] = __builtin_bit_cast(int, f8_decode2<false>(E(), u, sc));
           o[2 * w + 1] = __builtin_bit_cast(int, f8_decode2<true>(E(), u, sc));
         }
@@ -274,9 +283,10 @@ struct Operand {
       }
     }
   }
+  template <int P>
   __device__ __forceinline__ void store_all(short* __restrict__ s, int tid) const {
 #pragma unroll
-    for (int i = 0; i < CH; ++i) store(s, i, tid);
+    for (int i = 0; i < CH; ++i) store<P>(s, i, tid);
   }
 
   // This lane's offset into the part for the wave's rows w0 .., and the
@@ -316,14 +326,20 @@ __device__ __forceinline__ void slice_order() {
   }
 }
 
-template <class E, class C, int KA, int KB, bool STORE, bool LOAD, bool NEXT>
+// One K step on LDS stage `st`: register set P (the next tile) goes into stage
+// `nxt`, and the tile PF steps later is requested into it.  Each slice reads
+// the next slice's fragments under its own MFMAs; the step's one barrier sits
+// before the last slice, and the next stage's first fragments are read under
+// that slice's MFMAs.  Every step does all of it, the last ones with tiles
+// past the end, which load as zeros and are not used.
+template <class E, class C, int KA, int KB, int P>
 __device__ __forceinline__ void k_step(const short* __restrict__ st, short* __restrict__ nxt,
-                                       Operand<E, C::BM, C::NT, KA>& A,
-                                       Operand<E, C::BN, C::NT, KB>& B, long long k_next, int tid,
-                                       int aoff, int boff, short8 (&fa0)[C::FM],
+                                       Operand<E, C::BM, C::NT, KA, C::PF>& A,
+                                       Operand<E, C::BN, C::NT, KB, C::PF>& B, long long k_next,
+                                       int tid, int aoff, int boff, short8 (&fa0)[C::FM],
                                        short8 (&fb0)[C::FN], floatx16 (&acc)[C::FM][C::FN]) {
-  typedef Operand<E, C::BM, C::NT, KA> OA;
-  typedef Operand<E, C::BN, C::NT, KB> OB;
+  typedef Operand<E, C::BM, C::NT, KA, C::PF> OA;
+  typedef Operand<E, C::BN, C::NT, KB, C::PF> OB;
   constexpr int NS = BK / 16, NM = C::FM * C::FN;
   constexpr int NR = OA::READS * C::FM + OB::READS * C::FN;
   constexpr int SPREAD = C::SPREAD;                      // slices that share the staging
@@ -348,24 +364,20 @@ __device__ __forceinline__ void k_step(const short* __restrict__ st, short* __re
       for (int j = 0; j < C::FN; ++j) bf[cb ^ 1][j] = OB::frag(st + C::PART + boff, j, kk + 1);
     } else {
       __syncthreads();
-      if constexpr (NEXT) {
 #pragma unroll
-        for (int i = 0; i < C::FM; ++i) fa0[i] = OA::frag(nxt + aoff, i, 0);
+      for (int i = 0; i < C::FM; ++i) fa0[i] = OA::frag(nxt + aoff, i, 0);
 #pragma unroll
-        for (int j = 0; j < C::FN; ++j) fb0[j] = OB::frag(nxt + C::PART + boff, j, 0);
-      }
+      for (int j = 0; j < C::FN; ++j) fb0[j] = OB::frag(nxt + C::PART + boff, j, 0);
       __builtin_amdgcn_sched_barrier(0);
     }
-    if constexpr (STORE) {
 #pragma unroll
-      for (int c = c0; c < c1; ++c) {
-        if (c < OA::CH) {
-          A.store(nxt, c, tid);
-          if (LOAD) A.load(sa, c, tid);
-        } else {
-          B.store(nxt + C::PART, c - OA::CH, tid);
-          if (LOAD) B.load(sb, c - OA::CH, tid);
-        }
+    for (int c = c0; c < c1; ++c) {
+      if (c < OA::CH) {
+        A.template store<P>(nxt, c, tid);
+        A.template load<P>(sa, c, tid);
+      } else {
+        B.template store<P>(nxt + C::PART, c - OA::CH, tid);
+        B.template load<P>(sb, c - OA::CH, tid);
       }
     }
 #pragma unroll
@@ -376,9 +388,9 @@ __device__ __forceinline__ void k_step(const short* __restrict__ st, short* __re
       // (the reads are already ahead of the MFMAs)
     } else if constexpr (kk == 0 && SPREAD == 1) {
       __builtin_amdgcn_sched_group_barrier(kSgDsRead, NR, 0);
-      slice_order<NM, 0, STORE ? ops : 0, LOAD ? ops : 0, 0>();
+      slice_order<NM, 0, ops, ops, 0>();
     } else {
-      slice_order<NM, NR, STORE ? ops : 0, LOAD ? ops : 0, 0>();
+      slice_order<NM, NR, ops, ops, 0>();
     }
     __builtin_amdgcn_sched_barrier(0);
   };
@@ -386,6 +398,31 @@ __device__ __forceinline__ void k_step(const short* __restrict__ st, short* __re
   slice(Int<1>());
   slice(Int<2>());
   slice(Int<3>());
+}
+
+// PF K steps from step kt (a multiple of PF) on, the register sets in turn.
+template <class E, class C, int KA, int KB, int U>
+__device__ __forceinline__ void k_steps(short* lds, Operand<E, C::BM, C::NT, KA, C::PF>& A,
+                                        Operand<E, C::BN, C::NT, KB, C::PF>& B, long long k0, int kt,
+                                        int tid, int aoff, int boff, short8 (&fa0)[C::FM],
+                                        short8 (&fb0)[C::FN], floatx16 (&acc)[C::FM][C::FN]) {
+  if constexpr (U < C::PF) {
+    const int t = kt + U;
+    k_step<E, C, KA, KB, (U + 1) % C::PF>(lds + (t & 1) * C::STAGE, lds + ((t + 1) & 1) * C::STAGE, A,
+                                          B, k0 + (long long)(t + 1 + C::PF) * BK, tid, aoff, boff, fa0,
+                                          fb0, acc);
+    k_steps<E, C, KA, KB, U + 1>(lds, A, B, k0, kt, tid, aoff, boff, fa0, fb0, acc);
+  }
+}
+
+template <class E, class C, class OA, class OB, int P>
+__device__ __forceinline__ void load_ahead(OA& A, OB& B, long long k0, int tid) {
+  if constexpr (P < C::PF) {
+    A.template load_all<P>(k0 + P * BK, tid);
+    B.template load_all<P>(k0 + P * BK, tid);
+    __builtin_amdgcn_sched_barrier(0);      // (in tile order, as the loop's waits count them)
+    load_ahead<E, C, OA, OB, P + 1>(A, B, k0, tid);
+  }
 }
 
 // F32: C goes to G; PART: to the scratch (splits); else to Y.
@@ -427,40 +464,30 @@ __global__ __launch_bounds__(C::NT, C::PER_CU) void k_lin(LinP p) {
     long long k1 = k0 + (long long)p.steps * BK;
     if (k1 > p.K) k1 = p.K;
     const int nk = (int)((k1 - k0 + BK - 1) / BK);          // >= 1
-    typedef Operand<E, C::BM, C::NT, KA> OA;
-    typedef Operand<E, C::BN, C::NT, KB> OB;
+    typedef Operand<E, C::BM, C::NT, KA, C::PF> OA;
+    typedef Operand<E, C::BN, C::NT, KB, C::PF> OB;
     OA A;
     OB B;
-    A.init(p.A, nullptr, p.lda, p.M, p.K, m0, tid);
-    B.init(p.B, p.bs, p.ldb, p.N, p.K, n0, tid);
+    A.init(p.A, nullptr, p.lda, p.M, k1, m0, tid);       // (nothing past this part's K is read)
+    B.init(p.B, p.bs, p.ldb, p.N, k1, n0, tid);
     const int aoff = OA::frag_off(wm * C::WTM, lane), boff = OB::frag_off(wn * C::WTN, lane);
-    A.load_all(k0, tid);
-    B.load_all(k0, tid);
-    A.store_all(lds, tid);
-    B.store_all(lds + C::PART, tid);
-    if (nk > 1) {
-      A.load_all(k0 + BK, tid);
-      B.load_all(k0 + BK, tid);
-    }
+    // tile j passes through register set j % PF
+    load_ahead<E, C, OA, OB, 0>(A, B, k0, tid);
+    A.template store_all<0>(lds, tid);
+    B.template store_all<0>(lds + C::PART, tid);
+    A.template load_all<0>(k0 + C::PF * BK, tid);
+    B.template load_all<0>(k0 + C::PF * BK, tid);
+    __builtin_amdgcn_sched_barrier(0);
     __syncthreads();
     short8 fa0[C::FM], fb0[C::FN];
 #pragma unroll
     for (int i = 0; i < C::FM; ++i) fa0[i] = OA::frag(lds + aoff, i, 0);
 #pragma unroll
     for (int j = 0; j < C::FN; ++j) fb0[j] = OB::frag(lds + C::PART + boff, j, 0);
-    int kt = 0;
-    for (; kt + 2 < nk; ++kt)
-      k_step<E, C, KA, KB, true, true, true>(lds + (kt & 1) * C::STAGE, lds + ((kt + 1) & 1) * C::STAGE,
-                                             A, B, k0 + (long long)(kt + 2) * BK, tid, aoff, boff,
-                                             fa0, fb0, acc);
-    if (kt + 1 < nk) {
-      k_step<E, C, KA, KB, true, false, true>(lds + (kt & 1) * C::STAGE, lds + ((kt + 1) & 1) * C::STAGE,
-                                              A, B, 0, tid, aoff, boff, fa0, fb0, acc);
-      ++kt;
-    }
-    // the last step's barrier also frees the LDS for the epilogue
-    k_step<E, C, KA, KB, false, false, false>(lds + (kt & 1) * C::STAGE, lds + ((kt + 1) & 1) * C::STAGE,
-                                              A, B, 0, tid, aoff, boff, fa0, fb0, acc);
+    // whole rounds of the register sets: steps past the end multiply zeros
+    for (int kt = 0; kt < nk; kt += C::PF)
+      k_steps<E, C, KA, KB, 0>(lds, A, B, k0, kt, tid, aoff, boff, fa0, fb0, acc);
+    // (the last step's barrier also frees the LDS for the epilogue)
   }
 
   // Accumulators of a 32 x 32 block: lane l, value v holds row 8 (v / 4) +
@@ -527,25 +554,59 @@ __global__ __launch_bounds__(C::NT, C::PER_CU) void k_lin(LinP p) {
   }
 }
 
-// The splits' tiles added in order, then the epilogue.  One chunk of 8
-// columns a thread, the scratch's rows numbered through.
-template <class E, bool F32>
+// The splits' tiles added up, then the epilogue.  A workgroup takes 256 / GR
+// chunks of 8 columns (the scratch's rows numbered through), GR threads a
+// chunk, each the sum of a run of the splits in order; the runs join in order.
+// GR = 8 where one thread a chunk would leave most of the chip idle.
+template <class E, bool F32, int GR>
 __global__ __launch_bounds__(256) void k_lin_join(const float* __restrict__ part, long long stride,
                                                   int splits, long long M, unsigned nch, Finish f) {
-  const long long base = (long long)blockIdx.x * 256;
-  if (base + threadIdx.x >= M * nch) return;
-  const long long row0 = base / nch;
-  const unsigned c0 = (unsigned)(base - row0 * nch) + threadIdx.x;
-  const unsigned dr = c0 / nch;
-  const float* s = part + (base + threadIdx.x) * 8;
+  constexpr int CW = 256 / GR;
+  __shared__ float sh[GR > 1 ? GR - 1 : 1][CW][8 + 1];
+  const int ci = threadIdx.x % CW, g = threadIdx.x / CW;
+  const long long base = (long long)blockIdx.x * CW;
+  const bool in = base + ci < M * nch;
   float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  if (in) {
+    const float* s = part + (base + ci) * 8;
+    const int per = (splits + GR - 1) / GR;
+    const int i1 = min(splits, (g + 1) * per);
 #pragma unroll 4
-  for (int i = 0; i < splits; ++i) {
-    const float4 a = *(const float4*)(s + i * stride), b = *(const float4*)(s + i * stride + 4);
-    v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
-    v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+    for (int i = g * per; i < i1; ++i) {
+      const float4 a = *(const float4*)(s + i * stride), b = *(const float4*)(s + i * stride + 4);
+      v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
+      v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+    }
   }
+  if constexpr (GR > 1) {
+    if (g > 0) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sh[g - 1][ci][e] = v[e];
+    }
+    __syncthreads();
+    if (g > 0) return;
+    for (int q = 0; q < GR - 1; ++q)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] += sh[q][ci][e];
+  }
+  if (!in) return;
+  const long long row0 = base / nch;
+  const unsigned c0 = (unsigned)(base - row0 * nch) + ci;
+  const unsigned dr = c0 / nch;
   finish8<E, F32>(f, row0 + dr, (int)(c0 - dr * nch) * 8, v);
+}
+
+template <class E, bool F32>
+hipError_t launch_join(const float* part, long long stride, int splits, long long M, unsigned nch,
+                       const Finish& f, hipStream_t s) {
+  const long long chunks = M * nch;
+  if (splits >= 4 && chunks <= 65536)
+    hipLaunchKernelGGL((k_lin_join<E, F32, 8>), dim3((unsigned)((chunks + 31) / 32)), dim3(256), 0, s,
+                       part, stride, splits, M, nch, f);
+  else
+    hipLaunchKernelGGL((k_lin_join<E, F32, 1>), dim3((unsigned)((chunks + 255) / 256)), dim3(256), 0, s,
+                       part, stride, splits, M, nch, f);
+  return hipGetLastError();
 }
 
 // No K at all (a gradient over no tokens): C = 0.
@@ -679,29 +740,37 @@ struct LinPlan {
 
 long long up8(long long x) { return pad_to(x, 8); }
 
-// Tile shapes with their time model, fitted to whole rounds at K = 64 .. 4096
-// (8192 x 4096 x 4096 class sizes): microseconds of one K step and of the
-// fixed part (first loads, epilogue) of one round of workgroups.
-struct Tile { int bm, bn, slots; double step, fixed; };
-constexpr Tile kTiles[4] = {{256, 256, 256, 1.53, 11.0},
-                            {192, 256, 256, 1.24, 8.5},
-                            {128, 256, 256, 0.89, 6.5},
-                            {128, 128, 512, 1.05, 6.5}};
+// Tile shapes with their time model, microseconds: one K step of a workgroup
+// on an idle chip (lo) and with a workgroup on every CU (hi), and the fixed
+// part of a workgroup (first loads, epilogue).  Fitted to single launches at
+// K = 64 .. 16384 from a few tiles to 1400.  The two small tiles run 2 or 3
+// workgroups a CU at the same total rate, so a round is 256 of any shape.
+struct Tile { int bm, bn; double lo, hi, fixed; };
+constexpr int kNTiles = 5;
+constexpr Tile kTiles[kNTiles] = {{256, 256, 1.05, 1.53, 11.0},
+                                  {192, 256, 0.85, 1.22, 8.5},
+                                  {128, 256, 0.65, 0.89, 6.5},
+                                  {128, 128, 0.45, 0.53, 4.5},
+                                  {64, 64, 0.20, 0.24, 3.0}};
+constexpr int kCus = 256;
 
 // The cheapest tile shape and split of one rectangle: rounds of workgroups
 // over the 256 CUs, and for splits the join's launch and its traffic.
-double choose_tile(LinPart& q, long long K) {
+double choose_tile(LinPart& q, long long K, bool f8) {
   static const int kSplits[] = {1, 2, 3, 4, 5, 6, 7, 8, 10, 12, 14, 16, 20, 24, 28, 32, 40, 48, 64};
   const long long nk = (K + BK - 1) / BK;
   double best = 1e30;
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < kNTiles; ++i) {
     const Tile& t = kTiles[i];
     const long long tiles = ((q.M + t.bm - 1) / t.bm) * ((q.N + t.bn - 1) / t.bn);
     for (const int sp : kSplits) {
-      if (sp > 1 && (sp > nk || tiles * sp > 4 * t.slots)) break;
+      if (sp > 1 && (sp > nk || tiles * sp > 4 * kCus)) break;
       const int steps = (int)((nk + sp - 1) / sp);
-      const double rounds = ceil((double)(tiles * sp) / t.slots);
-      double us = rounds * (steps * t.step + t.fixed);
+      const double load = (double)(tiles * sp) / kCus, rounds = ceil(load);
+      // (on an idle chip the decoding of 8-bit operands is not hidden)
+      const double lo = f8 ? t.lo + 0.15 : t.lo, hi = t.hi > lo ? t.hi : lo;
+      const double step = lo + (hi - lo) * (load < 1.0 ? load : 1.0);
+      double us = rounds * (steps * step + t.fixed);
       if (sp > 1) us += 4.0 + 8.0 * sp * (double)q.M * q.N / 5.0e6;
       if (us < best) {
         best = us;
@@ -718,25 +787,25 @@ double choose_tile(LinPart& q, long long K) {
 // rounds, and what is left as a rectangle of its own with its own tile shape
 // (8192 x 11008 outputs are 5.4 rounds of the large tile: 5 rounds and 768
 // columns in one round of 128 x 256 tiles instead of 6).
-void choose_parts(LinPlan& q, long long M, long long N, long long K) {
+void choose_parts(LinPlan& q, long long M, long long N, long long K, bool f8) {
   LinPart whole = {0, 0, M, N, 0, 1, 0};
-  double best = choose_tile(whole, K);
+  double best = choose_tile(whole, K, f8);
   q.nparts = 1;
   q.part[0] = whole;
   const int nk = (int)((K + BK - 1) / BK);
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < kNTiles; ++i) {
     const Tile& t = kTiles[i];
     const long long tm = (M + t.bm - 1) / t.bm, tn = (N + t.bn - 1) / t.bn;
-    const long long full = tm * tn / t.slots;
+    const long long full = tm * tn / kCus;
     if (full < 1) continue;
-    const double us = (double)full * (nk * t.step + t.fixed) + 3.0;
+    const double us = (double)full * (nk * t.hi + t.fixed) + 8.0;
     for (int side = 0; side < 2; ++side) {
-      const long long cut = side ? full * t.slots / tn : full * t.slots / tm;   // tile rows / columns
+      const long long cut = full * kCus / (side ? tn : tm);               // tile rows / columns
       if (cut < 1 || cut >= (side ? tm : tn)) continue;
       const LinPart a = {0, 0, side ? cut * t.bm : M, side ? N : cut * t.bn, i, 1, nk};
       LinPart b = {side ? cut * t.bm : 0, side ? 0 : cut * t.bn, side ? M - cut * t.bm : M,
                    side ? N : N - cut * t.bn, 0, 1, 0};
-      const double both = us + choose_tile(b, K);
+      const double both = us + choose_tile(b, K, f8);
       if (both < best) {
         best = both;
         q.nparts = 2;
@@ -756,7 +825,7 @@ LinPlan lin_plan(const LinDesc& d) {
   if (q.thin) return q;
   q.copyA = !in_place(d.A, d.lda, q.colsA);
   q.copyB = !d.bs && !in_place(d.B, d.ldb, q.colsB);
-  choose_parts(q, d.M, d.N, d.K);
+  choose_parts(q, d.M, d.N, d.K, d.bs != nullptr);
   size_t off = 0;
   auto take = [&](size_t b) { const size_t o = off; off = (off + b + 255) & ~(size_t)255; return o; };
   if (q.copyA) q.oA = take((size_t)q.rowsA * up8(q.colsA) * 2);
@@ -794,8 +863,9 @@ hipError_t launch_cfg(LinP p, int tile, hipStream_t s) {
     case 0: return launch_tiles<E, CfgL, KA, KB, F32>(p, s);
     case 1: return launch_tiles<E, CfgM, KA, KB, F32>(p, s);
     case 2: return launch_tiles<E, CfgW, KA, KB, F32>(p, s);
+    case 3: return launch_tiles<E, CfgS, KA, KB, F32>(p, s);
   }
-  return launch_tiles<E, CfgS, KA, KB, F32>(p, s);
+  return launch_tiles<E, CfgT, KA, KB, F32>(p, s);
 }
 
 template <class E>
@@ -882,14 +952,8 @@ hipError_t launch_lin_t(const LinDesc& d, void* ws, hipStream_t s) {
     if (t.splits == 1) continue;
     TraceScope ts("linear_join", 0.0, 4.0 * (double)t.splits * t.M * t.N, s);
     const unsigned nch = (unsigned)(p.ldp / 8);
-    const dim3 grid((unsigned)((t.M * nch + 255) / 256));
-    if (d.G)
-      hipLaunchKernelGGL((k_lin_join<E, true>), grid, dim3(256), 0, s, p.part, p.part_stride,
-                         t.splits, t.M, nch, p.f);
-    else
-      hipLaunchKernelGGL((k_lin_join<E, false>), grid, dim3(256), 0, s, p.part, p.part_stride,
-                         t.splits, t.M, nch, p.f);
-    e = hipGetLastError();
+    e = d.G ? launch_join<E, true>(p.part, p.part_stride, t.splits, t.M, nch, p.f, s)
+            : launch_join<E, false>(p.part, p.part_stride, t.splits, t.M, nch, p.f, s);
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
