@@ -87,13 +87,13 @@ struct Chunk {
   __device__ __forceinline__ void init(const Finish& f, int c) {
     if constexpr (!F32) {
       if (!f.bias) return;
-      if (f.bias_f32) load8((const float*)f.bias, c, f.N, rows_aligned((const float*)f.bias, 8), b);
-      else load8((const E*)f.bias, c, f.N, rows_aligned((const E*)f.bias, 8), b);
+      if (f.bias_f32) load8((const float*)f.bias, c, f.N, b);
+      else load8((const E*)f.bias, c, f.N, b);
     }
   }
   static __device__ __forceinline__ void addend(const Finish& f, long long r, int c, float (&o)[8]) {
-    if constexpr (F32) load8((const float*)f.G + r * f.ldg, c, f.N, rows_aligned(f.G, f.ldg), o);
-    else load8((const E*)f.R + r * f.ldr, c, f.N, rows_aligned((const E*)f.R, f.ldr), o);
+    if constexpr (F32) load8((const float*)f.G + r * f.ldg, c, f.N, o);
+    else load8((const E*)f.R + r * f.ldr, c, f.N, o);
   }
   template <bool ADD>
   __device__ __forceinline__ void put(const Finish& f, long long r, int c, float (&v)[8],
@@ -103,19 +103,19 @@ struct Chunk {
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] += o[e];
       }
-      store8(f.G + r * f.ldg, c, f.N, rows_aligned(f.G, f.ldg), v);
+      store8(f.G + r * f.ldg, c, f.N, v);
     } else {
       if (f.bias) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] += b[e];
       }
-      if (f.Z) store8((E*)f.Z + r * f.ldz, c, f.N, rows_aligned((const E*)f.Z, f.ldz), v);
+      if (f.Z) store8((E*)f.Z + r * f.ldz, c, f.N, v);
       if (f.act != DION3_ACT_NONE) activate8(f.act, v);
       if constexpr (ADD) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] += o[e];
       }
-      store8((E*)f.Y + r * f.ldy, c, f.N, rows_aligned((const E*)f.Y, f.ldy), v);
+      store8((E*)f.Y + r * f.ldy, c, f.N, v);
     }
   }
 };
@@ -537,7 +537,7 @@ __global__ __launch_bounds__(C::NT, C::PER_CU) void k_lin(LinP p) {
           const long long row = r0 + (b + u) * RPP;
           if (!FULL.value && row >= p.M) continue;
           if constexpr (PART)
-            store8(p.part + split * p.part_stride + row * p.ldp, n0 + c, p.ldp, true, v[u]);
+            store8(p.part + split * p.part_stride + row * p.ldp, n0 + c, p.ldp, v[u]);
           else
             ch.template put<ADD.value>(p.f, row, n0 + c, v[u], o[u]);
         }

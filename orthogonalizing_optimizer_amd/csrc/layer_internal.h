@@ -21,51 +21,66 @@ __device__ __forceinline__ float to_f32(bf16 v) { return (float)v; }
 __device__ __forceinline__ float to_f32(f16 v) { return (float)v; }
 __device__ __forceinline__ float to_f32(float v) { return v; }
 
+// Chunks of 8 columns of a row of m elements.  16-byte accesses need no more
+// than the element's own alignment here (gfx950 splits unaligned ones), so any
+// row stride and any base take the same path.
+//
+// fetch8 asks for columns c .. c + 7 without a branch, at the row's end for
+// its last 8 columns, and chunk8 turns them into floats (zero past m); kept
+// apart, because turning the first tensor's chunk into floats would wait for
+// it before the next tensor's is asked for.  (fp32 rows, read once a
+// workgroup, take their last columns one by one.)
 template <class E>
-struct Vec8 {
+struct Raw8 {
   typedef E type __attribute__((ext_vector_type(8)));
+  struct __attribute__((packed, aligned(sizeof(E)))) Any { type v; };
+  type v;
 };
 
-// True when rows of E starting at p with stride ld elements allow 16-byte
-// accesses at every chunk.
 template <class E>
-__host__ __device__ inline bool rows_aligned(const E* p, long long ld) {
-  return ((uintptr_t)p & 15) == 0 && (ld * (long long)sizeof(E)) % 16 == 0;
-}
-
-// Columns c .. c + 7 of a row of m elements as floats (zero past m).
-template <class E>
-__device__ __forceinline__ void load8(const E* __restrict__ row, int c, int m, bool vec,
-                                      float (&v)[8]) {
-  if (vec && c + 8 <= m) {
-    if constexpr (sizeof(E) == 4) {
-      const float4 a = ((const float4*)(row + c))[0], b = ((const float4*)(row + c))[1];
-      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    } else {
-      const typename Vec8<E>::type x = *(const typename Vec8<E>::type*)(row + c);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = to_f32((E)x[e]);
-    }
+__device__ __forceinline__ Raw8<E> fetch8(const E* __restrict__ row, int c, int m) {
+  Raw8<E> r;
+  if (sizeof(E) == 2 ? m >= 8 : c + 8 <= m) {
+    r.v = ((const typename Raw8<E>::Any*)(row + min(c, m - 8)))->v;
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = c + e < m ? to_f32(row[c + e]) : 0.0f;
+    for (int e = 0; e < 8; ++e) r.v[e] = c + e < m ? row[c + e] : (E)0.0f;
+  }
+  return r;
+}
+
+template <class E>
+__device__ __forceinline__ void chunk8(const Raw8<E>& r, int c, int m, float (&v)[8]) {
+  // columns of r before c: 0 inside the row
+  const int s = sizeof(E) == 2 && m >= 8 ? c - min(c, m - 8) : 0;
+  if (s == 0) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = to_f32((E)r.v[e]);
+  } else if constexpr (sizeof(E) == 2) {
+    typedef unsigned long long u64x2 __attribute__((ext_vector_type(2)));
+    u64x2 w = __builtin_bit_cast(u64x2, r.v);
+    const int b = 16 * (s & 3);
+    const unsigned long long lo = s & 4 ? w[1] : w[0], hi = s & 4 ? 0 : w[1];
+    w[0] = lo >> b | (b ? hi << (64 - b) : 0);
+    w[1] = hi >> b;
+    const typename Raw8<E>::type t = __builtin_bit_cast(typename Raw8<E>::type, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = s < 8 ? to_f32((E)t[e]) : 0.0f;
   }
 }
 
 template <class E>
-__device__ __forceinline__ void store8(E* __restrict__ row, int c, int m, bool vec,
-                                       const float (&v)[8]) {
-  if (vec && c + 8 <= m) {
-    if constexpr (sizeof(E) == 4) {
-      ((float4*)(row + c))[0] = make_float4(v[0], v[1], v[2], v[3]);
-      ((float4*)(row + c))[1] = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
-      typename Vec8<E>::type x;
+__device__ __forceinline__ void load8(const E* __restrict__ row, int c, int m, float (&v)[8]) {
+  chunk8(fetch8(row, c, m), c, m, v);
+}
+
+template <class E>
+__device__ __forceinline__ void store8(E* __restrict__ row, int c, int m, const float (&v)[8]) {
+  if (c + 8 <= m) {
+    Raw8<E> r;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = (E)v[e];
-      *(typename Vec8<E>::type*)(row + c) = x;
-    }
+    for (int e = 0; e < 8; ++e) r.v[e] = (E)v[e];
+    ((typename Raw8<E>::Any*)(row + c))->v = r.v;
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
@@ -74,29 +89,61 @@ __device__ __forceinline__ void store8(E* __restrict__ row, int c, int m, bool v
 }
 
 // -------------------------------------------------------------- activations
+//
+// An element of an activation costs as much VALU time as it does HBM time
+// (without packed fp32 the chip does about 39 T operations a second, one per
+// 150 bytes moved at 5.8 TB/s), so the forms below are counted in
+// instructions: the hardware's exponential and reciprocal (each within one
+// step of fp32, for 16-bit outputs), constants folded into the exponent.
 
-// 1 / (1 + exp(-x)) by the hardware's exponential and reciprocal (each within
-// one step of fp32): a divide rounded to the last bit costs ten instructions
-// more for every output element, and the outputs are 16-bit.
-__device__ __forceinline__ float sigmoid(float x) {
-  return __builtin_amdgcn_rcpf(1.0f + __expf(-x));
-}
-
+constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGeluC = 0.7978845608028654f;    // sqrt(2 / pi)
 constexpr float kGeluA = 0.044715f;
-constexpr float kSqrtHalf = 0.7071067811865476f;
 constexpr float kInvSqrt2Pi = 0.3989422804014327f;
 
-// act(z).  gelu_tanh: 0.5 (1 + tanh u) = sigmoid(2 u), which keeps its
-// relative accuracy for large negative u.  gelu: 0.5 (1 + erf x) = 0.5 erfc(-x)
-// for the same reason.
+// 1 / (1 + 2^-u)
+__device__ __forceinline__ float sigmoid2(float u) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-u));
+}
+
+// gelu_tanh: 0.5 (1 + tanh v) = 1 / (1 + exp(-2 v)), which keeps its relative
+// accuracy for large negative v = sqrt(2 / pi) (z + 0.044715 z^3).
+__device__ __forceinline__ float gelu_tanh_gate(float z) {
+  constexpr float k = 2.0f * kGeluC * kLog2e;
+  return sigmoid2(z * __builtin_fmaf(k * kGeluA, z * z, k));
+}
+
+// The normal distribution function and e = exp(-z^2 / 2): with x = |z| / sqrt 2
+// and t = 1 / (1 + 0.3 x), erfc(x) exp(x^2) = t Q(t), Q of degree 8 fitted to
+// the smallest largest relative error over 0 <= x <= 12 (2e-8; 5e-7 as
+// evaluated in fp32).  The lower tail keeps its relative accuracy.
+__device__ __forceinline__ float normal_cdf(float z, float& e) {
+  const float t = __builtin_amdgcn_rcpf(
+      __builtin_fmaf(0.3f * 0.7071067811865476f, __builtin_fabsf(z), 1.0f));
+  float q = -0.129252436f;
+  q = __builtin_fmaf(q, t, 0.484298187f);
+  q = __builtin_fmaf(q, t, -0.509765608f);
+  q = __builtin_fmaf(q, t, 0.544959805f);
+  q = __builtin_fmaf(q, t, -0.0928215102f);
+  q = __builtin_fmaf(q, t, 0.214179651f);
+  q = __builtin_fmaf(q, t, 0.148521671f);
+  q = __builtin_fmaf(q, t, 0.170690875f);
+  q = __builtin_fmaf(q, t, 0.169189357f);
+  e = __builtin_amdgcn_exp2f(z * z * (-0.5f * kLog2e));
+  const float tail = 0.5f * t * q * e;
+  return z < 0.0f ? tail : 1.0f - tail;
+}
+
+// act(z)
 __device__ __forceinline__ float activate(int act, float z) {
   switch (act) {
     case DION3_ACT_RELU: return z < 0.0f ? 0.0f : z;
-    case DION3_ACT_GELU: return 0.5f * z * erfcf(-z * kSqrtHalf);
-    case DION3_ACT_GELU_TANH:
-      return z * sigmoid(2.0f * kGeluC * __builtin_fmaf(kGeluA * z * z, z, z));
-    case DION3_ACT_SILU: return z * sigmoid(z);
+    case DION3_ACT_GELU: {
+      float e;
+      return z * normal_cdf(z, e);
+    }
+    case DION3_ACT_GELU_TANH: return z * gelu_tanh_gate(z);
+    case DION3_ACT_SILU: return z * sigmoid2(z * kLog2e);
   }
   return z;
 }
@@ -121,16 +168,19 @@ __device__ __forceinline__ void activate8(int act, float (&v)[8]) {
 __device__ __forceinline__ float slope(int act, float z) {
   switch (act) {
     case DION3_ACT_RELU: return z > 0.0f ? 1.0f : 0.0f;
-    case DION3_ACT_GELU:
-      return __builtin_fmaf(z * kInvSqrt2Pi, __expf(-0.5f * z * z), 0.5f * erfcf(-z * kSqrtHalf));
+    case DION3_ACT_GELU: {
+      float e;
+      const float c = normal_cdf(z, e);
+      return __builtin_fmaf(z * kInvSqrt2Pi, e, c);
+    }
     case DION3_ACT_GELU_TANH: {
-      const float s = sigmoid(2.0f * kGeluC * __builtin_fmaf(kGeluA * z * z, z, z));
-      const float du = kGeluC * __builtin_fmaf(3.0f * kGeluA * z, z, 1.0f);
-      return __builtin_fmaf(2.0f * z * du, s * (1.0f - s), s);
+      const float s = gelu_tanh_gate(z);
+      const float du = z * __builtin_fmaf(6.0f * kGeluC * kGeluA, z * z, 2.0f * kGeluC);
+      return __builtin_fmaf(du, __builtin_fmaf(-s, s, s), s);
     }
     case DION3_ACT_SILU: {
-      const float s = sigmoid(z);
-      return s * __builtin_fmaf(z, 1.0f - s, 1.0f);
+      const float s = sigmoid2(z * kLog2e);
+      return __builtin_fmaf(z, __builtin_fmaf(-s, s, s), s);
     }
   }
   return 1.0f;
@@ -156,48 +206,59 @@ __device__ __forceinline__ float f8_inv_scale(int byte) {
   return __builtin_bit_cast(float, (unsigned)(254 - byte) << 23);
 }
 
-// The largest magnitude q may take: 448, except in a block whose scale is the
-// type's last, where 448 rounds to past the type's largest finite value and
-// the largest q is 240 (bf16, fp32: 240 * 2^120; fp16: 240 * 2^8 = 61440).
+// The value of lane ^ 1 (X = 1) or lane ^ 2 (X = 2), inside groups of 4 lanes.
+template <int X>
+__device__ __forceinline__ unsigned quad_xor(unsigned v) {
+  return __builtin_amdgcn_update_dpp(0, v, X == 1 ? 0xB1 : 0x4E, 0xF, 0xF, true);
+}
+__device__ __forceinline__ unsigned quad_max(unsigned v) {
+  v = max(v, quad_xor<1>(v));
+  return max(v, quad_xor<2>(v));
+}
+
+// A block of 32 columns, 8 in each of 4 neighbouring lanes (all of them take
+// part): its scale byte, and this lane's 8 values as e4m3, round to nearest
+// even.  Magnitudes are compared as the bits of |v|, whose order is that of
+// the floats.  Finite blocks below the type's last scale (nearly all) need one
+// multiplication and half a conversion a value; the others take the branch.
+constexpr unsigned kInfBits = 0x7f800000u;
 template <class E>
-__device__ __forceinline__ float f8_limit(int byte) {
-  return byte == (sizeof(E) == 2 && __is_same(E, f16) ? 127 + 8 : 127 + 120) ? 240.0f : 448.0f;
-}
-
-// |v| where v is finite, else 0 (infinities and NaN do not take part in the
-// scale; their q is NaN).
-__device__ __forceinline__ float finite_abs(float v) {
-  const float a = __builtin_fabsf(v);
-  return a <= 3.402823466e38f ? a : 0.0f;
-}
-
-// 8 scaled values as 8 bytes of e4m3 (round to nearest even).
-__device__ __forceinline__ uint2 f8_encode8(const float (&v)[8], float inv, float lim) {
-  unsigned w[2];
+__device__ __forceinline__ uint2 f8_encode_block(const float (&v)[8], int& byte) {
+  unsigned a = 0;
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    float u[4];
+  for (int e = 0; e < 8; ++e) a = max(a, __builtin_bit_cast(unsigned, v[e]) & 0x7fffffffu);
+  a = quad_max(a);
+  byte = f8_scale_byte(__builtin_bit_cast(float, a));
+  constexpr int last = __is_same(E, f16) ? 127 + 8 : 127 + 120;
+  float u[8];
+  if (a < kInfBits && byte != last) {
+    const float inv = f8_inv_scale(byte);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) u[e] = fminf(fmaxf(v[4 * h + e] * inv, -lim), lim);
-    int p = __builtin_amdgcn_cvt_pk_fp8_f32(u[0], u[1], 0, false);
-    p = __builtin_amdgcn_cvt_pk_fp8_f32(u[2], u[3], p, true);
-    w[h] = (unsigned)p;
+    for (int e = 0; e < 8; ++e) u[e] = v[e] * inv;
+  } else {
+    // infinities and NaN take no part in the scale and become NaN
+    a = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const unsigned b = __builtin_bit_cast(unsigned, v[e]) & 0x7fffffffu;
+      a = max(a, b < kInfBits ? b : 0u);
+    }
+    a = quad_max(a);
+    byte = f8_scale_byte(__builtin_bit_cast(float, a));
+    // 448 of the type's last scale would be past its largest finite value
+    const float inv = f8_inv_scale(byte), lim = byte == last ? 240.0f : 448.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const unsigned b = __builtin_bit_cast(unsigned, v[e]) & 0x7fffffffu;
+      const float c = fminf(fmaxf(v[e] * inv, -lim), lim);
+      u[e] = b < kInfBits ? c : __builtin_nanf("");
+    }
   }
-  // (fminf / fmaxf drop a NaN, and an infinity would take the limit)
-#pragma unroll
-  for (int e = 0; e < 8; ++e)
-    if (!(__builtin_fabsf(v[e]) <= 3.402823466e38f)) w[e >> 2] |= 0x7fu << (8 * (e & 3));
-  return make_uint2(w[0], w[1]);
-}
-
-// The largest finite magnitude of the 32-column block that 4 neighbouring
-// lanes hold 8 columns each of; every lane of the wave takes part.
-__device__ __forceinline__ float f8_block_amax(const float (&v)[8]) {
-  float a = 0.0f;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) a = fmaxf(a, finite_abs(v[e]));
-  a = fmaxf(a, __shfl_xor(a, 1, 64));
-  return fmaxf(a, __shfl_xor(a, 2, 64));
+  int w0 = __builtin_amdgcn_cvt_pk_fp8_f32(u[0], u[1], 0, false);
+  w0 = __builtin_amdgcn_cvt_pk_fp8_f32(u[2], u[3], w0, true);
+  int w1 = __builtin_amdgcn_cvt_pk_fp8_f32(u[4], u[5], 0, false);
+  w1 = __builtin_amdgcn_cvt_pk_fp8_f32(u[6], u[7], w1, true);
+  return make_uint2((unsigned)w0, (unsigned)w1);
 }
 
 // 2 of the 4 e4m3 bytes of `w` times 2^(byte - 127), the scale given as the

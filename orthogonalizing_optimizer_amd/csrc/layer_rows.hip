@@ -9,26 +9,43 @@
 namespace dion3 {
 namespace {
 
-// Sum over the NT threads that share a row, the same bits in every one of
-// them: butterfly inside each wave, then the waves' sums in wave order.  `sh`
-// holds two sets, used in turn by consecutive calls (`turn`), so that one
-// barrier a call is enough: a set is written again only after every thread
-// has passed the next call's barrier.
-template <int NT>
+// Sum over the threads that share a row, the same bits in every one of them:
+// butterfly inside each wave, then (WIDE: a row is the whole workgroup's) one
+// over the waves' sums, each 16 lanes reading all of them at once (a loop over
+// them waits for LDS once a wave; the 2048-wide norm took 57 us instead of
+// 44).  `sh` holds two sets, used in turn by consecutive
+// calls (`turn`), so that one barrier a call is enough: a set is written again
+// only after every thread has passed the next call's barrier.
+constexpr int kMaxWaves = 16;
+template <bool WIDE>
 __device__ __forceinline__ float row_sum(float v, float* sh, int turn) {
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o, 64);
-  if constexpr (NT > 64) {
-    constexpr int NW = NT / 64;
-    float* set = sh + (turn & 1) * NW;
+  if constexpr (WIDE) {
+    const int nw = blockDim.x >> 6;
+    float* set = sh + (turn & 1) * kMaxWaves;
     if ((threadIdx.x & 63) == 0) set[threadIdx.x >> 6] = v;
     __syncthreads();
-    float t = set[0];
+    const int w = threadIdx.x & (kMaxWaves - 1);
+    v = w < nw ? set[w] : 0.0f;
 #pragma unroll
-    for (int w = 1; w < NW; ++w) t += set[w];
-    v = t;
+    for (int o = 1; o < kMaxWaves; o <<= 1) v += __shfl_xor(v, o, 64);
   }
   return v;
+}
+
+// Threads of a row of m columns with at most `ch` chunks of 8 columns each: a
+// whole wave up to 512 columns (four rows a workgroup), else as many waves as
+// the chunks need, so that few lanes idle at any width.
+struct RowShape {
+  bool wide;
+  int ch, nt;       // chunks a thread, threads of the workgroup
+};
+RowShape row_shape(long long cols) {
+  const long long chunks = (cols + 7) / 8;
+  if (chunks <= 64) return {false, 1, 256};
+  const int ch = chunks <= 1024 ? 1 : chunks <= 2048 ? 2 : 4;
+  return {true, ch, (int)((chunks + 64 * ch - 1) / (64 * ch)) * 64};
 }
 
 // ------------------------------------------------------------------ the norm
@@ -36,9 +53,9 @@ __device__ __forceinline__ float row_sum(float v, float* sh, int turn) {
 //   h = E(x + r),  rstd = 1 / sqrt(mean_j h_j^2 + eps),  y = E(h rstd w),
 //   and y in 8 bits.  The statistics and y come from the rounded h, the one
 //   that the layers after this one read.
-// NT threads share a row (64: one wave; four rows a workgroup), each with CH
-// chunks of 8 columns in registers, so x and r are read once and h never read
-// back; a workgroup takes every gridDim-th row and keeps w in registers.
+// The threads of a row (RowShape) hold CH chunks of 8 columns each in
+// registers, so x and r are read once and h never read back; a workgroup takes
+// every gridDim-th row and keeps w in registers.
 struct NormP {
   const void* x; const void* r; const void* w;
   void* h; void* y;
@@ -54,46 +71,55 @@ __device__ __forceinline__ float norm_rstd(float sumsq, int m, float eps) {
   return 1.0f / sqrtf(sumsq / (float)m + eps);
 }
 
-template <class E, class WT, int NT, int CH>
-__global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_add_norm(NormP p) {
-  constexpr int RPW = NT < 256 ? 256 / NT : 1;   // rows a workgroup
-  static_assert(NT >= 256 || NT == 64, "a row belongs to one wave or to the whole workgroup");
-  __shared__ float sh[2 * (NT / 64)];
-  const int t = threadIdx.x % NT;
+template <class E, class WT, bool WIDE, int CH>
+__global__ __launch_bounds__(WIDE ? 1024 : 256) void k_add_norm(NormP p) {
+  const int NT = WIDE ? blockDim.x : 64, RPW = WIDE ? 1 : 4;   // threads a row, rows a workgroup
+  __shared__ float sh[2 * kMaxWaves];
+  const int t = WIDE ? threadIdx.x : threadIdx.x & 63;
   const int m = p.m, mp = (m + kF8Block - 1) / kF8Block * kF8Block;
-  const bool vx = rows_aligned((const E*)p.x, p.ldx);
-  const bool vr = rows_aligned((const E*)p.r, p.ldr);
-  const bool vh = rows_aligned((const E*)p.h, p.ldh);
-  const bool vy = rows_aligned((const E*)p.y, p.ldy);
-  const bool vw = rows_aligned((const WT*)p.w, 8);
   float w[CH][8];
 #pragma unroll
-  for (int i = 0; i < CH; ++i) load8((const WT*)p.w, (t + i * NT) * 8, m, vw, w[i]);
+  for (int i = 0; i < CH; ++i) load8((const WT*)p.w, (t + i * NT) * 8, m, w[i]);
   int turn = 0;
   const long long step = (long long)gridDim.x * RPW;
-  for (long long row = (long long)blockIdx.x * RPW + threadIdx.x / NT; row < p.T; row += step) {
-    const E* xr = (const E*)p.x + row * p.ldx;
+  long long row = (long long)blockIdx.x * RPW + (WIDE ? 0 : threadIdx.x >> 6);
+  // a row's chunks are on their way while the row before it is summed and
+  // written (where the registers hold them)
+  constexpr bool AHEAD = CH <= 2;
+  Raw8<E> rx[CH], rr[CH];
+  auto ask = [&](long long at) {
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      rx[i] = fetch8((const E*)p.x + at * p.ldx, (t + i * NT) * 8, m);
+      if (p.r) rr[i] = fetch8((const E*)p.r + at * p.ldr, (t + i * NT) * 8, m);
+    }
+  };
+  if (AHEAD && row < p.T) ask(row);
+  for (; row < p.T; row += step) {
+    if (!AHEAD) ask(row);
     float v[CH][8];
 #pragma unroll
-    for (int i = 0; i < CH; ++i) load8(xr, (t + i * NT) * 8, m, vx, v[i]);
-    if (p.r) {
-      const E* rr = (const E*)p.r + row * p.ldr;
-      float u[CH][8];
+    for (int i = 0; i < CH; ++i) {
+      chunk8(rx[i], (t + i * NT) * 8, m, v[i]);
+      if (p.r) {
+        float u[8];
+        chunk8(rr[i], (t + i * NT) * 8, m, u);
 #pragma unroll
-      for (int i = 0; i < CH; ++i) load8(rr, (t + i * NT) * 8, m, vr, u[i]);
-#pragma unroll
-      for (int i = 0; i < CH; ++i) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[i][e] = to_f32((E)(v[i][e] + u[i][e]));
-        if ((t + i * NT) * 8 < m) store8((E*)p.h + row * p.ldh, (t + i * NT) * 8, m, vh, v[i]);
+        for (int e = 0; e < 8; ++e) v[i][e] = to_f32((E)(v[i][e] + u[e]));
       }
+    }
+    if (AHEAD && row + step < p.T) ask(row + step);
+    if (p.r) {
+#pragma unroll
+      for (int i = 0; i < CH; ++i)
+        if ((t + i * NT) * 8 < m) store8((E*)p.h + row * p.ldh, (t + i * NT) * 8, m, v[i]);
     }
     float ss = 0.0f;
 #pragma unroll
     for (int i = 0; i < CH; ++i)
 #pragma unroll
       for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(v[i][e], v[i][e], ss);
-    ss = row_sum<NT>(ss, sh, turn++);
+    ss = row_sum<WIDE>(ss, sh, turn++);
     const float rs = norm_rstd<E>(ss, m, p.eps);
     if (t == 0 && p.rstd) p.rstd[row] = rs;
 #pragma unroll
@@ -101,15 +127,16 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_add_norm(NormP p) {
       const int c = (t + i * NT) * 8;
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[i][e] = to_f32((E)(v[i][e] * rs * w[i][e]));
-      if (p.y && c < m) store8((E*)p.y + row * p.ldy, c, m, vy, v[i]);
+      if (p.y && c < m) store8((E*)p.y + row * p.ldy, c, m, v[i]);
       if (p.q) {
         // columns past m hold zeros: inf rstd would make them NaN
 #pragma unroll
         for (int e = 0; e < 8; ++e)
           if (c + e >= m) v[i][e] = 0.0f;
-        const int byte = f8_scale_byte(f8_block_amax(v[i]));
+        int byte;
+        const uint2 q8 = f8_encode_block<E>(v[i], byte);
         if (c < mp) {
-          *(uint2*)(p.q + row * mp + c) = f8_encode8(v[i], f8_inv_scale(byte), f8_limit<E>(byte));
+          *(uint2*)(p.q + row * mp + c) = q8;
           if ((c & (kF8Block - 1)) == 0) p.s[row * (mp / kF8Block) + c / kF8Block] = byte;
         }
       }
@@ -122,14 +149,9 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_add_norm(NormP p) {
 template <class E, class WT>
 __global__ __launch_bounds__(1024) void k_add_norm_long(NormP p) {
   constexpr int NT = 1024;
-  __shared__ float sh[2 * (NT / 64)];
+  __shared__ float sh[2 * kMaxWaves];
   const int t = threadIdx.x;
   const int m = p.m, mp = (m + kF8Block - 1) / kF8Block * kF8Block;
-  const bool vx = rows_aligned((const E*)p.x, p.ldx);
-  const bool vr = rows_aligned((const E*)p.r, p.ldr);
-  const bool vh = rows_aligned((const E*)p.h, p.ldh);
-  const bool vy = rows_aligned((const E*)p.y, p.ldy);
-  const bool vw = rows_aligned((const WT*)p.w, 8);
   int turn = 0;
   for (long long row = blockIdx.x; row < p.T; row += gridDim.x) {
     const E* xr = (const E*)p.x + row * p.ldx;
@@ -137,38 +159,38 @@ __global__ __launch_bounds__(1024) void k_add_norm_long(NormP p) {
     float ss = 0.0f;
     for (int c = t * 8; c < m; c += NT * 8) {
       float v[8];
-      load8(xr, c, m, vx, v);
+      load8(xr, c, m, v);
       if (rr) {
         float u[8];
-        load8(rr, c, m, vr, u);
+        load8(rr, c, m, u);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = to_f32((E)(v[e] + u[e]));
-        store8((E*)p.h + row * p.ldh, c, m, vh, v);
+        store8((E*)p.h + row * p.ldh, c, m, v);
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(v[e], v[e], ss);
     }
-    ss = row_sum<NT>(ss, sh, turn++);
+    ss = row_sum<true>(ss, sh, turn++);
     const float rs = norm_rstd<E>(ss, m, p.eps);
     if (t == 0 && p.rstd) p.rstd[row] = rs;
     // (each thread reads back only what it wrote itself)
     const E* hr = p.r ? (const E*)p.h + row * p.ldh : xr;
-    const bool v2 = p.r ? vh : vx;
     for (int c0 = 0; c0 < mp; c0 += NT * 8) {      // whole waves stay for the block maxima
       const int c = c0 + t * 8;
       float v[8], w[8];
-      load8(hr, c, m, v2, v);
-      load8((const WT*)p.w, c, m, vw, w);
+      load8(hr, c, m, v);
+      load8((const WT*)p.w, c, m, w);
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = to_f32((E)(v[e] * rs * w[e]));
-      if (p.y && c < m) store8((E*)p.y + row * p.ldy, c, m, vy, v);
+      if (p.y && c < m) store8((E*)p.y + row * p.ldy, c, m, v);
       if (p.q) {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
           if (c + e >= m) v[e] = 0.0f;
-        const int byte = f8_scale_byte(f8_block_amax(v));
+        int byte;
+        const uint2 q8 = f8_encode_block<E>(v, byte);
         if (c < mp) {
-          *(uint2*)(p.q + row * mp + c) = f8_encode8(v, f8_inv_scale(byte), f8_limit<E>(byte));
+          *(uint2*)(p.q + row * mp + c) = q8;
           if ((c & (kF8Block - 1)) == 0) p.s[row * (mp / kF8Block) + c / kF8Block] = byte;
         }
       }
@@ -180,24 +202,22 @@ template <class E, class WT>
 hipError_t launch_norm_t(const NormP& p, hipStream_t s) {
   const long long T = p.T;
   const int mp = (int)f8_cols(p.m);
-  // eight workgroups of 256 threads a CU stay resident; more rows than that
-  // are taken in turns
-  auto grid = [&](long long rows_per_wg, long long most) {
-    const long long g = (T + rows_per_wg - 1) / rows_per_wg;
-    return dim3((unsigned)(g < most ? g : most));
-  };
-#define DION3_NORM(NT, CH) \
-  hipLaunchKernelGGL((k_add_norm<E, WT, NT, CH>), grid(NT < 256 ? 256 / NT : 1, 256LL * 2048 / (NT < 256 ? 256 : NT)), \
-                     dim3(NT < 256 ? 256 : NT), 0, s, p)
-  if (mp <= 512) DION3_NORM(64, 1);
-  else if (mp <= 1024) DION3_NORM(64, 2);
-  else if (mp <= 2048) DION3_NORM(256, 1);
-  else if (mp <= 4096) DION3_NORM(256, 2);
-  else if (mp <= 8192) DION3_NORM(512, 2);
-  else if (mp <= 16384) DION3_NORM(1024, 2);
-  else if (mp <= 32768) DION3_NORM(1024, 4);
-  else hipLaunchKernelGGL((k_add_norm_long<E, WT>), grid(1, 512), dim3(1024), 0, s, p);
-#undef DION3_NORM
+  if (mp > 32768) {
+    hipLaunchKernelGGL((k_add_norm_long<E, WT>), dim3((unsigned)(T < 512 ? T : 512)), dim3(1024), 0, s,
+                       p);
+    return hipGetLastError();
+  }
+  const RowShape q = row_shape(mp);
+  // workgroups that stay resident (6 waves a SIMD with one chunk a thread; more
+  // rows are taken in turns), and half as many again of the wider ones, whose
+  // sizes leave gaps (8192 x 4096 44 us, 4096 x 11008 72 us; 46 and 79 with
+  // the other's rule)
+  const long long rows = q.wide ? 1 : 4, need = (T + rows - 1) / rows, most = 256LL * (q.ch == 1 ? 1536 : 2048) / q.nt;
+  const dim3 grid((unsigned)(need < most ? need : most)), block(q.nt);
+  if (!q.wide) hipLaunchKernelGGL((k_add_norm<E, WT, false, 1>), grid, block, 0, s, p);
+  else if (q.ch == 1) hipLaunchKernelGGL((k_add_norm<E, WT, true, 1>), grid, block, 0, s, p);
+  else if (q.ch == 2) hipLaunchKernelGGL((k_add_norm<E, WT, true, 2>), grid, block, 0, s, p);
+  else hipLaunchKernelGGL((k_add_norm<E, WT, true, 4>), grid, block, 0, s, p);
   return hipGetLastError();
 }
 
@@ -205,10 +225,10 @@ hipError_t launch_norm_t(const NormP& p, hipStream_t s) {
 
 //   a = w dy, hat = h rstd, c = mean_j a_j hat_j,
 //   dx = E(rstd (a - hat c) + dh),  dw = sum over rows of dy hat.
-// The same split as the norm: NT threads share a row, CH chunks a thread; a
-// unit (a group of NT threads) takes every U-th row, keeps w and its part of
-// dw in registers and leaves its part as one row of the scratch, which
-// k_join_columns adds up in unit order.
+// The same split as the norm; a workgroup (a unit) takes every gridDim-th row
+// (or four rows at a time), keeps w and its part of dw in registers and leaves
+// its part as one row of the scratch, which k_join_columns adds up in unit
+// order.
 struct NormGradP {
   const void* dy; const void* h; const void* dh; const void* w;
   const float* rstd;
@@ -220,48 +240,58 @@ struct NormGradP {
   long long rows_per_unit; // the long form's row blocks
 };
 
-template <class E, class WT, int NT, int CH>
-__global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_norm_grad(NormGradP p) {
-  constexpr int RPW = NT < 256 ? 256 / NT : 1;
-  __shared__ float sh[2 * (NT / 64)];
-  const int t = threadIdx.x % NT;
-  const int unit = blockIdx.x * RPW + threadIdx.x / NT;
+template <class E, class WT, bool WIDE, int CH>
+__global__ __launch_bounds__(WIDE ? 1024 : 256) void k_norm_grad(NormGradP p) {
+  const int NT = WIDE ? blockDim.x : 64, RPW = WIDE ? 1 : 4;
+  __shared__ float sh[WIDE ? 2 * kMaxWaves : 3 * 512];
+  const int t = WIDE ? threadIdx.x : threadIdx.x & 63;
   const int m = p.m;
-  const bool vy = rows_aligned((const E*)p.dy, p.lddy);
-  const bool vh = rows_aligned((const E*)p.h, p.ldh);
-  const bool vd = rows_aligned((const E*)p.dh, p.lddh);
-  const bool vo = rows_aligned((const E*)p.dx, p.lddx);
-  const bool vw = rows_aligned((const WT*)p.w, 8);
   float w[CH][8], dw[CH][8];
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
-    load8((const WT*)p.w, (t + i * NT) * 8, m, vw, w[i]);
+    load8((const WT*)p.w, (t + i * NT) * 8, m, w[i]);
 #pragma unroll
     for (int e = 0; e < 8; ++e) dw[i][e] = 0.0f;
   }
   int turn = 0;
-  const long long U = (long long)gridDim.x * RPW;
-  for (long long row = unit; row < p.T; row += U) {
-    const float rs = p.rstd[row];
+  const long long step = (long long)gridDim.x * RPW;
+  long long row = (long long)blockIdx.x * RPW + (WIDE ? 0 : threadIdx.x >> 6);
+  const bool more = p.dh && p.dx;
+  Raw8<E> rh[CH], ry[CH], rd[CH];
+  float rs = 0.0f;
+  auto ask = [&](long long at) {
+    rs = p.rstd[at];
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      rh[i] = fetch8((const E*)p.h + at * p.ldh, (t + i * NT) * 8, m);
+      ry[i] = fetch8((const E*)p.dy + at * p.lddy, (t + i * NT) * 8, m);
+      if (more) rd[i] = fetch8((const E*)p.dh + at * p.lddh, (t + i * NT) * 8, m);
+    }
+  };
+  // (a row ahead costs more in resident workgroups than it hides: 8192 x 4096
+  // 66 us instead of 55)
+  for (; row < p.T; row += step) {
+    ask(row);
+    const float r1 = rs;
     float hat[CH][8], dy[CH][8], dh[CH][8];
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      load8((const E*)p.h + row * p.ldh, (t + i * NT) * 8, m, vh, hat[i]);
-      load8((const E*)p.dy + row * p.lddy, (t + i * NT) * 8, m, vy, dy[i]);
-      if (p.dh && p.dx) load8((const E*)p.dh + row * p.lddh, (t + i * NT) * 8, m, vd, dh[i]);
+      chunk8(rh[i], (t + i * NT) * 8, m, hat[i]);
+      chunk8(ry[i], (t + i * NT) * 8, m, dy[i]);
+      if (more) chunk8(rd[i], (t + i * NT) * 8, m, dh[i]);
     }
     float c = 0.0f;
 #pragma unroll
     for (int i = 0; i < CH; ++i)
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        hat[i][e] *= rs;
+        hat[i][e] *= r1;
         dw[i][e] = __builtin_fmaf(dy[i][e], hat[i][e], dw[i][e]);
         dy[i][e] *= w[i][e];
         c = __builtin_fmaf(dy[i][e], hat[i][e], c);
       }
     if (!p.dx) continue;
-    c = row_sum<NT>(c, sh, turn++) / (float)m;
+    c = row_sum<WIDE>(c, sh, turn++) / (float)m;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const int col = (t + i * NT) * 8;
@@ -269,19 +299,29 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_norm_grad(NormGradP p) 
       float o[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        o[e] = rs * __builtin_fmaf(-hat[i][e], c, dy[i][e]);
-        if (p.dh) o[e] += dh[i][e];
+        o[e] = r1 * __builtin_fmaf(-hat[i][e], c, dy[i][e]);
+        if (more) o[e] += dh[i][e];
       }
-      store8((E*)p.dx + row * p.lddx, col, m, vo, o);
+      store8((E*)p.dx + row * p.lddx, col, m, o);
     }
   }
-  if (p.part) {
+  if (!p.part) return;
+  if constexpr (!WIDE) {          // the four waves' parts, in wave order
+    const int wave = threadIdx.x >> 6;
+    if (wave > 0) {
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      const int col = (t + i * NT) * 8;
-      if (col < m)
-        store8(p.part + (long long)unit * m, col, m, (m & 3) == 0, dw[i]);
+      for (int e = 0; e < 8; ++e) sh[(wave - 1) * 512 + t * 8 + e] = dw[0][e];
     }
+    __syncthreads();
+    if (wave > 0) return;
+    for (int w = 0; w < 3; ++w)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) dw[0][e] += sh[w * 512 + t * 8 + e];
+  }
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int col = (t + i * NT) * 8;
+    if (col < m) store8(p.part + (long long)blockIdx.x * m, col, m, dw[i]);
   }
 }
 
@@ -289,24 +329,21 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_norm_grad(NormGradP p) 
 // columns, each thread on its own 8 columns of a block of rows.
 template <class E, class WT>
 __global__ __launch_bounds__(1024) void k_norm_grad_mean(NormGradP p) {
-  __shared__ float sh[2 * 16];
+  __shared__ float sh[2 * kMaxWaves];
   const int m = p.m;
-  const bool vy = rows_aligned((const E*)p.dy, p.lddy);
-  const bool vh = rows_aligned((const E*)p.h, p.ldh);
-  const bool vw = rows_aligned((const WT*)p.w, 8);
   int turn = 0;
   for (long long row = blockIdx.x; row < p.T; row += gridDim.x) {
     const float rs = p.rstd[row];
     float c = 0.0f;
     for (int col = threadIdx.x * 8; col < m; col += 1024 * 8) {
       float hat[8], dy[8], w[8];
-      load8((const E*)p.h + row * p.ldh, col, m, vh, hat);
-      load8((const E*)p.dy + row * p.lddy, col, m, vy, dy);
-      load8((const WT*)p.w, col, m, vw, w);
+      load8((const E*)p.h + row * p.ldh, col, m, hat);
+      load8((const E*)p.dy + row * p.lddy, col, m, dy);
+      load8((const WT*)p.w, col, m, w);
 #pragma unroll
       for (int e = 0; e < 8; ++e) c = __builtin_fmaf(dy[e] * w[e], hat[e] * rs, c);
     }
-    c = row_sum<1024>(c, sh, turn++) / (float)m;
+    c = row_sum<true>(c, sh, turn++) / (float)m;
     if (threadIdx.x == 0) p.c[row] = c;
   }
 }
@@ -315,20 +352,15 @@ template <class E, class WT>
 __global__ __launch_bounds__(256) void k_norm_grad_cols(NormGradP p) {
   const int m = p.m, col = (blockIdx.x * 256 + threadIdx.x) * 8;
   if (col >= m) return;
-  const bool vy = rows_aligned((const E*)p.dy, p.lddy);
-  const bool vh = rows_aligned((const E*)p.h, p.ldh);
-  const bool vd = rows_aligned((const E*)p.dh, p.lddh);
-  const bool vo = rows_aligned((const E*)p.dx, p.lddx);
-  const bool vw = rows_aligned((const WT*)p.w, 8);
   float w[8], dw[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  load8((const WT*)p.w, col, m, vw, w);
+  load8((const WT*)p.w, col, m, w);
   const long long r0 = (long long)blockIdx.y * p.rows_per_unit;
   const long long r1 = r0 + p.rows_per_unit < p.T ? r0 + p.rows_per_unit : p.T;
   for (long long row = r0; row < r1; ++row) {
     const float rs = p.rstd[row];
     float hat[8], dy[8], dh[8], o[8];
-    load8((const E*)p.h + row * p.ldh, col, m, vh, hat);
-    load8((const E*)p.dy + row * p.lddy, col, m, vy, dy);
+    load8((const E*)p.h + row * p.ldh, col, m, hat);
+    load8((const E*)p.dy + row * p.lddy, col, m, dy);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       hat[e] *= rs;
@@ -336,24 +368,23 @@ __global__ __launch_bounds__(256) void k_norm_grad_cols(NormGradP p) {
     }
     if (!p.dx) continue;
     const float c = p.c[row];
-    if (p.dh) load8((const E*)p.dh + row * p.lddh, col, m, vd, dh);
+    if (p.dh) load8((const E*)p.dh + row * p.lddh, col, m, dh);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       o[e] = rs * __builtin_fmaf(-hat[e], c, dy[e] * w[e]);
       if (p.dh) o[e] += dh[e];
     }
-    store8((E*)p.dx + row * p.lddx, col, m, vo, o);
+    store8((E*)p.dx + row * p.lddx, col, m, o);
   }
-  if (p.part) store8(p.part + (long long)blockIdx.y * m, col, m, (m & 3) == 0, dw);
+  if (p.part) store8(p.part + (long long)blockIdx.y * m, col, m, dw);
 }
 
 constexpr int kLongCols = 16384;      // rows up to this many columns stay in registers
 
-// Units (partial rows of dw) of the gradient: enough threads to fill the chip
-// twice over, so that one row's reduction overlaps the others' loads.
-int norm_grad_nt(long long m) {
-  return m <= 1024 ? 64 : m <= 4096 ? 256 : m <= 8192 ? 512 : 1024;
-}
+// Units (partial rows of dw) of the gradient: as many as stay resident, so that
+// one row's reduction overlaps the others' loads, and no more, since each unit
+// writes and reads a row of fp32 (8192 x 4096: 55 us with 6 waves a SIMD, 59
+// with 4, 65 with 8).
 RowsPlan norm_grad_plan(long long T, long long m) {
   RowsPlan q;
   if (m > kLongCols) {
@@ -362,10 +393,10 @@ RowsPlan norm_grad_plan(long long T, long long m) {
     q.units = (int)((T + q.rows_per_unit - 1) / q.rows_per_unit);
     return q;
   }
-  const int nt = norm_grad_nt(m), rpw = nt < 256 ? 256 / nt : 1;
-  const long long most = 256LL * 1024 / (nt < 256 ? 256 : nt);      // workgroups
-  const long long need = (T + rpw - 1) / rpw;
-  q.units = (int)(need < most ? need : most) * rpw;
+  const RowShape r = row_shape(m);
+  const long long most = 256LL * (r.ch == 1 ? 1536 : 1280) / r.nt, rows = r.wide ? 1 : 4;
+  const long long need = (T + rows - 1) / rows;
+  q.units = (int)(need < most ? need : most);
   q.rows_per_unit = 0;
   return q;
 }
@@ -385,17 +416,11 @@ hipError_t launch_norm_grad_t(NormGradP p, const RowsPlan& plan, hipStream_t s) 
                        s, p);
     return hipGetLastError();
   }
-  const int nt = norm_grad_nt(m), rpw = nt < 256 ? 256 / nt : 1;
-  const dim3 grid(plan.units / rpw);
-#define DION3_NORM_GRAD(NT, CH) \
-  hipLaunchKernelGGL((k_norm_grad<E, WT, NT, CH>), grid, dim3(NT < 256 ? 256 : NT), 0, s, p)
-  if (m <= 512) DION3_NORM_GRAD(64, 1);
-  else if (m <= 1024) DION3_NORM_GRAD(64, 2);
-  else if (m <= 2048) DION3_NORM_GRAD(256, 1);
-  else if (m <= 4096) DION3_NORM_GRAD(256, 2);
-  else if (m <= 8192) DION3_NORM_GRAD(512, 2);
-  else DION3_NORM_GRAD(1024, 2);
-#undef DION3_NORM_GRAD
+  const RowShape r = row_shape(m);
+  const dim3 grid(plan.units), block(r.nt);
+  if (!r.wide) hipLaunchKernelGGL((k_norm_grad<E, WT, false, 1>), grid, block, 0, s, p);
+  else if (r.ch == 1) hipLaunchKernelGGL((k_norm_grad<E, WT, true, 1>), grid, block, 0, s, p);
+  else hipLaunchKernelGGL((k_norm_grad<E, WT, true, 2>), grid, block, 0, s, p);
   return hipGetLastError();
 }
 
@@ -436,27 +461,25 @@ __global__ __launch_bounds__(256) void k_join_columns(const float* __restrict__ 
 
 // ------------------------------------------------------------- 8-bit format
 
-// One chunk of 8 columns a thread, the chunks of all rows numbered through
-// (a row has mp / 8 of them, a multiple of 4, so the 4 lanes of a scale's
-// block never straddle rows).
+// One chunk of 8 columns a thread, those of all rows numbered through (a row
+// has mp / 8 of them, a multiple of 4, so the 4 lanes of a scale's block never
+// straddle rows).  Two or four chunks a thread were no faster (8192 x 4096:
+// 20.5 us, 24 us with either).
 template <class E>
 __global__ __launch_bounds__(256) void k_pack(const E* __restrict__ x, long long ldx,
                                               unsigned char* __restrict__ q,
                                               unsigned char* __restrict__ sc, long long chunks,
                                               int m, unsigned nch) {
-  const long long base = (long long)blockIdx.x * 256;
+  const long long base = (long long)blockIdx.x * 256, at = base + threadIdx.x;
   const long long row0 = base / nch;
-  const unsigned c0 = (unsigned)(base - row0 * nch) + threadIdx.x;
-  const unsigned dr = c0 / nch;
-  const long long row = row0 + dr;
-  const int c = (int)(c0 - dr * nch) * 8;
-  const bool in = base + threadIdx.x < chunks;
+  const unsigned c0 = (unsigned)(base - row0 * nch) + threadIdx.x, dr = c0 / nch;
   float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  if (in) load8(x + row * ldx, c, m, rows_aligned(x, ldx), v);
-  const int byte = f8_scale_byte(f8_block_amax(v));
-  if (!in) return;
-  *(uint2*)(q + (base + threadIdx.x) * 8) = f8_encode8(v, f8_inv_scale(byte), f8_limit<E>(byte));
-  if ((threadIdx.x & 3) == 0) sc[(base + threadIdx.x) >> 2] = (unsigned char)byte;
+  if (at < chunks) load8(x + (row0 + dr) * ldx, (int)(c0 - dr * nch) * 8, m, v);
+  int byte;
+  const uint2 w = f8_encode_block<E>(v, byte);
+  if (at >= chunks) return;
+  *(uint2*)(q + at * 8) = w;
+  if ((threadIdx.x & 3) == 0) sc[at >> 2] = (unsigned char)byte;
 }
 
 template <class E>
@@ -487,14 +510,14 @@ __global__ __launch_bounds__(256) void k_unpack(const unsigned char* __restrict_
   if (c >= m) return;
   float v[8];
   f8_decode8<E>(*(const uint2*)(q + (base + threadIdx.x) * 8), sc[(base + threadIdx.x) >> 2], v);
-  store8(y + (row0 + dr) * ldy, c, m, rows_aligned(y, ldy), v);
+  store8(y + (row0 + dr) * ldy, c, m, v);
 }
 
 // ------------------------------------------------- the activation's gradient
 
 //   dz = E(dy act'(z)),  db = sum over rows of dy act'(z) (before rounding).
 // A wave takes 512 columns (8 a lane), a workgroup a block of rows, its 4
-// waves every fourth row of it, two rows' loads in flight per wave; the
+// waves every fourth row of it, the next row's loads in flight; the
 // waves' column sums join in LDS, the blocks' in k_join_columns.
 struct ActGradP {
   const void* dy; const void* z;
@@ -507,44 +530,43 @@ struct ActGradP {
 
 template <class E, int ACT>
 __global__ __launch_bounds__(256) void k_act_grad(ActGradP p) {
-  constexpr int U = 2;
   __shared__ float sh[3][512];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int n = p.n, np = (n + kF8Block - 1) / kF8Block * kF8Block;
   const int c = blockIdx.x * 512 + lane * 8;
-  const bool vy = rows_aligned((const E*)p.dy, p.lddy);
-  const bool vz = rows_aligned((const E*)p.z, p.ldz);
-  const bool vo = rows_aligned((const E*)p.dz, p.lddz);
   float db[8] = {0, 0, 0, 0, 0, 0, 0, 0};
   const long long r0 = (long long)blockIdx.y * p.rows_per_unit;
   const long long r1 = r0 + p.rows_per_unit < p.T ? r0 + p.rows_per_unit : p.T;
   if (c < n) {
-    for (long long row = r0 + wave; row < r1; row += 4 * U) {
-      float dy[U][8], z[U][8];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const long long r = row + 4 * u;
-        if (r >= r1) continue;
-        load8((const E*)p.dy + r * p.lddy, c, n, vy, dy[u]);
-        if (ACT != DION3_ACT_NONE) {
-          if (p.zq)
-            f8_decode8<float>(*(const uint2*)(p.zq + r * np + c),
-                              p.zs[r * (np / kF8Block) + c / kF8Block], z[u]);
-          else
-            load8((const E*)p.z + r * p.ldz, c, n, vz, z[u]);
-        }
+    Raw8<E> ry, rz;
+    uint2 zq = make_uint2(0, 0);
+    unsigned zs = 0;
+    auto ask = [&](long long r) {
+      ry = fetch8((const E*)p.dy + r * p.lddy, c, n);
+      if (ACT == DION3_ACT_NONE) return;
+      if (p.zq) {
+        zq = *(const uint2*)(p.zq + r * np + c);
+        zs = p.zs[r * (np / kF8Block) + c / kF8Block];
+      } else {
+        rz = fetch8((const E*)p.z + r * p.ldz, c, n);
       }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const long long r = row + 4 * u;
-        if (r >= r1) continue;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          if (ACT != DION3_ACT_NONE) dy[u][e] *= slope(ACT, z[u][e]);
-          db[e] += dy[u][e];
-        }
-        if (p.dz) store8((E*)p.dz + r * p.lddz, c, n, vo, dy[u]);
+    };
+    long long row = r0 + wave;
+    if (row < r1) ask(row);
+    for (; row < r1; row += 4) {
+      float dy[8], z[8];
+      chunk8(ry, c, n, dy);
+      if (ACT != DION3_ACT_NONE) {
+        if (p.zq) f8_decode8<float>(zq, zs, z);
+        else chunk8(rz, c, n, z);
       }
+      if (row + 4 < r1) ask(row + 4);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (ACT != DION3_ACT_NONE) dy[e] *= slope(ACT, z[e]);
+        db[e] += dy[e];
+      }
+      if (p.dz) store8((E*)p.dz + row * p.lddz, c, n, dy);
     }
   }
   if (!p.part) return;
@@ -558,15 +580,15 @@ __global__ __launch_bounds__(256) void k_act_grad(ActGradP p) {
     for (int w = 0; w < 3; ++w)
 #pragma unroll
       for (int e = 0; e < 8; ++e) db[e] += sh[w][lane * 8 + e];
-    store8(p.part + (long long)blockIdx.y * n, c, n, (n & 3) == 0, db);
+    store8(p.part + (long long)blockIdx.y * n, c, n, db);
   }
 }
 
-// Row blocks: about 2048 workgroups over the matrix, blocks of at least 16
+// Row blocks: about 3072 workgroups over the matrix, blocks of at least 16
 // rows and at most 1024 blocks.
 RowsPlan act_grad_plan(long long T, long long n) {
   const long long cols = (n + 511) / 512;
-  long long blocks = (2048 + cols - 1) / cols;
+    long long blocks = (3072 + cols - 1) / cols;
   if (blocks > 1024) blocks = 1024;
   if (blocks > (T + 15) / 16) blocks = (T + 15) / 16;
   if (blocks < 1) blocks = 1;
