@@ -9,7 +9,8 @@ from ._lib import (MAX_GROUPS, NS_GRAM, NS_STANDARD, PATH_AUTO, PATH_FUSED, PATH
                    step_groups, step_megabatch, symm_f16, syrk_f16, trace_disable, trace_enable,
                    trace_records, trace_reset, workspace_size, workspace_size_groups)
 from .layer import (ACTIVATIONS, PackedF8, act_grad, add_rms_norm, add_rms_norm_grad, linear,
-                    linear_grad_input, linear_grad_weight, pack_f8, unpack_f8)
+                    linear_grad_input, linear_grad_weight, linear_layer, pack_f8,
+                    rms_norm_residual, unpack_f8)
 from .optim import Dion3, Dion3Step
 
 __all__ = ["MAX_GROUPS", "NS_GRAM", "NS_STANDARD", "PATH_AUTO", "PATH_FUSED", "PATH_TILED",
@@ -18,5 +19,5 @@ __all__ = ["MAX_GROUPS", "NS_GRAM", "NS_STANDARD", "PATH_AUTO", "PATH_FUSED", "P
            "step", "step_groups", "step_megabatch", "symm_f16", "syrk_f16", "trace_disable",
            "trace_enable", "trace_records", "trace_reset", "workspace_size",
            "workspace_size_groups", "ACTIVATIONS", "PackedF8", "act_grad", "add_rms_norm",
-           "add_rms_norm_grad", "linear", "linear_grad_input", "linear_grad_weight", "pack_f8",
-           "unpack_f8", "Dion3", "Dion3Step"]
+           "add_rms_norm_grad", "linear", "linear_grad_input", "linear_grad_weight", "linear_layer",
+           "pack_f8", "rms_norm_residual", "unpack_f8", "Dion3", "Dion3Step"]

@@ -386,3 +386,133 @@ def linear_grad_weight(dz, x, out=None, accumulate: bool = False,
     _call("dion3_linear_grad_weight", dz.device, _ptr(dz), lddz, xp, ldx, sp, out.data_ptr(), ldg,
           int(bool(accumulate)), T, n, m, _DTYPES[dz.dtype], p, nb)
     return out
+
+
+# ------------------------------------------------- the differentiable forms
+
+def _as_rows(t):
+    """A gradient as its producer left it, or contiguous where that has no
+    rows that the library reads (an expanded gradient, a transposed one)."""
+    try:
+        _rows(t, "gradient")
+        return t
+    except ValueError:
+        return t.contiguous()
+
+
+class _RmsNormResidual(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, residual, eps, pack):
+        y, h, rstd, p = add_rms_norm(x, weight, residual, eps, pack)
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(h, rstd, weight)
+        ctx.has_residual = residual is not None
+        if residual is None:
+            h = x.view_as(x)
+        if p is None:
+            return y, h, None, None
+        ctx.mark_non_differentiable(p.q, p.scale)
+        return y, h, p.q, p.scale
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy, dh, _q, _s):
+        h, rstd, weight = ctx.saved_tensors
+        dx, dw = dh, None
+        if dy is not None:
+            need_x = ctx.needs_input_grad[0] or ctx.needs_input_grad[2]
+            dx, dw = add_rms_norm_grad(_as_rows(dy), h, rstd, weight.contiguous(),
+                                       None if dh is None else _as_rows(dh), need_dx=need_x,
+                                       need_dw=ctx.needs_input_grad[1])
+            if dw is not None:
+                dw = dw.to(weight.dtype)
+        return dx, dw, dx if ctx.has_residual else None, None, None
+
+
+def rms_norm_residual(x, weight, residual=None, eps: float = 1e-6, pack: bool = False):
+    """(y, h, packed) of ``add_rms_norm``, differentiable in x, weight and
+    residual through y and h.  Kept for the backward pass: h and one fp32
+    value per row.  ``packed`` (with ``pack``) is y in 8 bits, to be given to
+    the layers that read y as their ``checkpoint``."""
+    y, h, q, s = _RmsNormResidual.apply(x, weight, residual, eps, pack)
+    return y, h, PackedF8(q, s, x.shape[-1], x.shape) if pack else None
+
+
+class _LinearLayer(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, bias, residual, act, checkpoint, into):
+        w16 = w if w.dtype == x.dtype else w.to(x.dtype)
+        need_x, need_w, need_b, need_r = ctx.needs_input_grad[:4]
+        inner = need_x or need_w or need_b
+        y, z = linear(x, w16, bias, act, residual, return_preact=inner and act != "none")
+        full = checkpoint == "full" if isinstance(checkpoint, str) else False
+        ctx.x = ctx.z = None                     # shapes of what is kept in 8 bits
+        saved = [None] * 5                       # x or its q, its scale, z or its q, its scale, w
+        if need_w:
+            if full:
+                saved[0] = x
+            else:
+                p = checkpoint if isinstance(checkpoint, PackedF8) else pack_f8(x)
+                saved[0], saved[1], ctx.x = p.q, p.scale, (p.cols, p.shape)
+        if z is not None:
+            if full:
+                saved[2] = z
+            else:
+                p = pack_f8(z)
+                saved[2], saved[3], ctx.z = p.q, p.scale, (p.cols, p.shape)
+        if need_x:
+            saved[4] = w16
+        ctx.save_for_backward(*saved)
+        ctx.act, ctx.into, ctx.w = act, into, w if into is not None else None
+        ctx.wtype, ctx.btype = w.dtype, bias.dtype if bias is not None else None
+        return y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        x, xs, z, zs, w16 = ctx.saved_tensors
+        need_x, need_w, need_b, need_r = ctx.needs_input_grad[:4]
+        dx = dw = db = None
+        if need_x or need_w or need_b:
+            dyr = _as_rows(dy)
+            if ctx.z is not None:
+                z = PackedF8(z, zs, *ctx.z)
+            dz, db = act_grad(dyr, z, ctx.act, bias=need_b)
+            if need_x:
+                dx = linear_grad_input(dz, w16)
+            if need_w:
+                xin = PackedF8(x, xs, *ctx.x) if ctx.x is not None else x
+                if ctx.into is not None:
+                    linear_grad_weight(dz, xin, out=ctx.into.accumulate_grad(ctx.w), accumulate=True)
+                else:
+                    dw = linear_grad_weight(dz, xin).to(ctx.wtype)
+            if db is not None:
+                db = db.to(ctx.btype)
+        return dx, dw, db, dy if need_r else None, None, None, None
+
+
+def linear_layer(x, w, bias=None, act: str = "none", residual=None, checkpoint="f8", into=None):
+    """y = act(x w^T + bias) + residual, differentiable in x, w, bias and
+    residual.  ``w`` is of x's type or fp32 (then rounded to x's type for the
+    products; its gradient is fp32).
+
+    ``checkpoint``: what the backward pass reads of x and of the
+    preactivation: "f8" (default) keeps both in 8 bits, a PackedF8 is x in 8
+    bits as another layer or norm already keeps it (the preactivation is
+    packed too), "full" keeps both as they are.  The forward result and the
+    gradient of x are the same bits with every choice when act is "none".
+
+    ``into``: a ``Dion3`` that steps w.  The weight gradient is then summed
+    straight into w's momentum there, in the product's own epilogue; w gets no
+    ``.grad``, and the next ``step()`` steps it.  What has been summed cannot
+    be taken back by ``zero_grad()``."""
+    if isinstance(checkpoint, PackedF8):
+        if tuple(checkpoint.shape) != tuple(x.shape):
+            raise ValueError(f"checkpoint must stand for a tensor of shape {tuple(x.shape)}")
+    elif checkpoint not in ("f8", "full"):
+        raise ValueError('checkpoint must be "f8", "full" or a PackedF8')
+    if not isinstance(w, torch.Tensor) or (w.dtype != x.dtype and w.dtype != torch.float32):
+        raise TypeError(f"w must be {x.dtype} or float32")
+    if into is not None:
+        into.check_parameter(w)
+    return _LinearLayer.apply(x, w, bias, residual, act, checkpoint, into)

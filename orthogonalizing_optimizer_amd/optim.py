@@ -102,6 +102,14 @@ class Dion3(_optimizer_base()):
     float32 second-moment state per row (``beta2``, ``eps``), the reading of
     the pages' "per-neuron normalization inherited from NorMuon" stated in
     include/dion3.h at dion3_norm_cfg.
+
+    A layer may sum its weight gradient straight into the momentum
+    (``linear_layer(..., into=optimizer)``): M <- M + dW where the product is
+    computed, instead of a gradient buffer that ``step()`` adds.  The sums are
+    the same.  Such a parameter has no ``.grad``; ``step()`` steps the ones
+    that ``accumulate_grad`` has named since the last step.  (A captured
+    graph's replay names none: call ``accumulate_grad`` before a step outside
+    the graph.)
     """
 
     def __init__(self, params, lr: float = 0.02, fraction=Fraction(1, 4), mu: float = 0.95,
@@ -120,6 +128,28 @@ class Dion3(_optimizer_base()):
                     raise ValueError("Dion3 steps 2-D fp32 matrices with contiguous rows")
         self.cfg = cfg
         self._ws: Dict[str, _lib.Workspace] = {}
+        self._accumulated = set()      # parameters whose momentum already holds a new gradient
+
+    def check_parameter(self, p):
+        """Raise ValueError unless p is one of this optimizer's parameters."""
+        if not any(p is q for group in self.param_groups for q in group["params"]):
+            raise ValueError("not a parameter of this optimizer")
+
+    def momentum(self, p):
+        """p's momentum buffer (fp32, p's strides; zero before the first gradient)."""
+        st = self.state[p]
+        if "momentum" not in st:       # the parameter's own strides
+            import torch
+            st["momentum"] = torch.empty_strided(p.shape, p.stride(), dtype=p.dtype,
+                                                 device=p.device).zero_()
+        return st["momentum"]
+
+    def accumulate_grad(self, p):
+        """p's momentum buffer, for a gradient to be added to it: the next
+        ``step()`` steps p whether or not it has a ``.grad``."""
+        m = self.momentum(p)
+        self._accumulated.add(p)
+        return m
 
     def step(self, closure=None):
         import torch
@@ -132,31 +162,32 @@ class Dion3(_optimizer_base()):
                 f = float(group["fraction"])
                 buckets: "OrderedDict[Tuple, List]" = OrderedDict()
                 for p in group["params"]:
-                    if p.grad is None:
+                    if p.grad is None and p not in self._accumulated:
                         continue
-                    if p.grad.stride() != p.stride():
+                    if p.grad is not None and p.grad.stride() != p.stride():
                         raise ValueError("a gradient must have its parameter's strides")
+                    self.momentum(p)
                     st = self.state[p]
-                    if "momentum" not in st:   # the parameter's own strides
-                        st["momentum"] = torch.empty_strided(p.shape, p.stride(), dtype=p.dtype,
-                                                             device=p.device).zero_()
                     if group["normalize"] and "second_moment" not in st:
                         st["second_moment"] = torch.zeros(p.shape[0], dtype=torch.float32,
                                                           device=p.device)
-                    buckets.setdefault((tuple(p.shape), p.stride(), str(p.device)), []).append(p)
+                    buckets.setdefault((tuple(p.shape), p.stride(), str(p.device),
+                                        p.grad is not None), []).append(p)
                 # one library call per device over all of its shape buckets
                 by_dev: "OrderedDict[str, List]" = OrderedDict()
-                for (shape, _, dev), ps in buckets.items():
+                for (shape, _, dev, has_grad), ps in buckets.items():
                     k = _lib.k_from_fraction(f, shape[0])
                     Vs = ([self.state[p]["second_moment"] for p in ps] if group["normalize"]
                           else None)
                     by_dev.setdefault(dev, []).append(
                         _lib.Group(ps, [self.state[p]["momentum"] for p in ps], k,
-                                   group["lr"] / math.sqrt(f), Gs=[p.grad for p in ps], Vs=Vs))
+                                   group["lr"] / math.sqrt(f),
+                                   Gs=[p.grad for p in ps] if has_grad else None, Vs=Vs))
                 norm = (group["beta2"], group["eps"]) if group["normalize"] else None
                 for dev, grps in by_dev.items():
                     ws = self._ws.setdefault(dev, _lib.Workspace())
                     for i in range(0, len(grps), _lib.MAX_GROUPS):
                         _lib.step_groups(grps[i:i + _lib.MAX_GROUPS], group["mu"], self.cfg,
                                          norm=norm, ws=ws)
+        self._accumulated.clear()
         return loss
