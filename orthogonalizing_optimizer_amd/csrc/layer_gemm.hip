@@ -643,7 +643,7 @@ __global__ __launch_bounds__(256) void k_lin_copy(const unsigned short* __restri
 
 // ------------------------------------------------------------- few tokens
 
-// Y for at most 16 tokens: bound by reading W once.  A workgroup takes 16
+// Y for 2 to 16 tokens (see few_tokens): bound by reading W once.  A workgroup takes 16
 // rows of W, its 8 waves the K axis in turns of 128; a lane reads 64
 // contiguous bytes of one W row (four chunks, one per MFMA: the order of K
 // inside the product is free as long as both operands agree) and the same
@@ -714,7 +714,69 @@ __global__ __launch_bounds__(512) void k_lin_thin(ThinP p) {
   }
 }
 
+// Y for one token, by vector instructions: a wave's load is 1 KB of one W row
+// (the matrix form above reads 64 bytes of 16 rows a load: 24 us for 90 MB of
+// cold weights at 11008 x 4096, this one 19; 40 and 27 us at 13824 x 5120), the
+// token's 512 columns are read once for 4 rows.  A workgroup takes 8 rows, four
+// waves to each 4 of them, which take turns along K; many small waves hide the
+// loads better than two steps in flight each (27 and 31 us).  (The same for 4
+// tokens keeps too many registers to fill the chip: 34 us at 11008 x 4096.)
+template <class E>
+__global__ __launch_bounds__(512) void k_lin_vec(ThinP p) {
+  constexpr int R = 4, KW = 4;
+  __shared__ float sh[KW][8];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int rg = wave / KW, kh = wave % KW;
+  const long long n0 = (long long)blockIdx.x * 8;
+  const E* w[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {       // rows past the end repeat the last one, unused
+    const long long row = n0 + rg * R + r;
+    w[r] = (const E*)p.W + (row < p.N ? row : p.N - 1) * p.ldw;
+  }
+  float acc[R] = {0, 0, 0, 0};
+  for (int k0 = kh * 512; k0 < p.K; k0 += KW * 512) {
+    const int c = k0 + lane * 8;
+    Raw8<E> rw[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) rw[r] = fetch8(w[r], c, p.K);
+    const Raw8<E> rx = fetch8((const E*)p.X, c, p.K);
+    float a[8];
+    chunk8(rx, c, p.K, a);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float b[8];
+      chunk8(rw[r], c, p.K, b);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[r] = __builtin_fmaf(a[e], b[e], acc[r]);
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) acc[r] += __shfl_xor(acc[r], o, 64);
+    if (lane == 0) sh[kh][rg * R + r] = acc[r];
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    for (int q = 0; q < KW; ++q)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] += sh[q][e];
+    finish8<E, false>(p.f, 0, (int)n0, v);
+  }
+}
+
+// The forms for few tokens: by vectors for one; the 16 x 16 matrix form while
+// W is small (16 tokens: 4096 x 4096 13 us, 16 by the 64 x 64 tiles; 11008 x
+// 4096 36 us, 27 by the tiles: there the tokens, read once by every workgroup,
+// cost as much as W).
 constexpr int kThinTokens = 16;
+constexpr long long kThinWeights = 24LL << 20;
+bool few_tokens(const LinDesc& d) {
+  return !d.a_km && !d.b_kn && !d.G &&
+         (d.M == 1 || (d.M <= kThinTokens && d.N * d.K <= kThinWeights));
+}
 
 // ------------------------------------------------------------- host side
 
@@ -821,7 +883,7 @@ LinPlan lin_plan(const LinDesc& d) {
   if (d.M == 0 || d.K == 0) return q;
   q.rowsA = d.a_km ? d.K : d.M; q.colsA = d.a_km ? d.M : d.K;
   q.rowsB = d.b_kn ? d.K : d.N; q.colsB = d.b_kn ? d.N : d.K;
-  q.thin = !d.a_km && !d.b_kn && !d.G && d.M <= kThinTokens;
+  q.thin = few_tokens(d);
   if (q.thin) return q;
   q.copyA = !in_place(d.A, d.lda, q.colsA);
   q.copyB = !d.bs && !in_place(d.B, d.ldb, q.colsB);
@@ -886,7 +948,9 @@ hipError_t launch_lin_t(const LinDesc& d, void* ws, hipStream_t s) {
     const ThinP p = {d.A, d.B, d.lda, d.ldb, d.N, (int)d.M, (int)d.K, f};
     TraceScope ts("linear_thin", flops, 2.0 * (double)d.N * d.K, s);
     const dim3 grid((unsigned)((d.N + 15) / 16));
-    if (in_place(d.A, d.lda, d.K) && in_place(d.B, d.ldb, d.K))
+    if (d.M == 1)
+      hipLaunchKernelGGL((k_lin_vec<E>), dim3((unsigned)((d.N + 7) / 8)), dim3(512), 0, s, p);
+    else if (in_place(d.A, d.lda, d.K) && in_place(d.B, d.ldb, d.K))
       hipLaunchKernelGGL((k_lin_thin<E, true>), grid, dim3(512), 0, s, p);
     else
       hipLaunchKernelGGL((k_lin_thin<E, false>), grid, dim3(512), 0, s, p);

@@ -113,9 +113,11 @@ def _scratch(ws, nbytes, device):
     return p + (-p) % 256, nbytes, buf
 
 
-def _size(fn, *args):
+def _size(name, *args):
     out = ctypes.c_size_t(0)
-    _lib._check(getattr(_lib.lib(), fn)(*args, ctypes.byref(out)), fn)
+    status = _fn(name)(*args, ctypes.byref(out))
+    if status:
+        _lib._check(status, name)
     return out.value
 
 
@@ -124,14 +126,25 @@ def _size(fn, *args):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _call(fn, device, *args):
-    if device.index != torch.cuda.current_device():
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_fns: dict = {}                  # the library's entry points, looked up once
+
+
+def _fn(name):
+    f = _fns.get(name)
+    if f is None:
+        f = _fns[name] = getattr(_lib.lib(), name)
+    return f
+
+
+def _call(name, device, *args):
+    if device.index != _current_device():
         with torch.cuda.device(device):
-            return _lib._check(getattr(_lib.lib(), fn)(*args, _lib._stream(device)), fn)
+            return _lib._check(_fn(name)(*args, _lib._stream(device)), name)
     stream = _raw_stream(device.index) if _raw_stream is not None else _lib._stream(device)
-    status = getattr(_lib.lib(), fn)(*args, stream)
+    status = _fn(name)(*args, stream)
     if status:
-        _lib._check(status, fn)
+        _lib._check(status, name)
 
 
 # --------------------------------------------------------- the 8-bit format
