@@ -520,8 +520,9 @@ def linear_layer(x, w, bias=None, act: str = "none", residual=None, checkpoint="
     ``.grad``, and the next ``step()`` steps it.  What has been summed cannot
     be taken back by ``zero_grad()``."""
     if isinstance(checkpoint, PackedF8):
-        if tuple(checkpoint.shape) != tuple(x.shape):
-            raise ValueError(f"checkpoint must stand for a tensor of shape {tuple(x.shape)}")
+        if tuple(checkpoint.shape) != tuple(x.shape) or checkpoint.device != x.device:
+            raise ValueError(f"checkpoint must stand for a tensor of shape {tuple(x.shape)} on "
+                             f"{x.device}")
     elif checkpoint not in ("f8", "full"):
         raise ValueError('checkpoint must be "f8", "full" or a PackedF8')
     if not isinstance(w, torch.Tensor) or (w.dtype != x.dtype and w.dtype != torch.float32):

@@ -129,10 +129,12 @@ class Dion3(_optimizer_base()):
         self.cfg = cfg
         self._ws: Dict[str, _lib.Workspace] = {}
         self._accumulated = set()      # parameters whose momentum already holds a new gradient
+        self._streams = set()          # the streams on which those gradients were added
 
     def check_parameter(self, p):
         """Raise ValueError unless p is one of this optimizer's parameters."""
-        if not any(p is q for group in self.param_groups for q in group["params"]):
+        if p not in self.state and not any(p is q for group in self.param_groups
+                                           for q in group["params"]):
             raise ValueError("not a parameter of this optimizer")
 
     def momentum(self, p):
@@ -145,10 +147,14 @@ class Dion3(_optimizer_base()):
         return st["momentum"]
 
     def accumulate_grad(self, p):
-        """p's momentum buffer, for a gradient to be added to it: the next
-        ``step()`` steps p whether or not it has a ``.grad``."""
+        """p's momentum buffer, for a gradient to be added to it on the current
+        stream of its device: the next ``step()`` waits for that stream and
+        steps p whether or not it has a ``.grad``."""
+        import torch
         m = self.momentum(p)
         self._accumulated.add(p)
+        if m.is_cuda:
+            self._streams.add(torch.cuda.current_stream(m.device))
         return m
 
     def step(self, closure=None):
@@ -157,6 +163,12 @@ class Dion3(_optimizer_base()):
         if closure is not None:
             with torch.enable_grad():
                 loss = closure()
+        # autograd runs a layer's backward on its forward's stream, and joins
+        # that stream with the caller's only for gradients that it keeps itself
+        for stream in self._streams:
+            here = torch.cuda.current_stream(stream.device)
+            if stream != here:
+                here.wait_stream(stream)
         with torch.no_grad():
             for group in self.param_groups:
                 f = float(group["fraction"])
@@ -190,4 +202,5 @@ class Dion3(_optimizer_base()):
                         _lib.step_groups(grps[i:i + _lib.MAX_GROUPS], group["mu"], self.cfg,
                                          norm=norm, ws=ws)
         self._accumulated.clear()
+        self._streams.clear()
         return loss

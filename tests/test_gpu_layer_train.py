@@ -115,6 +115,12 @@ def test_partial_gradients():
     want = d3.add_rms_norm_grad(dout, x.detach(), d3.add_rms_norm(x.detach(), p["n1"].detach())[2],
                                 p["n1"].detach())[0]
     assert torch.equal(x.grad, want)
+    x.grad = None
+    y, h, _ = d3.rms_norm_residual(x, p["n1"].detach())
+    torch.autograd.backward([y, h], [dout, dout])          # x itself is the stream that goes on
+    want = d3.add_rms_norm_grad(dout, x.detach(), d3.add_rms_norm(x.detach(), p["n1"].detach())[2],
+                                p["n1"].detach(), dh=dout)[0]
+    assert torch.equal(x.grad, want)
     with torch.no_grad():
         assert not block(p, x, r).requires_grad
 
@@ -198,6 +204,33 @@ def test_momentum_accumulates_over_backward_passes():
     w1, m1 = p["w1"].detach().clone(), opt.momentum(p["w1"]).clone()
     opt.step()                                  # nothing accumulated since
     assert torch.equal(p["w1"].detach(), w1) and torch.equal(opt.momentum(p["w1"]), m1)
+
+
+def test_step_waits_for_the_stream_of_the_backward_pass():
+    """Forward on a side stream, backward and step from the default one: the
+    weight gradients, which autograd never sees, are summed before the step
+    reads them."""
+    def fresh():
+        p = params(15, 1024, 4096)
+        return p, d3.Dion3([p["w1"], p["w2"]], lr=0.02, fraction=0.25)
+
+    x, r, dout = data(16, 8192, hidden=1024)
+    p, opt = fresh()
+    block(p, x, r, into=opt).backward(dout)
+    opt.step()
+    want = [p["w1"].detach().clone(), opt.momentum(p["w1"]).clone()]
+    p, opt = fresh()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        out = d3.linear_layer(x, p["w1"], into=opt)      # (allocations and first launches)
+        out = block(p, x, r, into=opt)
+    torch.cuda.current_stream().wait_stream(side)
+    out.backward(dout)
+    assert side in opt._streams
+    opt.step()
+    assert not opt._streams and not opt._accumulated
+    assert torch.equal(p["w1"].detach(), want[0]) and torch.equal(opt.momentum(p["w1"]), want[1])
 
 
 def test_training_step_in_a_graph():
