@@ -425,7 +425,10 @@ __device__ __forceinline__ void load_ahead(OA& A, OB& B, long long k0, int tid) 
   }
 }
 
-// F32: C goes to G; PART: to the scratch (splits); else to Y.
+// One tile of the output.  8192 x 4096 x 4096 (two rounds of 256 x 256 tiles):
+// 215-231 us forward, 222-232 input gradient, 217-225 weight gradient (box to
+// box), of which about 1.5 us a K step and 10 us a round for first loads and
+// epilogue.  F32: C goes to G; PART: to the scratch (splits); else to Y.
 template <class E, class C, int KA, int KB, bool F32, bool PART>
 __global__ __launch_bounds__(C::NT, C::PER_CU) void k_lin(LinP p) {
   __shared__ __attribute__((aligned(16))) char lds_raw[C::BYTES];
@@ -557,7 +560,9 @@ __global__ __launch_bounds__(C::NT, C::PER_CU) void k_lin(LinP p) {
 // The splits' tiles added up, then the epilogue.  A workgroup takes 256 / GR
 // chunks of 8 columns (the scratch's rows numbered through), GR threads a
 // chunk, each the sum of a run of the splits in order; the runs join in order.
-// GR = 8 where one thread a chunk would leave most of the chip idle.
+// GR = 8 where one thread a chunk would leave most of the chip idle (64 parts of
+// 128 x 512: 3.8 us, 6.4 with one thread a chunk); bound by reading the parts,
+// mostly from the caches (2 parts of 1000 x 2048: 5.3 us).
 template <class E, bool F32, int GR>
 __global__ __launch_bounds__(256) void k_lin_join(const float* __restrict__ part, long long stride,
                                                   int splits, long long M, unsigned nch, Finish f) {
@@ -621,7 +626,8 @@ __global__ __launch_bounds__(256) void k_lin_zero(long long M, unsigned nch, Fin
 // An operand that the kernel cannot read in place (rows not 16-byte aligned,
 // or a contiguous side that is no multiple of 8) copied into rows of a whole
 // number of chunks, zeros at their ends.  The copy moves the operand twice
-// more, a small part of the product's time except at few tokens.
+// more, a small part of the product's time except at few tokens (1000 x 515:
+// 3.6 us, most of it the launch).
 __global__ __launch_bounds__(256) void k_lin_copy(const unsigned short* __restrict__ src,
                                                   long long ld, long long rows, int cols,
                                                   unsigned nch, unsigned short* __restrict__ dst) {
@@ -649,6 +655,7 @@ __global__ __launch_bounds__(256) void k_lin_copy(const unsigned short* __restri
 // inside the product is free as long as both operands agree) and the same
 // columns of its token.  The waves' 16 x 16 sums join in LDS in wave order.
 // VEC: both operands readable in 16-byte chunks; else element by element.
+// 4096 x 4096: 11 us at 2 tokens, 13 at 16.
 struct ThinP {
   const void* X; const void* W;
   long long ldx, ldw, N;
