@@ -15,6 +15,8 @@
 //   * K as rows in 8 bits: the same, decoded between the global load and the
 //     LDS store, two values an instruction (the scale is the instruction's
 //     operand), so the checkpoint crosses HBM and the caches at half the size.
+// Operands whose rows are not 16-byte aligned, or end inside a chunk, take the
+// ragged form of the first two (see Operand).
 // Tiles: 256 x 256, 192 x 256 and 128 x 256 (8 waves, one workgroup a CU; the
 // first has the best rate, 1.2-1.25 PFLOP/s on 8192 x 4096 x 4096, the others
 // fill the last round of workgroups better), 128 x 128 and 64 x 64 (4 waves,
@@ -172,10 +174,40 @@ typedef Cfg<128, 256, 2, 4, 3, 1> CfgW;
 typedef Cfg<128, 128, 2, 2, 1, 1> CfgS;
 typedef Cfg<64, 64, 2, 2, 1, 2> CfgT;
 
+template <bool B, class X, class Y>
+struct Pick { typedef X type; };
+template <class X, class Y>
+struct Pick<false, X, Y> { typedef Y type; };
+
+// 16 bytes at any alignment of 16-bit elements, and the 8 elements moved down
+// by s places with zeros behind (s from 8 on: zeros).
+struct __attribute__((packed, aligned(2))) Any16 { int4v v; };
+__device__ __forceinline__ int4v moved(int4v v, int s) {
+  typedef unsigned long long u64x2 __attribute__((ext_vector_type(2)));
+  u64x2 w = __builtin_bit_cast(u64x2, v);
+  const int b = 16 * (s & 3);
+  const unsigned long long hi = s & 4 ? 0 : w[1], lo = s & 4 ? w[1] : w[0];
+  w[0] = lo >> b | (hi << 1) << (63 - b);
+  w[1] = hi >> b;
+  const int4v r = __builtin_bit_cast(int4v, w);
+  return s < 8 ? r : int4v{0, 0, 0, 0};
+}
+
 enum Kind { kRowsK = 0, kColsK = 1, kColsF8 = 2 };
 
 // One operand of R output rows: its registers, LDS part and fragments.
-template <class E, int R, int NT, int KIND, int PF>
+//
+// RAG: rows of any alignment and length (at least 8).  Chunks come by unaligned
+// 16-byte loads, whose rows and columns are held inside the operand instead of
+// relying on a buffer's bounds: the last chunk of a row is the row's last 8
+// elements, moved into place before the LDS store, and what lies past K is
+// zeroed there.  A step costs 10 to 25 % more than an aligned one, against a
+// copy of the operand and its launch (bf16, one box, ragged against copied
+// first): forward 517 x 1000 x 515 7.4 us against 11.8, 1000 x 2049 x 2047 29.7
+// against 37.0, 8192 x 4095 x 4097 264 against 288; input gradient 10.4 against
+// 10.5, 28.9 against 37.5, 295 against 307; weight gradient 7.8 against 8.2,
+// 36 against 37, 289 against 372.
+template <class E, int R, int NT, int KIND, int PF, bool RAG>
 struct Operand {
   static constexpr int RS = R + kPadN;                                 // [K][R] LDS row
   static constexpr int CH = KIND == kColsF8 ? R * BK / 16 / NT : R * BK / 8 / NT;
@@ -191,12 +223,37 @@ struct Operand {
   int scols;
   static constexpr bool FIXED = NT % CPR == 0;    // a thread's chunks share their column
   int voff[FIXED ? 1 : CH];
+  static constexpr bool RAGGED = RAG && KIND != kColsF8;
+  long long Kt;          // RAGGED: the operand's own K (K: where this part of it ends)
+  int roff[RAGGED ? CH : 1];   // kRowsK: the chunks' rows
+  int cut;               // kColsK: elements of the chunk before its column
   int4v reg[PF][CH];
   unsigned sreg[PF][KIND == kColsF8 ? CH : 1];
 
   __device__ __forceinline__ void init(const void* p, const unsigned char* sc, long long ldp,
-                                       long long rows, long long k, long long r0, int tid) {
+                                       long long rows, long long k, long long kt, long long r0,
+                                       int tid) {
     K = k;
+    if constexpr (RAGGED) {
+      static_assert(NT % CPR == 0, "a thread's chunks share their column");
+      Kt = kt;
+      ld = ldp * 2;
+      if constexpr (KIND == kRowsK) {
+        base = (const char*)p + r0 * ld;
+        const int last = (int)(rows - r0 < R ? rows - r0 : R) - 1;
+#pragma unroll
+        for (int i = 0; i < CH; ++i) roff[i] = min((tid + NT * i) / CPR, last) * (int)ld;
+      } else {
+        // (a part of the output may have fewer than 8 columns left: its last 8
+        // then begin before it, in the same row)
+        const long long from = r0 < rows - 8 ? r0 : rows - 8;
+        const long long c = r0 + tid % CPR * 8, at = c < rows - 8 ? c : rows - 8;
+        base = (const char*)p + from * 2;
+        cut = (int)(c - at);
+        voff[0] = (int)(at - from) * 2;
+      }
+      return;
+    }
     if constexpr (KIND == kRowsK) {
       K = (k + 7) & ~7LL;        // rows end in whole chunks (zeros past K: see in_place)
       ld = ldp * 2;
@@ -225,8 +282,21 @@ struct Operand {
     __amdgpu_buffer_rsrc_t rs, ss;
     int v;
   };
-  __device__ __forceinline__ Src source(long long k0, int tid) const {
-    if constexpr (KIND == kRowsK) {
+  struct RagSrc {
+    const char* p;       // kColsK: row min(k0, Kt - 1)
+    int v;               // kRowsK: the chunk's column; kColsK: rows left from p on, less one
+  };
+  typedef typename Pick<RAGGED, RagSrc, Src>::type Source;
+  __device__ __forceinline__ Source source(long long k0, int tid) const {
+    if constexpr (RAGGED) {
+      if constexpr (KIND == kRowsK) {
+        const long long k = k0 + (tid & 7) * 8;
+        return {base, (int)(k < Kt - 8 ? k : Kt - 8) * 2};
+      } else {
+        const long long row = k0 < Kt - 1 ? k0 : Kt - 1;
+        return {base + row * ld, (int)(Kt - 1 - row < BK ? Kt - 1 - row : BK)};
+      }
+    } else if constexpr (KIND == kRowsK) {
       const __amdgpu_buffer_rsrc_t rs = rsrc(base, bytes);
       return {rs, rs, k0 + (tid & 7) * 8 < K ? voff[0] + (int)k0 * 2 : kOut};
     } else {
@@ -243,30 +313,44 @@ struct Operand {
 
   // Chunk i of the tile into this thread's register set P.
   template <int P>
-  __device__ __forceinline__ void load(const Src& s, int i, int tid) {
+  __device__ __forceinline__ void load(const Source& s, int i, int tid) {
     constexpr int STEP = NT / CPR;
+    if constexpr (RAGGED) {
+      const unsigned o = KIND == kRowsK ? (unsigned)(roff[i] + s.v)
+                                        : (unsigned)(min(tid / CPR + i * STEP, s.v) * (int)ld + voff[0]);
+      reg[P][i] = ((const Any16*)(s.p + o))->v;
+      return;
+    } else {
     static_assert(FIXED || KIND == kColsK, "other operands' chunks share their column");
     const int v = FIXED ? s.v + i * STEP * (int)ld : voff[FIXED ? 0 : i];
     reg[P][i] = __builtin_amdgcn_raw_buffer_load_b128(s.rs, v, 0, 0);
     if constexpr (KIND == kColsF8)
       sreg[P][i] = (unsigned char)__builtin_amdgcn_raw_buffer_load_b8(
           s.ss, (tid / CPR + i * STEP) * (int)(ld / kF8Block) + (tid % CPR) / 2, 0, 0);
+    }
   }
   template <int P>
   __device__ __forceinline__ void load_all(long long k0, int tid) {
-    const Src s = source(k0, tid);
+    const Source s = source(k0, tid);
 #pragma unroll
     for (int i = 0; i < CH; ++i) load<P>(s, i, tid);
   }
 
-  // Chunk i from the registers into the LDS part s.
+  // Chunk i of the tile at k0 from the registers into the LDS part s.
   template <int P>
-  __device__ __forceinline__ void store(short* __restrict__ s, int i, int tid) const {
+  __device__ __forceinline__ void store(short* __restrict__ s, int i, int tid, long long k0) const {
     const int c = tid + NT * i;
     if constexpr (KIND == kRowsK) {
-      *(int4v*)(s + (c / CPR) * LDSK + (c % CPR) * 8) = reg[P][i];
+      int4v v = reg[P][i];
+      if constexpr (RAGGED) {
+        const long long k = k0 + (tid & 7) * 8;
+        v = moved(v, k < K ? (int)(k < Kt - 8 ? 0 : k - (Kt - 8)) : 8);
+      }
+      *(int4v*)(s + (c / CPR) * LDSK + (c % CPR) * 8) = v;
     } else if constexpr (KIND == kColsK) {
-      *(int4v*)(s + (c / CPR) * RS + (c % CPR) * 8) = reg[P][i];
+      int4v v = reg[P][i];
+      if constexpr (RAGGED) v = moved(v, k0 + c / CPR < K ? cut : 8);
+      *(int4v*)(s + (c / CPR) * RS + (c % CPR) * 8) = v;
     } else {
       const float sc = f8_scale_float(sreg[P][i]);
       short* d = s + (c / CPR) * RS + (c % CPR) * 16;
@@ -284,9 +368,9 @@ struct Operand {
     }
   }
   template <int P>
-  __device__ __forceinline__ void store_all(short* __restrict__ s, int tid) const {
+  __device__ __forceinline__ void store_all(short* __restrict__ s, int tid, long long k0) const {
 #pragma unroll
-    for (int i = 0; i < CH; ++i) store<P>(s, i, tid);
+    for (int i = 0; i < CH; ++i) store<P>(s, i, tid, k0);
   }
 
   // This lane's offset into the part for the wave's rows w0 .., and the
@@ -332,14 +416,14 @@ __device__ __forceinline__ void slice_order() {
 // before the last slice, and the next stage's first fragments are read under
 // that slice's MFMAs.  Every step does all of it, the last ones with tiles
 // past the end, which load as zeros and are not used.
-template <class E, class C, int KA, int KB, int P>
+template <class E, class C, int KA, int KB, bool RAG, int P>
 __device__ __forceinline__ void k_step(const short* __restrict__ st, short* __restrict__ nxt,
-                                       Operand<E, C::BM, C::NT, KA, C::PF>& A,
-                                       Operand<E, C::BN, C::NT, KB, C::PF>& B, long long k_next,
+                                       Operand<E, C::BM, C::NT, KA, C::PF, RAG>& A,
+                                       Operand<E, C::BN, C::NT, KB, C::PF, RAG>& B, long long k_next,
                                        int tid, int aoff, int boff, short8 (&fa0)[C::FM],
                                        short8 (&fb0)[C::FN], floatx16 (&acc)[C::FM][C::FN]) {
-  typedef Operand<E, C::BM, C::NT, KA, C::PF> OA;
-  typedef Operand<E, C::BN, C::NT, KB, C::PF> OB;
+  typedef Operand<E, C::BM, C::NT, KA, C::PF, RAG> OA;
+  typedef Operand<E, C::BN, C::NT, KB, C::PF, RAG> OB;
   constexpr int NS = BK / 16, NM = C::FM * C::FN;
   constexpr int NR = OA::READS * C::FM + OB::READS * C::FN;
   constexpr int SPREAD = C::SPREAD;                      // slices that share the staging
@@ -349,8 +433,9 @@ __device__ __forceinline__ void k_step(const short* __restrict__ st, short* __re
   for (int i = 0; i < C::FM; ++i) af[0][i] = fa0[i];
 #pragma unroll
   for (int j = 0; j < C::FN; ++j) bf[0][j] = fb0[j];
-  const typename OA::Src sa = A.source(k_next, tid);
-  const typename OB::Src sb = B.source(k_next, tid);
+  const typename OA::Source sa = A.source(k_next, tid);
+  const typename OB::Source sb = B.source(k_next, tid);
+  const long long ks = k_next - C::PF * BK;              // the tile that is stored
   auto slice = [&](auto KK) {
     constexpr int kk = KK.value;
     constexpr int cb = kk & 1;
@@ -373,10 +458,10 @@ __device__ __forceinline__ void k_step(const short* __restrict__ st, short* __re
 #pragma unroll
     for (int c = c0; c < c1; ++c) {
       if (c < OA::CH) {
-        A.template store<P>(nxt, c, tid);
+        A.template store<P>(nxt, c, tid, ks);
         A.template load<P>(sa, c, tid);
       } else {
-        B.template store<P>(nxt + C::PART, c - OA::CH, tid);
+        B.template store<P>(nxt + C::PART, c - OA::CH, tid, ks);
         B.template load<P>(sb, c - OA::CH, tid);
       }
     }
@@ -401,17 +486,17 @@ __device__ __forceinline__ void k_step(const short* __restrict__ st, short* __re
 }
 
 // PF K steps from step kt (a multiple of PF) on, the register sets in turn.
-template <class E, class C, int KA, int KB, int U>
-__device__ __forceinline__ void k_steps(short* lds, Operand<E, C::BM, C::NT, KA, C::PF>& A,
-                                        Operand<E, C::BN, C::NT, KB, C::PF>& B, long long k0, int kt,
+template <class E, class C, int KA, int KB, bool RAG, int U>
+__device__ __forceinline__ void k_steps(short* lds, Operand<E, C::BM, C::NT, KA, C::PF, RAG>& A,
+                                        Operand<E, C::BN, C::NT, KB, C::PF, RAG>& B, long long k0, int kt,
                                         int tid, int aoff, int boff, short8 (&fa0)[C::FM],
                                         short8 (&fb0)[C::FN], floatx16 (&acc)[C::FM][C::FN]) {
   if constexpr (U < C::PF) {
     const int t = kt + U;
-    k_step<E, C, KA, KB, (U + 1) % C::PF>(lds + (t & 1) * C::STAGE, lds + ((t + 1) & 1) * C::STAGE, A,
+    k_step<E, C, KA, KB, RAG, (U + 1) % C::PF>(lds + (t & 1) * C::STAGE, lds + ((t + 1) & 1) * C::STAGE, A,
                                           B, k0 + (long long)(t + 1 + C::PF) * BK, tid, aoff, boff, fa0,
                                           fb0, acc);
-    k_steps<E, C, KA, KB, U + 1>(lds, A, B, k0, kt, tid, aoff, boff, fa0, fb0, acc);
+    k_steps<E, C, KA, KB, RAG, U + 1>(lds, A, B, k0, kt, tid, aoff, boff, fa0, fb0, acc);
   }
 }
 
@@ -429,7 +514,7 @@ __device__ __forceinline__ void load_ahead(OA& A, OB& B, long long k0, int tid) 
 // 215-231 us forward, 222-232 input gradient, 217-225 weight gradient (box to
 // box), of which about 1.5 us a K step and 10 us a round for first loads and
 // epilogue.  F32: C goes to G; PART: to the scratch (splits); else to Y.
-template <class E, class C, int KA, int KB, bool F32, bool PART>
+template <class E, class C, int KA, int KB, bool F32, bool PART, bool RAG>
 __global__ __launch_bounds__(C::NT, C::PER_CU) void k_lin(LinP p) {
   __shared__ __attribute__((aligned(16))) char lds_raw[C::BYTES];
   short* lds = (short*)lds_raw;
@@ -467,17 +552,17 @@ __global__ __launch_bounds__(C::NT, C::PER_CU) void k_lin(LinP p) {
     long long k1 = k0 + (long long)p.steps * BK;
     if (k1 > p.K) k1 = p.K;
     const int nk = (int)((k1 - k0 + BK - 1) / BK);          // >= 1
-    typedef Operand<E, C::BM, C::NT, KA, C::PF> OA;
-    typedef Operand<E, C::BN, C::NT, KB, C::PF> OB;
+    typedef Operand<E, C::BM, C::NT, KA, C::PF, RAG> OA;
+    typedef Operand<E, C::BN, C::NT, KB, C::PF, RAG> OB;
     OA A;
     OB B;
-    A.init(p.A, nullptr, p.lda, p.M, k1, m0, tid);       // (nothing past this part's K is read)
-    B.init(p.B, p.bs, p.ldb, p.N, k1, n0, tid);
+    A.init(p.A, nullptr, p.lda, p.M, k1, p.K, m0, tid);       // (nothing past this part's K is read)
+    B.init(p.B, p.bs, p.ldb, p.N, k1, p.K, n0, tid);
     const int aoff = OA::frag_off(wm * C::WTM, lane), boff = OB::frag_off(wn * C::WTN, lane);
     // tile j passes through register set j % PF
     load_ahead<E, C, OA, OB, 0>(A, B, k0, tid);
-    A.template store_all<0>(lds, tid);
-    B.template store_all<0>(lds + C::PART, tid);
+    A.template store_all<0>(lds, tid, k0);
+    B.template store_all<0>(lds + C::PART, tid, k0);
     A.template load_all<0>(k0 + C::PF * BK, tid);
     B.template load_all<0>(k0 + C::PF * BK, tid);
     __builtin_amdgcn_sched_barrier(0);
@@ -489,7 +574,7 @@ __global__ __launch_bounds__(C::NT, C::PER_CU) void k_lin(LinP p) {
     for (int j = 0; j < C::FN; ++j) fb0[j] = OB::frag(lds + C::PART + boff, j, 0);
     // whole rounds of the register sets: steps past the end multiply zeros
     for (int kt = 0; kt < nk; kt += C::PF)
-      k_steps<E, C, KA, KB, 0>(lds, A, B, k0, kt, tid, aoff, boff, fa0, fb0, acc);
+      k_steps<E, C, KA, KB, RAG, 0>(lds, A, B, k0, kt, tid, aoff, boff, fa0, fb0, acc);
     // (the last step's barrier also frees the LDS for the epilogue)
   }
 
@@ -623,11 +708,11 @@ __global__ __launch_bounds__(256) void k_lin_zero(long long M, unsigned nch, Fin
   finish8<E, F32>(f, e / nch, (int)(e % nch) * 8, v);
 }
 
-// An operand that the kernel cannot read in place (rows not 16-byte aligned,
-// or a contiguous side that is no multiple of 8) copied into rows of a whole
-// number of chunks, zeros at their ends.  The copy moves the operand twice
-// more, a small part of the product's time except at few tokens (1000 x 515:
-// 3.6 us, most of it the launch).
+// An operand that the aligned kernels cannot read in place (rows not 16-byte
+// aligned, or a contiguous side that is no multiple of 8) copied into rows of
+// a whole number of chunks, zeros at their ends, where the ragged form is
+// modelled to take longer or has no 8 elements in a row to read.  The copy
+// moves the operand twice more (1000 x 515: 3.6 us, most of it the launch).
 __global__ __launch_bounds__(256) void k_lin_copy(const unsigned short* __restrict__ src,
                                                   long long ld, long long rows, int cols,
                                                   unsigned nch, unsigned short* __restrict__ dst) {
@@ -654,7 +739,7 @@ __global__ __launch_bounds__(256) void k_lin_copy(const unsigned short* __restri
 // contiguous bytes of one W row (four chunks, one per MFMA: the order of K
 // inside the product is free as long as both operands agree) and the same
 // columns of its token.  The waves' 16 x 16 sums join in LDS in wave order.
-// VEC: both operands readable in 16-byte chunks; else element by element.
+// Both operands are readable in 16-byte chunks (in_place).
 // 4096 x 4096: 11 us at 2 tokens, 13 at 16.
 struct ThinP {
   const void* X; const void* W;
@@ -663,23 +748,14 @@ struct ThinP {
   Finish f;
 };
 
-template <class E, bool VEC>
 __device__ __forceinline__ short8 thin_chunk(__amdgpu_buffer_rsrc_t rs, int row_off, int k, int K) {
-  if constexpr (VEC) {
-    const int4v v = __builtin_amdgcn_raw_buffer_load_b128(rs, k < K ? row_off + k * 2 : kOut, 0, 0);
-    return __builtin_bit_cast(short8, v);
-  } else {
-    short8 o;
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      o[e] = (short)__builtin_amdgcn_raw_buffer_load_b16(rs, k + e < K ? row_off + (k + e) * 2 : kOut, 0, 0);
-    return o;
-  }
+  const int4v v = __builtin_amdgcn_raw_buffer_load_b128(rs, k < K ? row_off + k * 2 : kOut, 0, 0);
+  return __builtin_bit_cast(short8, v);
 }
 
-template <class E, bool VEC>
+template <class E>
 __global__ __launch_bounds__(512) void k_lin_thin(ThinP p) {
-  constexpr int NW = 8, U = VEC ? 2 : 1;
+  constexpr int NW = 8, U = 2;
   __shared__ float sh[NW][16][17];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const long long n0 = (long long)blockIdx.x * 16;
@@ -698,8 +774,8 @@ __global__ __launch_bounds__(512) void k_lin_thin(ThinP p) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int k = k0 + u * NW * 128 + g * 32 + i * 8;
-        a[u][i] = thin_chunk<E, VEC>(rw, wo, k, wK);
-        b[u][i] = thin_chunk<E, VEC>(rx, xo, k, xK);
+        a[u][i] = thin_chunk(rw, wo, k, wK);
+        b[u][i] = thin_chunk(rx, xo, k, xK);
       }
 #pragma unroll
     for (int u = 0; u < U; ++u)
@@ -774,6 +850,11 @@ __global__ __launch_bounds__(512) void k_lin_vec(ThinP p) {
   }
 }
 
+// Rows of an operand as the aligned kernels read it: 16-byte chunks.
+bool in_place(const void* p, long long ld, long long contiguous) {
+  return ((uintptr_t)p & 15) == 0 && ld % 8 == 0 && contiguous % 8 == 0;
+}
+
 // The forms for few tokens: by vectors for one; the 16 x 16 matrix form while
 // W is small (16 tokens: 4096 x 4096 13 us, 16 by the 64 x 64 tiles; 11008 x
 // 4096 36 us, 27 by the tiles: there the tokens, read once by every workgroup,
@@ -782,15 +863,11 @@ constexpr int kThinTokens = 16;
 constexpr long long kThinWeights = 24LL << 20;
 bool few_tokens(const LinDesc& d) {
   return !d.a_km && !d.b_kn && !d.G &&
-         (d.M == 1 || (d.M <= kThinTokens && d.N * d.K <= kThinWeights));
+         (d.M == 1 || (d.M <= kThinTokens && d.N * d.K <= kThinWeights &&
+                       in_place(d.A, d.lda, d.K) && in_place(d.B, d.ldb, d.K)));
 }
 
 // ------------------------------------------------------------- host side
-
-// Rows of an operand as the kernel reads it.
-bool in_place(const void* p, long long ld, long long contiguous) {
-  return ((uintptr_t)p & 15) == 0 && ld % 8 == 0 && contiguous % 8 == 0;
-}
 
 // A rectangle of the output by one tile shape, its K axis in `splits` parts of
 // `steps` K steps.
@@ -800,7 +877,8 @@ struct LinPart {
 };
 struct LinPlan {
   bool thin;
-  bool copyA, copyB;
+  bool ragged;             // operands read unaligned
+  bool copyA, copyB;       // or copied first
   long long rowsA, colsA, rowsB, colsB;     // as stored
   size_t oA, oB, oP, total;
   int nparts;
@@ -822,14 +900,20 @@ constexpr Tile kTiles[kNTiles] = {{256, 256, 1.05, 1.53, 11.0},
                                   {128, 128, 0.45, 0.53, 4.5},
                                   {64, 64, 0.20, 0.24, 3.0}};
 constexpr int kCus = 256;
+// A step of the ragged form against an aligned one.  Three shapes have it: the
+// large tile, 128 x 256 and 64 x 64, between which the model finds a time
+// within 10 % of the best of the five on the shapes named at Operand.
+constexpr double kRag = 1.15;
+constexpr bool has_ragged(int tile) { return tile == 0 || tile == 2 || tile == 4; }
 
 // The cheapest tile shape and split of one rectangle: rounds of workgroups
 // over the 256 CUs, and for splits the join's launch and its traffic.
-double choose_tile(LinPart& q, long long K, bool f8) {
+double choose_tile(LinPart& q, long long K, bool f8, bool rag) {
   static const int kSplits[] = {1, 2, 3, 4, 5, 6, 7, 8, 10, 12, 14, 16, 20, 24, 28, 32, 40, 48, 64};
   const long long nk = (K + BK - 1) / BK;
   double best = 1e30;
   for (int i = 0; i < kNTiles; ++i) {
+    if (rag && !has_ragged(i)) continue;
     const Tile& t = kTiles[i];
     const long long tiles = ((q.M + t.bm - 1) / t.bm) * ((q.N + t.bn - 1) / t.bn);
     for (const int sp : kSplits) {
@@ -837,7 +921,8 @@ double choose_tile(LinPart& q, long long K, bool f8) {
       const int steps = (int)((nk + sp - 1) / sp);
       const double load = (double)(tiles * sp) / kCus, rounds = ceil(load);
       // (on an idle chip the decoding of 8-bit operands is not hidden)
-      const double lo = f8 ? t.lo + 0.15 : t.lo, hi = t.hi > lo ? t.hi : lo;
+      const double lo = f8 ? t.lo + 0.15 : rag ? t.lo * kRag : t.lo;
+      const double hi = rag ? t.hi * kRag : t.hi > lo ? t.hi : lo;
       const double step = lo + (hi - lo) * (load < 1.0 ? load : 1.0);
       double us = rounds * (steps * step + t.fixed);
       if (sp > 1) us += 4.0 + 8.0 * sp * (double)q.M * q.N / 5.0e6;
@@ -856,25 +941,26 @@ double choose_tile(LinPart& q, long long K, bool f8) {
 // rounds, and what is left as a rectangle of its own with its own tile shape
 // (8192 x 11008 outputs are 5.4 rounds of the large tile: 5 rounds and 768
 // columns in one round of 128 x 256 tiles instead of 6).
-void choose_parts(LinPlan& q, long long M, long long N, long long K, bool f8) {
+double choose_parts(LinPlan& q, long long M, long long N, long long K, bool f8, bool rag) {
   LinPart whole = {0, 0, M, N, 0, 1, 0};
-  double best = choose_tile(whole, K, f8);
+  double best = choose_tile(whole, K, f8, rag);
   q.nparts = 1;
   q.part[0] = whole;
   const int nk = (int)((K + BK - 1) / BK);
   for (int i = 0; i < kNTiles; ++i) {
+    if (rag && !has_ragged(i)) continue;
     const Tile& t = kTiles[i];
     const long long tm = (M + t.bm - 1) / t.bm, tn = (N + t.bn - 1) / t.bn;
     const long long full = tm * tn / kCus;
     if (full < 1) continue;
-    const double us = (double)full * (nk * t.hi + t.fixed) + 8.0;
+    const double us = (double)full * (nk * t.hi * (rag ? kRag : 1.0) + t.fixed) + 8.0;
     for (int side = 0; side < 2; ++side) {
       const long long cut = full * kCus / (side ? tn : tm);               // tile rows / columns
       if (cut < 1 || cut >= (side ? tm : tn)) continue;
       const LinPart a = {0, 0, side ? cut * t.bm : M, side ? N : cut * t.bn, i, 1, nk};
       LinPart b = {side ? cut * t.bm : 0, side ? 0 : cut * t.bn, side ? M - cut * t.bm : M,
                    side ? N : N - cut * t.bn, 0, 1, 0};
-      const double both = us + choose_tile(b, K, f8);
+      const double both = us + choose_tile(b, K, f8, rag);
       if (both < best) {
         best = both;
         q.nparts = 2;
@@ -883,6 +969,7 @@ void choose_parts(LinPlan& q, long long M, long long N, long long K, bool f8) {
       }
     }
   }
+  return best;
 }
 
 LinPlan lin_plan(const LinDesc& d) {
@@ -894,7 +981,21 @@ LinPlan lin_plan(const LinDesc& d) {
   if (q.thin) return q;
   q.copyA = !in_place(d.A, d.lda, q.colsA);
   q.copyB = !d.bs && !in_place(d.B, d.ldb, q.colsB);
-  choose_parts(q, d.M, d.N, d.K, d.bs != nullptr);
+  double us = choose_parts(q, d.M, d.N, d.K, d.bs != nullptr, false);
+  // unaligned operands: copied first (a launch and their bytes twice), or read
+  // as they are by the ragged form (measured: see Operand)
+  if (q.copyA || q.copyB) {
+    if (q.copyA) us += 4.0 + 4.0 * (double)q.rowsA * q.colsA / 4.5e6;
+    if (q.copyB) us += 4.0 + 4.0 * (double)q.rowsB * q.colsB / 4.5e6;
+    if (q.colsA >= 8 && (d.bs || q.colsB >= 8)) {
+      LinPlan r = q;
+      if (choose_parts(r, d.M, d.N, d.K, d.bs != nullptr, true) < us) {
+        q = r;
+        q.ragged = true;
+        q.copyA = q.copyB = false;
+      }
+    }
+  }
   size_t off = 0;
   auto take = [&](size_t b) { const size_t o = off; off = (off + b + 255) & ~(size_t)255; return o; };
   if (q.copyA) q.oA = take((size_t)q.rowsA * up8(q.colsA) * 2);
@@ -912,29 +1013,38 @@ LinPlan lin_plan(const LinDesc& d) {
   return q;
 }
 
-template <class E, class C, int KA, int KB, bool F32>
+template <class E, class C, int KA, int KB, bool F32, bool RAG>
 hipError_t launch_tiles(const LinP& p, hipStream_t s) {
+  const dim3 grid((unsigned)p.total), block(C::NT);
   if (p.splits > 1)
-    hipLaunchKernelGGL((k_lin<E, C, KA, KB, F32, true>), dim3((unsigned)p.total), dim3(C::NT), 0, s, p);
+    hipLaunchKernelGGL((k_lin<E, C, KA, KB, F32, true, RAG>), grid, block, 0, s, p);
   else
-    hipLaunchKernelGGL((k_lin<E, C, KA, KB, F32, false>), dim3((unsigned)p.total), dim3(C::NT), 0, s, p);
+    hipLaunchKernelGGL((k_lin<E, C, KA, KB, F32, false, RAG>), grid, block, 0, s, p);
   return hipGetLastError();
 }
 
 template <class E, int KA, int KB, bool F32>
-hipError_t launch_cfg(LinP p, int tile, hipStream_t s) {
+hipError_t launch_cfg(LinP p, int tile, bool rag, hipStream_t s) {
   const Tile& t = kTiles[tile];
   p.tilesM = (int)((p.M + t.bm - 1) / t.bm);
   p.tilesN = (p.N + t.bn - 1) / t.bn;
   p.total = (long long)p.tilesM * p.tilesN * p.splits;
   if (p.total > 0x7fffffffLL) return hipErrorInvalidValue;
-  switch (tile) {
-    case 0: return launch_tiles<E, CfgL, KA, KB, F32>(p, s);
-    case 1: return launch_tiles<E, CfgM, KA, KB, F32>(p, s);
-    case 2: return launch_tiles<E, CfgW, KA, KB, F32>(p, s);
-    case 3: return launch_tiles<E, CfgS, KA, KB, F32>(p, s);
+  if (rag) {
+    switch (tile) {
+      case 0: return launch_tiles<E, CfgL, KA, KB, F32, true>(p, s);
+      case 2: return launch_tiles<E, CfgW, KA, KB, F32, true>(p, s);
+      case 4: return launch_tiles<E, CfgT, KA, KB, F32, true>(p, s);
+    }
+    return hipErrorInvalidValue;
   }
-  return launch_tiles<E, CfgT, KA, KB, F32>(p, s);
+  switch (tile) {
+    case 0: return launch_tiles<E, CfgL, KA, KB, F32, false>(p, s);
+    case 1: return launch_tiles<E, CfgM, KA, KB, F32, false>(p, s);
+    case 2: return launch_tiles<E, CfgW, KA, KB, F32, false>(p, s);
+    case 3: return launch_tiles<E, CfgS, KA, KB, F32, false>(p, s);
+  }
+  return launch_tiles<E, CfgT, KA, KB, F32, false>(p, s);
 }
 
 template <class E>
@@ -957,10 +1067,8 @@ hipError_t launch_lin_t(const LinDesc& d, void* ws, hipStream_t s) {
     const dim3 grid((unsigned)((d.N + 15) / 16));
     if (d.M == 1)
       hipLaunchKernelGGL((k_lin_vec<E>), dim3((unsigned)((d.N + 7) / 8)), dim3(512), 0, s, p);
-    else if (in_place(d.A, d.lda, d.K) && in_place(d.B, d.ldb, d.K))
-      hipLaunchKernelGGL((k_lin_thin<E, true>), grid, dim3(512), 0, s, p);
     else
-      hipLaunchKernelGGL((k_lin_thin<E, false>), grid, dim3(512), 0, s, p);
+      hipLaunchKernelGGL((k_lin_thin<E>), grid, dim3(512), 0, s, p);
     return hipGetLastError();
   }
   LinP p = {};
@@ -1014,10 +1122,10 @@ hipError_t launch_lin_t(const LinDesc& d, void* ws, hipStream_t s) {
     hipError_t e;
     {
       TraceScope ts(d.name, 2.0 * (double)t.M * t.N * d.K, 0.0, s);
-      if (d.bs) e = launch_cfg<E, kColsK, kColsF8, true>(p, t.tile, s);
-      else if (d.G) e = launch_cfg<E, kColsK, kColsK, true>(p, t.tile, s);
-      else if (d.b_kn) e = launch_cfg<E, kRowsK, kColsK, false>(p, t.tile, s);
-      else e = launch_cfg<E, kRowsK, kRowsK, false>(p, t.tile, s);
+      if (d.bs) e = launch_cfg<E, kColsK, kColsF8, true>(p, t.tile, q.ragged, s);
+      else if (d.G) e = launch_cfg<E, kColsK, kColsK, true>(p, t.tile, q.ragged, s);
+      else if (d.b_kn) e = launch_cfg<E, kRowsK, kColsK, false>(p, t.tile, q.ragged, s);
+      else e = launch_cfg<E, kRowsK, kRowsK, false>(p, t.tile, q.ragged, s);
     }
     if (e != hipSuccess) return e;
     if (t.splits == 1) continue;

@@ -291,6 +291,16 @@ def test_products_of_many_tiles(T, n, m):
     test_products_exact(T, n, m, BF)
 
 
+@pytest.mark.parametrize("how", ["odd", "off"])
+@pytest.mark.parametrize("T,n,m", [(2100, 4101, 77), (4101, 2123, 45), (77, 4103, 4101),
+                                   (2101, 77, 4100), (3001, 6301, 70), (1000, 1029, 5121),
+                                   (2048, 8193, 1001), (2048, 1001, 8193), (700, 8, 9), (9, 700, 8), (8, 9, 700), (300, 7, 5), (130, 66, 17)])
+def test_ragged_products(T, n, m, how):
+    """Unaligned operands read as they are, by every tile that does so, with
+    odd ends along K and along both sides, parts of the output and of K."""
+    test_products_places(T, n, m, how)
+
+
 @pytest.mark.parametrize("how", ["wide", "odd", "off"])
 @pytest.mark.parametrize("T,n,m", [(3, 40, 72), (5, 33, 101), (150, 264, 136), (141, 131, 203),
                                    (300, 257, 520)])

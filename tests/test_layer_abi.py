@@ -138,16 +138,18 @@ def test_workspaces():
     assert st == OK and nb >= N * 4
     for change in (dict(ws=None), dict(ws=P + 128), dict(nb=nb - 1)):
         assert call("dion3_act_grad", ACT_GRAD, **change) == ERR_WS
-    # an operand off its alignment is copied: the workspace holds it
+    # an operand off its alignment is read as it is, but rows of fewer than 8
+    # elements are copied: the workspace holds them
     odd = P + 2
-    st, nb = size("dion3_linear_workspace_size", odd, M, P, M, T, N, M)
-    st0, nb0 = size("dion3_linear_workspace_size", P, M, P, M, T, N, M)
-    assert st == st0 == OK and nb >= nb0 + T * M * 2
+    for fn in ("dion3_linear_workspace_size", "dion3_linear_grad_input_workspace_size"):
+        assert size(fn, odd, 24, P, 24, T, 24, 24) == size(fn, P, 24, P, 24, T, 24, 24) == (OK, 0)
+    st, nb = size("dion3_linear_workspace_size", odd, 7, P, 8, T, N, 7)
+    assert st == OK and nb >= (T + N) * 8 * 2
     for change in (dict(ws=None), dict(ws=P + 128), dict(nb=nb - 1)):
-        assert call("dion3_linear", LINEAR, X=odd, **change) == ERR_WS
-    st, nb = size("dion3_linear_grad_input_workspace_size", odd, N, P, M, T, N, M)
-    assert st == OK and nb >= T * N * 2
-    assert call("dion3_linear_grad_input", GRAD_INPUT, dZ=odd, nb=nb - 1) == ERR_WS
+        assert call("dion3_linear", LINEAR, X=odd, ldx=7, ldw=8, m=7, **change) == ERR_WS
+    st, nb = size("dion3_linear_grad_input_workspace_size", odd, 7, P, M, T, 7, M)
+    assert st == OK and nb >= T * 8 * 2
+    assert call("dion3_linear_grad_input", GRAD_INPUT, dZ=odd, lddz=7, n=7, nb=nb - 1) == ERR_WS
     # few tiles and many tokens: split, fp32 parts in the workspace
     st, nb = size("dion3_linear_grad_weight_workspace_size", P, 128, P, 512, None, 16384, 128, 512)
     assert st == OK and nb >= 2 * 128 * 512 * 4
