@@ -518,7 +518,14 @@ def linear_layer(x, w, bias=None, act: str = "none", residual=None, checkpoint="
     ``into``: a ``Dion3`` that steps w.  The weight gradient is then summed
     straight into w's momentum there, in the product's own epilogue; w gets no
     ``.grad``, and the next ``step()`` steps it.  What has been summed cannot
-    be taken back by ``zero_grad()``."""
+    be taken back by ``zero_grad()``.
+
+    Capturing into a graph: w's momentum must exist before (RuntimeError
+    otherwise; an earlier step or ``into.momentum(w)`` makes it).  torch's own
+    rule for a captured backward pass holds here too: let no graph of the same
+    leaves recorded outside the capture live (an earlier loss or output kept
+    in a variable), since its end would have to join streams that the capture
+    does not know."""
     if isinstance(checkpoint, PackedF8):
         if tuple(checkpoint.shape) != tuple(x.shape) or checkpoint.device != x.device:
             raise ValueError(f"checkpoint must stand for a tensor of shape {tuple(x.shape)} on "

@@ -132,10 +132,17 @@ class Dion3(_optimizer_base()):
         self._streams = set()          # the streams on which those gradients were added
 
     def check_parameter(self, p):
-        """Raise ValueError unless p is one of this optimizer's parameters."""
+        """Raise ValueError unless p is one of this optimizer's parameters, and
+        RuntimeError where its momentum would be made inside a captured graph
+        (every replay would clear it): call ``momentum(p)`` before."""
         if p not in self.state and not any(p is q for group in self.param_groups
                                            for q in group["params"]):
             raise ValueError("not a parameter of this optimizer")
+        if p.is_cuda and "momentum" not in self.state.get(p, ()):
+            import torch
+            with torch.cuda.device(p.device):
+                if torch.cuda.is_current_stream_capturing():
+                    raise RuntimeError("a parameter's momentum must exist before the capture")
 
     def momentum(self, p):
         """p's momentum buffer (fp32, p's strides; zero before the first gradient)."""
@@ -151,6 +158,7 @@ class Dion3(_optimizer_base()):
         stream of its device: the next ``step()`` waits for that stream and
         steps p whether or not it has a ``.grad``."""
         import torch
+        self.check_parameter(p)
         m = self.momentum(p)
         self._accumulated.add(p)
         if m.is_cuda:

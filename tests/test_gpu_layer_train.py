@@ -282,6 +282,26 @@ def test_training_step_in_a_graph():
             assert torch.equal(u, v)
 
 
+def test_momentum_is_not_made_in_a_capture(monkeypatch):
+    """The momentum's zeros would be part of the graph, and every replay would
+    start from them.  (Only the answer to whether a capture runs is forced.)"""
+    p = params(17)
+    x, _, _ = data(18, 8)
+    opt = d3.Dion3([p["w1"], p["w2"]])
+    opt.momentum(p["w2"])
+    with monkeypatch.context() as mp:
+        mp.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+        with pytest.raises(RuntimeError):
+            d3.linear_layer(x, p["w1"], into=opt)
+        with pytest.raises(RuntimeError):
+            opt.accumulate_grad(p["w1"])
+        assert not opt.state[p["w1"]] and not opt._accumulated and not opt._streams
+        assert opt.accumulate_grad(p["w2"]) is opt.momentum(p["w2"])
+    with pytest.raises(ValueError):
+        opt.accumulate_grad(x)
+    d3.linear_layer(x, p["w1"], into=opt)
+
+
 def test_refusals():
     p = params(13)
     x, r, _ = data(14, 8)
