@@ -202,7 +202,7 @@ enum Kind { kRowsK = 0, kColsK = 1, kColsF8 = 2 };
 // relying on a buffer's bounds: the last chunk of a row is the row's last 8
 // elements, moved into place before the LDS store, and what lies past K is
 // zeroed there.  A step costs 10 to 25 % more than an aligned one, against a
-// copy of the operand and its launch (bf16, one box, ragged against copied
+// copy of the operand and its launch (bf16, one card, ragged against copied
 // first): forward 517 x 1000 x 515 7.4 us against 11.8, 1000 x 2049 x 2047 29.7
 // against 37.0, 8192 x 4095 x 4097 264 against 288; input gradient 10.4 against
 // 10.5, 28.9 against 37.5, 295 against 307; weight gradient 7.8 against 8.2,
@@ -511,8 +511,8 @@ __device__ __forceinline__ void load_ahead(OA& A, OB& B, long long k0, int tid) 
 }
 
 // One tile of the output.  8192 x 4096 x 4096 (two rounds of 256 x 256 tiles):
-// 215-231 us forward, 222-232 input gradient, 217-225 weight gradient (box to
-// box), of which about 1.5 us a K step and 10 us a round for first loads and
+// 215-231 us forward, 222-232 input gradient, 217-225 weight gradient (card to
+// card), of which about 1.5 us a K step and 10 us a round for first loads and
 // epilogue.  F32: C goes to G; PART: to the scratch (splits); else to Y.
 template <class E, class C, int KA, int KB, bool F32, bool PART, bool RAG>
 __global__ __launch_bounds__(C::NT, C::PER_CU) void k_lin(LinP p) {
