@@ -331,7 +331,7 @@ DION3_API dion3_status dion3_symm_f16(const uint16_t* A, const uint16_t* B, cons
  * pointer is aligned to its element size (8-bit data: 16 bytes).  Any side
  * from 1 and any row stride that holds the row is taken; rows that are
  * 16-byte aligned with sides that are multiples of 8 are fastest (the
- * products read others 10 to 25 % more slowly, or copy them into the
+ * products read others up to 20 % more slowly, or copy them into the
  * workspace first, whichever is expected to take less).  T = 0 is
  * valid: nothing is written, except that gradients over no tokens are zero.
  * Statistics, products and column sums are held in fp32 and added in an order

@@ -201,12 +201,12 @@ enum Kind { kRowsK = 0, kColsK = 1, kColsF8 = 2 };
 // 16-byte loads, whose rows and columns are held inside the operand instead of
 // relying on a buffer's bounds: the last chunk of a row is the row's last 8
 // elements, moved into place before the LDS store, and what lies past K is
-// zeroed there.  A step costs 10 to 25 % more than an aligned one, against a
+// zeroed there.  A step costs up to 20 % more than an aligned one, against a
 // copy of the operand and its launch (bf16, one card, ragged against copied
-// first): forward 517 x 1000 x 515 7.4 us against 11.8, 1000 x 2049 x 2047 29.7
-// against 37.0, 8192 x 4095 x 4097 264 against 288; input gradient 10.4 against
-// 10.5, 28.9 against 37.5, 295 against 307; weight gradient 7.8 against 8.2,
-// 36 against 37, 289 against 372.
+// first): forward 517 x 1000 x 515 7.3 us against 11.8, 1000 x 2049 x 2047 29.3
+// against 36.5, 8192 x 4095 x 4097 250 against 289; input gradient 10.7 against
+// 10.6, 30 against 37.5, 268 against 311; weight gradient 8.0 against 8.4,
+// 27.8 against 37.5, 283 against 378.
 template <class E, int R, int NT, int KIND, int PF, bool RAG>
 struct Operand {
   static constexpr int RS = R + kPadN;                                 // [K][R] LDS row
@@ -225,8 +225,9 @@ struct Operand {
   int voff[FIXED ? 1 : CH];
   static constexpr bool RAGGED = RAG && KIND != kColsF8;
   long long Kt;          // RAGGED: the operand's own K (K: where this part of it ends)
-  int roff[RAGGED ? CH : 1];   // kRowsK: the chunks' rows
+  int roff[RAGGED ? CH : 1];   // kRowsK: the chunks' rows; kColsK: the first chunk's
   int cut;               // kColsK: elements of the chunk before its column
+  bool edge;             // kColsK: the columns end inside the tile
   int4v reg[PF][CH];
   unsigned sreg[PF][KIND == kColsF8 ? CH : 1];
 
@@ -250,7 +251,9 @@ struct Operand {
         const long long c = r0 + tid % CPR * 8, at = c < rows - 8 ? c : rows - 8;
         base = (const char*)p + from * 2;
         cut = (int)(c - at);
+        edge = r0 + R > rows;
         voff[0] = (int)(at - from) * 2;
+        roff[0] = tid / CPR * (int)ld;
       }
       return;
     }
@@ -284,7 +287,7 @@ struct Operand {
   };
   struct RagSrc {
     const char* p;       // kColsK: row min(k0, Kt - 1)
-    int v;               // kRowsK: the chunk's column; kColsK: rows left from p on, less one
+    int v;               // kRowsK: the chunk's column; kColsK: the last row that may be read
   };
   typedef typename Pick<RAGGED, RagSrc, Src>::type Source;
   __device__ __forceinline__ Source source(long long k0, int tid) const {
@@ -294,7 +297,7 @@ struct Operand {
         return {base, (int)(k < Kt - 8 ? k : Kt - 8) * 2};
       } else {
         const long long row = k0 < Kt - 1 ? k0 : Kt - 1;
-        return {base + row * ld, (int)(Kt - 1 - row < BK ? Kt - 1 - row : BK)};
+        return {base + row * ld, (int)(Kt - 1 - row < BK ? Kt - 1 - row : BK) * (int)ld};
       }
     } else if constexpr (KIND == kRowsK) {
       const __amdgpu_buffer_rsrc_t rs = rsrc(base, bytes);
@@ -317,7 +320,7 @@ struct Operand {
     constexpr int STEP = NT / CPR;
     if constexpr (RAGGED) {
       const unsigned o = KIND == kRowsK ? (unsigned)(roff[i] + s.v)
-                                        : (unsigned)(min(tid / CPR + i * STEP, s.v) * (int)ld + voff[0]);
+                                        : (unsigned)(min(roff[0] + i * STEP * (int)ld, s.v) + voff[0]);
       reg[P][i] = ((const Any16*)(s.p + o))->v;
       return;
     } else {
@@ -336,20 +339,40 @@ struct Operand {
     for (int i = 0; i < CH; ++i) load<P>(s, i, tid);
   }
 
+  // RAGGED: chunk i of the tile at k0 moved into place, and zeroed past K.
+  template <int P>
+  __device__ __forceinline__ int4v placed(int i, long long k0, int tid) const {
+    const long long k = k0 + (KIND == kRowsK ? (tid & 7) * 8 : (tid + NT * i) / CPR);
+    const int by = KIND == kRowsK ? (int)(k < Kt - 8 ? 0 : k - (Kt - 8)) : cut;
+    return moved(reg[P][i], k < K ? by : 8);
+  }
+  // All of them ahead of a step that reaches past an end (the choice is the
+  // workgroup's), so that the other steps pay nothing: 8192 x 4095 x 4097
+  // forward 250 us, 261 with every chunk placed as it is stored; input gradient
+  // 268 against 293.  The short steps of the small tile (PF 2) would wait for
+  // their loads there, and place late: 517 x 1000 x 515 input gradient 10.7 us
+  // against 12.8, weight gradient 8.1 against 11.0.
+  static constexpr bool LATE = RAGGED && PF > 1;
+  template <int P>
+  __device__ __forceinline__ void place(long long k0, int tid) {
+    if constexpr (RAGGED && !LATE) {
+      if (k0 + BK <= K && (KIND == kRowsK || !edge)) return;
+#pragma unroll
+      for (int i = 0; i < CH; ++i) reg[P][i] = placed<P>(i, k0, tid);
+    }
+  }
+
   // Chunk i of the tile at k0 from the registers into the LDS part s.
   template <int P>
   __device__ __forceinline__ void store(short* __restrict__ s, int i, int tid, long long k0) const {
     const int c = tid + NT * i;
     if constexpr (KIND == kRowsK) {
       int4v v = reg[P][i];
-      if constexpr (RAGGED) {
-        const long long k = k0 + (tid & 7) * 8;
-        v = moved(v, k < K ? (int)(k < Kt - 8 ? 0 : k - (Kt - 8)) : 8);
-      }
+      if constexpr (LATE) v = placed<P>(i, k0, tid);
       *(int4v*)(s + (c / CPR) * LDSK + (c % CPR) * 8) = v;
     } else if constexpr (KIND == kColsK) {
       int4v v = reg[P][i];
-      if constexpr (RAGGED) v = moved(v, k0 + c / CPR < K ? cut : 8);
+      if constexpr (LATE) v = placed<P>(i, k0, tid);
       *(int4v*)(s + (c / CPR) * RS + (c % CPR) * 8) = v;
     } else {
       const float sc = f8_scale_float(sreg[P][i]);
@@ -436,6 +459,8 @@ __device__ __forceinline__ void k_step(const short* __restrict__ st, short* __re
   const typename OA::Source sa = A.source(k_next, tid);
   const typename OB::Source sb = B.source(k_next, tid);
   const long long ks = k_next - C::PF * BK;              // the tile that is stored
+  A.template place<P>(ks, tid);
+  B.template place<P>(ks, tid);
   auto slice = [&](auto KK) {
     constexpr int kk = KK.value;
     constexpr int cb = kk & 1;
@@ -561,6 +586,8 @@ __global__ __launch_bounds__(C::NT, C::PER_CU) void k_lin(LinP p) {
     const int aoff = OA::frag_off(wm * C::WTM, lane), boff = OB::frag_off(wn * C::WTN, lane);
     // tile j passes through register set j % PF
     load_ahead<E, C, OA, OB, 0>(A, B, k0, tid);
+    A.template place<0>(k0, tid);
+    B.template place<0>(k0, tid);
     A.template store_all<0>(lds, tid, k0);
     B.template store_all<0>(lds + C::PART, tid, k0);
     A.template load_all<0>(k0 + C::PF * BK, tid);

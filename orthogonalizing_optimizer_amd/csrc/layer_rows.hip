@@ -594,7 +594,7 @@ __global__ __launch_bounds__(256) void k_act_grad(ActGradP p) {
 // rows and at most 1024 blocks.
 RowsPlan act_grad_plan(long long T, long long n) {
   const long long cols = (n + 511) / 512;
-    long long blocks = (4096 + cols - 1) / cols;
+  long long blocks = (4096 + cols - 1) / cols;
   if (blocks > 1024) blocks = 1024;
   if (blocks > (T + 15) / 16) blocks = (T + 15) / 16;
   if (blocks < 1) blocks = 1;
