@@ -451,6 +451,18 @@ def rms_norm_residual(x, weight, residual=None, eps: float = 1e-6, pack: bool = 
     return y, h, PackedF8(q, s, x.shape[-1], x.shape) if pack else None
 
 
+def _accumulates(node):
+    """What the running backward pass wants of the leaf behind ``node``, its
+    AccumulateGrad: True to accumulate its gradient, False nothing (a pass
+    restricted to other inputs), None its gradient as a value
+    (``torch.autograd.grad`` with respect to the leaf).  What a custom function
+    is told at its forward pass (``needs_input_grad``) knows no pass."""
+    try:
+        return torch._C._will_engine_execute_node(node)
+    except RuntimeError:         # raised for a leaf whose gradient is the pass's result
+        return None
+
+
 class _LinearLayer(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w, bias, residual, act, checkpoint, into):
@@ -485,6 +497,11 @@ class _LinearLayer(torch.autograd.Function):
     def backward(ctx, dy):
         x, xs, z, zs, w16 = ctx.saved_tensors
         need_x, need_w, need_b, need_r = ctx.needs_input_grad[:4]
+        into = None
+        if need_w and ctx.into is not None:
+            wanted = _accumulates(ctx.next_functions[1][0])      # (x and w are inputs 0 and 1)
+            need_w = wanted is not False
+            into = ctx.into if wanted else None
         dx = dw = db = None
         if need_x or need_w or need_b:
             dyr = _as_rows(dy)
@@ -495,8 +512,8 @@ class _LinearLayer(torch.autograd.Function):
                 dx = linear_grad_input(dz, w16)
             if need_w:
                 xin = PackedF8(x, xs, *ctx.x) if ctx.x is not None else x
-                if ctx.into is not None:
-                    linear_grad_weight(dz, xin, out=ctx.into.accumulate_grad(ctx.w), accumulate=True)
+                if into is not None:
+                    linear_grad_weight(dz, xin, out=into.accumulate_grad(ctx.w), accumulate=True)
                 else:
                     dw = linear_grad_weight(dz, xin).to(ctx.wtype)
             if db is not None:
@@ -518,7 +535,10 @@ def linear_layer(x, w, bias=None, act: str = "none", residual=None, checkpoint="
     ``into``: a ``Dion3`` that steps w.  The weight gradient is then summed
     straight into w's momentum there, in the product's own epilogue; w gets no
     ``.grad``, and the next ``step()`` steps it.  What has been summed cannot
-    be taken back by ``zero_grad()``.
+    be taken back by ``zero_grad()``.  This happens in the passes in which w's
+    ``.grad`` would grow, and in no other: ``backward(inputs=[x])`` and
+    ``torch.autograd.grad(y, x)`` leave the momentum alone, and
+    ``torch.autograd.grad(y, w)`` returns the gradient.
 
     Capturing into a graph: w's momentum must exist before (RuntimeError
     otherwise; an earlier step or ``into.momentum(w)`` makes it).  torch's own

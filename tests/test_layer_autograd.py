@@ -1,0 +1,100 @@
+"""The autograd side of the layer operators, on the CPU: which gradients a
+backward pass asks for, and what the optimizer's momentum receives.  The
+kernels are replaced by their formulas; what runs here is the package's own
+bookkeeping."""
+import pytest
+import torch
+
+import orthogonalizing_optimizer_amd as d3
+from orthogonalizing_optimizer_amd import layer
+
+
+@pytest.fixture(autouse=True)
+def formulas(monkeypatch):
+    """The calls of the library that linear_layer(..., checkpoint="full") makes."""
+    def linear(x, w, bias=None, act="none", residual=None, return_preact=False):
+        z = x @ w.t() if bias is None else x @ w.t() + bias
+        return (z if residual is None else z + residual), (z if return_preact else None)
+
+    def grad_weight(dz, x, out=None, accumulate=False):
+        dw = dz.reshape(-1, dz.shape[-1]).t() @ x.reshape(-1, x.shape[-1])
+        if out is None:
+            return dw
+        return out.add_(dw) if accumulate else out.copy_(dw)
+
+    monkeypatch.setattr(layer, "linear", linear)
+    monkeypatch.setattr(layer, "act_grad",
+                        lambda dy, z, act, bias=False: (dy, dy.sum(0) if bias else None))
+    monkeypatch.setattr(layer, "linear_grad_input", lambda dz, w: dz @ w)
+    monkeypatch.setattr(layer, "linear_grad_weight", grad_weight)
+
+
+def setting(seed=1, T=6, n=4, m=5):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(T, m, generator=g, requires_grad=True)
+    w = torch.randn(n, m, generator=g, requires_grad=True)
+    b = torch.randn(n, generator=g, requires_grad=True)
+    dy = torch.randn(T, n, generator=g)
+    opt = d3.Dion3([w])
+    y = d3.linear_layer(x, w, b, checkpoint="full", into=opt)
+    return x, w, b, dy, opt, y
+
+
+def untouched(opt, w):
+    return not opt._accumulated and not opt.momentum(w).any() and w.grad is None
+
+
+def test_whole_backward_pass_sums_into_the_momentum():
+    x, w, b, dy, opt, y = setting()
+    y.backward(dy)
+    assert torch.equal(opt.momentum(w), dy.t() @ x.detach()) and w.grad is None
+    assert w in opt._accumulated
+    assert torch.equal(x.grad, dy @ w.detach()) and torch.equal(b.grad, dy.sum(0))
+
+
+def test_pass_for_other_inputs_leaves_the_momentum():
+    x, w, b, dy, opt, y = setting()
+    gx, gb = torch.autograd.grad(y, (x, b), dy, retain_graph=True)
+    assert torch.equal(gx, dy @ w.detach()) and torch.equal(gb, dy.sum(0))
+    assert untouched(opt, w)
+    y.backward(dy, inputs=[x], retain_graph=True)
+    assert torch.equal(x.grad, gx) and b.grad is None
+    assert untouched(opt, w)
+    y.backward(dy, inputs=[b, w])              # asked for by name
+    assert torch.equal(opt.momentum(w), dy.t() @ x.detach()) and w in opt._accumulated
+
+
+def test_weight_gradient_as_a_value():
+    x, w, b, dy, opt, y = setting()
+    gw, = torch.autograd.grad(y, w, dy, retain_graph=True)
+    assert torch.equal(gw, dy.t() @ x.detach())
+    gw, gx = torch.autograd.grad(y, (w, x), dy)
+    assert torch.equal(gw, dy.t() @ x.detach()) and torch.equal(gx, dy @ w.detach())
+    assert untouched(opt, w)
+
+
+def test_weight_used_twice():
+    x, w, _, _, opt, _ = setting(n=5)
+    y1 = d3.linear_layer(x, w, checkpoint="full", into=opt)
+    y = d3.linear_layer(y1, w, checkpoint="full", into=opt)
+    dy = torch.randn_like(y)
+    torch.autograd.grad(y, x, dy, retain_graph=True)
+    torch.autograd.grad(y, y1, dy, retain_graph=True)
+    assert untouched(opt, w)
+    with torch.no_grad():
+        want = dy.t() @ y1 + (dy @ w).t() @ x
+    gw, = torch.autograd.grad(y, w, dy, retain_graph=True)
+    assert torch.allclose(gw, want, rtol=1e-5, atol=1e-5) and untouched(opt, w)
+    y.backward(dy)
+    assert torch.allclose(opt.momentum(w), want, rtol=1e-5, atol=1e-5)
+
+
+@pytest.mark.parametrize("reentrant", [False, True])
+def test_recomputed_layer(reentrant):
+    from torch.utils.checkpoint import checkpoint
+    x, w, _, dy, opt, _ = setting()
+    y = checkpoint(lambda t: d3.linear_layer(t, w, checkpoint="full", into=opt), x,
+                   use_reentrant=reentrant)
+    y.backward(dy)
+    assert torch.equal(opt.momentum(w), dy.t() @ x.detach())
+    assert torch.equal(x.grad, dy @ w.detach())
