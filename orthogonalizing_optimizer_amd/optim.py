@@ -85,6 +85,27 @@ def _optimizer_base():
     return torch.optim.Optimizer
 
 
+def _stream(t):
+    """The current stream of t's device; None for a host tensor."""
+    import torch
+    return torch.cuda.current_stream(t.device) if t.is_cuda else None
+
+
+def _capturing(stream) -> bool:
+    """Whether a graph is being captured from this stream."""
+    import torch
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
+def _follow(here, last, t=None):
+    """Stream ``here`` waits for what ``last`` holds so far; t's memory, made on
+    another stream, is not given away while ``here`` may use it."""
+    here.wait_stream(last)
+    if t is not None:
+        t.record_stream(here)
+
+
 class Dion3(_optimizer_base()):
     """torch.optim-style Dion3 for 2-D fp32 parameters.
 
@@ -129,7 +150,13 @@ class Dion3(_optimizer_base()):
         self.cfg = cfg
         self._ws: Dict[str, _lib.Workspace] = {}
         self._accumulated = set()      # parameters whose momentum already holds a new gradient
-        self._streams = set()          # the streams on which those gradients were added
+        # The stream that used a parameter's momentum last.  Sums into one
+        # buffer read and write it without atomics, each on its layer's own
+        # stream, and autograd, which sees none of them, does not order them:
+        # a use on another stream waits for the last one.  Uses inside captures
+        # are kept apart, since nothing there can wait for work outside.
+        self._last: Dict = {}
+        self._last_captured: Dict = {}
 
     def check_parameter(self, p):
         """Raise ValueError unless p is one of this optimizer's parameters, and
@@ -144,26 +171,50 @@ class Dion3(_optimizer_base()):
                 if torch.cuda.is_current_stream_capturing():
                     raise RuntimeError("a parameter's momentum must exist before the capture")
 
-    def momentum(self, p):
-        """p's momentum buffer (fp32, p's strides; zero before the first gradient)."""
+    def _buffer(self, p):
+        """p's momentum buffer, made on the current stream if need be."""
         st = self.state[p]
         if "momentum" not in st:       # the parameter's own strides
             import torch
             st["momentum"] = torch.empty_strided(p.shape, p.stride(), dtype=p.dtype,
                                                  device=p.device).zero_()
+            here = _stream(p)
+            if here is not None:
+                self._last[p] = here
         return st["momentum"]
 
-    def accumulate_grad(self, p):
-        """p's momentum buffer, for a gradient to be added to it on the current
-        stream of its device: the next ``step()`` waits for that stream and
-        steps p whether or not it has a ``.grad``."""
-        import torch
+    def momentum(self, p):
+        """p's momentum buffer (fp32, p's strides; zero before the first
+        gradient), to be used on the current stream of its device: that stream
+        waits for the buffer's last use on another one, and the next use on
+        another stream waits for this one."""
         self.check_parameter(p)
+        m = self._buffer(p)
+        here = _stream(m)
+        if here is not None:
+            captured = _capturing(here)
+            uses = self._last_captured if captured else self._last
+            last = uses.get(p)
+            if last is not None and last != here and (not captured or _capturing(last)):
+                _follow(here, last, None if captured else m)
+            uses[p] = here
+        return m
+
+    def accumulate_grad(self, p):
+        """p's momentum buffer (``momentum(p)``), for a gradient to be added to
+        it on the current stream of its device: the next ``step()`` waits for
+        that stream and steps p whether or not it has a ``.grad``."""
         m = self.momentum(p)
         self._accumulated.add(p)
-        if m.is_cuda:
-            self._streams.add(torch.cuda.current_stream(m.device))
         return m
+
+    def _used_on(self, params):
+        return {self._last[p] for p in params if p in self._last}
+
+    @property
+    def _streams(self):
+        """Where the gradients that the next ``step()`` takes were added last."""
+        return self._used_on(self._accumulated)
 
     def step(self, closure=None):
         import torch
@@ -173,10 +224,12 @@ class Dion3(_optimizer_base()):
                 loss = closure()
         # autograd runs a layer's backward on its forward's stream, and joins
         # that stream with the caller's only for gradients that it keeps itself
-        for stream in self._streams:
+        params = [p for group in self.param_groups for p in group["params"]
+                  if p.grad is not None or p in self._accumulated]
+        for stream in self._used_on(params):
             here = torch.cuda.current_stream(stream.device)
             if stream != here:
-                here.wait_stream(stream)
+                _follow(here, stream)
         with torch.no_grad():
             for group in self.param_groups:
                 f = float(group["fraction"])
@@ -186,7 +239,7 @@ class Dion3(_optimizer_base()):
                         continue
                     if p.grad is not None and p.grad.stride() != p.stride():
                         raise ValueError("a gradient must have its parameter's strides")
-                    self.momentum(p)
+                    self._buffer(p)
                     st = self.state[p]
                     if group["normalize"] and "second_moment" not in st:
                         st["second_moment"] = torch.zeros(p.shape[0], dtype=torch.float32,
@@ -209,6 +262,9 @@ class Dion3(_optimizer_base()):
                     for i in range(0, len(grps), _lib.MAX_GROUPS):
                         _lib.step_groups(grps[i:i + _lib.MAX_GROUPS], group["mu"], self.cfg,
                                          norm=norm, ws=ws)
+        for p in params:
+            here = _stream(p)
+            if here is not None:
+                self._last[p] = here
         self._accumulated.clear()
-        self._streams.clear()
         return loss

@@ -39,3 +39,61 @@ def test_passes_that_do_not_ask_for_the_weight(act, checkpoint):
     assert torch.equal(opt.momentum(w), gw) and w.grad is None
     opt.step()
     assert not torch.equal(w.detach(), before)
+
+
+@pytest.mark.parametrize("shared", [True, False])
+def test_two_backward_passes_on_two_streams(shared):
+    """One weight on two streams: the sums and the momentum's first zeros do not
+    meet.  Shared: two branches of one backward pass; else two passes."""
+    T, n, m = 8192, 512, 1024
+    batches = [setting(s, T, n, m)[::2] for s in (2, 3)]
+    w0 = setting(2, T, n, m)[1].detach()
+    want = None
+    for streams in [[torch.cuda.current_stream()] * 2, [torch.cuda.Stream() for _ in range(2)]]:
+        w = w0.clone().requires_grad_(True)
+        opt = d3.Dion3([w], lr=0.02, fraction=0.25)
+        torch.cuda.synchronize()
+        ys = []
+        for s, (x, _) in zip(streams, batches):
+            s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s):
+                ys.append(d3.linear_layer(x, w, into=opt))
+        for s in streams:
+            torch.cuda.current_stream().wait_stream(s)
+        if shared:
+            torch.autograd.backward(ys, [dy for _, dy in batches])
+        else:
+            for s, y, (_, dy) in zip(streams, ys, batches):
+                s.wait_stream(torch.cuda.current_stream())
+                with torch.cuda.stream(s):
+                    y.backward(dy)
+        opt.step()
+        got = [opt.momentum(w).clone(), w.detach().clone()]
+        if want is None:
+            want = got
+        # (two sums into zeros: a + b is b + a, whichever came first)
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+
+
+def test_sum_behind_a_step_on_another_stream():
+    """A backward pass of an older forward pass, on its own stream, after a
+    step on another: the sum follows the step."""
+    T, n, m = 4096, 512, 1024
+    x, w, dy, opt = setting(4, T, n, m)
+    x2, _, dy2, _ = setting(5, T, n, m)
+    w0 = w.detach().clone()
+    results = []
+    for side in (torch.cuda.current_stream(), torch.cuda.Stream()):
+        v = w0.clone().requires_grad_(True)
+        opt = d3.Dion3([v], lr=0.02, fraction=0.25)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            ys = [d3.linear_layer(t, v, into=opt) for t in (x, x2)]
+        torch.cuda.current_stream().wait_stream(side)
+        ys[0].backward(dy)
+        opt.step()
+        with torch.cuda.stream(side):
+            ys[1].backward(dy2)
+        results.append(opt.momentum(v).clone())          # (the current stream waits for the sum)
+    assert torch.equal(*results)

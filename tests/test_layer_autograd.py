@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import orthogonalizing_optimizer_amd as d3
-from orthogonalizing_optimizer_amd import layer
+from orthogonalizing_optimizer_amd import layer, optim
 
 
 @pytest.fixture(autouse=True)
@@ -98,3 +98,52 @@ def test_recomputed_layer(reentrant):
     y.backward(dy)
     assert torch.equal(opt.momentum(w), dy.t() @ x.detach())
     assert torch.equal(x.grad, dy @ w.detach())
+
+
+# ---------------------------------------------------- the order of the sums
+
+class Streams:
+    """Streams as names: the current one, those being captured, and the waits asked for."""
+
+    def __init__(self, monkeypatch):
+        self.here, self.captured, self.waits = "a", set(), []
+        monkeypatch.setattr(optim, "_stream", lambda t: self.here)
+        monkeypatch.setattr(optim, "_capturing", lambda s: s in self.captured)
+        monkeypatch.setattr(optim, "_follow",
+                            lambda here, last, t=None: self.waits.append((here, last)))
+
+    def sums(self, opt, w, here):
+        """The waits before a gradient is added to w's momentum on stream `here`."""
+        self.here = here
+        self.waits.clear()
+        opt.accumulate_grad(w)
+        return list(self.waits)
+
+
+def test_sums_on_several_streams_follow_each_other(monkeypatch):
+    w, v = (torch.randn(4, 5, requires_grad=True) for _ in range(2))
+    opt, s = d3.Dion3([w, v]), Streams(monkeypatch)
+    assert s.sums(opt, w, "a") == []                  # (its zeros were made there)
+    assert s.sums(opt, w, "b") == [("b", "a")]        # behind the first sum and the zeros
+    assert s.sums(opt, w, "b") == []
+    assert s.sums(opt, v, "c") == []                  # another buffer
+    assert s.sums(opt, w, "c") == [("c", "b")]
+    assert opt._streams == {"c"}
+    s.here = "d"
+    s.waits.clear()
+    opt.momentum(w)                                   # a reader
+    assert s.waits == [("d", "c")]
+    assert s.sums(opt, w, "a") == [("a", "d")]
+
+
+def test_captured_sums_follow_captured_ones_only(monkeypatch):
+    w = torch.randn(4, 5, requires_grad=True)
+    opt, s = d3.Dion3([w]), Streams(monkeypatch)
+    s.sums(opt, w, "a")
+    s.captured = {"c", "d"}
+    assert s.sums(opt, w, "c") == []                  # cannot wait for work outside
+    assert s.sums(opt, w, "d") == [("d", "c")]
+    s.captured = set()
+    assert s.sums(opt, w, "b") == [("b", "a")]        # nor is the capture work to wait for
+    s.captured = {"e"}
+    assert s.sums(opt, w, "e") == []                  # another capture
