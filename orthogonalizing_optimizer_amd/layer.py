@@ -541,7 +541,10 @@ def linear_layer(x, w, bias=None, act: str = "none", residual=None, checkpoint="
     ``torch.autograd.grad(y, w)`` returns the gradient.
 
     Capturing into a graph: w's momentum must exist before (RuntimeError
-    otherwise; an earlier step or ``into.momentum(w)`` makes it).  torch's own
+    otherwise; an earlier step or ``into.momentum(w)`` makes it), and the
+    optimizer does not see replays: call ``into.accumulate_grad(w)`` before
+    each, on its stream, for the sum to be ordered behind earlier uses and for
+    the next ``step()`` to step w.  torch's own
     rule for a captured backward pass holds here too: let no graph of the same
     leaves recorded outside the capture live (an earlier loss or output kept
     in a variable), since its end would have to join streams that the capture

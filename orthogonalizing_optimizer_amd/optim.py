@@ -128,9 +128,10 @@ class Dion3(_optimizer_base()):
     (``linear_layer(..., into=optimizer)``): M <- M + dW where the product is
     computed, instead of a gradient buffer that ``step()`` adds.  The sums are
     the same.  Such a parameter has no ``.grad``; ``step()`` steps the ones
-    that ``accumulate_grad`` has named since the last step.  (A captured
-    graph's replay names none: call ``accumulate_grad`` before a step outside
-    the graph.)
+    that ``accumulate_grad`` has named since the last step.  A captured
+    backward pass names none, neither when it is captured nor when it is
+    replayed: for every parameter that it sums into, call
+    ``accumulate_grad(p)`` before the replay, on the replay's stream.
     """
 
     def __init__(self, params, lr: float = 0.02, fraction=Fraction(1, 4), mu: float = 0.95,
@@ -183,29 +184,37 @@ class Dion3(_optimizer_base()):
                 self._last[p] = here
         return st["momentum"]
 
+    def _use(self, p):
+        """(p's momentum buffer, whether the use is part of a capture), the
+        current stream of its device behind the buffer's last use."""
+        self.check_parameter(p)
+        m = self._buffer(p)
+        here = _stream(m)
+        if here is None:
+            return m, False
+        captured = _capturing(here)
+        uses = self._last_captured if captured else self._last
+        last = uses.get(p)
+        if last is not None and last != here and (not captured or _capturing(last)):
+            _follow(here, last, None if captured else m)
+        uses[p] = here
+        return m, captured
+
     def momentum(self, p):
         """p's momentum buffer (fp32, p's strides; zero before the first
         gradient), to be used on the current stream of its device: that stream
         waits for the buffer's last use on another one, and the next use on
         another stream waits for this one."""
-        self.check_parameter(p)
-        m = self._buffer(p)
-        here = _stream(m)
-        if here is not None:
-            captured = _capturing(here)
-            uses = self._last_captured if captured else self._last
-            last = uses.get(p)
-            if last is not None and last != here and (not captured or _capturing(last)):
-                _follow(here, last, None if captured else m)
-            uses[p] = here
-        return m
+        return self._use(p)[0]
 
     def accumulate_grad(self, p):
         """p's momentum buffer (``momentum(p)``), for a gradient to be added to
         it on the current stream of its device: the next ``step()`` waits for
-        that stream and steps p whether or not it has a ``.grad``."""
-        m = self.momentum(p)
-        self._accumulated.add(p)
+        that stream and steps p whether or not it has a ``.grad``.  Inside a
+        capture nothing is added yet, and p is not named for the step."""
+        m, captured = self._use(p)
+        if not captured:
+            self._accumulated.add(p)
         return m
 
     def _used_on(self, params):

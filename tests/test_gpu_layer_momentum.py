@@ -97,3 +97,43 @@ def test_sum_behind_a_step_on_another_stream():
             ys[1].backward(dy2)
         results.append(opt.momentum(v).clone())          # (the current stream waits for the sum)
     assert torch.equal(*results)
+
+
+def test_steps_around_a_captured_backward_pass():
+    """Capturing steps nothing; a replay announced by accumulate_grad is stepped
+    as the eager pass is."""
+    batches = [setting(s)[::2] for s in (6, 7, 8, 9)]
+    w0 = setting(6)[1].detach()
+
+    def fresh():
+        w = w0.clone().requires_grad_(True)
+        return w, d3.Dion3([w], lr=0.02, fraction=0.25)
+
+    w, opt = fresh()
+    want = []
+    for x, dy in batches:
+        d3.linear_layer(x.detach(), w, act="silu", into=opt).backward(dy)
+        opt.step()
+        want.append([w.detach().clone(), opt.momentum(w).clone()])
+    w, opt = fresh()
+    x, dy = (t.detach().clone() for t in batches[0])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):                     # first launches
+        v, other = fresh()
+        d3.linear_layer(x, v, act="silu", into=other).backward(dy)
+    torch.cuda.current_stream().wait_stream(side)
+    opt.momentum(w)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        d3.linear_layer(x, w, act="silu", into=opt).backward(dy)
+    opt.step()
+    assert torch.equal(w.detach(), w0) and not opt.momentum(w).any()
+    for (xb, dyb), (ww, mw) in zip(batches, want):
+        x.copy_(xb.detach())
+        dy.copy_(dyb)
+        opt.accumulate_grad(w)
+        graph.replay()
+        opt.step()
+        torch.cuda.synchronize()
+        assert torch.equal(w.detach(), ww) and torch.equal(opt.momentum(w), mw)

@@ -147,3 +147,16 @@ def test_captured_sums_follow_captured_ones_only(monkeypatch):
     assert s.sums(opt, w, "b") == [("b", "a")]        # nor is the capture work to wait for
     s.captured = {"e"}
     assert s.sums(opt, w, "e") == []                  # another capture
+
+
+def test_captures_name_no_parameters(monkeypatch):
+    """Capturing a backward pass adds nothing yet, so the next step has nothing to step."""
+    w = torch.randn(4, 5, requires_grad=True)
+    opt, s = d3.Dion3([w]), Streams(monkeypatch)
+    opt.momentum(w)
+    s.captured = {"c"}
+    s.sums(opt, w, "c")
+    assert not opt._accumulated and not opt._streams
+    s.captured = set()
+    s.sums(opt, w, "a")                               # before a replay
+    assert w in opt._accumulated and opt._streams == {"a"}
