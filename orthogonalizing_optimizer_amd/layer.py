@@ -513,7 +513,10 @@ class _LinearLayer(torch.autograd.Function):
             if need_w:
                 xin = PackedF8(x, xs, *ctx.x) if ctx.x is not None else x
                 if into is not None:
-                    linear_grad_weight(dz, xin, out=into.accumulate_grad(ctx.w), accumulate=True)
+                    # (accumulate_grad, but a product that is refused names nothing)
+                    m, captured = into._use(ctx.w)
+                    linear_grad_weight(dz, xin, out=m, accumulate=True)
+                    into._name(ctx.w, captured)
                 else:
                     dw = linear_grad_weight(dz, xin).to(ctx.wtype)
             if db is not None:

@@ -213,9 +213,12 @@ class Dion3(_optimizer_base()):
         that stream and steps p whether or not it has a ``.grad``.  Inside a
         capture nothing is added yet, and p is not named for the step."""
         m, captured = self._use(p)
+        self._name(p, captured)
+        return m
+
+    def _name(self, p, captured):
         if not captured:
             self._accumulated.add(p)
-        return m
 
     def _used_on(self, params):
         return {self._last[p] for p in params if p in self._last}

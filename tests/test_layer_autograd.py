@@ -160,3 +160,20 @@ def test_captures_name_no_parameters(monkeypatch):
     s.captured = set()
     s.sums(opt, w, "a")                               # before a replay
     assert w in opt._accumulated and opt._streams == {"a"}
+
+
+def test_refused_product_names_no_parameter(monkeypatch):
+    """A weight gradient that raises (no memory, a stride past the limit) has
+    added nothing, so a step that follows all the same leaves w alone."""
+    x, w, _, dy, opt, y = setting()
+
+    def refuse(dz, x, out=None, accumulate=False):
+        raise d3.Dion3Error(-3, "dion3_linear_grad_weight")
+
+    with monkeypatch.context() as mp:
+        mp.setattr(layer, "linear_grad_weight", refuse)
+        with pytest.raises(d3.Dion3Error):
+            y.backward(dy, retain_graph=True)
+    assert untouched(opt, w)
+    y.backward(dy)
+    assert w in opt._accumulated
