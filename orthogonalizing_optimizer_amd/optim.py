@@ -220,6 +220,19 @@ class Dion3(_optimizer_base()):
         if not captured:
             self._accumulated.add(p)
 
+    def load_state_dict(self, state_dict):
+        """As in torch.  Gradients summed into a momentum since the last step
+        are part of it: they go with the momentum that is replaced, and the
+        next step does not count them.  A graph captured before sums into the
+        momentum that was replaced: capture anew."""
+        super().load_state_dict(state_dict)
+        self._accumulated.clear()
+        self._last.clear()
+        for p in self.state:
+            here = _stream(p)
+            if here is not None:         # the copies are made there
+                self._last[p] = here
+
     def _used_on(self, params):
         return {self._last[p] for p in params if p in self._last}
 

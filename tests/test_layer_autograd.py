@@ -177,3 +177,17 @@ def test_refused_product_names_no_parameter(monkeypatch):
     assert untouched(opt, w)
     y.backward(dy)
     assert w in opt._accumulated
+
+
+def test_loaded_state_holds_no_pending_gradient(monkeypatch):
+    x, w, _, dy, opt, y = setting()
+    opt.momentum(w)
+    saved = opt.state_dict()
+    saved["state"][0]["momentum"] = torch.full_like(w, 3.0)
+    y.backward(dy)
+    assert w in opt._accumulated
+    s = Streams(monkeypatch)
+    s.here = "b"
+    opt.load_state_dict(saved)
+    assert not opt._accumulated and (opt.momentum(w) == 3).all()
+    assert s.sums(opt, w, "c") == [("c", "b")]        # behind the copy
