@@ -230,7 +230,7 @@ class Dion3(_optimizer_base()):
         self._last.clear()
         for p in self.state:
             here = _stream(p)
-            if here is not None:         # the copies are made there
+            if here is not None:         # what is loaded was made there
                 self._last[p] = here
 
     def _used_on(self, params):

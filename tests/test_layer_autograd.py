@@ -2,6 +2,8 @@
 backward pass asks for, and what the optimizer's momentum receives.  The
 kernels are replaced by their formulas; what runs here is the package's own
 bookkeeping."""
+import copy
+
 import pytest
 import torch
 
@@ -181,13 +183,12 @@ def test_refused_product_names_no_parameter(monkeypatch):
 
 def test_loaded_state_holds_no_pending_gradient(monkeypatch):
     x, w, _, dy, opt, y = setting()
-    opt.momentum(w)
-    saved = opt.state_dict()
-    saved["state"][0]["momentum"] = torch.full_like(w, 3.0)
+    opt.momentum(w).fill_(3)
+    saved = copy.deepcopy(opt.state_dict())           # as read from a file
     y.backward(dy)
     assert w in opt._accumulated
     s = Streams(monkeypatch)
     s.here = "b"
     opt.load_state_dict(saved)
     assert not opt._accumulated and (opt.momentum(w) == 3).all()
-    assert s.sums(opt, w, "c") == [("c", "b")]        # behind the copy
+    assert s.sums(opt, w, "c") == [("c", "b")]        # behind the load
