@@ -28,6 +28,7 @@ import torch
 from . import _lib
 
 F8_BLOCK = 32
+_MAX_LD = 1 << 21                # the library's largest row stride
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 
@@ -405,12 +406,14 @@ def linear_grad_weight(dz, x, out=None, accumulate: bool = False,
 
 def _as_rows(t):
     """A gradient as its producer left it, or contiguous where that has no
-    rows that the library reads (an expanded gradient, a transposed one)."""
+    rows that the library reads (an expanded gradient, a transposed one, a
+    slice of very long rows): its layout is autograd's choice, not the user's."""
     try:
-        _rows(t, "gradient")
-        return t
+        if _rows(t, "gradient")[2] <= _MAX_LD:
+            return t
     except ValueError:
-        return t.contiguous()
+        pass
+    return t.contiguous()
 
 
 class _RmsNormResidual(torch.autograd.Function):

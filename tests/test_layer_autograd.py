@@ -192,3 +192,15 @@ def test_loaded_state_holds_no_pending_gradient(monkeypatch):
     opt.load_state_dict(saved)
     assert not opt._accumulated and (opt.momentum(w) == 3).all()
     assert s.sums(opt, w, "c") == [("c", "b")]        # behind the load
+
+
+def test_gradients_of_any_layout():
+    """What the library cannot read in place is copied: no rows, or rows past its stride limit."""
+    t = torch.randn(3, 8)
+    assert layer._as_rows(t) is t
+    wide = torch.empty(2, (1 << 21) + 8, dtype=torch.bfloat16)
+    for v in (wide[:, :8], t.t(), t[:1].expand(4, 8), torch.ones(()).expand(3, 8)):
+        c = layer._as_rows(v)
+        assert c.is_contiguous() and c.data_ptr() != v.data_ptr() and c.shape == v.shape
+    v = wide[:, 8:].as_strided((2, 8), (1 << 21, 1))
+    assert layer._as_rows(v) is v
