@@ -174,9 +174,12 @@ __device__ __forceinline__ float slope(int act, float z) {
       return __builtin_fmaf(z * kInvSqrt2Pi, e, c);
     }
     case DION3_ACT_GELU_TANH: {
+      // s + z s (1 - s) u'(z).  From |z| = 32 on s is 0 or 1, and so is the
+      // slope; z^2 ends there, since the cubic's overflow times 0 would be NaN
       const float s = gelu_tanh_gate(z);
-      const float du = z * __builtin_fmaf(6.0f * kGeluC * kGeluA, z * z, 2.0f * kGeluC);
-      return __builtin_fmaf(du, __builtin_fmaf(-s, s, s), s);
+      const float q = z * __builtin_fmaf(-s, s, s);
+      return __builtin_fmaf(
+          q, __builtin_fmaf(6.0f * kGeluC * kGeluA, fminf(z * z, 1024.0f), 2.0f * kGeluC), s);
     }
     case DION3_ACT_SILU: {
       const float s = sigmoid2(z * kLog2e);
