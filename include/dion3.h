@@ -341,7 +341,7 @@ DION3_API dion3_status dion3_symm_f16(const uint16_t* A, const uint16_t* B, cons
  * DION3_ERR_ARG: a null required pointer, a negative T, a side below 1, a
  * row stride below the row, an unknown type or activation, an unaligned
  * pointer.  DION3_ERR_UNSUPPORTED: T above DION3_MAX_TOKENS, a side above
- * DION3_MAX_DIM, a row stride above 2^21 or more than 2^42 elements.
+ * DION3_MAX_DIM, a row stride above 2^21 or a matrix of more than 2^38 elements.
  * DION3_ERR_WORKSPACE: as elsewhere; a call whose workspace size is 0 takes
  * ws = NULL. */
 #define DION3_F32 0

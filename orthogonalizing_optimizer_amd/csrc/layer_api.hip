@@ -25,9 +25,10 @@ bool type16(int t) { return t == DION3_BF16 || t == DION3_F16; }
 dion3_status check_sizes(long long T, long long a, long long b) {
   if (T < 0 || a < 1 || b < 1) return DION3_ERR_ARG;
   if (T > DION3_MAX_TOKENS || a > DION3_MAX_DIM || b > DION3_MAX_DIM) return DION3_ERR_UNSUPPORTED;
-  // the elementwise passes number 256 chunks of 8 a workgroup
-  const long long m = a > b ? a : b;
-  if (T > 0 && (T * ((m + 31) / 32 * 4) + 255) / 256 > 0x7fffffffLL) return DION3_ERR_UNSUPPORTED;
+  // a launch's side holds fewer than 2^32 threads, which 2^22 of the tiles that
+  // outputs of this size take (256 x 256) stay below
+  constexpr long long most = 1LL << 38;
+  if (T * a > most || T * b > most || a * b > most) return DION3_ERR_UNSUPPORTED;
   return DION3_OK;
 }
 

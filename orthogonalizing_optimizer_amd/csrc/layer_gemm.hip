@@ -729,7 +729,7 @@ hipError_t launch_join(const float* part, long long stride, int splits, long lon
 // No K at all (a gradient over no tokens): C = 0.
 template <class E, bool F32>
 __global__ __launch_bounds__(256) void k_lin_zero(long long M, unsigned nch, Finish f) {
-  const long long e = (long long)blockIdx.x * 256 + threadIdx.x;
+  const long long e = flat_base() + threadIdx.x;
   if (e >= M * nch) return;
   float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
   finish8<E, F32>(f, e / nch, (int)(e % nch) * 8, v);
@@ -743,7 +743,7 @@ __global__ __launch_bounds__(256) void k_lin_zero(long long M, unsigned nch, Fin
 __global__ __launch_bounds__(256) void k_lin_copy(const unsigned short* __restrict__ src,
                                                   long long ld, long long rows, int cols,
                                                   unsigned nch, unsigned short* __restrict__ dst) {
-  const long long base = (long long)blockIdx.x * 256;
+  const long long base = flat_base();
   if (base + threadIdx.x >= rows * nch) return;
   const long long row0 = base / nch;
   const unsigned c0 = (unsigned)(base - row0 * nch) + threadIdx.x;
@@ -1056,7 +1056,8 @@ hipError_t launch_cfg(LinP p, int tile, bool rag, hipStream_t s) {
   p.tilesM = (int)((p.M + t.bm - 1) / t.bm);
   p.tilesN = (p.N + t.bn - 1) / t.bn;
   p.total = (long long)p.tilesM * p.tilesN * p.splits;
-  if (p.total > 0x7fffffffLL) return hipErrorInvalidValue;
+  // (fewer than 2^32 threads; no size within the library's limits gets here)
+  if (p.total >= 1LL << 23) return hipErrorInvalidValue;
   if (rag) {
     switch (tile) {
       case 0: return launch_tiles<E, CfgL, KA, KB, F32, true>(p, s);
@@ -1083,8 +1084,7 @@ hipError_t launch_lin_t(const LinDesc& d, void* ws, hipStream_t s) {
   if (d.M == 0) return hipSuccess;
   if (d.K == 0) {
     if (d.accumulate) return hipSuccess;
-    const dim3 grid((unsigned)((d.M * nch + 255) / 256));
-    hipLaunchKernelGGL((k_lin_zero<E, true>), grid, dim3(256), 0, s, d.M, nch, f);
+    hipLaunchKernelGGL((k_lin_zero<E, true>), flat_grid(d.M * nch), dim3(256), 0, s, d.M, nch, f);
     return hipGetLastError();
   }
   const double flops = 2.0 * (double)d.M * d.N * d.K;
@@ -1104,7 +1104,7 @@ hipError_t launch_lin_t(const LinDesc& d, void* ws, hipStream_t s) {
     const unsigned n = (unsigned)(up8(cols) / 8);
     unsigned short* dst = (unsigned short*)((char*)ws + o);
     TraceScope ts("linear_copy", 0.0, 4.0 * (double)rows * cols, s);
-    hipLaunchKernelGGL(k_lin_copy, dim3((unsigned)((rows * n + 255) / 256)), dim3(256), 0, s,
+    hipLaunchKernelGGL(k_lin_copy, flat_grid(rows * n), dim3(256), 0, s,
                        (const unsigned short*)src, ld, rows, (int)cols, n, dst);
     return hipGetLastError();
   };

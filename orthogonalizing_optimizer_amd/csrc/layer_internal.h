@@ -287,6 +287,18 @@ __device__ __forceinline__ f32x2 f8_decode2(float, unsigned w, float s) {
 
 // ------------------------------------------------------------------ launches
 
+// One workgroup of 256 threads for each 256 of n items numbered through.  A
+// side of a grid holds fewer than 2^32 threads (HIP's limit), so workgroups
+// past 2^23 go to further rows of the grid.
+inline dim3 flat_grid(long long n) {
+  const long long groups = (n + 255) / 256, row = 1LL << 23;
+  return groups <= row ? dim3((unsigned)groups)
+                       : dim3((unsigned)row, (unsigned)((groups + row - 1) / row));
+}
+__device__ __forceinline__ long long flat_base() {       // the workgroup's first item
+  return ((long long)blockIdx.y * gridDim.x + blockIdx.x) * 256;
+}
+
 // A scratch layout: partial column sums, one row of m floats per unit.
 struct RowsPlan {
   int units;            // partial rows

@@ -474,7 +474,7 @@ __global__ __launch_bounds__(256) void k_pack(const E* __restrict__ x, long long
                                               unsigned char* __restrict__ q,
                                               unsigned char* __restrict__ sc, long long chunks,
                                               int m, unsigned nch) {
-  const long long base = (long long)blockIdx.x * 256, at = base + threadIdx.x;
+  const long long base = flat_base(), at = base + threadIdx.x;
   const long long row0 = base / nch;
   const unsigned c0 = (unsigned)(base - row0 * nch) + threadIdx.x, dr = c0 / nch;
   float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
@@ -506,7 +506,7 @@ __global__ __launch_bounds__(256) void k_unpack(const unsigned char* __restrict_
                                                 const unsigned char* __restrict__ sc,
                                                 E* __restrict__ y, long long ldy,
                                                 long long chunks, int m, unsigned nch) {
-  const long long base = (long long)blockIdx.x * 256;
+  const long long base = flat_base();
   if (base + threadIdx.x >= chunks) return;
   const long long row0 = base / nch;
   const unsigned c0 = (unsigned)(base - row0 * nch) + threadIdx.x;
@@ -673,7 +673,7 @@ hipError_t launch_pack_f8(const void* x, long long ldx, unsigned char* q, unsign
                           long long T, int m, int dtype, hipStream_t s) {
   const unsigned nch = (unsigned)(f8_cols(m) / kChunk);
   const long long chunks = T * nch;
-  const dim3 grid((unsigned)((chunks + 255) / 256));
+  const dim3 grid = flat_grid(chunks);
   TraceScope ts("pack_f8", 0.0, (double)T * m * ((dtype == DION3_F32 ? 4.0 : 2.0) + 1.0 + 1.0 / kF8Block), s);
   if (dtype == DION3_BF16)
     hipLaunchKernelGGL((k_pack<bf16>), grid, dim3(256), 0, s, (const bf16*)x, ldx, q, sc, chunks, m, nch);
@@ -688,7 +688,7 @@ hipError_t launch_unpack_f8(const unsigned char* q, const unsigned char* sc, voi
                             long long T, int m, int dtype, hipStream_t s) {
   const unsigned nch = (unsigned)(f8_cols(m) / kChunk);
   const long long chunks = T * nch;
-  const dim3 grid((unsigned)((chunks + 255) / 256));
+  const dim3 grid = flat_grid(chunks);
   TraceScope ts("unpack_f8", 0.0, (double)T * m * ((dtype == DION3_F32 ? 4.0 : 2.0) + 1.0 + 1.0 / kF8Block), s);
   if (dtype == DION3_BF16)
     hipLaunchKernelGGL((k_unpack<bf16>), grid, dim3(256), 0, s, q, sc, (bf16*)y, ldy, chunks, m, nch);

@@ -176,3 +176,15 @@ def test_binding_refuses_host_tensors():
               lambda: d3.PackedF8(x.to(torch.float8_e4m3fn), torch.zeros(4, 1, dtype=torch.uint8), 8)):
         with pytest.raises(TypeError):
             f()
+
+
+def test_most_elements():
+    """A matrix of up to 2^38 elements passes the checks, a larger one does not."""
+    t, m = 1 << 24, 1 << 14
+    for fn in ("dion3_add_rms_norm_grad_workspace_size", "dion3_act_grad_workspace_size"):
+        assert size(fn, t, m)[0] == OK
+        assert size(fn, t, m + 1) == (ERR_UNSUP, 12345)
+    for fn in ("dion3_linear_workspace_size", "dion3_linear_grad_input_workspace_size"):
+        assert size(fn, P, m, P, m, t, 64 if "input" not in fn else m, m)[0] == OK
+        for T_, n_, m_ in ((t, m + 1, 64), (t, 64, m + 1), (1, 1 << 20, (1 << 18) + 1)):
+            assert size(fn, P, 1 << 20, P, 1 << 20, T_, n_, m_) == (ERR_UNSUP, 12345)
