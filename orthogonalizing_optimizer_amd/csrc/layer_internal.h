@@ -91,8 +91,8 @@ __device__ __forceinline__ void store8(E* __restrict__ row, int c, int m, const 
 // -------------------------------------------------------------- activations
 //
 // An element of an activation costs as much VALU time as it does HBM time
-// (without packed fp32 the chip does about 39 T operations a second, one per
-// 150 bytes moved at 5.8 TB/s), so the forms below are counted in
+// (without packed fp32 the chip does about 39 T operations a second, 7 for
+// each byte moved at 5.8 TB/s), so the forms below are counted in
 // instructions: the hardware's exponential and reciprocal (each within one
 // step of fp32, for 16-bit outputs), constants folded into the exponent.
 
