@@ -68,7 +68,6 @@ struct NormP {
   float eps;
 };
 
-template <class E>
 __device__ __forceinline__ float norm_rstd(float sumsq, int m, float eps) {
   return 1.0f / sqrtf(sumsq / (float)m + eps);
 }
@@ -122,7 +121,7 @@ __global__ __launch_bounds__(WIDE ? 1024 : 256) void k_add_norm(NormP p) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(v[i][e], v[i][e], ss);
     ss = row_sum<WIDE>(ss, sh, turn++);
-    const float rs = norm_rstd<E>(ss, m, p.eps);
+    const float rs = norm_rstd(ss, m, p.eps);
     if (t == 0 && p.rstd) p.rstd[row] = rs;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
@@ -173,7 +172,7 @@ __global__ __launch_bounds__(1024) void k_add_norm_long(NormP p) {
       for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(v[e], v[e], ss);
     }
     ss = row_sum<true>(ss, sh, turn++);
-    const float rs = norm_rstd<E>(ss, m, p.eps);
+    const float rs = norm_rstd(ss, m, p.eps);
     if (t == 0 && p.rstd) p.rstd[row] = rs;
     // (each thread reads back only what it wrote itself)
     const E* hr = p.r ? (const E*)p.h + row * p.ldh : xr;
@@ -239,7 +238,7 @@ struct NormGradP {
   float* part;             // null: dw not wanted
   float* c;                // the long form's row means
   long long lddy, ldh, lddh, lddx, T;
-  int m, units;
+  int m;
   long long rows_per_unit; // the long form's row blocks
 };
 
@@ -649,7 +648,7 @@ hipError_t launch_add_rms_norm_grad(const NormGradArgs& a, void* ws, hipStream_t
     plan = norm_grad_plan(a.T, a.m);
     NormGradP p = {a.dy, a.h, a.dh, a.w, a.rstd, a.dx, a.dw ? (float*)ws : nullptr,
                    (float*)ws + (size_t)plan.units * a.m,
-                   a.lddy, a.ldh, a.lddh, a.lddx, a.T, a.m, plan.units, 0};
+                   a.lddy, a.ldh, a.lddh, a.lddx, a.T, a.m, 0};
     TraceScope ts("rms_norm_grad", 0.0, (double)a.T * a.m * (4.0 + (a.dx ? 2.0 : 0.0) +
                                                              (a.dx && a.dh ? 2.0 : 0.0)), s);
     if (a.dtype == DION3_BF16)

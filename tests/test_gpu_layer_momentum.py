@@ -137,3 +137,19 @@ def test_steps_around_a_captured_backward_pass():
         opt.step()
         torch.cuda.synchronize()
         assert torch.equal(w.detach(), ww) and torch.equal(opt.momentum(w), mw)
+
+
+@pytest.mark.parametrize("lead", [(0,), (2, 0)])
+def test_no_tokens(lead):
+    """A batch without tokens: zero gradients, nothing added to the momentum."""
+    x, w, _, opt = setting(10)
+    x = x.detach()[:0].view(*lead, 264).requires_grad_(True)
+    b = torch.zeros(136, device="cuda", requires_grad=True)
+    n1 = torch.ones(264, device="cuda", requires_grad=True)
+    for into in (None, opt):
+        y, h, packed = d3.rms_norm_residual(x, n1, residual=x, pack=True)
+        out = d3.linear_layer(y, w, b, act="silu", checkpoint=packed, into=into)
+        assert out.shape == (*lead, 136)
+        out.sum().backward()
+        assert x.grad.shape == x.shape and not b.grad.any() and not n1.grad.any()
+    assert not w.grad.any() and not opt.momentum(w).any()
