@@ -94,6 +94,8 @@ def _stream(t):
 def _capturing(stream) -> bool:
     """Whether a graph is being captured from this stream."""
     import torch
+    if stream == torch.cuda.current_stream():
+        return torch.cuda.is_current_stream_capturing()
     with torch.cuda.stream(stream):
         return torch.cuda.is_current_stream_capturing()
 
