@@ -330,8 +330,8 @@ DION3_API dion3_status dion3_symm_f16(const uint16_t* A, const uint16_t* B, cons
  * 16-bit data (`dtype`: DION3_BF16 or DION3_F16) is passed as void*; every
  * pointer is aligned to its element size (8-bit data: 16 bytes).  Any side
  * from 1 and any row stride that holds the row is taken; rows that are
- * 16-byte aligned with sides that are multiples of 8 are fastest (the
- * products read others up to 20 % more slowly, or copy them into the
+ * 16-byte aligned with sides that are multiples of 8 are fastest (over others
+ * the products take a fifth to three fifths longer, or copy them into the
  * workspace first, whichever is expected to take less).  T = 0 is
  * valid: nothing is written, except that gradients over no tokens are zero.
  * Statistics, products and column sums are held in fp32 and added in an order
@@ -372,7 +372,9 @@ DION3_API dion3_status dion3_symm_f16(const uint16_t* A, const uint16_t* B, cons
  * rounded h.  R and H are both given, or both NULL (then h = X); H may be X
  * or R.  w has m entries of wtype (DION3_F32 or dtype).  Outputs: Y and / or
  * Q and S (the packed form of Y's rounded values), and rstd (T floats)
- * unless NULL. */
+ * unless NULL.  The squares are summed in fp32 as they are: a row whose sum
+ * passes its largest value (one of |h| = 1.9e19 does) gets rstd = 0, and h
+ * below 1e-23 count as zeros. */
 DION3_API dion3_status dion3_add_rms_norm(const void* X, int64_t ldx, const void* R, int64_t ldr,
                                           const void* w, int32_t wtype, void* H, int64_t ldh,
                                           void* Y, int64_t ldy, uint8_t* Q, uint8_t* S, float* rstd,
@@ -413,8 +415,9 @@ DION3_API dion3_status dion3_linear(const void* X, int64_t ldx, const void* W, i
 
 /* dZ = dY act'(z) and db = sum over tokens of dY act'(z) (fp32, n entries,
  * summed before dZ's rounding).  z comes from Z, or from its 8-bit form ZQ,
- * ZS; neither is read for DION3_ACT_NONE.  dZ and db may each be NULL, not
- * both; dZ may be dY or Z.  The workspace is used for db only. */
+ * ZS (whose values stand for z, zeros too: a z below 4.4e-6 of its block's
+ * largest may be one, where the slope of relu is 0); neither is read for
+ * DION3_ACT_NONE.  dZ and db may each be NULL, not both; dZ may be dY or Z.  The workspace is used for db only. */
 DION3_API dion3_status dion3_act_grad_workspace_size(int64_t T, int64_t n, size_t* bytes);
 DION3_API dion3_status dion3_act_grad(const void* dY, int64_t lddy, const void* Z, int64_t ldz,
                                       const uint8_t* ZQ, const uint8_t* ZS, void* dZ, int64_t lddz,

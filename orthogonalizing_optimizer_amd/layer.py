@@ -537,6 +537,9 @@ def linear_layer(x, w, bias=None, act: str = "none", residual=None, checkpoint="
     bits as another layer or norm already keeps it (the preactivation is
     packed too), "full" keeps both as they are.  The forward result and the
     gradient of x are the same bits with every choice when act is "none".
+    In 8 bits a value is off by up to 2^-4 of itself, and one below 4.4e-6 of
+    the largest of its 32 columns may be 0: with "relu" such a preactivation
+    passes no gradient.
 
     ``into``: a ``Dion3`` that steps w.  The weight gradient is then summed
     straight into w's momentum there, in the product's own epilogue; w gets no
@@ -544,7 +547,12 @@ def linear_layer(x, w, bias=None, act: str = "none", residual=None, checkpoint="
     be taken back by ``zero_grad()``.  This happens in the passes in which w's
     ``.grad`` would grow, and in no other: ``backward(inputs=[x])`` and
     ``torch.autograd.grad(y, x)`` leave the momentum alone, and
-    ``torch.autograd.grad(y, w)`` returns the gradient.
+    ``torch.autograd.grad(y, w)`` returns the gradient.  What works on
+    ``.grad`` does not see the sum: hooks of w get None and its post-accumulate
+    hooks no ``.grad``; gradient clipping and reduction across processes pass
+    it by; a scaled loss (fp16) enters the momentum scaled, cannot be unscaled
+    there, and one overflow leaves infinities or NaN in it.  Train without
+    ``into`` where you need any of these.
 
     Capturing into a graph: w's momentum must exist before (RuntimeError
     otherwise; an earlier step or ``into.momentum(w)`` makes it), and the

@@ -35,6 +35,16 @@ def test_activations_of_large_values(act, dtype):
         assert float(db) == 0.75 * float(on.float().sum())
 
 
+@pytest.mark.parametrize("m", [40, 4096, 40000])
+def test_norm_at_the_ends_of_its_sums(m):
+    """Sums of squares past fp32's range give rstd = 0, below it none."""
+    x = torch.ones(3, m, dtype=BF, device="cuda")
+    x[0, 5], x[1] = 1.9e19, 1e-24
+    y, _, rstd, _ = d3.add_rms_norm(x, torch.ones(m, device="cuda"), eps=1e-6)
+    assert float(rstd[0]) == 0 and not y[0].any()
+    assert abs(float(rstd[1]) - 1e3) <= 1e3 * 2.0 ** -22 and (y[2] == 1).all()
+
+
 def room(nbytes):
     """Skip unless the GPU has this much free memory (and hand back torch's own)."""
     torch.cuda.empty_cache()
