@@ -100,12 +100,14 @@ def _capturing(stream) -> bool:
         return torch.cuda.is_current_stream_capturing()
 
 
-def _follow(here, last, t=None):
-    """Stream ``here`` waits for what ``last`` holds so far; t's memory, made on
-    another stream, is not given away while ``here`` may use it."""
+def _follow(here, last):
+    """Stream ``here`` waits for what ``last`` holds so far."""
     here.wait_stream(last)
-    if t is not None:
-        t.record_stream(here)
+
+
+def _hold(t, stream):
+    """t's memory, made on another stream, is not given away while ``stream`` may use it."""
+    t.record_stream(stream)
 
 
 class Dion3(_optimizer_base()):
@@ -198,7 +200,9 @@ class Dion3(_optimizer_base()):
         uses = self._last_captured if captured else self._last
         last = uses.get(p)
         if last is not None and last != here and (not captured or _capturing(last)):
-            _follow(here, last, None if captured else m)
+            _follow(here, last)
+            if not captured:
+                _hold(m, here)
         uses[p] = here
         return m, captured
 
@@ -230,18 +234,16 @@ class Dion3(_optimizer_base()):
         super().load_state_dict(state_dict)
         self._accumulated.clear()
         self._last.clear()
-        for p in self.state:
-            here = _stream(p)
-            if here is not None:         # what is loaded was made there
-                self._last[p] = here
-
-    def _used_on(self, params):
-        return {self._last[p] for p in params if p in self._last}
+        for group in self.param_groups:
+            for p in group["params"]:
+                here = _stream(p)
+                if p in self.state and here is not None:     # what is loaded was made there
+                    self._last[p] = here
 
     @property
     def _streams(self):
         """Where the gradients that the next ``step()`` takes were added last."""
-        return self._used_on(self._accumulated)
+        return {self._last[p] for p in self._accumulated if p in self._last}
 
     def step(self, closure=None):
         import torch
@@ -253,10 +255,17 @@ class Dion3(_optimizer_base()):
         # that stream with the caller's only for gradients that it keeps itself
         params = [p for group in self.param_groups for p in group["params"]
                   if p.grad is not None or p in self._accumulated]
-        for stream in self._used_on(params):
-            here = torch.cuda.current_stream(stream.device)
-            if stream != here:
-                _follow(here, stream)
+        here, followed = {}, set()
+        for p in params:
+            if p.device not in here:
+                here[p.device] = _stream(p)
+            stream, last = here[p.device], self._last.get(p)
+            if last is None or last == stream:
+                continue
+            if last not in followed:
+                followed.add(last)
+                _follow(stream, last)
+            _hold(self.state[p]["momentum"], stream)
         with torch.no_grad():
             for group in self.param_groups:
                 f = float(group["fraction"])
@@ -290,8 +299,7 @@ class Dion3(_optimizer_base()):
                         _lib.step_groups(grps[i:i + _lib.MAX_GROUPS], group["mu"], self.cfg,
                                          norm=norm, ws=ws)
         for p in params:
-            here = _stream(p)
-            if here is not None:
-                self._last[p] = here
+            if here[p.device] is not None:
+                self._last[p] = here[p.device]
         self._accumulated.clear()
         return loss

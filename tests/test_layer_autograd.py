@@ -111,8 +111,9 @@ class Streams:
         self.here, self.captured, self.waits = "a", set(), []
         monkeypatch.setattr(optim, "_stream", lambda t: self.here)
         monkeypatch.setattr(optim, "_capturing", lambda s: s in self.captured)
-        monkeypatch.setattr(optim, "_follow",
-                            lambda here, last, t=None: self.waits.append((here, last)))
+        self.held = []
+        monkeypatch.setattr(optim, "_follow", lambda here, last: self.waits.append((here, last)))
+        monkeypatch.setattr(optim, "_hold", lambda t, stream: self.held.append((t, stream)))
 
     def sums(self, opt, w, here):
         """The waits before a gradient is added to w's momentum on stream `here`."""
@@ -204,3 +205,24 @@ def test_gradients_of_any_layout():
         assert c.is_contiguous() and c.data_ptr() != v.data_ptr() and c.shape == v.shape
     v = wide[:, 8:].as_strided((2, 8), (1 << 21, 1))
     assert layer._as_rows(v) is v
+
+
+def test_step_follows_every_momentum_it_takes(monkeypatch):
+    """One wait a stream; each buffer last used elsewhere is held for the step's stream."""
+    ws = [torch.randn(4, 5, requires_grad=True) for _ in range(4)]
+    opt, s = d3.Dion3(ws), Streams(monkeypatch)
+    monkeypatch.setattr(optim._lib, "Group", lambda *a, **k: None)
+    monkeypatch.setattr(optim._lib, "step_groups", lambda *a, **k: None)
+    s.sums(opt, ws[0], "b")
+    s.sums(opt, ws[1], "b")
+    s.sums(opt, ws[2], "c")
+    ws[3].grad = torch.ones_like(ws[3])
+    s.here = "a"
+    s.waits.clear()
+    s.held.clear()
+    opt.step()
+    assert s.waits == [("a", "b"), ("a", "c")]
+    assert [(t is opt.state[w]["momentum"], at) for (t, at), w in zip(s.held, ws)] == [(True, "a")] * 3
+    assert not opt._accumulated and not opt._streams
+    assert s.sums(opt, ws[0], "b") == [("b", "a")]    # behind the step
+    assert s.sums(opt, ws[3], "b") == [("b", "a")]
