@@ -88,16 +88,21 @@ def test_more_elements_than_a_grid_side_holds():
 # ------------------------------------------------------- outputs in place
 
 def call(name, *args, size=None):
-    """A C call on torch's current stream; size: its workspace call's arguments."""
+    """A C call on torch's current stream; size: its workspace call's
+    arguments.  The workspace is exactly as large as asked for, and what lies
+    behind it stays as it was."""
     lib = d3.lib()
-    tail = []
+    tail, ws = [], None
     if size is not None:
         nb = ctypes.c_size_t()
         assert getattr(lib, name + "_workspace_size")(*size, ctypes.byref(nb)) == 0
-        ws = torch.empty(nb.value + 256, dtype=torch.uint8, device="cuda")
-        tail = [ws.data_ptr() + (-ws.data_ptr()) % 256, nb.value]
+        ws = torch.full((nb.value + 256 + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+        at = -ws.data_ptr() % 256
+        tail = [ws.data_ptr() + at, nb.value]
     args = [a.data_ptr() if isinstance(a, torch.Tensor) else a for a in args]
     assert getattr(lib, name)(*args, *tail, torch.cuda.current_stream().cuda_stream) == 0
+    if ws is not None:
+        assert (ws[:at] == 0xA5).all() and (ws[at + nb.value:] == 0xA5).all()
 
 
 def normal(g, *shape, std=1.0, dtype=BF):
@@ -177,3 +182,78 @@ def test_products_over_their_addends(T, n, m, dtype):
     call("dion3_linear_grad_input", dz, n, w, m, rx, m, rx, m, T, n, m, CODE[dtype],
          size=(dz.data_ptr(), n, w.data_ptr(), m, T, n, m))
     assert torch.equal(rx, dx)
+
+
+# ---------------------------------- what lies between and behind the outputs
+
+class Out:
+    """A [T, m] output at an odd place in a buffer of sevens."""
+
+    def __init__(self, T, m, dtype, ld=None, off=0):
+        self.ld = ld or m
+        self.buf = torch.full((T * self.ld + off + 512,), 7, dtype=dtype, device="cuda")
+        self.t = self.buf.as_strided((T, m), (self.ld, 1), off)
+        self.ptr = self.t.data_ptr()
+
+    def take(self):
+        """Its values; all around them still sevens."""
+        v = self.t.clone()
+        self.t.fill_(7)
+        assert (self.buf == 7).all()
+        return v
+
+
+@pytest.mark.parametrize("pad,off", [(0, 0), (3, 1), (16, 8)])
+@pytest.mark.parametrize("T,m", [(1, 1), (3, 20), (70, 515), (9, 2049), (3, 16390), (3, 33003)])
+def test_row_operators_write_their_outputs_only(T, m, pad, off):
+    g = torch.Generator().manual_seed(T * m + pad)
+    x, r, dy = (normal(g, T, m) for _ in range(3))
+    w = 1 + normal(g, m, std=0.1, dtype=torch.float32)
+    y, h, rstd, p = d3.add_rms_norm(x, w, residual=r, pack=True)
+    mp, ld = p.q.shape[1], m + pad
+    Y, H = Out(T, m, BF, ld, off), Out(T, m, BF, ld, off)
+    Q, S, RS = Out(T, mp, torch.uint8, off=16), Out(T, mp // 32, torch.uint8, off=off), Out(T, 1, torch.float32, off=off)
+    call("dion3_add_rms_norm", x, m, r, m, w, 0, H.ptr, ld, Y.ptr, ld, Q.ptr, S.ptr, RS.ptr, T, m,
+         1e-6, 1)
+    assert torch.equal(Y.take(), y) and torch.equal(H.take(), h)
+    assert torch.equal(Q.take(), p.q.view(torch.uint8)) and torch.equal(S.take(), p.scale)
+    assert torch.equal(RS.take()[:, 0], rstd)
+    call("dion3_pack_f8", y, m, Q.ptr, S.ptr, T, m, 1)
+    assert torch.equal(Q.take(), p.q.view(torch.uint8)) and torch.equal(S.take(), p.scale)
+    for t, code in ((BF, 1), (FP, 2), (torch.float32, 0)):
+        V = Out(T, m, t, ld, off)
+        call("dion3_unpack_f8", p.q, p.scale, V.ptr, ld, T, m, code)
+        assert torch.equal(V.take(), d3.unpack_f8(p, t))
+    dx, dw = d3.add_rms_norm_grad(dy, h, rstd, w, dh=r)
+    DX, DW = Out(T, m, BF, ld, off), Out(1, m, torch.float32, off=off)
+    call("dion3_add_rms_norm_grad", dy, m, h, m, rstd, w, 0, r, m, DX.ptr, ld, DW.ptr, T, m, 1,
+         size=(T, m))
+    assert torch.equal(DX.take(), dx) and torch.equal(DW.take()[0], dw)
+    dz, db = d3.act_grad(dy, x, "silu", bias=True)
+    call("dion3_act_grad", dy, m, x, m, None, None, DX.ptr, ld, DW.ptr, T, m, 4, 1, size=(T, m))
+    assert torch.equal(DX.take(), dz) and torch.equal(DW.take()[0], db)
+
+
+@pytest.mark.parametrize("pad,off", [(0, 0), (3, 1), (16, 8)])
+@pytest.mark.parametrize("T,n,m", [(1, 1, 1), (1, 4099, 515), (9, 100, 64), (16, 24, 520), (5, 7, 9),
+                                   (70, 515, 77), (300, 260, 2100), (2100, 4101, 72),
+                                   (4100, 2120, 40), (5000, 100, 60), (0, 33, 20)])
+def test_products_write_their_outputs_only(T, n, m, pad, off):
+    g = torch.Generator().manual_seed(T + n + m + pad)
+    x, w, dz, r = normal(g, T, m), normal(g, n, m), normal(g, T, n), normal(g, T, n)
+    y, z = d3.linear(x, w, act="silu", residual=r, return_preact=True)
+    Y, Z = Out(T, n, BF, n + pad, off), Out(T, n, BF, n + pad, off)
+    call("dion3_linear", x, m, w, m, None, 0, r, n, Y.ptr, n + pad, Z.ptr, n + pad, T, n, m, 4, 1,
+         size=(x.data_ptr(), m, w.data_ptr(), m, T, n, m))
+    assert torch.equal(Y.take(), y) and torch.equal(Z.take(), z)
+    DX = Out(T, m, BF, m + pad, off)
+    call("dion3_linear_grad_input", dz, n, w, m, None, 0, DX.ptr, m + pad, T, n, m, 1,
+         size=(dz.data_ptr(), n, w.data_ptr(), m, T, n, m))
+    assert torch.equal(DX.take(), d3.linear_grad_input(dz, w))
+    p = d3.pack_f8(x)
+    for a, s in ((x, None), (p.q, p.scale)):
+        G = Out(n, m, torch.float32, m + pad, off)
+        sp = None if s is None else s.data_ptr()
+        call("dion3_linear_grad_weight", dz, n, a, m, sp, G.ptr, m + pad, 0, T, n, m, 1,
+             size=(dz.data_ptr(), n, a.data_ptr(), m, sp, T, n, m))
+        assert torch.equal(G.take(), d3.linear_grad_weight(dz, x if s is None else p))
