@@ -417,7 +417,8 @@ DION3_API dion3_status dion3_linear(const void* X, int64_t ldx, const void* W, i
  * summed before dZ's rounding).  z comes from Z, or from its 8-bit form ZQ,
  * ZS (whose values stand for z, zeros too: a z below 4.4e-6 of its block's
  * largest may be one, where the slope of relu is 0); neither is read for
- * DION3_ACT_NONE.  dZ and db may each be NULL, not both; dZ may be dY or Z.  The workspace is used for db only. */
+ * DION3_ACT_NONE.  dZ and db may each be NULL, not both; dZ may be dY or Z.
+ * The workspace is used for db only. */
 DION3_API dion3_status dion3_act_grad_workspace_size(int64_t T, int64_t n, size_t* bytes);
 DION3_API dion3_status dion3_act_grad(const void* dY, int64_t lddy, const void* Z, int64_t ldz,
                                       const uint8_t* ZQ, const uint8_t* ZS, void* dZ, int64_t lddz,

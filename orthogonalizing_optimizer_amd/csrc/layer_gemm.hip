@@ -207,10 +207,10 @@ enum Kind { kRowsK = 0, kColsK = 1, kColsF8 = 2 };
 // 225 and 220; 1000 x 2049 x 2047 27.0, 27.7 and 26.4, 1000 x 2048 x 2048
 // 19.9, 22.5 and 16.6; 517 x 1000 x 515 7.0, 10.7 and 7.9, 520 x 1000 x 520
 // 5.1, 6.8 and 5.5.  Against a copy of the operand and its launch (another
-// card, ragged and copied first): forward 517 x 1000 x 515 7.3 us against 11.8, 1000 x 2049 x 2047 29.3
-// against 36.5, 8192 x 4095 x 4097 250 against 289; input gradient 10.7 against
-// 10.6, 30 against 37.5, 268 against 311; weight gradient 8.0 against 8.4,
-// 27.8 against 37.5, 283 against 378.
+// card, ragged and copied first): forward 517 x 1000 x 515 7.3 us against
+// 11.8, 1000 x 2049 x 2047 29.3 against 36.5, 8192 x 4095 x 4097 250 against
+// 289; input gradient 10.7 against 10.6, 30 against 37.5, 268 against 311;
+// weight gradient 8.0 against 8.4, 27.8 against 37.5, 283 against 378.
 template <class E, int R, int NT, int KIND, int PF, bool RAG>
 struct Operand {
   static constexpr int RS = R + kPadN;                                 // [K][R] LDS row
@@ -931,9 +931,8 @@ constexpr Tile kTiles[kNTiles] = {{256, 256, 1.05, 1.53, 11.0},
                                   {128, 128, 0.45, 0.53, 4.5},
                                   {64, 64, 0.20, 0.24, 3.0}};
 constexpr int kCus = 256;
-// A step of the ragged form against an aligned one, as the plan counts it (the
-// whole products differ by more, see Operand: their ends, and one shape for
-// another).  Three shapes have it: the
+// A step of the ragged form against an aligned one, as the plan counts it
+// (whole products differ by more, see Operand).  Three shapes have it: the
 // large tile, 128 x 256 and 64 x 64, between which the model finds a time
 // within 10 % of the best of the five on the shapes named at Operand.
 constexpr double kRag = 1.15;

@@ -237,7 +237,8 @@ class Dion3(_optimizer_base()):
         for group in self.param_groups:
             for p in group["params"]:
                 here = _stream(p)
-                if p in self.state and here is not None:     # what is loaded was made there
+                # (what is loaded was made there)
+                if here is not None and "momentum" in self.state.get(p, ()):
                     self._last[p] = here
 
     @property

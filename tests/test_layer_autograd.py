@@ -226,3 +226,14 @@ def test_step_follows_every_momentum_it_takes(monkeypatch):
     assert not opt._accumulated and not opt._streams
     assert s.sums(opt, ws[0], "b") == [("b", "a")]    # behind the step
     assert s.sums(opt, ws[3], "b") == [("b", "a")]
+
+
+def test_hooks_see_no_gradient():
+    """A summed gradient passes by w's hooks, which run with None and without a .grad."""
+    x, w, _, dy, opt, y = setting()
+    seen = []
+    w.register_hook(lambda g: seen.append(("hook", g)))
+    w.register_post_accumulate_grad_hook(lambda p: seen.append(("post", p.grad)))
+    y.backward(dy)
+    assert seen == [("hook", None), ("post", None)]
+    assert torch.equal(opt.momentum(w), dy.t() @ x.detach())
