@@ -450,6 +450,49 @@ DION3_API dion3_status dion3_linear_grad_weight(const void* dZ, int64_t lddz, co
                                                 int32_t dtype, void* ws, size_t ws_bytes,
                                                 void* stream);
 
+/* ---------------------------------------------------------------------------
+ * The global norm of many gradients, and their clipping.
+ *
+ * A gradient is rows x cols elements of dtype (DION3_F32, _BF16 or _F16) with
+ * row stride ldg; M, where given, is an fp32 buffer of the same shape with row
+ * stride ldm.  (Tensors of any shape without gaps are one row.)  A gradient
+ * without elements may have null pointers.  What a call writes must not
+ * overlap anything else in the list.
+ * DION3_ERR_ARG: a negative count or size, a null or unaligned pointer, a row
+ * stride below the row, an unknown type, scale not finite and positive,
+ * max_norm negative or NaN.  DION3_ERR_UNSUPPORTED: more than 2^20 gradients
+ * or 2^38 elements. */
+typedef struct {
+  void* G;
+  float* M;
+  int64_t rows, cols;
+  int64_t ldg, ldm;
+  int32_t dtype;
+} dion3_grad;
+
+/* sizeof(dion3_grad) as this library was built (for bindings). */
+DION3_API size_t dion3_grad_size(void);
+
+/* norm = scale sqrt(sum over all gradients of g^2) (one float, rounded once)
+ * and, unless NULL, norms[i] = the same of gradient i alone.  Squares are
+ * summed in 64 bits in an order fixed by the sizes: no finite gradient
+ * overflows the sum, and none is too small for it.  `grads` is a host array;
+ * it is read during the call only.  The workspace serves both calls. */
+DION3_API dion3_status dion3_grad_norm_workspace_size(const dion3_grad* grads, int32_t count,
+                                                      size_t* bytes);
+DION3_API dion3_status dion3_grad_norm(const dion3_grad* grads, int32_t count, float scale,
+                                       float* norm, float* norms, void* ws, size_t ws_bytes,
+                                       void* stream);
+
+/* With that norm and c = 1 where norm <= max_norm, else max_norm / norm (in 64
+ * bits, like the products below, which are rounded to fp32 once): each
+ * gradient with an M is summed into it, M <- M + c scale G (G is not written),
+ * each other one is scaled in place, G <- c scale G rounded to its type.  An infinite norm gives
+ * c = 0, a NaN c = NaN.  norm: one float, or NULL.  max_norm may be infinite. */
+DION3_API dion3_status dion3_clip_grad_norm(const dion3_grad* grads, int32_t count, float max_norm,
+                                            float scale, float* norm, void* ws, size_t ws_bytes,
+                                            void* stream);
+
 /* Kernel timing trace, for benchmarks.  dion3_trace_enable(capacity > 0)
  * creates 2 * capacity HIP events (no device memory) and starts recording:
  * each kernel the library then launches is timed by events on the caller's

@@ -8,6 +8,7 @@ from ._lib import (MAX_GROUPS, NS_GRAM, NS_STANDARD, PATH_AUTO, PATH_FUSED, PATH
                    k_from_fraction, lib, ns_cfg, pointer_array, row_select, status_string, step,
                    step_groups, step_megabatch, symm_f16, syrk_f16, trace_disable, trace_enable,
                    trace_records, trace_reset, workspace_size, workspace_size_groups)
+from .clip import clip_grad_norm, grad_norm
 from .layer import (ACTIVATIONS, PackedF8, act_grad, add_rms_norm, add_rms_norm_grad, linear,
                     linear_grad_input, linear_grad_weight, linear_layer, pack_f8,
                     rms_norm_residual, unpack_f8)
@@ -20,4 +21,4 @@ __all__ = ["MAX_GROUPS", "NS_GRAM", "NS_STANDARD", "PATH_AUTO", "PATH_FUSED", "P
            "trace_enable", "trace_records", "trace_reset", "workspace_size",
            "workspace_size_groups", "ACTIVATIONS", "PackedF8", "act_grad", "add_rms_norm",
            "add_rms_norm_grad", "linear", "linear_grad_input", "linear_grad_weight", "linear_layer",
-           "pack_f8", "rms_norm_residual", "unpack_f8", "Dion3", "Dion3Step"]
+           "pack_f8", "rms_norm_residual", "unpack_f8", "clip_grad_norm", "grad_norm", "Dion3", "Dion3Step"]

@@ -46,6 +46,13 @@ class NormCfg(ctypes.Structure):
     _fields_ = [("beta2", ctypes.c_float), ("eps", ctypes.c_float)]
 
 
+class GradDesc(ctypes.Structure):
+    """Mirror of dion3_grad (one gradient of a list)."""
+    _fields_ = [("G", ctypes.c_void_p), ("M", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64), ("ldg", ctypes.c_int64), ("ldm", ctypes.c_int64),
+                ("dtype", ctypes.c_int32)]
+
+
 class GroupDesc(ctypes.Structure):
     """Mirror of dion3_group (one shape group of a grouped step)."""
     _fields_ = [("W", ctypes.c_void_p), ("M", ctypes.c_void_p), ("G", ctypes.c_void_p),
@@ -117,6 +124,10 @@ def _declare(lib):
                                                               c.POINTER(sz)]),
         "dion3_linear_grad_weight": (c.c_int, [vp, i64, vp, i64, vp, vp, i64, i32, i64, i64, i64,
                                                i32, vp, sz, vp]),
+        "dion3_grad_size": (sz, []),
+        "dion3_grad_norm_workspace_size": (c.c_int, [vp, i32, c.POINTER(sz)]),
+        "dion3_grad_norm": (c.c_int, [vp, i32, f32, vp, vp, vp, sz, vp]),
+        "dion3_clip_grad_norm": (c.c_int, [vp, i32, f32, f32, vp, vp, sz, vp]),
         "dion3_trace_enable": (c.c_int, [i32]),
         "dion3_trace_count": (i32, []),
         "dion3_trace_reset": (None, []),
@@ -143,7 +154,8 @@ EXPORTED = ("dion3_version", "dion3_ns_cfg_size", "dion3_ns_cfg_default", "dion3
             "dion3_act_grad_workspace_size", "dion3_act_grad",
             "dion3_linear_grad_input_workspace_size", "dion3_linear_grad_input",
             "dion3_linear_grad_weight_workspace_size", "dion3_linear_grad_weight",
-            "dion3_trace_enable",
+            "dion3_grad_size", "dion3_grad_norm_workspace_size", "dion3_grad_norm",
+            "dion3_clip_grad_norm", "dion3_trace_enable",
             "dion3_trace_count", "dion3_trace_reset", "dion3_trace_record", "dion3_status_string",
             "dion3_last_hip_error")
 
@@ -163,6 +175,9 @@ def lib():
             raise ImportError(f"{LIB_PATH}: dion3_group is {loaded.dion3_group_size()} bytes, "
                               f"the binding's GroupDesc {ctypes.sizeof(GroupDesc)}: rebuild the "
                               "library")
+        if loaded.dion3_grad_size() != ctypes.sizeof(GradDesc):
+            raise ImportError(f"{LIB_PATH}: dion3_grad is {loaded.dion3_grad_size()} bytes, the "
+                              f"binding's GradDesc {ctypes.sizeof(GradDesc)}: rebuild the library")
         _lib = loaded
     return _lib
 

@@ -15,7 +15,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libdion3.so")
 
 SOURCES = ["gemm_f16.hip", "gram_small.hip", "rows.hip", "normalize.hip", "dion3_api.hip", "trace.hip",
-           "noalloc.hip", "layer_rows.hip", "layer_gemm.hip", "layer_api.hip"]
+           "noalloc.hip", "layer_rows.hip", "layer_gemm.hip", "layer_api.hip",
+           "grad_clip.hip"]
 ARCH = "gfx950"
 
 # Packed-fp32 instructions are switched off for all device code.

@@ -1,0 +1,133 @@
+"""The global norm of many gradients, and their clipping.
+
+Each function is one call of libdion3.so (include/dion3.h states the
+formulas): two passes over the gradients, whatever their number, types and
+shapes, without a copy to the host or to the device, so that they can be
+captured into a graph.
+"""
+from __future__ import annotations
+
+import array
+from typing import Optional
+
+import torch
+
+from . import _lib
+from .layer import _DTYPES, _call, _rows, _scratch, _size
+
+
+def _whole(t) -> bool:
+    """t's elements fill one stretch of memory, each once, in some order."""
+    if t.is_contiguous():
+        return True
+    n = 1
+    for stride, size in sorted((s, k) for k, s in zip(t.shape, t.stride()) if k != 1):
+        if stride != n:
+            return False
+        n *= size
+    return True
+
+
+def _layout(g, m, i):
+    """(rows, cols, row stride of g, row stride of m)."""
+    n = g.numel()
+    if m is None:
+        if _whole(g):
+            return 1, n, n, n
+        rows, cols, ld = _rows(g, f"gradient {i}")
+        return rows, cols, ld, cols
+    if g.is_contiguous() and m.is_contiguous() or g.stride() == m.stride() and _whole(g):
+        return 1, n, n, n
+    rows, cols, ldg = _rows(g, f"gradient {i}")
+    _, _, ldm = _rows(m, f"sum {i}")
+    return rows, cols, ldg, ldm
+
+
+def _table(grads, into, written):
+    """(the library's table, its length, the device)."""
+    grads = list(grads)
+    if into is not None:
+        into = list(into)
+        if len(into) != len(grads):
+            raise ValueError("need one sum per gradient")
+    table, device, seen = array.array("q"), None, set()
+    for i, g in enumerate(grads):
+        if g is None:
+            table.extend((0, 0, 0, 0, 0, 0, 0))
+            continue
+        if not isinstance(g, torch.Tensor) or g.device.type != "cuda" or g.layout != torch.strided:
+            raise TypeError(f"gradient {i} must be a dense CUDA (HIP) tensor")
+        if g.requires_grad:
+            raise TypeError(f"gradient {i} requires a gradient itself: pass p.grad, not p")
+        code = _DTYPES.get(g.dtype)
+        if code is None:
+            raise TypeError(f"gradient {i} must be float32, bfloat16 or float16")
+        if device is None:
+            device = g.device
+        elif g.device != device:
+            raise ValueError("all gradients must be on one device")
+        m = into[i] if into is not None else None
+        if m is not None:
+            if not isinstance(m, torch.Tensor) or m.device != device or m.dtype != torch.float32:
+                raise TypeError(f"sum {i} must be a float32 tensor on {device}")
+            if m.shape != g.shape:
+                raise ValueError(f"sum {i} must have shape {tuple(g.shape)}")
+        elif into is not None:
+            raise TypeError(f"sum {i} is missing")
+        n = g.numel()
+        if n == 0:
+            table.extend((0, 0, 0, 0, 0, 0, code))
+            continue
+        gp, mp = g.data_ptr(), m.data_ptr() if m is not None else 0
+        if written:
+            if (mp or gp) in seen:
+                raise ValueError(f"{'sum' if mp else 'gradient'} {i} is listed twice")
+            seen.add(mp or gp)
+        rows, cols, ldg, ldm = _layout(g, m, i)
+        table.extend((gp, mp, rows, cols, ldg, ldm, code))
+    return table, len(grads), device
+
+
+def grad_norm(grads, scale: float = 1.0, per_tensor: bool = False,
+              ws: Optional[_lib.Workspace] = None):
+    """scale * the square root of the sum of all the tensors' squares (0-dim
+    fp32, on their device; squares are summed in 64 bits).  ``grads``: tensors
+    of one device, fp32, bf16 or fp16; None stands for no gradient.  With
+    ``per_tensor`` (norm, norms): norms[i] is the norm of tensor i alone."""
+    table, count, device = _table(grads, None, False)
+    if device is None:
+        norm = torch.zeros(())
+        return (norm, torch.zeros(count)) if per_tensor else norm
+    at = table.buffer_info()[0]
+    norm = torch.empty((), dtype=torch.float32, device=device)
+    norms = torch.empty(count, dtype=torch.float32, device=device) if per_tensor else None
+    p, nb, keep = _scratch(ws, _size("dion3_grad_norm_workspace_size", at, count), device)
+    _call("dion3_grad_norm", device, at, count, float(scale), norm.data_ptr(),
+          norms.data_ptr() if per_tensor else None, p, nb)
+    return (norm, norms) if per_tensor else norm
+
+
+def clip_grad_norm(grads, max_norm: float, scale: float = 1.0, into=None,
+                   ws: Optional[_lib.Workspace] = None):
+    """Scale the gradients in place by ``scale`` * min(1, max_norm / norm), with
+    norm = ``grad_norm(grads, scale)``, and return norm.  ``scale``: 1 / the
+    loss's scale, for fp16.  A norm that is infinite zeroes the finite
+    gradients, one that is NaN makes all of them NaN.
+
+    ``into``: fp32 tensors, one for each gradient and of its shape; the scaled
+    gradients are then added to them and the gradients stay as they are.
+    ``[optimizer.accumulate_grad(p) for p in ps]`` are the momenta of a
+    ``Dion3``, whose next ``step()`` steps these parameters (leave their
+    ``.grad`` None by then, or it is added again).
+
+    No tensor that is written may be listed twice or overlap another one.
+    Pass gradients, not parameters; None stands for no gradient."""
+    table, count, device = _table(grads, into, True)
+    if device is None:
+        return torch.zeros(())
+    at = table.buffer_info()[0]
+    norm = torch.empty((), dtype=torch.float32, device=device)
+    p, nb, keep = _scratch(ws, _size("dion3_grad_norm_workspace_size", at, count), device)
+    _call("dion3_clip_grad_norm", device, at, count, float(max_norm), float(scale),
+          norm.data_ptr(), p, nb)
+    return norm

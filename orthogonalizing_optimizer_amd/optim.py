@@ -226,6 +226,17 @@ class Dion3(_optimizer_base()):
         if not captured:
             self._accumulated.add(p)
 
+    def clip_grad_norm(self, max_norm, scale: float = 1.0):
+        """Clip the ``.grad`` of all parameters by their global norm, in place,
+        and return the norm (``clip_grad_norm``).  RuntimeError if gradients
+        have been summed straight into momenta since the last step: those are
+        no longer apart from earlier ones."""
+        from .clip import clip_grad_norm
+        if self._accumulated:
+            raise RuntimeError("gradients summed into the momentum cannot be clipped")
+        return clip_grad_norm([p.grad for group in self.param_groups for p in group["params"]],
+                              max_norm, scale)
+
     def load_state_dict(self, state_dict):
         """As in torch.  Gradients summed into a momentum since the last step
         are part of it: they go with the momentum that is replaced, and the
