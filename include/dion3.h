@@ -451,6 +451,57 @@ DION3_API dion3_status dion3_linear_grad_weight(const void* dZ, int64_t lddz, co
                                                 void* stream);
 
 /* ---------------------------------------------------------------------------
+ * Norms of queries and keys per head with the rotation by their positions in
+ * the same pass, and the gradient.
+ *
+ * A side (the queries, or the keys) is T tokens of `heads` heads of D columns:
+ * element (t, h, j) of X is X[t ldx + h hsx + j], so that the parts of one
+ * product's output, or heads before tokens, are read as they lie; Y and dY
+ * likewise.  All are of dtype; w (D entries) is DION3_F32 or of dtype.
+ *   rstd = 1 / sqrt(mean_j x_j^2 + eps) and u = x rstd w per head;
+ *   the first r columns are turned: (y_a, y_b) = (u_a c - u_b s, u_b c + u_a s)
+ *   with c, s the cosine and sine of pos[t] freqs[i] for the pairs i < r / 2,
+ *   (a, b) = (i, i + r / 2), or (2 i, 2 i + 1) when interleaved;
+ *   the other columns are u.
+ * freqs: r / 2 doubles (radians a position); pos: T integers of pos_bits (32
+ * or 64) bits.  Angles are computed in 64 bits, statistics in 32, Y is rounded
+ * once.  k may be NULL.  Y may be X.
+ *
+ * The gradient, from X as the forward pass read it: Y receives dX (may be X or
+ * dY; NULL: not wanted), dw (2 D floats: those of q's w, then of k's, or NULL)
+ * the sums over tokens and heads, in an order fixed by the sizes; k NULL: the
+ * second half is zeros.  The workspace is used for dw only.
+ * DION3_ERR_ARG, _UNSUPPORTED: as for the layers' operators; r odd, negative
+ * or above D; heads below 1; a stride below D where there is more than one;
+ * unsupported: D above 1024 (a head takes at most 64 pieces of 16 columns,
+ * counted for the turned columns and the others apart), more than 65536
+ * heads, a stride above 2^38. */
+typedef struct {
+  const void* X; int64_t ldx, hsx;
+  const void* w;
+  const void* dY; int64_t lddy, hsdy;   /* gradient only */
+  void* Y; int64_t ldy, hsy;
+  int32_t heads;
+} dion3_heads;
+
+/* sizeof(dion3_heads) as this library was built (for bindings). */
+DION3_API size_t dion3_heads_size(void);
+
+DION3_API dion3_status dion3_qk_norm_rope(const dion3_heads* q, const dion3_heads* k,
+                                          const double* freqs, const void* pos, int32_t pos_bits,
+                                          int64_t T, int32_t D, int32_t r, int32_t interleaved,
+                                          float eps, int32_t wtype, int32_t dtype, void* stream);
+DION3_API dion3_status dion3_qk_norm_rope_grad_workspace_size(int64_t T, int32_t hq, int32_t hk,
+                                                              int32_t D, int32_t r,
+                                                              int32_t interleaved, size_t* bytes);
+DION3_API dion3_status dion3_qk_norm_rope_grad(const dion3_heads* q, const dion3_heads* k,
+                                               const double* freqs, const void* pos,
+                                               int32_t pos_bits, float* dw, int64_t T, int32_t D,
+                                               int32_t r, int32_t interleaved, float eps,
+                                               int32_t wtype, int32_t dtype, void* ws,
+                                               size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
  * The global norm of many gradients, and their clipping.
  *
  * A gradient is rows x cols elements of dtype (DION3_F32, _BF16 or _F16) with

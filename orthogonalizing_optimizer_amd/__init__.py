@@ -12,6 +12,7 @@ from .clip import clip_grad_norm, grad_norm
 from .layer import (ACTIVATIONS, PackedF8, act_grad, add_rms_norm, add_rms_norm_grad, linear,
                     linear_grad_input, linear_grad_weight, linear_layer, pack_f8,
                     rms_norm_residual, unpack_f8)
+from .model import qk_norm_rope, qk_norm_rope_grad, qk_norm_rope_layer
 from .optim import Dion3, Dion3Step
 
 __all__ = ["MAX_GROUPS", "NS_GRAM", "NS_STANDARD", "PATH_AUTO", "PATH_FUSED", "PATH_TILED",
@@ -21,4 +22,5 @@ __all__ = ["MAX_GROUPS", "NS_GRAM", "NS_STANDARD", "PATH_AUTO", "PATH_FUSED", "P
            "trace_enable", "trace_records", "trace_reset", "workspace_size",
            "workspace_size_groups", "ACTIVATIONS", "PackedF8", "act_grad", "add_rms_norm",
            "add_rms_norm_grad", "linear", "linear_grad_input", "linear_grad_weight", "linear_layer",
-           "pack_f8", "rms_norm_residual", "unpack_f8", "clip_grad_norm", "grad_norm", "Dion3", "Dion3Step"]
+           "pack_f8", "rms_norm_residual", "unpack_f8", "clip_grad_norm", "grad_norm",
+           "qk_norm_rope", "qk_norm_rope_grad", "qk_norm_rope_layer", "Dion3", "Dion3Step"]

@@ -46,6 +46,14 @@ class NormCfg(ctypes.Structure):
     _fields_ = [("beta2", ctypes.c_float), ("eps", ctypes.c_float)]
 
 
+class HeadsDesc(ctypes.Structure):
+    """Mirror of dion3_heads (the queries or the keys of a call)."""
+    _fields_ = [("X", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("hsx", ctypes.c_int64),
+                ("w", ctypes.c_void_p), ("dY", ctypes.c_void_p), ("lddy", ctypes.c_int64),
+                ("hsdy", ctypes.c_int64), ("Y", ctypes.c_void_p), ("ldy", ctypes.c_int64),
+                ("hsy", ctypes.c_int64), ("heads", ctypes.c_int32)]
+
+
 class GradDesc(ctypes.Structure):
     """Mirror of dion3_grad (one gradient of a list)."""
     _fields_ = [("G", ctypes.c_void_p), ("M", ctypes.c_void_p), ("rows", ctypes.c_int64),
@@ -124,6 +132,14 @@ def _declare(lib):
                                                               c.POINTER(sz)]),
         "dion3_linear_grad_weight": (c.c_int, [vp, i64, vp, i64, vp, vp, i64, i32, i64, i64, i64,
                                                i32, vp, sz, vp]),
+        "dion3_heads_size": (sz, []),
+        "dion3_qk_norm_rope": (c.c_int, [c.POINTER(HeadsDesc), c.POINTER(HeadsDesc), vp, vp, i32,
+                                         i64, i32, i32, i32, f32, i32, i32, vp]),
+        "dion3_qk_norm_rope_grad_workspace_size": (c.c_int, [i64, i32, i32, i32, i32, i32,
+                                                             c.POINTER(sz)]),
+        "dion3_qk_norm_rope_grad": (c.c_int, [c.POINTER(HeadsDesc), c.POINTER(HeadsDesc), vp, vp,
+                                              i32, vp, i64, i32, i32, i32, f32, i32, i32, vp, sz,
+                                              vp]),
         "dion3_grad_size": (sz, []),
         "dion3_grad_norm_workspace_size": (c.c_int, [vp, i32, c.POINTER(sz)]),
         "dion3_grad_norm": (c.c_int, [vp, i32, f32, vp, vp, vp, sz, vp]),
@@ -154,7 +170,8 @@ EXPORTED = ("dion3_version", "dion3_ns_cfg_size", "dion3_ns_cfg_default", "dion3
             "dion3_act_grad_workspace_size", "dion3_act_grad",
             "dion3_linear_grad_input_workspace_size", "dion3_linear_grad_input",
             "dion3_linear_grad_weight_workspace_size", "dion3_linear_grad_weight",
-            "dion3_grad_size", "dion3_grad_norm_workspace_size", "dion3_grad_norm",
+            "dion3_heads_size", "dion3_qk_norm_rope", "dion3_qk_norm_rope_grad_workspace_size",
+            "dion3_qk_norm_rope_grad", "dion3_grad_size", "dion3_grad_norm_workspace_size", "dion3_grad_norm",
             "dion3_clip_grad_norm", "dion3_trace_enable",
             "dion3_trace_count", "dion3_trace_reset", "dion3_trace_record", "dion3_status_string",
             "dion3_last_hip_error")
@@ -178,6 +195,9 @@ def lib():
         if loaded.dion3_grad_size() != ctypes.sizeof(GradDesc):
             raise ImportError(f"{LIB_PATH}: dion3_grad is {loaded.dion3_grad_size()} bytes, the "
                               f"binding's GradDesc {ctypes.sizeof(GradDesc)}: rebuild the library")
+        if loaded.dion3_heads_size() != ctypes.sizeof(HeadsDesc):
+            raise ImportError(f"{LIB_PATH}: dion3_heads is {loaded.dion3_heads_size()} bytes, the "
+                              f"binding's HeadsDesc {ctypes.sizeof(HeadsDesc)}: rebuild the library")
         _lib = loaded
     return _lib
 

@@ -1,0 +1,214 @@
+"""Operators around the layers in a model's training step.
+
+Queries and keys normed per head and rotated by their positions in one pass
+(``qk_norm_rope``), and its gradient.  As in ``layer``, every function is one
+call of libdion3.so (include/dion3.h states the formulas), runs on torch's
+current stream of the tensors' device and takes its workspace from torch's
+allocator per call (or from ``ws``); there is no fallback.
+``qk_norm_rope_layer`` is the differentiable form.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional
+
+import torch
+
+from . import _lib
+from .layer import _DTYPES, _call, _ptr, _same, _scratch, _size, _t16, _vector
+
+_MAX_STRIDE = 1 << 38
+
+
+def _lead(shape, strides, name):
+    """(entries, the one stride of the leading dimensions) of a tensor of that
+    shape and strides, None as the stride of a single entry."""
+    n, ld = 1, None
+    for size, stride in zip(reversed(shape), reversed(strides)):
+        if size == 1:
+            continue
+        if ld is None:
+            ld = stride
+        elif size > 0 and n > 0 and stride != ld * n:
+            raise ValueError(f"{name}: its leading dimensions do not share one stride")
+        n *= size
+    return n, ld
+
+
+# ------------------------------------------------- heads: norm and rotation
+
+def _heads(t, name):
+    """(tokens, token stride, heads, head stride, columns) of [..., heads, columns]."""
+    if t.dim() < 2:
+        raise ValueError(f"{name} must be [..., heads, columns]")
+    h, D = t.shape[-2:]
+    if h < 1 or D < 1:
+        raise ValueError(f"{name} needs at least one head and one column")
+    if D > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must have contiguous columns")
+    T, ld = _lead(t.shape[:-2], t.stride()[:-2], name)
+    hs = t.stride(-2) if h > 1 else D
+    ld = h * D if ld is None else ld
+    if (T > 1 and ld < D) or hs < D:
+        raise ValueError(f"{name}: its heads overlap")
+    return T, ld, h, hs, D
+
+
+def _positions(positions, lead, device):
+    if not isinstance(positions, torch.Tensor) or positions.device != device:
+        raise TypeError(f"positions must be a tensor on {device}")
+    if positions.dtype not in (torch.int64, torch.int32):
+        raise TypeError("positions must be int64 or int32")
+    if positions.shape != lead:
+        positions = positions.expand(lead)           # (ValueError in torch's own words)
+    return positions.contiguous()
+
+
+def _freqs(freqs, D, device):
+    if not isinstance(freqs, torch.Tensor) or freqs.device != device:
+        raise TypeError(f"freqs must be a tensor on {device}")
+    if freqs.dtype != torch.float64:
+        raise TypeError("freqs must be float64")
+    if freqs.dim() != 1 or 2 * freqs.shape[0] > D or not freqs.is_contiguous():
+        raise ValueError(f"freqs must be a contiguous vector of at most {D // 2} entries")
+    return 2 * freqs.shape[0]
+
+
+class _Sides:
+    """The checked queries and keys of a call, as the library takes them."""
+
+    def __init__(self, q, k, q_weight, k_weight, positions, freqs):
+        _t16(q, "q")
+        self.q, self.k = q, k
+        self.T, ld, hq, hs, self.D = _heads(q, "q")
+        self.lead = q.shape[:-2]
+        _vector(q_weight, self.D, q, "q_weight")
+        self.desc = [_lib.HeadsDesc(X=_ptr(q), ldx=ld, hsx=hs, w=q_weight.data_ptr(), heads=hq), None]
+        if (k is None) != (k_weight is None):
+            raise ValueError("k and k_weight belong together")
+        if k is not None:
+            _same(k, q, "k")
+            T, ld, hk, hs, D = _heads(k, "k")
+            if k.shape[:-2] != self.lead or D != self.D:
+                raise ValueError(f"k must have q's tokens and {self.D} columns a head")
+            _vector(k_weight, D, q, "k_weight")
+            if k_weight.dtype != q_weight.dtype:
+                raise TypeError("q_weight and k_weight must have one type")
+            self.desc[1] = _lib.HeadsDesc(X=_ptr(k), ldx=ld, hsx=hs, w=k_weight.data_ptr(), heads=hk)
+        self.pos = _positions(positions, self.lead, q.device)
+        self.r = _freqs(freqs, self.D, q.device)
+        self.wtype, self.dtype = _DTYPES[q_weight.dtype], _DTYPES[q.dtype]
+        self.freqs = freqs
+        self.bits = 64 if self.pos.dtype == torch.int64 else 32
+
+    def output(self, i):
+        """A contiguous output of side i, put into its description."""
+        t = (self.q, self.k)[i]
+        y = t.new_empty(t.shape)
+        self.desc[i].Y, self.desc[i].ldy, self.desc[i].hsy = _ptr(y), t.shape[-2] * self.D, self.D
+        return y
+
+    def refs(self):
+        return tuple(ctypes.byref(s) if s is not None else None for s in self.desc)
+
+
+def qk_norm_rope(q, k, q_weight, k_weight, positions, freqs, eps: float = 1e-6,
+                 interleaved: bool = False):
+    """(yq, yk): queries [..., hq, D] and keys [..., hk, D] with each head
+    normed, u = x / sqrt(mean x^2 + eps) * weight, and its first
+    2 * len(freqs) columns turned by the angles positions * freqs: the pairs
+    are columns (i, i + len(freqs)), or neighbours with ``interleaved``.
+
+    q and k are bf16 or fp16 with contiguous columns and any strides of heads
+    and tokens (views of one product's output, say; leading dimensions share a
+    stride); outputs are contiguous.  Weights [D] are fp32 or of q's type.
+    ``positions``: int64 or int32, one a token (or of a shape that expands to
+    the tokens').  ``freqs``: float64, radians a position, for instance
+    base ** (-torch.arange(0, r, 2, dtype=torch.float64) / r).  k and k_weight
+    may be None (queries alone; yk is None)."""
+    s = _Sides(q, k, q_weight, k_weight, positions, freqs)
+    yq = s.output(0)
+    yk = s.output(1) if k is not None else None
+    _call("dion3_qk_norm_rope", q.device, *s.refs(), _ptr(freqs), _ptr(s.pos), s.bits, s.T, s.D,
+          s.r, int(bool(interleaved)), float(eps), s.wtype, s.dtype)
+    return yq, yk
+
+
+def qk_norm_rope_grad(dyq, dyk, q, k, q_weight, k_weight, positions, freqs, eps: float = 1e-6,
+                      interleaved: bool = False, need_dx: bool = True, need_dw: bool = True,
+                      ws: Optional[_lib.Workspace] = None):
+    """(dq, dk, dq_weight, dk_weight) of ``qk_norm_rope`` from its inputs; the
+    weights' gradients are fp32.  What is not needed comes back as None."""
+    s = _Sides(q, k, q_weight, k_weight, positions, freqs)
+    if (dyk is None) != (k is None):
+        raise ValueError("k and its gradient belong together")
+    for i, (dy, t) in enumerate(((dyq, q), (dyk, k))):
+        if t is not None:
+            _same(dy, t, "dyq" if i == 0 else "dyk", t.shape)
+            _, ld, _, hs, _ = _heads(dy, "dyq" if i == 0 else "dyk")
+            s.desc[i].dY, s.desc[i].lddy, s.desc[i].hsdy = _ptr(dy), ld, hs
+    if not need_dx and not need_dw:
+        return None, None, None, None
+    dq = s.output(0) if need_dx else None
+    dk = s.output(1) if need_dx and k is not None else None
+    dw = q.new_empty((2, s.D), dtype=torch.float32) if need_dw else None
+    p, nb, keep = _scratch(ws, _size("dion3_qk_norm_rope_grad_workspace_size", s.T, q.shape[-2],
+                                     k.shape[-2] if k is not None else 0, s.D, s.r,
+                                     int(bool(interleaved))) if need_dw else 0, q.device)
+    _call("dion3_qk_norm_rope_grad", q.device, *s.refs(), _ptr(freqs), _ptr(s.pos), s.bits, _ptr(dw),
+          s.T, s.D, s.r, int(bool(interleaved)), float(eps), s.wtype, s.dtype, p, nb)
+    return (dq, dk, dw[0] if need_dw else None,
+            dw[1] if need_dw and k is not None else None)
+
+
+def _as_heads(t):
+    """A gradient as its producer left it, or contiguous where the library does
+    not read its layout: that is autograd's choice, not the user's."""
+    try:
+        _, ld, _, hs, _ = _heads(t, "gradient")
+        if max(ld, hs) <= _MAX_STRIDE:
+            return t
+    except ValueError:
+        pass
+    return t.contiguous()
+
+
+class _QkNormRope(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, q_weight, k_weight, positions, freqs, eps, interleaved):
+        yq, yk = qk_norm_rope(q, k, q_weight, k_weight, positions, freqs, eps, interleaved)
+        ctx.save_for_backward(q, k, q_weight, k_weight, positions, freqs)
+        ctx.set_materialize_grads(False)
+        ctx.eps, ctx.interleaved = eps, interleaved
+        return yq, yk
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dyq, dyk):
+        q, k, wq, wk, positions, freqs = ctx.saved_tensors
+        out = [None] * 8
+        # the sides that a gradient reaches, and of these what is asked for
+        sides = [(i, dy, x, w) for i, (dy, x, w) in enumerate(((dyq, q, wq), (dyk, k, wk)))
+                 if dy is not None and (ctx.needs_input_grad[i] or ctx.needs_input_grad[2 + i])]
+        if not sides:
+            return tuple(out)
+        args = [(_as_heads(dy), x, w) for _, dy, x, w in sides] + [(None, None, None)]
+        (dy0, x0, w0), (dy1, x1, w1) = args[:2]
+        need_dx = any(ctx.needs_input_grad[i] for i, *_ in sides)
+        need_dw = any(ctx.needs_input_grad[2 + i] for i, *_ in sides)
+        dx0, dx1, dw0, dw1 = qk_norm_rope_grad(dy0, dy1, x0, x1, w0, w1, positions, freqs, ctx.eps,
+                                               ctx.interleaved, need_dx, need_dw)
+        for (i, _, _, w), dx, dw in zip(sides, (dx0, dx1), (dw0, dw1)):
+            if ctx.needs_input_grad[i]:
+                out[i] = dx
+            if ctx.needs_input_grad[2 + i]:
+                out[2 + i] = dw.to(w.dtype)
+        return tuple(out)
+
+
+def qk_norm_rope_layer(q, k, q_weight, k_weight, positions, freqs, eps: float = 1e-6,
+                       interleaved: bool = False):
+    """``qk_norm_rope``, differentiable in q, k and the weights.  Kept for the
+    backward pass: q and k as they are."""
+    return _QkNormRope.apply(q, k, q_weight, k_weight, positions, freqs, float(eps),
+                             bool(interleaved))
