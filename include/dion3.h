@@ -502,6 +502,46 @@ DION3_API dion3_status dion3_qk_norm_rope_grad(const dion3_heads* q, const dion3
                                                size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * Log probabilities of given tokens, the entropy and the best alternatives,
+ * and the gradient.
+ *
+ * X holds T rows of n logits of dtype (DION3_F32, _BF16 or _F16) with row
+ * stride ldx; z = scale X.  target: T integers of target_bits (32 or 64) bits,
+ * or NULL; one outside [0, n) marks a row without a token (its logp is 0 and
+ * it sends no gradient).
+ *   stats[t] = (m, l): m = max_j z_j, l = ln sum_j exp(z_j - m);
+ *   logp[t] = (z_target - m) - l (given and NULL together with target);
+ *   entropy[t] = -sum_j p_j ln p_j with p_j = exp((z_j - m) - l) (or NULL);
+ *   top_logp[t][i], top_index[t][i], i < top <= DION3_MAX_TOP (and n): the
+ *   largest logits in order, equal ones by their index, NaN before all.
+ * A row whose logits are all -infinity has stats (-infinity, 0), logp and
+ * top_logp -infinity, entropy and gradient 0; one with NaN or +infinity (also
+ * as the product with scale) has NaN.  The maximum is held apart from the sum
+ * so that rows at the type's lowest value keep their probabilities.
+ *
+ * The gradient: dX_j = scale (g (1[j = target] - p_j) - gH p_j (ln p_j + H))
+ * rounded to dtype, with g = dlogp[t] (given and NULL together with target),
+ * gH = dentropy[t] (or NULL) and H = entropy[t] (read with dentropy only).
+ * dX may be X.
+ * Sums are held in fp32 in an order fixed by n.  Errors: as for the layers'
+ * operators (sides: n); top negative or above n is an argument error, above
+ * DION3_MAX_TOP unsupported. */
+#define DION3_MAX_TOP 64
+DION3_API dion3_status dion3_log_probs_workspace_size(int64_t T, int64_t n, int32_t top,
+                                                      size_t* bytes);
+DION3_API dion3_status dion3_log_probs(const void* X, int64_t ldx, const void* target,
+                                       int32_t target_bits, float* logp, float* stats,
+                                       float* entropy, float* top_logp, int64_t* top_index,
+                                       int64_t T, int64_t n, int32_t top, float scale,
+                                       int32_t dtype, void* ws, size_t ws_bytes, void* stream);
+DION3_API dion3_status dion3_log_probs_grad(const float* dlogp, const void* X, int64_t ldx,
+                                            const void* target, int32_t target_bits,
+                                            const float* stats, const float* entropy,
+                                            const float* dentropy, void* dX, int64_t lddx,
+                                            int64_t T, int64_t n, float scale, int32_t dtype,
+                                            void* stream);
+
+/* ---------------------------------------------------------------------------
  * The global norm of many gradients, and their clipping.
  *
  * A gradient is rows x cols elements of dtype (DION3_F32, _BF16 or _F16) with

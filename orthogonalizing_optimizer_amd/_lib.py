@@ -140,6 +140,11 @@ def _declare(lib):
         "dion3_qk_norm_rope_grad": (c.c_int, [c.POINTER(HeadsDesc), c.POINTER(HeadsDesc), vp, vp,
                                               i32, vp, i64, i32, i32, i32, f32, i32, i32, vp, sz,
                                               vp]),
+        "dion3_log_probs_workspace_size": (c.c_int, [i64, i64, i32, c.POINTER(sz)]),
+        "dion3_log_probs": (c.c_int, [vp, i64, vp, i32, vp, vp, vp, vp, vp, i64, i64, i32, f32,
+                                      i32, vp, sz, vp]),
+        "dion3_log_probs_grad": (c.c_int, [vp, vp, i64, vp, i32, vp, vp, vp, vp, i64, i64, i64,
+                                           f32, i32, vp]),
         "dion3_grad_size": (sz, []),
         "dion3_grad_norm_workspace_size": (c.c_int, [vp, i32, c.POINTER(sz)]),
         "dion3_grad_norm": (c.c_int, [vp, i32, f32, vp, vp, vp, sz, vp]),
@@ -171,7 +176,8 @@ EXPORTED = ("dion3_version", "dion3_ns_cfg_size", "dion3_ns_cfg_default", "dion3
             "dion3_linear_grad_input_workspace_size", "dion3_linear_grad_input",
             "dion3_linear_grad_weight_workspace_size", "dion3_linear_grad_weight",
             "dion3_heads_size", "dion3_qk_norm_rope", "dion3_qk_norm_rope_grad_workspace_size",
-            "dion3_qk_norm_rope_grad", "dion3_grad_size", "dion3_grad_norm_workspace_size", "dion3_grad_norm",
+            "dion3_qk_norm_rope_grad", "dion3_log_probs_workspace_size", "dion3_log_probs",
+            "dion3_log_probs_grad", "dion3_grad_size", "dion3_grad_norm_workspace_size", "dion3_grad_norm",
             "dion3_clip_grad_norm", "dion3_trace_enable",
             "dion3_trace_count", "dion3_trace_reset", "dion3_trace_record", "dion3_status_string",
             "dion3_last_hip_error")

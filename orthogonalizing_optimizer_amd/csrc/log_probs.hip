@@ -1,0 +1,502 @@
+// Log probabilities of given tokens from rows of logits, with the entropy and
+// the best alternatives, and the gradient.
+//
+//   z = scale x,  m = max_j z_j,  l = ln sum_j exp(z_j - m)   per row of n,
+//   logp = (z_target - m) - l,  H = l - sum_j exp(z_j - m) (z_j - m) / exp(l),
+//   dx_j = scale (g (1[j = target] - p_j) - gH p_j (ln p_j + H)),
+//   p_j = exp((z_j - m) - l).
+//
+// Bound by HBM, not far from the vector units (an exponential a logit, 4
+// issue slots of the about 10 a logit takes; 2 bytes of HBM time are 13).
+//
+// A workgroup takes one piece of one row, 32 logits a thread, and holds it in
+// registers: the maximum first, then the sums, then the best of the piece, all
+// from one read.  What the pieces of a row leave (maximum, sums, candidates)
+// is joined by a second launch, so that few long rows fill the chip as many
+// rows do.  The pair (m, l) is kept apart up to the gradient: where logits are
+// large, down to the type's lowest value, m + l would have no bits left for l.
+#include "checks.h"
+
+namespace dion3 {
+namespace {
+
+constexpr int kChunks = 4;                       // chunks of 8 logits a thread
+constexpr int kMaxTop = DION3_MAX_TOP;
+constexpr float kLowest = -3.402823466e38f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float exp_(float d) { return __builtin_amdgcn_exp2f(d * kLog2e); }
+
+// The sums of a set of logits relative to m (kLowest for an empty set or one
+// of -infinity): s = sum exp(z - m), e = sum exp(z - m) (z - m).
+struct Part {
+  float m, s, e, pad;
+};
+__device__ __forceinline__ Part merge(const Part& a, const Part& b) {
+  const float m = fmaxf(a.m, b.m);
+  // (bounded: 0 times an infinite distance would be NaN)
+  const float da = fmaxf(a.m - m, -1e30f), db = fmaxf(b.m - m, -1e30f);
+  const float fa = exp_(a.m - m), fb = exp_(b.m - m);      // infinities less themselves: NaN
+  return {m, __builtin_fmaf(a.s, fa, b.s * fb),
+          __builtin_fmaf(__builtin_fmaf(a.s, da, a.e), fa, __builtin_fmaf(b.s, db, b.e) * fb), 0.0f};
+}
+
+// Whole numbers in the order of the logits; zeros of both signs alike, NaN
+// above all, none is 0.  The lower kLow bits of a type's keys are those of
+// their sign: all clear in the upper half of the order, all set in the lower.
+template <class E>
+constexpr int kLow = __is_same(E, bf16) ? 16 : __is_same(E, f16) ? 13 : 0;
+template <class E>
+__device__ __forceinline__ unsigned order_key(float x) {
+  const unsigned u = __builtin_bit_cast(unsigned, x + 0.0f);
+  return x != x ? 0xffffffffu << kLow<E> : u ^ (unsigned)((int)u >> 31 | (int)0x80000000);
+}
+__device__ __forceinline__ float order_value(unsigned k) {
+  return __builtin_bit_cast(float, k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
+
+struct Best {
+  unsigned key;
+  int at;
+};
+__device__ __forceinline__ bool before(const Best& a, const Best& b) {
+  return a.key > b.key || (a.key == b.key && a.at < b.at);
+}
+
+// Writes the `top` best of the nc candidates c (LDS, all different) in order
+// by counting, for each, those before it.
+template <class F>
+__device__ __forceinline__ void pick(const Best* c, int nc, int top, F put) {
+  for (int i = threadIdx.x; i < nc; i += blockDim.x) {
+    const Best mine = c[i];
+    int rank = 0;
+    for (int j = 0; j < nc; ++j) rank += before(c[j], mine) ? 1 : 0;
+    if (rank < top) put(rank, mine);
+  }
+}
+
+struct LogpP {
+  const void* x; long long ldx;
+  const void* target; int target64;
+  float* logp; float* stats; float* entropy;
+  float* top_logp; long long* top_index;
+  Part* part; Best* best;                  // of piece (t, s): part[t S + s], best[(t S + s) top ..]
+  long long T;
+  int n, top, S, len;                      // pieces a row, logits a piece (a multiple of 8)
+  float scale;
+};
+
+__device__ __forceinline__ long long flat_block() {
+  return (long long)blockIdx.y * gridDim.x + blockIdx.x;
+}
+dim3 blocks_grid(long long blocks) {
+  const long long row = 1LL << 21;
+  return blocks <= row ? dim3((unsigned)blocks)
+                       : dim3((unsigned)row, (unsigned)((blocks + row - 1) / row));
+}
+
+constexpr int kWaveBest = 128;     // candidates a wave leaves at most (at least kMaxTop)
+
+// The wave's candidates for the `top` best of its keys (absent ones are 0): at
+// least those, at most kWaveBest.  Keys at or above the top-th largest of the
+// lanes' maxima are a superset, most often of few more than `top`; where it is
+// too large (many equal logits, or one lane's), the top-th largest key itself
+// is found by its bits and of the equal ones the first are taken.
+template <int SH>
+__device__ __forceinline__ int wave_best(const unsigned (&key)[kChunks][8], const int (&col)[kChunks],
+                                         int top, Best* out) {
+  unsigned cm[kChunks], lm = 0;
+#pragma unroll
+  for (int i = 0; i < kChunks; ++i) {
+    cm[i] = key[i][0];
+#pragma unroll
+    for (int e = 1; e < 8; ++e) cm[i] = max(cm[i], key[i][e]);
+    lm = max(lm, cm[i]);
+  }
+  unsigned tau = 0;
+  for (int b = 31; b >= SH; --b) {
+    const unsigned c = tau | 1u << b;
+    if (__popcll(__ballot(lm >= c)) >= top) tau = c;
+  }
+  const unsigned long long below = (1ull << (threadIdx.x & 63)) - 1;
+  int have = 0;
+#pragma unroll
+  for (int i = 0; i < kChunks; ++i) {
+    if (!__ballot(cm[i] >= tau)) continue;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const bool in = key[i][e] >= tau;
+      const unsigned long long b = __ballot(in);
+      const int at = have + __popcll(b & below);
+      if (in && at < kWaveBest) out[at] = {key[i][e], col[i] + e};
+      have += __popcll(b);
+    }
+  }
+  if (have <= kWaveBest) return have;
+  tau = 0;
+  for (int b = 31; b >= SH; --b) {
+    const unsigned c = tau | 1u << b;
+    int cnt = 0;
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) cnt += __popcll(__ballot(key[i][e] >= c));
+    if (cnt >= top) tau = c;
+  }
+  if constexpr (SH > 0) {
+    if (tau && !(tau & 0x80000000u)) tau |= (1u << SH) - 1;
+  }
+  have = 0;
+#pragma unroll
+  for (int i = 0; i < kChunks; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const bool in = key[i][e] > tau;
+      const unsigned long long b = __ballot(in);
+      const int at = have + __popcll(b & below);
+      if (in && at < kWaveBest) out[at] = {key[i][e], col[i] + e};
+      have += __popcll(b);
+    }
+#pragma unroll
+  for (int i = 0; i < kChunks; ++i) {          // the columns' order: chunks, lanes, then e
+    int mine = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) mine += key[i][e] == tau ? 1 : 0;
+    int at = have;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const unsigned long long w = __ballot(mine >> b & 1);
+      at += __popcll(w & below) << b;
+      have += __popcll(w) << b;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (key[i][e] == tau) {
+        if (at < top) out[at] = {tau, col[i] + e};
+        ++at;
+      }
+  }
+  return top;
+}
+
+template <class E, bool TOP>
+__global__ __launch_bounds__(1024) void k_logp_piece(LogpP p) {
+  extern __shared__ Best cand[];                    // TOP: kWaveBest a wave
+  __shared__ Part sh[16];
+  __shared__ int count[17];
+  const long long block = flat_block();
+  if (block >= p.T * p.S) return;
+  const int nt = blockDim.x, wave = threadIdx.x >> 6, nw = nt >> 6;
+  const long long t = block / p.S;
+  const int from = (int)(block - t * p.S) * p.len;
+  const int to = min(from + p.len, p.n);            // (a piece of a short row may be empty)
+  const E* row = (const E*)p.x + t * p.ldx;
+  float v[kChunks][8];
+  int col[kChunks];
+  {
+    Raw8<E> raw[kChunks];
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+      col[i] = from + (i * nt + (int)threadIdx.x) * 8;
+      if (col[i] < to) raw[i] = fetch8(row, col[i], p.n);
+    }
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+      if (col[i] < to) {
+        chunk8(raw[i], col[i], p.n, v[i]);
+        if (col[i] + 8 > to) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (col[i] + e >= to) v[i][e] = -__builtin_inff();
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[i][e] = -__builtin_inff();
+      }
+    }
+  }
+  float mx = -__builtin_inff();
+#pragma unroll
+  for (int i = 0; i < kChunks; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) mx = fmaxf(mx, v[i][e]);
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) mx = fmaxf(mx, __shfl_xor(mx, o, 64));
+  Part w = {fmaxf(mx * p.scale, kLowest), 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < kChunks; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float d = __builtin_fmaf(v[i][e], p.scale, -w.m);
+      const float q = exp_(d);
+      w.s += q;
+      w.e = __builtin_fmaf(q, fmaxf(d, -1e30f), w.e);
+    }
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    w.s += __shfl_xor(w.s, o, 64);
+    w.e += __shfl_xor(w.e, o, 64);
+  }
+  if ((threadIdx.x & 63) == 0) sh[wave] = w;
+  if constexpr (TOP) {
+    unsigned key[kChunks][8];
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) key[i][e] = col[i] + e < to ? order_key<E>(v[i][e]) : 0u;
+    const int c = wave_best<kLow<E>>(key, col, p.top, cand + wave * kWaveBest);
+    if ((threadIdx.x & 63) == 0) count[wave] = c;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    Part a = sh[0];
+    for (int i = 1; i < nw; ++i) a = merge(a, sh[i]);
+    p.part[block] = a;
+  }
+  if constexpr (TOP) {
+    // every candidate against all waves' candidates
+    const int nc = nw * kWaveBest;
+    for (int i = threadIdx.x; i < nc; i += nt) {
+      if ((i & (kWaveBest - 1)) >= count[i / kWaveBest]) continue;
+      const Best mine = cand[i];
+      int rank = 0;
+      for (int u = 0; u < nw; ++u)
+        for (int j = 0; j < count[u]; ++j) rank += before(cand[u * kWaveBest + j], mine) ? 1 : 0;
+      if (rank < p.top) p.best[block * p.top + rank] = mine;
+    }
+  }
+}
+
+__device__ __forceinline__ long long target_of(const void* target, int is64, long long t) {
+  return is64 ? ((const long long*)target)[t] : (long long)((const int*)target)[t];
+}
+
+// Rows from their pieces: a wave a row for the sums, and with TOP a workgroup a
+// row, whose threads rank the pieces' candidates.
+template <class E, bool TOP>
+__global__ __launch_bounds__(256) void k_logp_join(LogpP p) {
+  extern __shared__ Best cand[];
+  const int lane = threadIdx.x & 63;
+  const long long t = TOP ? flat_block() : flat_block() * 4 + (threadIdx.x >> 6);
+  if (t >= p.T) return;
+  Part a = {kLowest, 0.0f, 0.0f, 0.0f};
+  for (int s = lane; s < p.S; s += 64) a = merge(a, p.part[t * p.S + s]);
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1)
+    a = merge(a, {__shfl_xor(a.m, o, 64), __shfl_xor(a.s, o, 64), __shfl_xor(a.e, o, 64), 0.0f});
+  const bool none = a.s == 0.0f && a.m < 0.0f;         // every logit is -infinity
+  // (an infinite maximum, of a logit or of its product with scale, has no log)
+  const float l = none ? 0.0f : a.m > -kLowest ? __builtin_nanf("") : logf(a.s);
+  if (none) a.m = -__builtin_inff();
+  if (lane == 0 && (!TOP || threadIdx.x == 0)) {
+    p.stats[2 * t] = a.m;
+    p.stats[2 * t + 1] = l;
+    if (p.entropy) p.entropy[t] = none ? 0.0f : l - a.e / a.s;
+    if (p.target) {
+      const long long j = target_of(p.target, p.target64, t);
+      float v = 0.0f;                                  // no token: nothing
+      if (j >= 0 && j < p.n)
+        v = none ? -__builtin_inff()
+                 : __builtin_fmaf(to_f32(((const E*)p.x)[t * p.ldx + j]), p.scale, -a.m) - l;
+      p.logp[t] = v;
+    }
+  }
+  if constexpr (TOP) {
+    const int nc = p.S * p.top;
+    for (int i = threadIdx.x; i < nc; i += 256) cand[i] = p.best[t * nc + i];
+    __syncthreads();
+    pick(cand, nc, p.top, [&](int rank, const Best& b) {
+      p.top_logp[t * p.top + rank] =
+          none ? -__builtin_inff() : __builtin_fmaf(order_value(b.key), p.scale, -a.m) - l;
+      p.top_index[t * p.top + rank] = b.at;
+    });
+  }
+}
+
+struct GradP {
+  const float* g; const void* x; const void* target; const float* stats;
+  const float* entropy; const float* gh;
+  void* dx;
+  long long ldx, lddx, T;
+  int target64, n, S, len;
+  float scale;
+};
+
+// One read and one write of a logit; in place where dX is X (a thread reads
+// its logits before it writes them, and nobody else's).
+template <class E, bool ENT>
+__global__ __launch_bounds__(256) void k_logp_grad(GradP p) {
+  const long long block = flat_block();
+  if (block >= p.T * p.S) return;
+  const long long t = block / p.S;
+  const int from = (int)(block - t * p.S) * p.len, to = min(from + p.len, p.n);
+  const E* row = (const E*)p.x + t * p.ldx;
+  Raw8<E> raw[kChunks];
+#pragma unroll
+  for (int i = 0; i < kChunks; ++i) {
+    const int c = from + (i * 256 + (int)threadIdx.x) * 8;
+    if (c < to) raw[i] = fetch8(row, c, p.n);
+  }
+  const float m = p.stats[2 * t], l = p.stats[2 * t + 1];
+  long long j = p.target ? target_of(p.target, p.target64, t) : -1;
+  if (j < 0 || j >= p.n) j = -1;
+  const bool none = m == -__builtin_inff() || (!ENT && j < 0);    // no gradient
+  const float g = j >= 0 ? p.scale * p.g[t] : 0.0f;
+  // dx = p (a + b ln p) + g at the target; a statistic that is NaN reaches
+  // every logit through a
+  float a = -g + (l - l), b = 0.0f;
+  if (ENT) {
+    b = -p.scale * p.gh[t];
+    a = __builtin_fmaf(b, p.entropy[t], a);
+  }
+#pragma unroll
+  for (int i = 0; i < kChunks; ++i) {
+    const int c = from + (i * 256 + (int)threadIdx.x) * 8;
+    if (c >= to) continue;
+    float v[8];
+    chunk8(raw[i], c, p.n, v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float q = __builtin_fmaf(v[e], p.scale, -m) - l;
+      const float pr = exp_(q);
+      // (bounded: 0 times an infinite ln p would be NaN)
+      v[e] = none ? 0.0f : pr * (ENT ? __builtin_fmaf(b, fmaxf(q, -1e30f), a) : a);
+      if (c + e == j && !none) v[e] += g;
+    }
+    store8((E*)p.dx + t * p.lddx, c, min(to, p.n), v);
+  }
+}
+
+// --------------------------------------------------------------- the launches
+
+// Pieces of at most 8192 logits (4 waves), of 32768 (16 waves) where a row
+// would have more than 16, of equal length.
+struct Pieces {
+  int S, len, threads;
+};
+Pieces pieces_of(int n) {
+  Pieces q;
+  q.threads = n > 16 * 8192 ? 1024 : 256;
+  const int most = q.threads * 8 * kChunks;
+  q.S = (n + most - 1) / most;
+  q.len = ((n + q.S - 1) / q.S + 7) / 8 * 8;
+  return q;
+}
+
+size_t logp_scratch(long long T, int n, int top) {
+  const Pieces q = pieces_of(n);
+  return (size_t)T * q.S * (sizeof(Part) + (size_t)top * sizeof(Best));
+}
+
+template <class E>
+hipError_t launch_logp(const LogpP& p, const Pieces& q, hipStream_t s) {
+  const dim3 grid = blocks_grid(p.T * q.S), block(q.threads);
+  const size_t lds = (size_t)(q.threads / 64) * kWaveBest * sizeof(Best);
+  if (p.top) hipLaunchKernelGGL((k_logp_piece<E, true>), grid, block, lds, s, p);
+  else hipLaunchKernelGGL((k_logp_piece<E, false>), grid, block, 0, s, p);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  if (p.top)
+    hipLaunchKernelGGL((k_logp_join<E, true>), blocks_grid(p.T), dim3(256),
+                       (size_t)q.S * p.top * sizeof(Best), s, p);
+  else
+    hipLaunchKernelGGL((k_logp_join<E, false>), blocks_grid((p.T + 3) / 4), dim3(256), 0, s, p);
+  return hipGetLastError();
+}
+
+template <class E>
+hipError_t launch_logp_grad(const GradP& p, hipStream_t s) {
+  const dim3 grid = blocks_grid(p.T * p.S);
+  if (p.gh) hipLaunchKernelGGL((k_logp_grad<E, true>), grid, dim3(256), 0, s, p);
+  else hipLaunchKernelGGL((k_logp_grad<E, false>), grid, dim3(256), 0, s, p);
+  return hipGetLastError();
+}
+
+bool any_type(int t) { return type16(t) || t == DION3_F32; }
+int size_of(int t) { return t == DION3_F32 ? 4 : 2; }
+
+dion3_status check_targets(const void* target, int bits) {
+  if (!target) return DION3_OK;
+  if (bits != 32 && bits != 64) return DION3_ERR_ARG;
+  return elem_aligned(target, bits / 8) ? DION3_OK : DION3_ERR_ARG;
+}
+
+}  // namespace
+}  // namespace dion3
+
+using namespace dion3;
+
+extern "C" {
+
+dion3_status dion3_log_probs_workspace_size(int64_t T, int64_t n, int32_t top, size_t* bytes) {
+  if (!bytes) return DION3_ERR_ARG;
+  TRY(check_sizes(T, n, 1));
+  if (top < 0 || top > n) return DION3_ERR_ARG;
+  if (top > kMaxTop) return DION3_ERR_UNSUPPORTED;
+  *bytes = logp_scratch(T, (int)n, top);
+  return DION3_OK;
+}
+
+dion3_status dion3_log_probs(const void* X, int64_t ldx, const void* target, int32_t target_bits,
+                             float* logp, float* stats, float* entropy, float* top_logp,
+                             int64_t* top_index, int64_t T, int64_t n, int32_t top, float scale,
+                             int32_t dtype, void* ws, size_t ws_bytes, void* stream) {
+  if (!any_type(dtype) || !(scale > 0.0f) || !isfinite(scale)) return DION3_ERR_ARG;
+  TRY(check_sizes(T, n, 1));
+  if (top < 0 || top > n) return DION3_ERR_ARG;
+  if (top > kMaxTop) return DION3_ERR_UNSUPPORTED;
+  TRY(check_ld(ldx, n));
+  TRY(check_targets(target, target_bits));
+  if (T == 0) return DION3_OK;
+  if (!X || !stats || (target != nullptr) != (logp != nullptr)) return DION3_ERR_ARG;
+  if (top && (!top_logp || !top_index)) return DION3_ERR_ARG;
+  if (!elem_aligned(X, size_of(dtype)) || !elem_aligned(logp, 4) || !elem_aligned(stats, 4) ||
+      !elem_aligned(entropy, 4) || !elem_aligned(top_logp, 4) || !elem_aligned(top_index, 8))
+    return DION3_ERR_ARG;
+  TRY(check_scratch(ws, ws_bytes, logp_scratch(T, (int)n, top)));
+  const Pieces q = pieces_of((int)n);
+  LogpP p = {};
+  p.x = X; p.ldx = ldx; p.target = target; p.target64 = target_bits == 64;
+  p.logp = logp; p.stats = stats; p.entropy = entropy;
+  p.top_logp = top_logp; p.top_index = (long long*)top_index;
+  p.part = (Part*)ws; p.best = (Best*)(p.part + T * q.S);
+  p.T = T; p.n = (int)n; p.top = top; p.S = q.S; p.len = q.len; p.scale = scale;
+  hipStream_t s = (hipStream_t)stream;
+  TraceScope ts("log_probs", 0.0, (double)T * n * size_of(dtype), s);
+  if (dtype == DION3_BF16) HIP_TRY(launch_logp<bf16>(p, q, s));
+  else if (dtype == DION3_F16) HIP_TRY(launch_logp<f16>(p, q, s));
+  else HIP_TRY(launch_logp<float>(p, q, s));
+  return DION3_OK;
+}
+
+dion3_status dion3_log_probs_grad(const float* dlogp, const void* X, int64_t ldx,
+                                  const void* target, int32_t target_bits, const float* stats,
+                                  const float* entropy, const float* dentropy, void* dX,
+                                  int64_t lddx, int64_t T, int64_t n, float scale, int32_t dtype,
+                                  void* stream) {
+  if (!any_type(dtype) || !(scale > 0.0f) || !isfinite(scale)) return DION3_ERR_ARG;
+  TRY(check_sizes(T, n, 1));
+  TRY(check_ld(ldx, n));
+  TRY(check_ld(lddx, n));
+  TRY(check_targets(target, target_bits));
+  if ((target != nullptr) != (dlogp != nullptr) && T > 0) return DION3_ERR_ARG;
+  if (T == 0) return DION3_OK;
+  if (!X || !stats || !dX || (dentropy && !entropy) || (!dlogp && !dentropy)) return DION3_ERR_ARG;
+  const int e = size_of(dtype);
+  if (!elem_aligned(X, e) || !elem_aligned(dX, e) || !elem_aligned(dlogp, 4) ||
+      !elem_aligned(stats, 4) || !elem_aligned(entropy, 4) || !elem_aligned(dentropy, 4))
+    return DION3_ERR_ARG;
+  GradP p = {dlogp, X, target, stats, entropy, dentropy, dX, ldx, lddx, T,
+             target_bits == 64, (int)n, 0, 0, scale};
+  const int most = 256 * 8 * kChunks;
+  p.S = ((int)n + most - 1) / most;
+  p.len = (((int)n + p.S - 1) / p.S + 7) / 8 * 8;
+  hipStream_t s = (hipStream_t)stream;
+  TraceScope ts("log_probs_grad", 0.0, 2.0 * T * n * e, s);
+  if (dtype == DION3_BF16) HIP_TRY(launch_logp_grad<bf16>(p, s));
+  else if (dtype == DION3_F16) HIP_TRY(launch_logp_grad<f16>(p, s));
+  else HIP_TRY(launch_logp_grad<float>(p, s));
+  return DION3_OK;
+}
+
+}  // extern "C"

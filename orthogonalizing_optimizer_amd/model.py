@@ -1,11 +1,12 @@
 """Operators around the layers in a model's training step.
 
 Queries and keys normed per head and rotated by their positions in one pass
-(``qk_norm_rope``), and its gradient.  As in ``layer``, every function is one
-call of libdion3.so (include/dion3.h states the formulas), runs on torch's
-current stream of the tensors' device and takes its workspace from torch's
-allocator per call (or from ``ws``); there is no fallback.
-``qk_norm_rope_layer`` is the differentiable form.
+(``qk_norm_rope``); log probabilities of given tokens with the entropy and the
+best alternatives (``log_probs``); their gradients.  As in ``layer``, every
+function is one call of libdion3.so (include/dion3.h states the formulas), runs
+on torch's current stream of the tensors' device and takes its workspace from
+torch's allocator per call (or from ``ws``); there is no fallback.
+``qk_norm_rope_layer`` and ``token_log_probs`` are the differentiable forms.
 """
 from __future__ import annotations
 
@@ -15,7 +16,7 @@ from typing import Optional
 import torch
 
 from . import _lib
-from .layer import _DTYPES, _call, _ptr, _same, _scratch, _size, _t16, _vector
+from .layer import _DTYPES, _call, _ptr, _rows, _same, _scratch, _size, _t16, _vector
 
 _MAX_STRIDE = 1 << 38
 
@@ -212,3 +213,126 @@ def qk_norm_rope_layer(q, k, q_weight, k_weight, positions, freqs, eps: float = 
     backward pass: q and k as they are."""
     return _QkNormRope.apply(q, k, q_weight, k_weight, positions, freqs, float(eps),
                              bool(interleaved))
+
+
+# ------------------------------------------------------ log probabilities
+
+def _logits(x):
+    if not isinstance(x, torch.Tensor) or x.device.type != "cuda":
+        raise TypeError("logits must be a CUDA (HIP) tensor")
+    if x.dtype not in _DTYPES:
+        raise TypeError("logits must be bfloat16, float16 or float32")
+    return _rows(x, "logits")
+
+
+def _indices(t, shape, device, name):
+    """(t contiguous, its bits): whole numbers, one a token."""
+    if not isinstance(t, torch.Tensor) or t.device != device:
+        raise TypeError(f"{name} must be a tensor on {device}")
+    if t.dtype not in (torch.int64, torch.int32):
+        raise TypeError(f"{name} must be int64 or int32")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    return t.contiguous(), 64 if t.dtype == torch.int64 else 32
+
+
+def _per_row(t, shape, device, name):
+    if not isinstance(t, torch.Tensor) or t.device != device or t.dtype != torch.float32:
+        raise TypeError(f"{name} must be a float32 tensor on {device}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    return t.contiguous()
+
+
+def log_probs(logits, targets=None, scale: float = 1.0, entropy: bool = False, top: int = 0,
+              ws: Optional[_lib.Workspace] = None):
+    """(logp, stats, entropy, top_logp, top_index) of rows of logits [..., n]
+    (bf16, fp16 or fp32) times ``scale`` (one over a temperature), all fp32 but
+    the int64 indices; what is not asked for is None.
+
+    ``targets`` [...] (int64 or int32): logp is their log probability; one
+    outside [0, n) (a padded place's -100) gets 0.  stats [..., 2] holds the
+    maximum m and l = ln sum exp(z - m): their sum is the log of the sum of
+    exponentials, and ``log_probs_grad`` reads them.  ``top`` (up to 64): the
+    best alternatives' log probabilities and indices [..., top], best first,
+    equal logits by their index."""
+    T, n, ld = _logits(logits)
+    lead, device = logits.shape[:-1], logits.device
+    bits = 0
+    logp = H = tl = ti = None
+    if targets is not None:
+        targets, bits = _indices(targets, lead, device, "targets")
+        logp = logits.new_empty(lead, dtype=torch.float32)
+    stats = logits.new_empty(lead + (2,), dtype=torch.float32)
+    if entropy:
+        H = logits.new_empty(lead, dtype=torch.float32)
+    if top:
+        if not 0 < top <= n:
+            raise ValueError(f"top must be between 0 and {n}")
+        tl = logits.new_empty(lead + (top,), dtype=torch.float32)
+        ti = logits.new_empty(lead + (top,), dtype=torch.int64)
+    p, nb, keep = _scratch(ws, _size("dion3_log_probs_workspace_size", T, n, top), device)
+    _call("dion3_log_probs", device, _ptr(logits), ld, _ptr(targets), bits, _ptr(logp), _ptr(stats),
+          _ptr(H), _ptr(tl), _ptr(ti), T, n, top, float(scale), _DTYPES[logits.dtype], p, nb)
+    return logp, stats, H, tl, ti
+
+
+def log_probs_grad(dlogp, logits, targets, stats, scale: float = 1.0, entropy=None, dentropy=None,
+                   out=None):
+    """The gradient in the logits, in their type, from the gradients of logp
+    and (with ``entropy`` and ``dentropy``) of the entropy; ``dlogp`` and
+    ``targets`` may both be None.  ``out``: where it is written, for instance
+    over the logits themselves."""
+    T, n, ld = _logits(logits)
+    lead, device = logits.shape[:-1], logits.device
+    if (dlogp is None) != (targets is None):
+        raise ValueError("dlogp and targets belong together")
+    if dlogp is None and dentropy is None:
+        raise ValueError("need the gradient of logp, of the entropy or of both")
+    bits = 0
+    if targets is not None:
+        targets, bits = _indices(targets, lead, device, "targets")
+        dlogp = _per_row(dlogp, lead, device, "dlogp")
+    stats = _per_row(stats, lead + (2,), device, "stats")
+    if dentropy is not None:
+        if entropy is None:
+            raise ValueError("dentropy needs the entropy")
+        entropy = _per_row(entropy, lead, device, "entropy")
+        dentropy = _per_row(dentropy, lead, device, "dentropy")
+    if out is None:
+        out = logits.new_empty(logits.shape)
+    _same(out, logits, "out", logits.shape)
+    _, _, ldo = _rows(out, "out")
+    _call("dion3_log_probs_grad", device, _ptr(dlogp), _ptr(logits), ld, _ptr(targets), bits,
+          _ptr(stats), _ptr(entropy) if dentropy is not None else None, _ptr(dentropy), _ptr(out),
+          ldo, T, n, float(scale), _DTYPES[logits.dtype])
+    return out
+
+
+class _TokenLogProbs(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, targets, scale, entropy):
+        logp, stats, H, _, _ = log_probs(logits, targets, scale, entropy)
+        ctx.save_for_backward(logits, targets, stats, H)
+        ctx.set_materialize_grads(False)
+        ctx.scale = scale
+        return logp, H
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dlogp, dentropy):
+        logits, targets, stats, H = ctx.saved_tensors
+        if dlogp is None and dentropy is None:
+            return None, None, None, None
+        if dlogp is None:
+            targets = None
+        return (log_probs_grad(dlogp, logits, targets, stats, ctx.scale, H, dentropy),
+                None, None, None)
+
+
+def token_log_probs(logits, targets, scale: float = 1.0, entropy: bool = False):
+    """(logp, entropy) of ``log_probs``, differentiable in the logits; entropy
+    is None unless asked for.  -logp.sum() / count is the cross entropy over
+    the rows whose target is a token.  Kept for the backward pass: the logits
+    and two or three fp32 values a row."""
+    return _TokenLogProbs.apply(logits, targets, float(scale), bool(entropy))
