@@ -451,6 +451,32 @@ DION3_API dion3_status dion3_linear_grad_weight(const void* dZ, int64_t lddz, co
                                                 void* stream);
 
 /* ---------------------------------------------------------------------------
+ * Embedding lookup with scaling, and its gradient.
+ *
+ * token: T integers of token_bits (32 or 64) bits; W: n x m of wtype, Y: T x m
+ * of dtype (each DION3_F32, _BF16 or _F16; wtype is DION3_F32 or dtype).
+ *   Y[t] = scale W[token[t]], rounded once.
+ * A token outside [0, n) stands for none (padding, or a row of another part of
+ * the vocabulary): its row of Y is zeros, and it sends no gradient.
+ *
+ * The gradient: dW[v] = scale times the sum of dY[t] over the t with token[t]
+ * = v (fp32, n x m; zeros for a row without tokens), or with accumulate != 0
+ * that is added to dW, and rows without tokens are neither read nor written.
+ * Sums are held in fp32, without atomics, in an order fixed by the tokens.
+ * Errors: as for the layers' operators; scale must be finite. */
+DION3_API dion3_status dion3_embedding(const void* token, int32_t token_bits, const void* W,
+                                       int64_t ldw, int32_t wtype, void* Y, int64_t ldy, int64_t T,
+                                       int64_t n, int64_t m, float scale, int32_t dtype,
+                                       void* stream);
+DION3_API dion3_status dion3_embedding_grad_workspace_size(int64_t T, int64_t n, int64_t m,
+                                                           size_t* bytes);
+DION3_API dion3_status dion3_embedding_grad(const void* token, int32_t token_bits, const void* dY,
+                                            int64_t lddy, float* dW, int64_t ldw,
+                                            int32_t accumulate, int64_t T, int64_t n, int64_t m,
+                                            float scale, int32_t dtype, void* ws, size_t ws_bytes,
+                                            void* stream);
+
+/* ---------------------------------------------------------------------------
  * Norms of queries and keys per head with the rotation by their positions in
  * the same pass, and the gradient.
  *

@@ -12,8 +12,8 @@ from .clip import clip_grad_norm, grad_norm
 from .layer import (ACTIVATIONS, PackedF8, act_grad, add_rms_norm, add_rms_norm_grad, linear,
                     linear_grad_input, linear_grad_weight, linear_layer, pack_f8,
                     rms_norm_residual, unpack_f8)
-from .model import (log_probs, log_probs_grad, qk_norm_rope, qk_norm_rope_grad,
-                    qk_norm_rope_layer, token_log_probs)
+from .model import (embedding, embedding_grad, embedding_layer, log_probs, log_probs_grad,
+                    qk_norm_rope, qk_norm_rope_grad, qk_norm_rope_layer, token_log_probs)
 from .optim import Dion3, Dion3Step
 
 __all__ = ["MAX_GROUPS", "NS_GRAM", "NS_STANDARD", "PATH_AUTO", "PATH_FUSED", "PATH_TILED",
@@ -24,5 +24,6 @@ __all__ = ["MAX_GROUPS", "NS_GRAM", "NS_STANDARD", "PATH_AUTO", "PATH_FUSED", "P
            "workspace_size_groups", "ACTIVATIONS", "PackedF8", "act_grad", "add_rms_norm",
            "add_rms_norm_grad", "linear", "linear_grad_input", "linear_grad_weight", "linear_layer",
            "pack_f8", "rms_norm_residual", "unpack_f8", "clip_grad_norm", "grad_norm",
-           "log_probs", "log_probs_grad", "qk_norm_rope", "qk_norm_rope_grad", "qk_norm_rope_layer",
-           "token_log_probs", "Dion3", "Dion3Step"]
+           "embedding", "embedding_grad", "embedding_layer", "log_probs", "log_probs_grad",
+           "qk_norm_rope", "qk_norm_rope_grad", "qk_norm_rope_layer", "token_log_probs", "Dion3",
+           "Dion3Step"]

@@ -132,6 +132,10 @@ def _declare(lib):
                                                               c.POINTER(sz)]),
         "dion3_linear_grad_weight": (c.c_int, [vp, i64, vp, i64, vp, vp, i64, i32, i64, i64, i64,
                                                i32, vp, sz, vp]),
+        "dion3_embedding": (c.c_int, [vp, i32, vp, i64, i32, vp, i64, i64, i64, i64, f32, i32, vp]),
+        "dion3_embedding_grad_workspace_size": (c.c_int, [i64, i64, i64, c.POINTER(sz)]),
+        "dion3_embedding_grad": (c.c_int, [vp, i32, vp, i64, vp, i64, i32, i64, i64, i64, f32, i32,
+                                           vp, sz, vp]),
         "dion3_heads_size": (sz, []),
         "dion3_qk_norm_rope": (c.c_int, [c.POINTER(HeadsDesc), c.POINTER(HeadsDesc), vp, vp, i32,
                                          i64, i32, i32, i32, f32, i32, i32, vp]),
@@ -175,6 +179,7 @@ EXPORTED = ("dion3_version", "dion3_ns_cfg_size", "dion3_ns_cfg_default", "dion3
             "dion3_act_grad_workspace_size", "dion3_act_grad",
             "dion3_linear_grad_input_workspace_size", "dion3_linear_grad_input",
             "dion3_linear_grad_weight_workspace_size", "dion3_linear_grad_weight",
+            "dion3_embedding", "dion3_embedding_grad_workspace_size", "dion3_embedding_grad",
             "dion3_heads_size", "dion3_qk_norm_rope", "dion3_qk_norm_rope_grad_workspace_size",
             "dion3_qk_norm_rope_grad", "dion3_log_probs_workspace_size", "dion3_log_probs",
             "dion3_log_probs_grad", "dion3_grad_size", "dion3_grad_norm_workspace_size", "dion3_grad_norm",

@@ -16,7 +16,8 @@ LIB = os.path.join(PKG, "libdion3.so")
 
 SOURCES = ["gemm_f16.hip", "gram_small.hip", "rows.hip", "normalize.hip", "dion3_api.hip", "trace.hip",
            "noalloc.hip", "layer_rows.hip", "layer_gemm.hip", "layer_api.hip",
-           "grad_clip.hip", "heads.hip", "log_probs.hip"]
+           "grad_clip.hip", "heads.hip", "log_probs.hip",
+           "embedding.hip"]
 ARCH = "gfx950"
 
 # Packed-fp32 instructions are switched off for all device code.

@@ -1,0 +1,548 @@
+// Embedding lookup with scaling, and its gradient by sorted tokens.
+//
+//   y_t = E(scale W[token_t]),     dW[v] = scale sum over t with token_t = v of dy_t.
+//
+// The lookup is a copy of rows, bound by HBM.
+//
+// The gradient is summed without atomics, in an order fixed by the tokens:
+// their places are sorted by token, places of one token in order.  The sorted
+// list is cut into chunks of kChunk places, a wave sums the rows of one chunk
+// for 512 columns, and writes a token's sum at the end of its run.  A run that
+// crosses chunks leaves one partial row a chunk, which a last launch adds up
+// in order, so that a token that fills the batch is split as well as others.
+// Rows of dW without a token are cleared by further workgroups of the same
+// launch, which find the tokens of their rows in the sorted list.  Bound by
+// HBM: dW is written once (fp32, most of the bytes), dy read once.
+#include "checks.h"
+
+namespace dion3 {
+namespace {
+
+constexpr int kChunk = 32;            // places of one wave
+constexpr int kZeroRows = 32;         // rows of dW that one workgroup clears
+constexpr int kCountMax = 8192;       // tokens up to which places are counted, not sorted by digits
+constexpr int kTile = 4096;           // tokens of a workgroup of the sort by digits
+
+__device__ __forceinline__ int token_key(const void* tokens, int is64, long long t, int n) {
+  const long long v = is64 ? ((const long long*)tokens)[t] : (long long)((const int*)tokens)[t];
+  return v >= 0 && v < n ? (int)v : n;             // no token: behind all rows
+}
+
+// ------------------------------------------------------------------ the lookup
+
+template <class WT, class E>
+__global__ __launch_bounds__(256) void k_embed(const void* __restrict__ tokens, int is64,
+                                               const WT* __restrict__ w, long long ldw,
+                                               E* __restrict__ y, long long ldy, long long chunks,
+                                               int n, int m, unsigned nch, float scale) {
+  const long long base = flat_base();
+  if (base + threadIdx.x >= chunks) return;
+  const long long row0 = base / nch;
+  const unsigned c0 = (unsigned)(base - row0 * nch) + threadIdx.x, dr = c0 / nch;
+  const int c = (int)(c0 - dr * nch) * 8;
+  const int key = token_key(tokens, is64, row0 + dr, n);
+  float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  if (key < n) {
+    load8(w + key * ldw, c, m, v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] *= scale;
+  }
+  store8(y + (row0 + dr) * ldy, c, m, v);
+}
+
+// ------------------------------------------------------------ places by token
+
+// Up to kCountMax tokens: the place of t in the order is the number of tokens
+// before it, counted by comparing all with all (two instructions a pair).  A
+// workgroup places 32 tokens; 8 groups of 32 lanes take an eighth of the keys
+// each, in blocks of 32: a block before the workgroup's own counts keys up to
+// the token's, one behind it keys below, its own both by their places.
+__global__ __launch_bounds__(256) void k_embed_count(const void* __restrict__ tokens, int is64,
+                                                     int T, int n, int* __restrict__ skey,
+                                                     int* __restrict__ spos) {
+  extern __shared__ __attribute__((aligned(16))) int keys[];    // padded to whole blocks with n + 1
+  __shared__ int part[8][32];
+  const int nb = (T + 31) / 32;
+  for (int i = threadIdx.x; i < nb * 32; i += 256) keys[i] = i < T ? token_key(tokens, is64, i, n) : n + 1;
+  __syncthreads();
+  const int mine = threadIdx.x & 31, group = threadIdx.x >> 5, own = blockIdx.x;
+  const int key = keys[own * 32 + mine];
+  int cnt = 0;
+  for (int b = group; b < nb; b += 8) {
+    const int lim = key + (b < own ? 1 : 0);
+    const int4* k4 = (const int4*)(keys + b * 32);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int4 k = k4[i];
+      cnt += (k.x < lim) + (k.y < lim) + (k.z < lim) + (k.w < lim);
+    }
+  }
+  if (group == (own & 7)) {
+    for (int i = 0; i < mine; ++i) cnt += keys[own * 32 + i] == key;
+  }
+  part[group][mine] = cnt;
+  __syncthreads();
+  const int t = own * 32 + mine;
+  if (group == 0 && t < T) {
+    for (int g = 1; g < 8; ++g) cnt += part[g][mine];
+    skey[cnt] = key;
+    spos[cnt] = t;
+  }
+}
+
+// More tokens: a stable sort by digits of 8 bits, the lowest first.  Per digit:
+// a histogram of every tile, an exclusive scan over (digit, tile), and the
+// tiles' tokens to their places.  The first digit reads the tokens themselves.
+struct DigitP {
+  const void* tokens; int is64;       // first digit, else null
+  const int* key; const int* pos;
+  int* okey; int* opos;
+  int* hist;                          // [256][tiles]
+  long long T;
+  int n, tiles, shift;
+};
+__device__ __forceinline__ int digit_key(const DigitP& p, long long i) {
+  return p.tokens ? token_key(p.tokens, p.is64, i, p.n) : p.key[i];
+}
+
+__global__ __launch_bounds__(256) void k_embed_hist(DigitP p) {
+  __shared__ int h[256];
+  h[threadIdx.x] = 0;
+  __syncthreads();
+  const long long from = (long long)blockIdx.x * kTile;
+  for (int i = threadIdx.x; i < kTile; i += 256)
+    if (from + i < p.T) atomicAdd(&h[digit_key(p, from + i) >> p.shift & 255], 1);
+  __syncthreads();
+  p.hist[(long long)threadIdx.x * p.tiles + blockIdx.x] = h[threadIdx.x];
+}
+
+__global__ __launch_bounds__(1024) void k_embed_scan(int* __restrict__ hist, int count) {
+  __shared__ int sums[16];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int carry = 0;
+  for (int from = 0; from < count; from += 4096) {          // 4 entries a thread
+    int v[4], s = 0;
+    const int at = from + (int)threadIdx.x * 4;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v[k] = at + k < count ? hist[at + k] : 0;
+      s += v[k];
+    }
+    int run = s;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int u = __shfl_up(run, o, 64);
+      if (lane >= o) run += u;
+    }
+    if (lane == 63) sums[wave] = run;
+    __syncthreads();
+    int before = carry, all = 0;
+    for (int i = 0; i < 16; ++i) {
+      if (i < wave) before += sums[i];
+      all += sums[i];
+    }
+    before += run - s;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (at + k < count) hist[at + k] = before;
+      before += v[k];
+    }
+    carry += all;
+    __syncthreads();
+  }
+}
+
+__global__ __launch_bounds__(256) void k_embed_place(DigitP p) {
+  __shared__ int count[4][256];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) count[i][threadIdx.x] = 0;
+  __syncthreads();
+  // a wave takes 1024 tokens in order, 64 at a time
+  const long long from = (long long)blockIdx.x * kTile + wave * 1024;
+  const unsigned long long below = (1ull << lane) - 1;
+  int key[16], pos[16], at[16];
+#pragma unroll
+  for (int r = 0; r < 16; ++r) {
+    const long long i = from + r * 64 + lane;
+    const bool in = i < p.T;
+    key[r] = in ? digit_key(p, i) : 0;
+    pos[r] = in ? (p.tokens ? (int)i : p.pos[i]) : 0;
+    const int dig = key[r] >> p.shift & 255;
+    unsigned long long same = __ballot(in);
+#pragma unroll
+    for (int b = 0; b < 8; ++b) {
+      const unsigned long long w = __ballot(dig >> b & 1);
+      same &= dig >> b & 1 ? w : ~w;
+    }
+    const int rank = __popcll(same & below);
+    volatile int* c = &count[wave][dig];
+    const int had = *c;
+    __builtin_amdgcn_wave_barrier();
+    if (in && rank == 0) *c = had + __popcll(same);
+    __builtin_amdgcn_wave_barrier();
+    at[r] = had + rank;
+  }
+  __syncthreads();
+  {                                   // the waves' counts to their first places
+    int first = p.hist[(long long)threadIdx.x * p.tiles + blockIdx.x];
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const int c = count[w][threadIdx.x];
+      count[w][threadIdx.x] = first;
+      first += c;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < 16; ++r) {
+    if (from + r * 64 + lane >= p.T) continue;
+    const int to = count[wave][key[r] >> p.shift & 255] + at[r];
+    p.okey[to] = key[r];
+    p.opos[to] = pos[r];
+  }
+}
+
+// --------------------------------------------------------------- the gradient
+
+struct EmbedGradP {
+  const void* dy; long long lddy;
+  const int* key; const int* pos;     // sorted
+  float* dw; long long ldw;
+  float* part;                        // [chunks][2][m]: a run from before, one that goes on
+  long long T, sum_blocks;
+  int n, m, slices;                   // slices of 512 columns
+  float scale;
+  int accumulate;
+};
+
+__device__ __forceinline__ void put_row(const EmbedGradP& p, int row, int c, float (&v)[8]) {
+  float* d = p.dw + row * p.ldw;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] *= p.scale;
+  if (p.accumulate) {
+    float o[8];
+    load8(d, c, p.m, o);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] += o[e];
+  }
+  store8(d, c, p.m, v);
+}
+
+// One wave: chunk x slice.
+template <class E>
+__device__ __forceinline__ void sum_chunk(const EmbedGradP& p, long long chunk, int slice) {
+  const int lane = threadIdx.x & 63, c = slice * 512 + lane * 8;
+  const long long from = chunk * kChunk;
+  const int cnt = (int)(p.T - from < kChunk ? p.T - from : kChunk);
+  const int k = lane < cnt ? p.key[from + lane] : p.n;
+  const int at = lane < cnt ? p.pos[from + lane] : 0;
+  const int before = from > 0 ? p.key[from - 1] : -1;
+  const int behind = from + kChunk < p.T ? p.key[from + kChunk] : -1;
+  float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  bool head = __builtin_amdgcn_readlane(k, 0) == before;
+  constexpr int U = 8;
+  for (int i0 = 0; i0 < cnt; i0 += U) {
+    Raw8<E> raw[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (i0 + u >= cnt) continue;
+      const E* row = (const E*)p.dy + __builtin_amdgcn_readlane(at, i0 + u) * p.lddy;
+      if (c < p.m) raw[u] = fetch8(row, c, p.m);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u;
+      if (i >= cnt) continue;
+      const int key = __builtin_amdgcn_readlane(k, i);
+      if (key == p.n) return;                       // no tokens from here on
+      if (c < p.m) {
+        float v[8];
+        chunk8(raw[u], c, p.m, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] += v[e];
+      }
+      const int next = i + 1 < cnt ? __builtin_amdgcn_readlane(k, i + 1) : -1;
+      if (next == key) continue;
+      const bool tail = i + 1 == cnt && behind == key;
+      if (c < p.m) {
+        if (head || tail) store8(p.part + (chunk * 2 + (head ? 0 : 1)) * p.m, c, p.m, acc);
+        else put_row(p, key, c, acc);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
+      head = false;
+    }
+  }
+}
+
+// The first of the sorted keys that is v or above, by 64 probes at a time (the
+// whole wave takes part).
+__device__ __forceinline__ long long first_at(const int* __restrict__ key, long long T, int v) {
+  const int lane = threadIdx.x & 63;
+  long long lo = 0, len = T;                        // the answer lies in [lo, lo + len]
+  while (len > 0) {
+    const long long step = (len + 63) / 64, i = lo + (lane + 1) * step - 1;
+    const bool less = i < lo + len && key[i] < v;
+    const int c = __popcll(__ballot(less));         // probes below v: their stretches are too
+    const long long left = len - c * step;
+    lo += c * step;
+    len = left < step - 1 ? left : step - 1;
+    if (len < 0) len = 0;
+  }
+  return lo;
+}
+
+template <class E>
+__global__ __launch_bounds__(256) void k_embed_grad(EmbedGradP p) {
+  const int wave = threadIdx.x >> 6;
+  const long long block = (long long)blockIdx.y * gridDim.x + blockIdx.x;
+  if (block < p.sum_blocks) {
+    const long long task = block * 4 + wave, chunk = task / p.slices;
+    if (chunk * kChunk >= p.T) return;
+    sum_chunk<E>(p, chunk, (int)(task - chunk * p.slices));
+    return;
+  }
+  __shared__ long long ends[2];
+  __shared__ int there[kZeroRows];
+  const long long v0 = (block - p.sum_blocks) * kZeroRows;
+  if (v0 >= p.n || p.accumulate) return;            // (a grid may hold more blocks than asked for)
+  const int rows = (int)(p.n - v0 < kZeroRows ? p.n - v0 : kZeroRows);
+  if (wave < 2) {
+    const long long at = first_at(p.key, p.T, (int)v0 + (wave ? rows : 0));
+    if ((threadIdx.x & 63) == 0) ends[wave] = at;
+  }
+  __syncthreads();
+  if ((int)threadIdx.x < rows) {
+    long long lo = ends[0], hi = ends[1];
+    const int v = (int)v0 + threadIdx.x;
+    const long long end = hi;
+    while (lo < hi) {
+      const long long mid = (lo + hi) / 2;
+      if (p.key[mid] < v) lo = mid + 1;
+      else hi = mid;
+    }
+    there[threadIdx.x] = lo < end && p.key[lo] == v;
+  }
+  __syncthreads();
+  const float zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  for (int r = 0; r < rows; ++r) {
+    if (there[r]) continue;
+    float* row = p.dw + (v0 + r) * p.ldw;
+    for (int c = threadIdx.x * 8; c < p.m; c += 2048) store8(row, c, p.m, zero);
+  }
+}
+
+// The runs that cross chunks: the workgroup of the chunk in which one begins
+// adds up its partial rows, 256 columns a wave across, the 4 waves a quarter
+// of the rows each.
+__global__ __launch_bounds__(256) void k_embed_join(EmbedGradP p, long long chunks) {
+  __shared__ float sh[3][64][4];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const long long block = (long long)blockIdx.y * gridDim.x + blockIdx.x;
+  const int cols = (p.m + 255) / 256;
+  const long long c0 = block / cols, from = c0 * kChunk;
+  if (c0 >= chunks) return;
+  const long long last = from + kChunk - 1;
+  if (last + 1 >= p.T) return;                                    // the last chunk
+  const int key = p.key[last];
+  if (key == p.n || p.key[last + 1] != key) return;               // no run goes on
+  if (p.key[from] == key && from > 0 && p.key[from - 1] == key) return;   // begun before
+  const long long end = first_at(p.key, p.T, key + 1);            // one behind the run
+  const long long c1 = (end - 1) / kChunk;                        // its last chunk
+  const int c = (int)(block - c0 * cols) * 256 + lane * 4;
+  const long long count = c1 - c0 + 1, per = (count + 3) / 4;
+  const long long a = wave * per, b = a + per < count ? a + per : count;
+  float v[4] = {0, 0, 0, 0};
+  const bool vec = c + 4 <= p.m;
+  struct __attribute__((packed, aligned(4))) F4 { float x[4]; };
+#pragma unroll 8
+  for (long long i = a; i < b; ++i) {
+    const float* row = p.part + ((c0 + i) * 2 + (i == 0 ? 1 : 0)) * p.m;
+    if (vec) {
+      const F4 f = *(const F4*)(row + c);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] += f.x[e];
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (c + e < p.m) v[e] += row[c + e];
+    }
+  }
+  if (wave > 0) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sh[wave - 1][lane][e] = v[e];
+  }
+  __syncthreads();
+  if (wave > 0) return;
+  for (int w = 0; w < 3; ++w)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] += sh[w][lane][e];
+  float* d = p.dw + key * p.ldw;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (c + e < p.m) d[c + e] = p.accumulate ? d[c + e] + p.scale * v[e] : p.scale * v[e];
+}
+
+// --------------------------------------------------------------- the launches
+
+dim3 grid_of(long long blocks) {
+  const long long row = 1LL << 21;
+  return blocks <= row ? dim3((unsigned)blocks)
+                       : dim3((unsigned)row, (unsigned)((blocks + row - 1) / row));
+}
+
+// The workspace: sorted keys and places (twice for the sort by digits, which
+// swaps them, and its histograms), then the partial rows.
+struct EmbedPlan {
+  int digits, tiles;
+  long long chunks;
+  size_t at_hist, at_part, bytes;
+};
+EmbedPlan plan_embed(long long T, int n, int m) {
+  EmbedPlan q = {};
+  q.chunks = (T + kChunk - 1) / kChunk;
+  const size_t list = (size_t)pad_to(T, 64) * 4;
+  size_t b = 2 * list;
+  if (T > kCountMax) {
+    q.tiles = (int)((T + kTile - 1) / kTile);
+    for (int k = n; k; k >>= 8) ++q.digits;        // keys 0 .. n
+    b += 2 * list;
+    q.at_hist = b;
+    b += (size_t)q.tiles * 1024;
+  }
+  q.at_part = b;
+  q.bytes = T ? b + (size_t)q.chunks * 2 * m * 4 : 0;
+  return q;
+}
+
+hipError_t sort_tokens(const void* tokens, int is64, long long T, int n, const EmbedPlan& q,
+                       char* ws, const int*& key, const int*& pos, hipStream_t s) {
+  const size_t list = (size_t)pad_to(T, 64) * 4;
+  int* buf[2][2] = {{(int*)ws, (int*)(ws + list)}, {(int*)(ws + 2 * list), (int*)(ws + 3 * list)}};
+  if (!q.digits) {
+    hipLaunchKernelGGL(k_embed_count, dim3((unsigned)((T + 31) / 32)), dim3(256),
+                       (size_t)pad_to(T, 32) * 4, s, tokens, is64, (int)T, n, buf[0][0], buf[0][1]);
+    key = buf[0][0];
+    pos = buf[0][1];
+    return hipGetLastError();
+  }
+  for (int d = 0; d < q.digits; ++d) {
+    const int o = d & 1;
+    const DigitP p = {d ? nullptr : tokens, is64, buf[1 - o][0], buf[1 - o][1], buf[o][0], buf[o][1],
+                      (int*)(ws + q.at_hist), T, n, q.tiles, 8 * d};
+    hipLaunchKernelGGL(k_embed_hist, dim3(q.tiles), dim3(256), 0, s, p);
+    hipLaunchKernelGGL(k_embed_scan, dim3(1), dim3(1024), 0, s, p.hist, 256 * q.tiles);
+    hipLaunchKernelGGL(k_embed_place, dim3(q.tiles), dim3(256), 0, s, p);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    key = buf[o][0];
+    pos = buf[o][1];
+  }
+  return hipSuccess;
+}
+
+template <class WT, class E>
+hipError_t launch_embed(const void* tokens, int is64, const void* W, long long ldw, void* Y,
+                        long long ldy, long long T, int n, int m, float scale, hipStream_t s) {
+  const unsigned nch = (unsigned)((m + 7) / 8);
+  const long long chunks = T * nch;
+  hipLaunchKernelGGL((k_embed<WT, E>), flat_grid(chunks), dim3(256), 0, s, tokens, is64,
+                     (const WT*)W, ldw, (E*)Y, ldy, chunks, n, m, nch, scale);
+  return hipGetLastError();
+}
+
+bool any_type(int t) { return type16(t) || t == DION3_F32; }
+int size_of(int t) { return t == DION3_F32 ? 4 : 2; }
+
+dion3_status check_tokens(const void* tokens, int bits, int64_t T) {
+  if (bits != 32 && bits != 64) return DION3_ERR_ARG;
+  if (T > 0 && (!tokens || !elem_aligned(tokens, bits / 8))) return DION3_ERR_ARG;
+  return DION3_OK;
+}
+
+}  // namespace
+}  // namespace dion3
+
+using namespace dion3;
+
+extern "C" {
+
+dion3_status dion3_embedding(const void* tokens, int32_t token_bits, const void* W, int64_t ldw,
+                             int32_t wtype, void* Y, int64_t ldy, int64_t T, int64_t n, int64_t m,
+                             float scale, int32_t dtype, void* stream) {
+  if (!any_type(dtype) || (wtype != DION3_F32 && wtype != dtype) || !isfinite(scale))
+    return DION3_ERR_ARG;
+  TRY(check_sizes(T, n, m));
+  TRY(check_ld(ldw, m));
+  TRY(check_ld(ldy, m));
+  TRY(check_tokens(tokens, token_bits, T));
+  if (T == 0) return DION3_OK;
+  if (!W || !Y || !elem_aligned(W, size_of(wtype)) || !elem_aligned(Y, size_of(dtype)))
+    return DION3_ERR_ARG;
+  hipStream_t s = (hipStream_t)stream;
+  const int is64 = token_bits == 64, N = (int)n, M = (int)m;
+  TraceScope ts("embedding", 0.0, (double)T * m * (size_of(wtype) + size_of(dtype)), s);
+  if (wtype == DION3_F32) {
+    if (dtype == DION3_F32) HIP_TRY((launch_embed<float, float>(tokens, is64, W, ldw, Y, ldy, T, N, M, scale, s)));
+    else if (dtype == DION3_BF16) HIP_TRY((launch_embed<float, bf16>(tokens, is64, W, ldw, Y, ldy, T, N, M, scale, s)));
+    else HIP_TRY((launch_embed<float, f16>(tokens, is64, W, ldw, Y, ldy, T, N, M, scale, s)));
+  } else if (dtype == DION3_BF16) {
+    HIP_TRY((launch_embed<bf16, bf16>(tokens, is64, W, ldw, Y, ldy, T, N, M, scale, s)));
+  } else {
+    HIP_TRY((launch_embed<f16, f16>(tokens, is64, W, ldw, Y, ldy, T, N, M, scale, s)));
+  }
+  return DION3_OK;
+}
+
+dion3_status dion3_embedding_grad_workspace_size(int64_t T, int64_t n, int64_t m, size_t* bytes) {
+  if (!bytes) return DION3_ERR_ARG;
+  TRY(check_sizes(T, n, m));
+  *bytes = plan_embed(T, (int)n, (int)m).bytes;
+  return DION3_OK;
+}
+
+dion3_status dion3_embedding_grad(const void* tokens, int32_t token_bits, const void* dY,
+                                  int64_t lddy, float* dW, int64_t ldw, int32_t accumulate,
+                                  int64_t T, int64_t n, int64_t m, float scale, int32_t dtype,
+                                  void* ws, size_t ws_bytes, void* stream) {
+  if (!any_type(dtype) || !isfinite(scale)) return DION3_ERR_ARG;
+  TRY(check_sizes(T, n, m));
+  TRY(check_ld(lddy, m));
+  TRY(check_ld(ldw, m));
+  TRY(check_tokens(tokens, token_bits, T));
+  if (!dW || !elem_aligned(dW, 4)) return DION3_ERR_ARG;
+  if (T > 0 && (!dY || !elem_aligned(dY, size_of(dtype)))) return DION3_ERR_ARG;
+  const EmbedPlan q = plan_embed(T, (int)n, (int)m);
+  TRY(check_scratch(ws, ws_bytes, q.bytes));
+  if (T == 0 && accumulate) return DION3_OK;
+  hipStream_t s = (hipStream_t)stream;
+  EmbedGradP p = {};
+  p.dy = dY; p.lddy = lddy; p.dw = dW; p.ldw = ldw;
+  p.T = T; p.n = (int)n; p.m = (int)m; p.slices = (int)((m + 511) / 512);
+  p.scale = scale; p.accumulate = accumulate != 0;
+  p.part = (float*)((char*)ws + q.at_part);
+  if (T > 0) {
+    TraceScope ts("embedding_sort", 0.0, 16.0 * T, s);
+    HIP_TRY(sort_tokens(tokens, token_bits == 64, T, (int)n, q, (char*)ws, p.key, p.pos, s));
+  }
+  p.sum_blocks = (q.chunks * p.slices + 3) / 4;
+  const long long zero_blocks = accumulate ? 0 : (n + kZeroRows - 1) / kZeroRows;
+  {
+    TraceScope ts("embedding_grad", 0.0, (double)T * m * size_of(dtype) + 4.0 * (accumulate ? 0 : n) * m, s);
+    const dim3 grid = grid_of(p.sum_blocks + zero_blocks);
+    if (dtype == DION3_BF16) hipLaunchKernelGGL((k_embed_grad<bf16>), grid, dim3(256), 0, s, p);
+    else if (dtype == DION3_F16) hipLaunchKernelGGL((k_embed_grad<f16>), grid, dim3(256), 0, s, p);
+    else hipLaunchKernelGGL((k_embed_grad<float>), grid, dim3(256), 0, s, p);
+    HIP_TRY(hipGetLastError());
+  }
+  if (q.chunks > 1) {
+    TraceScope ts("embedding_join", 0.0, 0.0, s);
+    hipLaunchKernelGGL(k_embed_join, grid_of(q.chunks * ((m + 255) / 256)), dim3(256), 0, s, p,
+                       q.chunks);
+    HIP_TRY(hipGetLastError());
+  }
+  return DION3_OK;
+}
+
+}  // extern "C"

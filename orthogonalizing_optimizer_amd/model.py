@@ -1,12 +1,13 @@
 """Operators around the layers in a model's training step.
 
-Queries and keys normed per head and rotated by their positions in one pass
-(``qk_norm_rope``); log probabilities of given tokens with the entropy and the
+Tokens' rows of an embedding (``embedding``); queries and keys normed per head
+and rotated by their positions in one pass (``qk_norm_rope``); log probabilities of given tokens with the entropy and the
 best alternatives (``log_probs``); their gradients.  As in ``layer``, every
 function is one call of libdion3.so (include/dion3.h states the formulas), runs
 on torch's current stream of the tensors' device and takes its workspace from
 torch's allocator per call (or from ``ws``); there is no fallback.
-``qk_norm_rope_layer`` and ``token_log_probs`` are the differentiable forms.
+``embedding_layer``, ``qk_norm_rope_layer`` and ``token_log_probs`` are the
+differentiable forms.
 """
 from __future__ import annotations
 
@@ -16,7 +17,7 @@ from typing import Optional
 import torch
 
 from . import _lib
-from .layer import _DTYPES, _call, _ptr, _rows, _same, _scratch, _size, _t16, _vector
+from .layer import _DTYPES, _as_rows, _call, _matrix, _ptr, _rows, _same, _scratch, _size, _t16, _vector
 
 _MAX_STRIDE = 1 << 38
 
@@ -34,6 +35,88 @@ def _lead(shape, strides, name):
             raise ValueError(f"{name}: its leading dimensions do not share one stride")
         n *= size
     return n, ld
+
+
+# ----------------------------------------------------------- embedding
+
+def _indices(t, shape, device, name):
+    """(t contiguous, its bits): whole numbers, one a token."""
+    if not isinstance(t, torch.Tensor) or t.device != device:
+        raise TypeError(f"{name} must be a tensor on {device}")
+    if t.dtype not in (torch.int64, torch.int32):
+        raise TypeError(f"{name} must be int64 or int32")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    return t.contiguous(), 64 if t.dtype == torch.int64 else 32
+
+
+def embedding(tokens, w, scale: float = 1.0, dtype=None):
+    """scale * w[tokens], rounded once to ``dtype``: [..., m] for tokens [...]
+    (int64 or int32) and w [n, m].  ``dtype`` is w's type (the default) or, for
+    fp32 w, also bf16 or fp16.  A token outside [0, n) stands for none: its row
+    is zeros."""
+    if not isinstance(w, torch.Tensor) or w.device.type != "cuda":
+        raise TypeError("w must be a CUDA (HIP) tensor")
+    dtype = w.dtype if dtype is None else dtype
+    if w.dtype not in _DTYPES or dtype not in _DTYPES or w.dtype not in (torch.float32, dtype):
+        raise TypeError("w must be float32 or of dtype, dtype float32, bfloat16 or float16")
+    n, m, ldw = _matrix(w, w, "w")
+    if not isinstance(tokens, torch.Tensor):
+        raise TypeError(f"tokens must be a tensor on {w.device}")
+    tokens, bits = _indices(tokens, tokens.shape, w.device, "tokens")
+    y = w.new_empty(tokens.shape + (m,), dtype=dtype)
+    _call("dion3_embedding", w.device, _ptr(tokens), bits, _ptr(w), ldw, _DTYPES[w.dtype], _ptr(y), m,
+          tokens.numel(), n, m, float(scale), _DTYPES[dtype])
+    return y
+
+
+def embedding_grad(tokens, dy, n: int, scale: float = 1.0, out=None, accumulate: bool = False,
+                   ws: Optional[_lib.Workspace] = None):
+    """The gradient of ``embedding`` in its n rows, fp32: row v is scale times
+    the sum of the rows of dy whose token is v (the same bits for the same
+    tokens and dy).  With ``out`` (fp32 [n, m], contiguous rows) it is written
+    there, and with ``accumulate`` added to it (a tied head's gradient, say):
+    rows without tokens are then left alone."""
+    if not isinstance(dy, torch.Tensor) or dy.device.type != "cuda":
+        raise TypeError("dy must be a CUDA (HIP) tensor")
+    if dy.dtype not in _DTYPES:
+        raise TypeError("dy must be bfloat16, float16 or float32")
+    T, m, lddy = _rows(dy, "dy")
+    tokens, bits = _indices(tokens, dy.shape[:-1], dy.device, "tokens")
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs out")
+        out = dy.new_empty((n, m), dtype=torch.float32)
+    if not isinstance(out, torch.Tensor) or out.device != dy.device or out.dtype != torch.float32:
+        raise TypeError(f"out must be a float32 tensor on {dy.device}")
+    if tuple(out.shape) != (n, m):
+        raise ValueError(f"out must have shape {(n, m)}")
+    _, _, ldw = _rows(out, "out")
+    p, nb, keep = _scratch(ws, _size("dion3_embedding_grad_workspace_size", T, n, m), dy.device)
+    _call("dion3_embedding_grad", dy.device, _ptr(tokens), bits, _ptr(dy), lddy, _ptr(out), ldw,
+          int(bool(accumulate)), T, n, m, float(scale), _DTYPES[dy.dtype], p, nb)
+    return out
+
+
+class _Embedding(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, w, tokens, scale, dtype):
+        ctx.save_for_backward(tokens)
+        ctx.scale, ctx.n, ctx.wtype = scale, w.shape[0], w.dtype
+        return embedding(tokens, w, scale, dtype)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        tokens, = ctx.saved_tensors
+        dw = embedding_grad(tokens, _as_rows(dy), ctx.n, ctx.scale)
+        return dw.to(ctx.wtype), None, None, None
+
+
+def embedding_layer(tokens, w, scale: float = 1.0, dtype=None):
+    """``embedding``, differentiable in w (a dense gradient of w's type, summed
+    in fp32)."""
+    return _Embedding.apply(w, tokens, float(scale), dtype)
 
 
 # ------------------------------------------------- heads: norm and rotation
@@ -223,17 +306,6 @@ def _logits(x):
     if x.dtype not in _DTYPES:
         raise TypeError("logits must be bfloat16, float16 or float32")
     return _rows(x, "logits")
-
-
-def _indices(t, shape, device, name):
-    """(t contiguous, its bits): whole numbers, one a token."""
-    if not isinstance(t, torch.Tensor) or t.device != device:
-        raise TypeError(f"{name} must be a tensor on {device}")
-    if t.dtype not in (torch.int64, torch.int32):
-        raise TypeError(f"{name} must be int64 or int32")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    return t.contiguous(), 64 if t.dtype == torch.int64 else 32
 
 
 def _per_row(t, shape, device, name):
