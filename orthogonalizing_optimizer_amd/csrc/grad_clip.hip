@@ -5,17 +5,18 @@
 //   c = norm <= max_norm ? 1 : max_norm / norm,
 //   g <- E(c scale g)   or   M <- fp32(M + c scale g).
 //
-// Bound by HBM: the norm reads every gradient once, the second pass reads it
-// again (2^28 elements pass the 256 MB cache) and writes it, or reads and
-// writes the sums.  Squares are summed in 64 bits: no gradient of a 16- or
+// Bound by HBM: the norm reads every gradient once (303 M bf16 elements 104 us,
+// 5.8 TB/s), the second pass reads it again (such sizes pass the 256 MB cache)
+// and writes it, or reads and writes the sums (both passes 675 us, 5.4 TB/s).  Squares are summed in 64 bits: no gradient of a 16- or
 // 32-bit type leaves their range, and a conversion and a 64-bit fma an element
 // take less than the element's time on HBM.  So do the products with c, whose
 // factor leaves fp32's normal range where gradients are huge.
 //
 // A workgroup takes one chunk of one tensor and leaves one partial sum; the
-// second pass adds all partial sums up in every workgroup, in one order, so no
-// launch stands between the two and no atomics are needed.  Chunks are as long
-// as about 2048 partial sums make them (16 KB to add up).  The tensors' table
+// second pass adds all partial sums up in every workgroup, in one order, so
+// that no launch stands between the two and no atomics are needed.  Where that
+// would be more than about 2048 (16 KB for each workgroup to read), one
+// workgroup adds them up in between.  The tensors' table
 // travels in the kernel's arguments, kBatch tensors a launch: nothing is
 // copied to the device, so a call can be captured.
 #include "checks.h"
@@ -25,7 +26,8 @@ namespace {
 
 constexpr int kBatch = 56;              // 56 bytes each: 3.1 KB of arguments
 constexpr long long kChunkMin = 8192;   // elements; a multiple of 256 threads x 8
-constexpr int kPartials = 2048;
+constexpr long long kChunkMax = 32768;
+constexpr int kPartials = 2048;         // partial sums that every workgroup adds up by itself
 
 struct Entry {
   void* g; float* m;
@@ -38,13 +40,14 @@ struct Table {
   long long chunk;                      // elements
 };
 
-// The entry whose chunk this workgroup has, and the chunk's elements [lo, hi).
-__device__ __forceinline__ const Entry& my_entry(const Table& t, long long& lo, long long& hi) {
+// The entry that a chunk belongs to, and the chunk's elements [lo, hi).
+__device__ __forceinline__ const Entry& my_entry(const Table& t, int chunk, long long& lo,
+                                                 long long& hi) {
   const int lane = threadIdx.x & 63;
-  const bool mine = lane < t.count && t.e[lane < t.count ? lane : 0].chunk0 <= (int)blockIdx.x;
+  const bool mine = lane < t.count && t.e[lane < t.count ? lane : 0].chunk0 <= chunk;
   const int i = __builtin_amdgcn_readfirstlane(__popcll(__ballot(mine)) - 1);
   const Entry& e = t.e[i];
-  lo = ((long long)blockIdx.x - e.chunk0) * t.chunk;
+  lo = ((long long)chunk - e.chunk0) * t.chunk;
   hi = lo + t.chunk < e.n ? lo + t.chunk : e.n;
   return e;
 }
@@ -115,7 +118,7 @@ __device__ __forceinline__ double sum_squares(const Entry& e, long long lo, long
 __global__ __launch_bounds__(256) void k_grad_squares(Table t, double* __restrict__ part) {
   __shared__ double sh[4];
   long long lo, hi;
-  const Entry& e = my_entry(t, lo, hi);
+  const Entry& e = my_entry(t, blockIdx.x, lo, hi);
   double s;
   if (e.dtype == DION3_F32) s = sum_squares<float>(e, lo, hi);
   else if (e.dtype == DION3_BF16) s = sum_squares<bf16>(e, lo, hi);
@@ -124,13 +127,22 @@ __global__ __launch_bounds__(256) void k_grad_squares(Table t, double* __restric
   if (threadIdx.x == 0) part[t.part0 + blockIdx.x] = s;
 }
 
-// scale times the root of the sum of part[0 .. n), the same bits in every thread.
-__device__ __forceinline__ double norm_of(const double* __restrict__ part, int n, float scale,
-                                          double* sh) {
+// The sum of part[0 .. n), the same bits in every thread.
+__device__ __forceinline__ double total_of(const double* __restrict__ part, int n, double* sh) {
   double s = 0.0;
 #pragma unroll 8
   for (int i = threadIdx.x; i < n; i += 256) s += part[i];
-  return sqrt(block_sum(s, sh)) * (double)scale;
+  return block_sum(s, sh);
+}
+__device__ __forceinline__ double norm_of(double total, float scale) {
+  return sqrt(total) * (double)scale;
+}
+
+// Many partial sums to one.
+__global__ __launch_bounds__(256) void k_grad_total(double* __restrict__ part, int n) {
+  __shared__ double sh[4];
+  const double v = total_of(part, n, sh);
+  if (threadIdx.x == 0) part[n] = v;
 }
 
 // Norms of single tensors (blocks: the tensors of the table) or of all of them.
@@ -141,7 +153,7 @@ __global__ __launch_bounds__(256) void k_grad_norm(Ranges r, const double* __res
                                                    float scale, float* __restrict__ out) {
   __shared__ double sh[4];
   const int b = r.begin[blockIdx.x], e = r.begin[blockIdx.x + 1];
-  const double v = norm_of(part + b, e - b, scale, sh);
+  const double v = norm_of(total_of(part + b, e - b, sh), scale);
   if (threadIdx.x == 0) out[blockIdx.x] = (float)v;
 }
 
@@ -162,16 +174,27 @@ __device__ __forceinline__ void scale_chunk(const Entry& e, long long lo, long l
     }
     return;
   }
-  typedef float fw __attribute__((ext_vector_type(W)));
-  struct __attribute__((packed, aligned(4))) FAny { fw v; };
+  // W sums.  They pass by once, and nontemporally leave the cache to the
+  // gradients (303 M elements from bf16: 675 us, 693 with plain accesses)
+  typedef float f4 __attribute__((ext_vector_type(4), aligned(4)));
+  struct Sums { f4 q[W / 4]; };
+  auto load = [&](long long at) {
+    Sums r;
+#pragma unroll
+    for (int k = 0; k < W / 4; ++k) r.q[k] = __builtin_nontemporal_load((const f4*)(m + at) + k);
+    return r;
+  };
   constexpr int S = 256 * W;
   long long i = lo + threadIdx.x * W;
-  auto one = [&](const typename Vec<E>::type& v, long long at, const fw& s) {
+  auto one = [&](const typename Vec<E>::type& v, long long at, Sums s) {
     if (m) {
-      fw o;
 #pragma unroll
-      for (int k = 0; k < W; ++k) o[k] = (float)__builtin_fma((double)to_f32((E)v[k]), c, (double)s[k]);
-      ((FAny*)(m + at))->v = o;
+      for (int k = 0; k < W; ++k) {
+        float& x = ((float*)&s)[k];
+        x = (float)__builtin_fma((double)to_f32((E)v[k]), c, (double)x);
+      }
+#pragma unroll
+      for (int k = 0; k < W / 4; ++k) __builtin_nontemporal_store(s.q[k], (f4*)(m + at) + k);
     } else {
       typename Vec<E>::type o;
 #pragma unroll
@@ -181,20 +204,20 @@ __device__ __forceinline__ void scale_chunk(const Entry& e, long long lo, long l
   };
   for (; i + (U - 1) * S + W <= hi; i += U * S) {
     typename Vec<E>::type v[U];
-    fw s[U];
+    Sums s[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) v[u] = ((const typename Vec<E>::Any*)(g + i + u * S))->v;
     if (m) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) s[u] = ((const FAny*)(m + i + u * S))->v;
+      for (int u = 0; u < U; ++u) s[u] = load(i + u * S);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) one(v[u], i + u * S, s[u]);
   }
   for (; i < hi; i += S) {
     if (i + W <= hi) {
-      fw s;
-      if (m) s = ((const FAny*)(m + i))->v;
+      Sums s;
+      if (m) s = load(i);
       one(((const typename Vec<E>::Any*)(g + i))->v, i, s);
     } else {
       for (long long j = i; j < hi; ++j) {
@@ -210,12 +233,14 @@ __global__ __launch_bounds__(256) void k_grad_clip(Table t, const double* __rest
                                                    int parts, float max_norm, float scale,
                                                    float* __restrict__ norm) {
   __shared__ double sh[4];
-  const double v = norm_of(part, parts, scale, sh);
+  const double v = norm_of(total_of(part, parts, sh), scale);
   if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)v;
   // (a norm that is NaN makes c NaN, an infinite one 0)
   const double c = (v <= (double)max_norm ? 1.0 : (double)max_norm / v) * (double)scale;
   long long lo, hi;
-  const Entry& e = my_entry(t, lo, hi);
+  // (from the end: what the first pass read last is still in the cache; 693
+  // us at 303 M elements, 707 from the start)
+  const Entry& e = my_entry(t, gridDim.x - 1 - blockIdx.x, lo, hi);
   if (c == 1.0 && !e.m) return;          // g <- 1 g
   if (e.dtype == DION3_F32) scale_chunk<float>(e, lo, hi, c);
   else if (e.dtype == DION3_BF16) scale_chunk<bf16>(e, lo, hi, c);
@@ -228,12 +253,16 @@ bool dense(const dion3_grad& d) {
   return d.rows == 1 || (d.ldg == d.cols && (!d.M || d.ldm == d.cols));
 }
 
-// Elements of a chunk: at most about kPartials chunks, and one more a tensor.
+// Elements of a chunk: about kPartials chunks up to kChunkMax, more beyond, and
+// no more than 2^21 (2^38 elements).
 long long chunk_size(const dion3_grad* d, int count) {
   long long total = 0;
   for (int i = 0; i < count; ++i) total += elements(d[i]);
   const long long c = (total / kPartials + 2047) / 2048 * 2048;
-  return c < kChunkMin ? kChunkMin : c;
+  if (c < kChunkMin) return kChunkMin;
+  if (c < kChunkMax) return c;
+  const long long least = (total >> 21) / 2048 * 2048;
+  return least > kChunkMax ? least : kChunkMax;
 }
 int chunks_of(const dion3_grad& d, long long chunk) {
   return (int)((elements(d) + chunk - 1) / chunk);
@@ -290,6 +319,9 @@ int partials(const dion3_grad* d, int count, long long chunk) {
   return p;
 }
 
+// The partial sums, and their total where there are many.
+size_t scratch_of(int parts) { return ((size_t)parts + (parts > kPartials ? 1 : 0)) * 8; }
+
 constexpr int kMaxGrads = 1 << 20;
 
 dion3_status check_grads(const dion3_grad* d, int count, bool sums) {
@@ -327,7 +359,7 @@ size_t dion3_grad_size(void) { return sizeof(dion3_grad); }
 dion3_status dion3_grad_norm_workspace_size(const dion3_grad* grads, int32_t count, size_t* bytes) {
   if (!bytes) return DION3_ERR_ARG;
   TRY(check_grads(grads, count, true));
-  *bytes = (size_t)partials(grads, count, chunk_size(grads, count)) * 8;
+  *bytes = scratch_of(partials(grads, count, chunk_size(grads, count)));
   return DION3_OK;
 }
 
@@ -338,7 +370,7 @@ dion3_status dion3_grad_norm(const dion3_grad* grads, int32_t count, float scale
   if (!norm || !elem_aligned(norm, 4) || !elem_aligned(norms, 4)) return DION3_ERR_ARG;
   const long long chunk = chunk_size(grads, count);
   const int parts = partials(grads, count, chunk);
-  TRY(check_scratch(ws, ws_bytes, (size_t)parts * 8));
+  TRY(check_scratch(ws, ws_bytes, scratch_of(parts)));
   hipStream_t s = (hipStream_t)stream;
   double* part = (double*)ws;
   HIP_TRY(launch_squares(grads, count, chunk, part, s));
@@ -372,7 +404,7 @@ dion3_status dion3_clip_grad_norm(const dion3_grad* grads, int32_t count, float 
   if (!elem_aligned(norm, 4)) return DION3_ERR_ARG;
   const long long chunk = chunk_size(grads, count);
   const int parts = partials(grads, count, chunk);
-  TRY(check_scratch(ws, ws_bytes, (size_t)parts * 8));
+  TRY(check_scratch(ws, ws_bytes, scratch_of(parts)));
   hipStream_t s = (hipStream_t)stream;
   double* part = (double*)ws;
   if (parts == 0) {                      // no elements at all
@@ -384,9 +416,16 @@ dion3_status dion3_clip_grad_norm(const dion3_grad* grads, int32_t count, float 
     return DION3_OK;
   }
   HIP_TRY(launch_squares(grads, count, chunk, part, s));
+  int terms = parts;
+  if (parts > kPartials) {
+    hipLaunchKernelGGL(k_grad_total, dim3(1), dim3(256), 0, s, part, parts);
+    HIP_TRY(hipGetLastError());
+    part += parts;
+    terms = 1;
+  }
   TraceScope ts("grad_clip", 0.0, grad_bytes(grads, count, 8.0), s);
   HIP_TRY(for_batches(grads, count, chunk, [&](const Table& t, int chunks, bool first) {
-    hipLaunchKernelGGL(k_grad_clip, dim3(chunks), dim3(256), 0, s, t, part, parts, max_norm, scale,
+    hipLaunchKernelGGL(k_grad_clip, dim3(chunks), dim3(256), 0, s, t, part, terms, max_norm, scale,
                        first ? norm : nullptr);
     return hipGetLastError();
   }));
