@@ -6,20 +6,22 @@
 //
 // The gradient is summed without atomics, in an order fixed by the tokens:
 // their places are sorted by token, places of one token in order.  The sorted
-// list is cut into chunks of kChunk places, a wave sums the rows of one chunk
+// list is cut into chunks of up to 32 places, a wave sums the rows of one chunk
 // for 512 columns, and writes a token's sum at the end of its run.  A run that
 // crosses chunks leaves one partial row a chunk, which a last launch adds up
 // in order, so that a token that fills the batch is split as well as others.
 // Rows of dW without a token are cleared by further workgroups of the same
 // launch, which find the tokens of their rows in the sorted list.  Bound by
-// HBM: dW is written once (fp32, most of the bytes), dy read once.
+// HBM: dW is written once (fp32, most of the bytes), dy read once (8192 tokens
+// of 32000 x 4096: 10 us for the places, 100 us, 5.9 TB/s, for the sums, 6 us
+// for the joins).
 #include "checks.h"
 
 namespace dion3 {
 namespace {
 
-constexpr int kChunk = 32;            // places of one wave
-constexpr int kZeroRows = 32;         // rows of dW that one workgroup clears
+constexpr int kMaxChunk = 32;         // places of one wave at most
+constexpr int kZeroRows = 8;          // rows of dW that one workgroup clears
 constexpr int kCountMax = 8192;       // tokens up to which places are counted, not sorted by digits
 constexpr int kTile = 4096;           // tokens of a workgroup of the sort by digits
 
@@ -54,21 +56,34 @@ __global__ __launch_bounds__(256) void k_embed(const void* __restrict__ tokens, 
 
 // Up to kCountMax tokens: the place of t in the order is the number of tokens
 // before it, counted by comparing all with all (two instructions a pair).  A
-// workgroup places 32 tokens; 8 groups of 32 lanes take an eighth of the keys
-// each, in blocks of 32: a block before the workgroup's own counts keys up to
+// workgroup places 32 tokens; its groups of 32 lanes share out the keys in
+// blocks of 32: a block before the workgroup's own counts keys up to
 // the token's, one behind it keys below, its own both by their places.
-__global__ __launch_bounds__(256) void k_embed_count(const void* __restrict__ tokens, int is64,
-                                                     int T, int n, int* __restrict__ skey,
-                                                     int* __restrict__ spos) {
+constexpr int kGroups = 32;           // groups of 32 lanes in a workgroup
+__global__ __launch_bounds__(1024) void k_embed_count(const void* __restrict__ tokens, int is64,
+                                                      int T, int n, int* __restrict__ skey,
+                                                      int* __restrict__ spos) {
   extern __shared__ __attribute__((aligned(16))) int keys[];    // padded to whole blocks with n + 1
-  __shared__ int part[8][32];
+  __shared__ int part[kGroups][33];
   const int nb = (T + 31) / 32;
-  for (int i = threadIdx.x; i < nb * 32; i += 256) keys[i] = i < T ? token_key(tokens, is64, i, n) : n + 1;
+  for (int i0 = 0; i0 < nb * 32; i0 += 1024 * 8) {        // 8 loads on their way at a time
+    int k[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int i = i0 + u * 1024 + (int)threadIdx.x;
+      k[u] = token_key(tokens, is64, i < T ? i : T - 1, n);
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int i = i0 + u * 1024 + (int)threadIdx.x;
+      if (i < nb * 32) keys[i] = i < T ? k[u] : n + 1;
+    }
+  }
   __syncthreads();
   const int mine = threadIdx.x & 31, group = threadIdx.x >> 5, own = blockIdx.x;
   const int key = keys[own * 32 + mine];
   int cnt = 0;
-  for (int b = group; b < nb; b += 8) {
+  for (int b = group; b < nb; b += kGroups) {
     const int lim = key + (b < own ? 1 : 0);
     const int4* k4 = (const int4*)(keys + b * 32);
 #pragma unroll
@@ -77,15 +92,18 @@ __global__ __launch_bounds__(256) void k_embed_count(const void* __restrict__ to
       cnt += (k.x < lim) + (k.y < lim) + (k.z < lim) + (k.w < lim);
     }
   }
-  if (group == (own & 7)) {
+  if (group == (own & (kGroups - 1))) {
     for (int i = 0; i < mine; ++i) cnt += keys[own * 32 + i] == key;
   }
   part[group][mine] = cnt;
   __syncthreads();
-  const int t = own * 32 + mine;
-  if (group == 0 && t < T) {
-    for (int g = 1; g < 8; ++g) cnt += part[g][mine];
-    skey[cnt] = key;
+  // (a group a token here: its lanes hold the groups' counts)
+  cnt = part[mine][group];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) cnt += __shfl_xor(cnt, o, 64);
+  const int t = own * 32 + group;
+  if (mine == 0 && t < T) {
+    skey[cnt] = keys[t];
     spos[cnt] = t;
   }
 }
@@ -211,44 +229,37 @@ struct EmbedGradP {
   float* dw; long long ldw;
   float* part;                        // [chunks][2][m]: a run from before, one that goes on
   long long T, sum_blocks;
-  int n, m, slices;                   // slices of 512 columns
+  int n, m, slices, len;              // slices of 512 columns, places of a chunk
   float scale;
   int accumulate;
 };
 
-__device__ __forceinline__ void put_row(const EmbedGradP& p, int row, int c, float (&v)[8]) {
-  float* d = p.dw + row * p.ldw;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] *= p.scale;
-  if (p.accumulate) {
-    float o[8];
-    load8(d, c, p.m, o);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] += o[e];
-  }
-  store8(d, c, p.m, v);
-}
-
-// One wave: chunk x slice.
-template <class E>
+// One wave: chunk x slice.  Rows are asked for U at a time, and with ACC the rows
+// of dW that their runs end in too (one by one, each waits for its own).
+template <class E, bool ACC>
 __device__ __forceinline__ void sum_chunk(const EmbedGradP& p, long long chunk, int slice) {
   const int lane = threadIdx.x & 63, c = slice * 512 + lane * 8;
-  const long long from = chunk * kChunk;
-  const int cnt = (int)(p.T - from < kChunk ? p.T - from : kChunk);
+  const long long from = chunk * p.len;
+  const int cnt = (int)(p.T - from < p.len ? p.T - from : p.len);
   const int k = lane < cnt ? p.key[from + lane] : p.n;
   const int at = lane < cnt ? p.pos[from + lane] : 0;
   const int before = from > 0 ? p.key[from - 1] : -1;
-  const int behind = from + kChunk < p.T ? p.key[from + kChunk] : -1;
+  const int behind = from + p.len < p.T ? p.key[from + p.len] : -1;
   float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
   bool head = __builtin_amdgcn_readlane(k, 0) == before;
-  constexpr int U = 8;
+  constexpr int U = ACC ? 4 : 8;
   for (int i0 = 0; i0 < cnt; i0 += U) {
     Raw8<E> raw[U];
+    float old[ACC ? U : 1][8];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (i0 + u >= cnt) continue;
-      const E* row = (const E*)p.dy + __builtin_amdgcn_readlane(at, i0 + u) * p.lddy;
-      if (c < p.m) raw[u] = fetch8(row, c, p.m);
+      const int i = i0 + u;
+      if (i >= cnt) continue;
+      const int key = __builtin_amdgcn_readlane(k, i);
+      if (key == p.n || c >= p.m) continue;
+      raw[u] = fetch8((const E*)p.dy + __builtin_amdgcn_readlane(at, i) * p.lddy, c, p.m);
+      if (ACC && (i + 1 == cnt || __builtin_amdgcn_readlane(k, i + 1) != key))
+        load8(p.dw + key * p.ldw, c, p.m, old[u]);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -266,8 +277,13 @@ __device__ __forceinline__ void sum_chunk(const EmbedGradP& p, long long chunk, 
       if (next == key) continue;
       const bool tail = i + 1 == cnt && behind == key;
       if (c < p.m) {
-        if (head || tail) store8(p.part + (chunk * 2 + (head ? 0 : 1)) * p.m, c, p.m, acc);
-        else put_row(p, key, c, acc);
+        if (head || tail) {
+          store8(p.part + (chunk * 2 + (head ? 0 : 1)) * p.m, c, p.m, acc);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) acc[e] = ACC ? old[u][e] + p.scale * acc[e] : p.scale * acc[e];
+          store8(p.dw + key * p.ldw, c, p.m, acc);
+        }
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
@@ -293,20 +309,20 @@ __device__ __forceinline__ long long first_at(const int* __restrict__ key, long 
   return lo;
 }
 
-template <class E>
+template <class E, bool ACC>
 __global__ __launch_bounds__(256) void k_embed_grad(EmbedGradP p) {
   const int wave = threadIdx.x >> 6;
   const long long block = (long long)blockIdx.y * gridDim.x + blockIdx.x;
   if (block < p.sum_blocks) {
     const long long task = block * 4 + wave, chunk = task / p.slices;
-    if (chunk * kChunk >= p.T) return;
-    sum_chunk<E>(p, chunk, (int)(task - chunk * p.slices));
+    if (chunk * p.len >= p.T) return;
+    sum_chunk<E, ACC>(p, chunk, (int)(task - chunk * p.slices));
     return;
   }
   __shared__ long long ends[2];
   __shared__ int there[kZeroRows];
   const long long v0 = (block - p.sum_blocks) * kZeroRows;
-  if (v0 >= p.n || p.accumulate) return;            // (a grid may hold more blocks than asked for)
+  if (v0 >= p.n || ACC) return;                     // (a grid may hold more blocks than asked for)
   const int rows = (int)(p.n - v0 < kZeroRows ? p.n - v0 : kZeroRows);
   if (wave < 2) {
     const long long at = first_at(p.key, p.T, (int)v0 + (wave ? rows : 0));
@@ -325,11 +341,19 @@ __global__ __launch_bounds__(256) void k_embed_grad(EmbedGradP p) {
     there[threadIdx.x] = lo < end && p.key[lo] == v;
   }
   __syncthreads();
-  const float zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  // (nontemporal: 32000 x 4096 of 8192 tokens 100 us, 116 with plain stores,
+  // which push dy's rows and the sums out of the cache)
+  typedef float f4 __attribute__((ext_vector_type(4), aligned(4)));
   for (int r = 0; r < rows; ++r) {
     if (there[r]) continue;
     float* row = p.dw + (v0 + r) * p.ldw;
-    for (int c = threadIdx.x * 8; c < p.m; c += 2048) store8(row, c, p.m, zero);
+    for (int c = threadIdx.x * 4; c < p.m; c += 1024) {
+      if (c + 4 <= p.m) {
+        __builtin_nontemporal_store(f4{0, 0, 0, 0}, (f4*)(row + c));
+      } else {
+        for (int e = c; e < p.m; ++e) row[e] = 0.0f;
+      }
+    }
   }
 }
 
@@ -341,15 +365,20 @@ __global__ __launch_bounds__(256) void k_embed_join(EmbedGradP p, long long chun
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const long long block = (long long)blockIdx.y * gridDim.x + blockIdx.x;
   const int cols = (p.m + 255) / 256;
-  const long long c0 = block / cols, from = c0 * kChunk;
-  if (c0 >= chunks) return;
-  const long long last = from + kChunk - 1;
-  if (last + 1 >= p.T) return;                                    // the last chunk
-  const int key = p.key[last];
-  if (key == p.n || p.key[last + 1] != key) return;               // no run goes on
-  if (p.key[from] == key && from > 0 && p.key[from - 1] == key) return;   // begun before
-  const long long end = first_at(p.key, p.T, key + 1);            // one behind the run
-  const long long c1 = (end - 1) / kChunk;                        // its last chunk
+  const long long c0 = block / cols, from = c0 * p.len, last = from + p.len - 1;
+  if (c0 >= chunks || last + 1 >= p.T) return;                    // (the last chunk)
+  const int key = p.key[last], next = p.key[last + 1], first = p.key[from];
+  const int before = from > 0 ? p.key[from - 1] : -1;
+  if (key == p.n || next != key) return;                          // no run goes on
+  if (first == key && before == key) return;                      // begun before
+  long long c1 = c0 + 1;                                          // the run's last chunk:
+  for (;;) {                                                      // those it fills, 64 at a time
+    const long long i = (c1 + lane) * p.len + p.len - 1;
+    const unsigned long long not_full = ~__ballot(i + 1 < p.T && p.key[i] == key && p.key[i + 1] == key);
+    const int full = not_full ? __builtin_ctzll(not_full) : 64;
+    c1 += full;
+    if (full < 64) break;
+  }
   const int c = (int)(block - c0 * cols) * 256 + lane * 4;
   const long long count = c1 - c0 + 1, per = (count + 3) / 4;
   const long long a = wave * per, b = a + per < count ? a + per : count;
@@ -393,15 +422,18 @@ dim3 grid_of(long long blocks) {
 }
 
 // The workspace: sorted keys and places (twice for the sort by digits, which
-// swaps them, and its histograms), then the partial rows.
+// swaps them, and its histograms), then the partial rows.  A chunk is of
+// kMaxChunk places, of fewer where there would be too few waves.
 struct EmbedPlan {
-  int digits, tiles;
+  int digits, tiles, len;
   long long chunks;
   size_t at_hist, at_part, bytes;
 };
 EmbedPlan plan_embed(long long T, int n, int m) {
   EmbedPlan q = {};
-  q.chunks = (T + kChunk - 1) / kChunk;
+  q.len = kMaxChunk;
+  while (q.len > 8 && T / q.len * ((m + 511) / 512) < 2048) q.len /= 2;
+  q.chunks = (T + q.len - 1) / q.len;
   const size_t list = (size_t)pad_to(T, 64) * 4;
   size_t b = 2 * list;
   if (T > kCountMax) {
@@ -421,7 +453,7 @@ hipError_t sort_tokens(const void* tokens, int is64, long long T, int n, const E
   const size_t list = (size_t)pad_to(T, 64) * 4;
   int* buf[2][2] = {{(int*)ws, (int*)(ws + list)}, {(int*)(ws + 2 * list), (int*)(ws + 3 * list)}};
   if (!q.digits) {
-    hipLaunchKernelGGL(k_embed_count, dim3((unsigned)((T + 31) / 32)), dim3(256),
+    hipLaunchKernelGGL(k_embed_count, dim3((unsigned)((T + 31) / 32)), dim3(1024),
                        (size_t)pad_to(T, 32) * 4, s, tokens, is64, (int)T, n, buf[0][0], buf[0][1]);
     key = buf[0][0];
     pos = buf[0][1];
@@ -450,6 +482,12 @@ hipError_t launch_embed(const void* tokens, int is64, const void* W, long long l
   hipLaunchKernelGGL((k_embed<WT, E>), flat_grid(chunks), dim3(256), 0, s, tokens, is64,
                      (const WT*)W, ldw, (E*)Y, ldy, chunks, n, m, nch, scale);
   return hipGetLastError();
+}
+
+template <class E>
+void launch_embed_grad(const EmbedGradP& p, dim3 grid, hipStream_t s) {
+  if (p.accumulate) hipLaunchKernelGGL((k_embed_grad<E, true>), grid, dim3(256), 0, s, p);
+  else hipLaunchKernelGGL((k_embed_grad<E, false>), grid, dim3(256), 0, s, p);
 }
 
 bool any_type(int t) { return type16(t) || t == DION3_F32; }
@@ -520,7 +558,7 @@ dion3_status dion3_embedding_grad(const void* tokens, int32_t token_bits, const 
   EmbedGradP p = {};
   p.dy = dY; p.lddy = lddy; p.dw = dW; p.ldw = ldw;
   p.T = T; p.n = (int)n; p.m = (int)m; p.slices = (int)((m + 511) / 512);
-  p.scale = scale; p.accumulate = accumulate != 0;
+  p.scale = scale; p.accumulate = accumulate != 0; p.len = q.len;
   p.part = (float*)((char*)ws + q.at_part);
   if (T > 0) {
     TraceScope ts("embedding_sort", 0.0, 16.0 * T, s);
@@ -531,9 +569,9 @@ dion3_status dion3_embedding_grad(const void* tokens, int32_t token_bits, const 
   {
     TraceScope ts("embedding_grad", 0.0, (double)T * m * size_of(dtype) + 4.0 * (accumulate ? 0 : n) * m, s);
     const dim3 grid = grid_of(p.sum_blocks + zero_blocks);
-    if (dtype == DION3_BF16) hipLaunchKernelGGL((k_embed_grad<bf16>), grid, dim3(256), 0, s, p);
-    else if (dtype == DION3_F16) hipLaunchKernelGGL((k_embed_grad<f16>), grid, dim3(256), 0, s, p);
-    else hipLaunchKernelGGL((k_embed_grad<float>), grid, dim3(256), 0, s, p);
+    if (dtype == DION3_BF16) launch_embed_grad<bf16>(p, grid, s);
+    else if (dtype == DION3_F16) launch_embed_grad<f16>(p, grid, s);
+    else launch_embed_grad<float>(p, grid, s);
     HIP_TRY(hipGetLastError());
   }
   if (q.chunks > 1) {
