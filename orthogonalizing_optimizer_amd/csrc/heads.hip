@@ -12,9 +12,11 @@
 // once and written once, and the backward pass needs nothing but x.  A lane
 // holds 16 columns, both members of 8 pairs, so the rotation moves nothing
 // between lanes; a head takes G lanes (8 for 128 columns), a wave 64 / G heads
-// at a time, and every lane of a wave needs the same 8 angles for all of a
-// token's heads, which are computed once for them.
+// (a batch) at a time.  Waves stay and take batch after batch, of queries or of
+// keys (one weight and one sum of its gradient in registers), the next one's
+// columns on their way; a token's angles are computed once a wave.
 #include "checks.h"
+#include "wave.h"
 
 namespace dion3 {
 namespace {
@@ -23,15 +25,15 @@ struct Side {
   const void* x; const void* w; const void* dy;
   void* y;
   long long ldx, hsx, lddy, hsdy, ldy, hsy;
-  int heads, batches;             // batches of 64 / G heads
+  int heads, batches, parts, units;   // batches of 64 / G heads; waves that share a token's; workgroups
 };
 struct HeadsP {
   Side s[2];                      // queries, keys
   const double* freqs;
   const void* pos;
-  float* part;                    // gradient: one row of 2 D floats a workgroup, or null
-  long long T, tasks;
-  int D, r, G, parts;             // tasks: parts waves share a token's batches
+  float* part;                    // gradient: one row of D floats a workgroup, or null
+  long long T;
+  int D, r, G, pitch;             // pitch: angles of a wave in LDS (r / 2 rounded up to 8)
   int pos64, wtype;
   float eps;
 };
@@ -70,24 +72,61 @@ __device__ __forceinline__ Item my_item(int j, int D, int r) {
   return it;
 }
 
-// cos and sin of the lane's 8 angles: the angle in turns, reduced in 64 bits
-// (a position of 2^20 times a frequency of 1 leaves no bits of a fraction in 32).
-__device__ __forceinline__ void my_freqs(const HeadsP& p, int j, double (&f)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    f[i] = 8 * j + i < p.r / 2 ? p.freqs[8 * j + i] * 0.15915494309189533577 : 0.0;
-}
-__device__ __forceinline__ void turn_of(double at, const double (&f)[8], float (&co)[8],
-                                        float (&si)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const double t = at * f[i];
-    sincospif(2.0f * (float)(t - rint(t)), &si[i], &co[i]);
-  }
-}
 __device__ __forceinline__ double position(const HeadsP& p, long long t) {
   return p.pos64 ? (double)((const long long*)p.pos)[t] : (double)((const int*)p.pos)[t];
 }
+
+// A wave's angles: each lane turns one position and frequency (in turns,
+// reduced in 64 bits: a position of 2^20 times a frequency of 1 leaves no bits
+// of a fraction in 32) into a cosine and a sine, and takes the 8 of its
+// columns from LDS.  Nobody else touches the wave's part of it.
+struct Angles {
+  float2* at;
+  double first;                   // the lane's frequency in turns
+  __device__ Angles(const HeadsP& p, float2* lds, int wave) {
+    at = lds + wave * p.pitch;
+    first = frequency(p, threadIdx.x & 63);
+  }
+  __device__ static double frequency(const HeadsP& p, int i) {
+    return i < p.r / 2 ? p.freqs[i] * 0.15915494309189533577 : 0.0;
+  }
+  __device__ void set(const HeadsP& p, double pos, int pair, float sign, float (&co)[8],
+                      float (&si)[8]) {
+    __builtin_amdgcn_wave_barrier();
+    for (int i = threadIdx.x & 63; i < p.pitch; i += 64) {
+      const double t = pos * (i < 64 ? first : frequency(p, i));
+      float2 v;
+      sincospif(2.0f * (float)(t - rint(t)), &v.y, &v.x);
+      at[i] = v;
+    }
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      const float4 v = *(const float4*)(at + pair + i);
+      co[i] = v.x; si[i] = sign * v.y;
+      co[i + 1] = v.z; si[i + 1] = sign * v.w;
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+};
+
+// The batches of heads that a wave takes, token by token.
+struct Walk {
+  long long task, t;
+  int b;
+  __device__ Walk(const HeadsP& p, const Side& s, long long first) : task(first) { place(p, s); }
+  __device__ void place(const HeadsP& p, const Side& s) {
+    t = task / s.parts;
+    b = (int)(task - t * s.parts);
+  }
+  __device__ bool more(const HeadsP& p) const { return t < p.T; }
+  __device__ void next(const HeadsP& p, const Side& s, long long step) {
+    b += s.parts;
+    if (b < s.batches) return;
+    task += step;
+    place(p, s);
+  }
+};
 
 // Pairs (a, b) of the lane's columns: (v[0][i], v[1][i]), or neighbours.
 template <bool IL>
@@ -110,123 +149,139 @@ __device__ __forceinline__ void load_weight(const HeadsP& p, const Side& s, cons
   for (int k = 0; k < 2; ++k) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) w[k][e] = 0.0f;
-    if (!it.on || s.heads == 0) continue;
+    if (!it.on) continue;
     if (p.wtype == DION3_F32) load8((const float*)s.w + it.base[k], it.c[k], it.lim[k], w[k]);
     else load8((const E*)s.w + it.base[k], it.c[k], it.lim[k], w[k]);
   }
 }
 
 __device__ __forceinline__ float head_sum(float v, int G) {
-  for (int o = 1; o < G; o <<= 1) v += __shfl_xor(v, o, 64);
-  return v;
+  return group_reduce(v, G, [](float a, float b) { return a + b; });
+}
+
+// The lane's 16 columns of head h of token t, asked for and as floats (zeros
+// where the lane has none).
+template <class E>
+__device__ __forceinline__ void ask(const void* x, long long ld, long long hs, long long t, int h,
+                                    const Item& it, bool mine, Raw8<E> (&raw)[2]) {
+  if (!mine) return;
+  const E* row = (const E*)x + t * ld + h * hs;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) raw[k] = fetch8(row + it.base[k], it.c[k], it.lim[k]);
+}
+template <class E>
+__device__ __forceinline__ void take(const Raw8<E> (&raw)[2], const Item& it, bool mine,
+                                     float (&v)[2][8]) {
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    if (mine) {
+      chunk8(raw[k], it.c[k], it.lim[k], v[k]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[k][e] = 0.0f;
+    }
+  }
+}
+template <class E>
+__device__ __forceinline__ void put(void* y, long long ld, long long hs, long long t, int h,
+                                    const Item& it, const float (&v)[2][8]) {
+  E* row = (E*)y + t * ld + h * hs;
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    if (it.c[k] < it.lim[k]) store8(row + it.base[k], it.c[k], it.lim[k], v[k]);
+}
+__device__ __forceinline__ float head_rstd(const float (&v)[2][8], int G, int D, float eps) {
+  float ss = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) ss = __builtin_fmaf(v[i / 8][i % 8], v[i / 8][i % 8], ss);
+  return 1.0f / sqrtf(head_sum(ss, G) / (float)D + eps);
 }
 
 template <class E, bool IL>
 __global__ __launch_bounds__(256) void k_heads(HeadsP p) {
-  const int lane = threadIdx.x & 63, G = p.G, per = 64 / G;
-  const long long task = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (task >= p.tasks) return;
-  const long long t = task / p.parts;
-  const int part = (int)(task - t * p.parts), nb = p.s[0].batches + p.s[1].batches;
-  const Item it = my_item<IL>(lane & (G - 1), p.D, p.r);
+  extern __shared__ __attribute__((aligned(16))) float2 turns[];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int G = p.G, per = 64 / G, j = lane & (G - 1), slot = lane / G;
+  const bool isk = (int)blockIdx.x >= p.s[0].units;
+  const Side& s = p.s[isk];
+  const long long step = s.units * 4LL;
+  Walk at(p, s, ((int)blockIdx.x - (isk ? p.s[0].units : 0)) * 4LL + wave);
+  if (!at.more(p)) return;
+  const Item it = my_item<IL>(j, p.D, p.r);
   Raw8<E> raw[2];
-  bool mine = false;
-  auto ask = [&](int b) {
-    const bool isk = b >= p.s[0].batches;
-    const Side& s = p.s[isk];
-    const int h = (isk ? b - p.s[0].batches : b) * per + lane / G;
-    mine = it.on && h < s.heads;
-    if (!mine) return;
-    const E* row = (const E*)s.x + t * s.ldx + h * s.hsx;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) raw[k] = fetch8(row + it.base[k], it.c[k], it.lim[k]);
-  };
-  ask(part);
-  float w[2][2][8], co[8], si[8];
-  load_weight<E>(p, p.s[0], it, w[0]);
-  load_weight<E>(p, p.s[1], it, w[1]);
-  double f[8];
-  my_freqs(p, lane & (G - 1), f);
-  turn_of(position(p, t), f, co, si);
-  for (int b = part; b < nb; b += p.parts) {
-    const bool isk = b >= p.s[0].batches;
-    const Side& s = p.s[isk];
-    const int h = (isk ? b - p.s[0].batches : b) * per + lane / G;
+  bool mine = it.on && at.b * per + slot < s.heads;
+  ask(s.x, s.ldx, s.hsx, at.t, at.b * per + slot, it, mine, raw);
+  double pos = position(p, at.t);
+  float w[2][8], co[8], si[8];
+  load_weight<E>(p, s, it, w);
+  Angles ang(p, turns, wave);
+  for (bool fresh = true;;) {
+    if (fresh) ang.set(p, pos, it.rot ? 8 * j : 0, 1.0f, co, si);
     float v[2][8];
-    float ss = 0.0f;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      if (mine) chunk8(raw[k], it.c[k], it.lim[k], v[k]);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        v[k][e] = mine ? v[k][e] : 0.0f;
-        ss = __builtin_fmaf(v[k][e], v[k][e], ss);
-      }
+    take(raw, it, mine, v);
+    // the next batch's columns, and the next token's position, on their way
+    const Walk now = at;
+    const bool own = mine;
+    at.next(p, s, step);
+    const bool go = at.more(p);
+    if (go) {
+      mine = it.on && at.b * per + slot < s.heads;
+      ask(s.x, s.ldx, s.hsx, at.t, at.b * per + slot, it, mine, raw);
+      fresh = at.t != now.t;
+      if (fresh) pos = position(p, at.t);
     }
-    const bool now = mine;
-    if (b + p.parts < nb) ask(b + p.parts);
-    const float rs = 1.0f / sqrtf(head_sum(ss, G) / (float)p.D + p.eps);
+    const float rs = head_rstd(v, G, p.D, p.eps);
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[k][e] = v[k][e] * rs * (isk ? w[1][k][e] : w[0][k][e]);
+    for (int i = 0; i < 16; ++i) v[i / 8][i % 8] *= rs * w[i / 8][i % 8];
     rotate<IL>(v, co, si, it.rot);
-    if (!now) continue;
-    E* row = (E*)s.y + t * s.ldy + h * s.hsy;
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-      if (it.c[k] < it.lim[k]) store8(row + it.base[k], it.c[k], it.lim[k], v[k]);
+    if (own) put<E>(s.y, s.ldy, s.hsy, now.t, now.b * per + slot, it, v);
+    if (!go) return;
   }
 }
 
 // The weights' gradients: a lane adds up its columns over its tokens and
 // heads, the lanes of equal columns and the workgroup's waves are joined at
-// the end, and the workgroups' rows by k_join_columns, each in a fixed order.
+// the end, and the workgroups' rows by k_heads_join, each in a fixed order.
 template <class E, bool IL>
 __global__ __launch_bounds__(256) void k_heads_grad(HeadsP p) {
-  extern __shared__ float sh[];                        // 3 waves x 2 sides x D
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, G = p.G, per = 64 / G;
-  const int nb = p.s[0].batches + p.s[1].batches;
-  const Item it = my_item<IL>(lane & (G - 1), p.D, p.r);
-  float w[2][2][8], dw[2][2][8];
-  load_weight<E>(p, p.s[0], it, w[0]);
-  load_weight<E>(p, p.s[1], it, w[1]);
+  extern __shared__ __attribute__((aligned(16))) float2 turns[];
+  float* sh = (float*)turns + 8 * p.pitch;             // 3 waves x D
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int G = p.G, per = 64 / G, j = lane & (G - 1), slot = lane / G;
+  const bool isk = (int)blockIdx.x >= p.s[0].units;
+  const Side& s = p.s[isk];
+  const long long step = s.units * 4LL;
+  Walk at(p, s, ((int)blockIdx.x - (isk ? p.s[0].units : 0)) * 4LL + wave);
+  const Item it = my_item<IL>(j, p.D, p.r);
+  float dw[2][8];
 #pragma unroll
-  for (int i = 0; i < 32; ++i) dw[i / 16][i / 8 % 2][i % 8] = 0.0f;
-  double f[8];
-  my_freqs(p, lane & (G - 1), f);
-  for (long long task = (long long)blockIdx.x * 4 + wave; task < p.tasks; task += gridDim.x * 4LL) {
-    const long long t = task / p.parts;
-    const int part = (int)(task - t * p.parts);
-    float co[8], si[8];
-    turn_of(position(p, t), f, co, si);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) si[i] = -si[i];
-    for (int b = part; b < nb; b += p.parts) {
-      const bool isk = b >= p.s[0].batches;
-      const Side& s = p.s[isk];
-      const int h = (isk ? b - p.s[0].batches : b) * per + lane / G;
-      const bool mine = it.on && h < s.heads;
-      float x[2][8], u[2][8], ss = 0.0f;
-      if (mine) {
-        Raw8<E> rx[2], ry[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          rx[k] = fetch8((const E*)s.x + t * s.ldx + h * s.hsx + it.base[k], it.c[k], it.lim[k]);
-          ry[k] = fetch8((const E*)s.dy + t * s.lddy + h * s.hsdy + it.base[k], it.c[k], it.lim[k]);
-        }
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          chunk8(rx[k], it.c[k], it.lim[k], x[k]);
-          chunk8(ry[k], it.c[k], it.lim[k], u[k]);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) x[i / 8][i % 8] = u[i / 8][i % 8] = 0.0f;
+  for (int i = 0; i < 16; ++i) dw[i / 8][i % 8] = 0.0f;
+  if (at.more(p)) {
+    Raw8<E> rx[2], ry[2];
+    bool mine = it.on && at.b * per + slot < s.heads;
+    ask(s.x, s.ldx, s.hsx, at.t, at.b * per + slot, it, mine, rx);
+    ask(s.dy, s.lddy, s.hsdy, at.t, at.b * per + slot, it, mine, ry);
+    double pos = position(p, at.t);
+    float w[2][8], co[8], si[8];
+    load_weight<E>(p, s, it, w);
+    Angles ang(p, turns, wave);
+    for (bool fresh = true;;) {
+      if (fresh) ang.set(p, pos, it.rot ? 8 * j : 0, -1.0f, co, si);
+      float x[2][8], u[2][8];
+      take(rx, it, mine, x);
+      take(ry, it, mine, u);
+      const Walk now = at;
+      const bool own = mine;
+      at.next(p, s, step);
+      const bool go = at.more(p);
+      if (go) {
+        mine = it.on && at.b * per + slot < s.heads;
+        ask(s.x, s.ldx, s.hsx, at.t, at.b * per + slot, it, mine, rx);
+        ask(s.dy, s.lddy, s.hsdy, at.t, at.b * per + slot, it, mine, ry);
+        fresh = at.t != now.t;
+        if (fresh) pos = position(p, at.t);
       }
-#pragma unroll
-      for (int i = 0; i < 16; ++i) ss = __builtin_fmaf(x[i / 8][i % 8], x[i / 8][i % 8], ss);
-      const float rs = 1.0f / sqrtf(head_sum(ss, G) / (float)p.D + p.eps);
+      const float rs = head_rstd(x, G, p.D, p.eps);
       rotate<IL>(u, co, si, it.rot);
       float c = 0.0f;
 #pragma unroll
@@ -234,51 +289,67 @@ __global__ __launch_bounds__(256) void k_heads_grad(HeadsP p) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           x[k][e] *= rs;
-          if (isk) dw[1][k][e] = __builtin_fmaf(u[k][e], x[k][e], dw[1][k][e]);
-          else dw[0][k][e] = __builtin_fmaf(u[k][e], x[k][e], dw[0][k][e]);
-          u[k][e] *= isk ? w[1][k][e] : w[0][k][e];
+          dw[k][e] = __builtin_fmaf(u[k][e], x[k][e], dw[k][e]);
+          u[k][e] *= w[k][e];
           c = __builtin_fmaf(u[k][e], x[k][e], c);
         }
       c = head_sum(c, G) / (float)p.D;
-      if (!mine || !s.y) continue;
-      E* row = (E*)s.y + t * s.ldy + h * s.hsy;
+      if (own && s.y) {
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) u[k][e] = rs * __builtin_fmaf(-x[k][e], c, u[k][e]);
-        if (it.c[k] < it.lim[k]) store8(row + it.base[k], it.c[k], it.lim[k], u[k]);
+        for (int i = 0; i < 16; ++i)
+          u[i / 8][i % 8] = rs * __builtin_fmaf(-x[i / 8][i % 8], c, u[i / 8][i % 8]);
+        put<E>(s.y, s.ldy, s.hsy, now.t, now.b * per + slot, it, u);
       }
+      if (!go) break;
     }
   }
   if (!p.part) return;
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    float& v = dw[i / 16][i / 8 % 2][i % 8];
-    for (int o = G; o < 64; o <<= 1) v += __shfl_xor(v, o, 64);
-  }
+  for (int i = 0; i < 16; ++i)
+    for (int o = G; o < 64; o <<= 1) dw[i / 8][i % 8] += __shfl_xor(dw[i / 8][i % 8], o, 64);
   const bool mine = it.on && lane < G;                 // one lane for each column
   if (mine && wave > 0) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (it.c[i & 1] < it.lim[i & 1])
-        store8(sh + ((wave - 1) * 2 + i / 2) * p.D + it.base[i & 1], it.c[i & 1], it.lim[i & 1],
-               dw[i / 2][i & 1]);
+    for (int k = 0; k < 2; ++k)
+      if (it.c[k] < it.lim[k])
+        store8(sh + (wave - 1) * p.D + it.base[k], it.c[k], it.lim[k], dw[k]);
   }
   __syncthreads();
   if (wave > 0 || !mine) return;
   for (int o = 0; o < 3; ++o)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int k = 0; k < 2; ++k) {
       float v[8];
-      load8(sh + (o * 2 + i / 2) * p.D + it.base[i & 1], it.c[i & 1], it.lim[i & 1], v);
+      load8(sh + o * p.D + it.base[k], it.c[k], it.lim[k], v);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) dw[i / 2][i & 1][e] += v[e];
+      for (int e = 0; e < 8; ++e) dw[k][e] += v[e];
     }
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (it.c[i & 1] < it.lim[i & 1])
-      store8(p.part + (blockIdx.x * 2LL + i / 2) * p.D + it.base[i & 1], it.c[i & 1], it.lim[i & 1],
-             dw[i / 2][i & 1]);
+  for (int k = 0; k < 2; ++k)
+    if (it.c[k] < it.lim[k])
+      store8(p.part + (long long)blockIdx.x * p.D + it.base[k], it.c[k], it.lim[k], dw[k]);
+}
+
+// dw[side][c] = the sum over the side's workgroups: 16 columns a workgroup, 64
+// slices of the rows, added in slice order.
+__global__ __launch_bounds__(1024) void k_heads_join(const float* __restrict__ part, int qunits,
+                                                     int kunits, int D, float* __restrict__ dw) {
+  __shared__ float sh[64][17];
+  const int col = threadIdx.x & 15, slice = threadIdx.x >> 4, c = blockIdx.x * 16 + col;
+  const int units = blockIdx.y ? kunits : qunits, per = (units + 63) / 64;
+  const float* rows = part + (blockIdx.y ? (long long)qunits * D : 0);
+  const int u1 = min(units, (slice + 1) * per);
+  float a = 0.0f;
+#pragma unroll 8
+  for (int u = slice * per; u < u1; ++u)
+    if (c < D) a += rows[(long long)u * D + c];
+  sh[slice][col] = a;
+  __syncthreads();
+  if (slice == 0 && c < D) {
+    a = 0.0f;
+    for (int i = 0; i < 64; ++i) a += sh[i][col];
+    dw[blockIdx.y * D + c] = a;
+  }
 }
 
 // ------------------------------------------------------------------ the calls
@@ -286,34 +357,39 @@ __global__ __launch_bounds__(256) void k_heads_grad(HeadsP p) {
 constexpr int kMaxHeadDim = 1024, kMaxHeads = 1 << 16;
 constexpr long long kMaxStride = 1LL << 38;
 
-struct Split {
-  int G, batches[2], parts;
-  long long tasks;
-};
 // 16-column pieces of a head.
 int pieces(int D, int r, bool il) {
   return (il ? (r + 15) / 16 : (r / 2 + 7) / 8) + (D - r + 15) / 16;
 }
 // A head takes the power of two of lanes that holds its columns, 16 a lane.
-// About 4096 waves at least (4 a SIMD): a token's heads are shared out between
-// waves where there are few tokens.
-Split split_heads(long long T, int hq, int hk, int D, int r, bool il) {
+// kWaves waves are shared out between queries and keys by their batches; a
+// token's batches between waves where there are few tokens.
+constexpr int kWaves = 4096;
+struct Split {
+  int G, batches[2], parts[2], units[2];
+};
+Split split_heads(long long T, int hq, int hk, int D, int r, bool il, int waves) {
   Split q;
   q.G = 1;
   while (q.G < pieces(D, r, il)) q.G *= 2;
-  const int per = 64 / q.G;
-  q.batches[0] = (hq + per - 1) / per;
-  q.batches[1] = (hk + per - 1) / per;
+  const int per = 64 / q.G, heads[2] = {hq, hk};
+  for (int i = 0; i < 2; ++i) q.batches[i] = (heads[i] + per - 1) / per;
   const int nb = q.batches[0] + q.batches[1];
-  const long long want = T > 0 ? (4096 + T - 1) / T : 1;
-  q.parts = (int)(want < nb ? want : nb);
-  q.tasks = T * q.parts;
+  for (int i = 0; i < 2; ++i) {
+    if (q.batches[i] == 0) {
+      q.parts[i] = 1;
+      q.units[i] = 0;
+      continue;
+    }
+    const long long share = (long long)waves * q.batches[i] / nb + 1;
+    const long long parts = T > 0 ? (share + T - 1) / T : 1;
+    q.parts[i] = (int)(parts < q.batches[i] ? parts : q.batches[i]);
+    const long long tasks = T * q.parts[i], most = (share + 3) / 4;
+    q.units[i] = (int)((tasks + 3) / 4 < most ? (tasks + 3) / 4 : most);
+  }
   return q;
 }
-int grad_units(const Split& q) {
-  const long long need = (q.tasks + 3) / 4;
-  return (int)(need < 1024 ? need : 1024);
-}
+int units_of(const Split& q) { return q.units[0] + q.units[1]; }
 
 dion3_status check_heads(const dion3_heads* q, const dion3_heads* k, const double* freqs,
                          const void* pos, int pos_bits, int64_t T, int D, int r, int interleaved,
@@ -359,10 +435,10 @@ HeadsP describe(const dion3_heads* q, const dion3_heads* k, const Split& sp, con
     if (both[i]) {
       const dion3_heads& s = *both[i];
       p.s[i] = {s.X, s.w, s.dY, s.Y, s.ldx, s.hsx, s.lddy, s.hsdy, s.ldy, s.hsy, s.heads,
-                sp.batches[i]};
+                sp.batches[i], sp.parts[i], sp.units[i]};
     }
-  p.freqs = freqs; p.pos = pos; p.T = T; p.tasks = sp.tasks;
-  p.D = D; p.r = r; p.G = sp.G; p.parts = sp.parts;
+  p.freqs = freqs; p.pos = pos; p.T = T;
+  p.D = D; p.r = r; p.G = sp.G; p.pitch = r ? (r / 2 + 7) / 8 * 8 : 8;
   p.pos64 = pos_bits == 64; p.wtype = wtype; p.eps = eps;
   return p;
 }
@@ -383,16 +459,17 @@ dion3_status dion3_qk_norm_rope(const dion3_heads* q, const dion3_heads* k, cons
   TRY(check_heads(q, k, freqs, pos, pos_bits, T, D, r, interleaved, eps, wtype, dtype, false));
   if (T == 0) return DION3_OK;
   hipStream_t s = (hipStream_t)stream;
-  const Split sp = split_heads(T, q->heads, k ? k->heads : 0, D, r, interleaved);
+  const Split sp = split_heads(T, q->heads, k ? k->heads : 0, D, r, interleaved, kWaves);
   const HeadsP p = describe(q, k, sp, freqs, pos, pos_bits, T, D, r, eps, wtype);
   TraceScope ts("qk_norm_rope", 0.0, 4.0 * T * D * (q->heads + (k ? k->heads : 0)), s);
-  const dim3 grid((unsigned)((sp.tasks + 3) / 4)), block(256);
+  const dim3 grid((unsigned)units_of(sp)), block(256);
+  const size_t lds = (size_t)p.pitch * 4 * 8;
   if (dtype == DION3_BF16) {
-    if (interleaved) hipLaunchKernelGGL((k_heads<bf16, true>), grid, block, 0, s, p);
-    else hipLaunchKernelGGL((k_heads<bf16, false>), grid, block, 0, s, p);
+    if (interleaved) hipLaunchKernelGGL((k_heads<bf16, true>), grid, block, lds, s, p);
+    else hipLaunchKernelGGL((k_heads<bf16, false>), grid, block, lds, s, p);
   } else {
-    if (interleaved) hipLaunchKernelGGL((k_heads<f16, true>), grid, block, 0, s, p);
-    else hipLaunchKernelGGL((k_heads<f16, false>), grid, block, 0, s, p);
+    if (interleaved) hipLaunchKernelGGL((k_heads<f16, true>), grid, block, lds, s, p);
+    else hipLaunchKernelGGL((k_heads<f16, false>), grid, block, lds, s, p);
   }
   HIP_TRY(hipGetLastError());
   return DION3_OK;
@@ -405,7 +482,7 @@ dion3_status dion3_qk_norm_rope_grad_workspace_size(int64_t T, int32_t hq, int32
   if (T > DION3_MAX_TOKENS || D > kMaxHeadDim || hq > kMaxHeads || hk > kMaxHeads ||
       pieces(D, r, interleaved) > 64)
     return DION3_ERR_UNSUPPORTED;
-  *bytes = (size_t)grad_units(split_heads(T, hq, hk, D, r, interleaved)) * 2 * D * 4;
+  *bytes = (size_t)units_of(split_heads(T, hq, hk, D, r, interleaved, kWaves)) * D * 4;
   return DION3_OK;
 }
 
@@ -418,15 +495,14 @@ dion3_status dion3_qk_norm_rope_grad(const dion3_heads* q, const dion3_heads* k,
   if (!elem_aligned(dw, 4)) return DION3_ERR_ARG;
   if (T > 0 && !dw && !q->Y && !(k && k->Y)) return DION3_ERR_ARG;
   hipStream_t s = (hipStream_t)stream;
-  const Split sp = split_heads(T, q->heads, k ? k->heads : 0, D, r, interleaved);
-  const int units = grad_units(sp);
-  if (dw) TRY(check_scratch(ws, ws_bytes, (size_t)units * 2 * D * 4));
+  const Split sp = split_heads(T, q->heads, k ? k->heads : 0, D, r, interleaved, kWaves);
+  if (dw) TRY(check_scratch(ws, ws_bytes, (size_t)units_of(sp) * D * 4));
   if (T > 0) {
     HeadsP p = describe(q, k, sp, freqs, pos, pos_bits, T, D, r, eps, wtype);
     p.part = dw ? (float*)ws : nullptr;
     TraceScope ts("qk_norm_rope_grad", 0.0, 6.0 * T * D * (q->heads + (k ? k->heads : 0)), s);
-    const dim3 grid(units), block(256);
-    const size_t lds = dw ? (size_t)6 * D * 4 : 0;
+    const dim3 grid((unsigned)units_of(sp)), block(256);
+    const size_t lds = (size_t)p.pitch * 4 * 8 + (dw ? (size_t)3 * D * 4 : 0);
     if (dtype == DION3_BF16) {
       if (interleaved) hipLaunchKernelGGL((k_heads_grad<bf16, true>), grid, block, lds, s, p);
       else hipLaunchKernelGGL((k_heads_grad<bf16, false>), grid, block, lds, s, p);
@@ -436,7 +512,11 @@ dion3_status dion3_qk_norm_rope_grad(const dion3_heads* q, const dion3_heads* k,
     }
     HIP_TRY(hipGetLastError());
   }
-  if (dw) HIP_TRY(launch_join_columns((const float*)ws, units, 2 * D, dw, s));
+  if (dw) {
+    hipLaunchKernelGGL(k_heads_join, dim3((D + 15) / 16, 2), dim3(1024), 0, s, (const float*)ws,
+                       sp.units[0], sp.units[1], D, dw);
+    HIP_TRY(hipGetLastError());
+  }
   return DION3_OK;
 }
 

@@ -16,6 +16,7 @@
 // rows do.  The pair (m, l) is kept apart up to the gradient: where logits are
 // large, down to the type's lowest value, m + l would have no bits left for l.
 #include "checks.h"
+#include "wave.h"
 
 namespace dion3 {
 namespace {
@@ -41,6 +42,16 @@ __device__ __forceinline__ Part merge(const Part& a, const Part& b) {
           __builtin_fmaf(__builtin_fmaf(a.s, da, a.e), fa, __builtin_fmaf(b.s, db, b.e) * fb), 0.0f};
 }
 
+// The merge of all lanes' parts, in every lane.
+__device__ __forceinline__ Part wave_merge(Part a) {
+  a = merge(a, {other<1>(a.m), other<1>(a.s), other<1>(a.e), 0.0f});
+  a = merge(a, {other<2>(a.m), other<2>(a.s), other<2>(a.e), 0.0f});
+  a = merge(a, {other<4>(a.m), other<4>(a.s), other<4>(a.e), 0.0f});
+  a = merge(a, {other<8>(a.m), other<8>(a.s), other<8>(a.e), 0.0f});
+  auto row = [&](int i) { return Part{lane_of(a.m, i), lane_of(a.s, i), lane_of(a.e, i), 0.0f}; };
+  return merge(merge(row(0), row(16)), merge(row(32), row(48)));
+}
+
 // Whole numbers in the order of the logits; zeros of both signs alike, NaN
 // above all, none is 0.  The lower kLow bits of a type's keys are those of
 // their sign: all clear in the upper half of the order, all set in the lower.
@@ -55,24 +66,22 @@ __device__ __forceinline__ float order_value(unsigned k) {
   return __builtin_bit_cast(float, k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
 
-struct Best {
-  unsigned key;
-  int at;
-};
-__device__ __forceinline__ bool before(const Best& a, const Best& b) {
-  return a.key > b.key || (a.key == b.key && a.at < b.at);
+// A candidate as one number: the larger, the earlier (0: none).
+typedef unsigned long long u64;
+__device__ __forceinline__ u64 candidate(unsigned key, int at) {
+  return (u64)key << 32 | (0xffffffffu - (unsigned)at);
 }
 
-// Writes the `top` best of the nc candidates c (LDS, all different) in order
-// by counting, for each, those before it.
-template <class F>
-__device__ __forceinline__ void pick(const Best* c, int nc, int top, F put) {
-  for (int i = threadIdx.x; i < nc; i += blockDim.x) {
-    const Best mine = c[i];
-    int rank = 0;
-    for (int j = 0; j < nc; ++j) rank += before(c[j], mine) ? 1 : 0;
-    if (rank < top) put(rank, mine);
+// How many of c[from .. nc) (LDS, padded with zeros to a multiple of 4), taken 4
+// at a time, `step` apart, come before `mine`.
+__device__ __forceinline__ int count_before(const u64* c, int from, int nc, int step, u64 mine) {
+  int n = 0;
+#pragma unroll 4
+  for (int j = from; j < nc; j += step) {
+    const ulonglong2 a = *(const ulonglong2*)(c + j), b = *(const ulonglong2*)(c + j + 2);
+    n += (a.x > mine) + (a.y > mine) + (b.x > mine) + (b.y > mine);
   }
+  return n;
 }
 
 struct LogpP {
@@ -80,7 +89,7 @@ struct LogpP {
   const void* target; int target64;
   float* logp; float* stats; float* entropy;
   float* top_logp; long long* top_index;
-  Part* part; Best* best;                  // of piece (t, s): part[t S + s], best[(t S + s) top ..]
+  Part* part; u64* best;                   // of piece (t, s): part[t S + s], best[(t S + s) top ..]
   long long T;
   int n, top, S, len;                      // pieces a row, logits a piece (a multiple of 8)
   float scale;
@@ -97,101 +106,147 @@ dim3 blocks_grid(long long blocks) {
 
 constexpr int kWaveBest = 128;     // candidates a wave leaves at most (at least kMaxTop)
 
-// The wave's candidates for the `top` best of its keys (absent ones are 0): at
-// least those, at most kWaveBest.  Keys at or above the top-th largest of the
-// lanes' maxima are a superset, most often of few more than `top`; where it is
-// too large (many equal logits, or one lane's), the top-th largest key itself
-// is found by its bits and of the equal ones the first are taken.
-template <int SH>
-__device__ __forceinline__ int wave_best(const unsigned (&key)[kChunks][8], const int (&col)[kChunks],
-                                         int top, Best* out) {
-  unsigned cm[kChunks], lm = 0;
-#pragma unroll
-  for (int i = 0; i < kChunks; ++i) {
-    cm[i] = key[i][0];
-#pragma unroll
-    for (int e = 1; e < 8; ++e) cm[i] = max(cm[i], key[i][e]);
-    lm = max(lm, cm[i]);
-  }
-  unsigned tau = 0;
-  for (int b = 31; b >= SH; --b) {
-    const unsigned c = tau | 1u << b;
-    if (__popcll(__ballot(lm >= c)) >= top) tau = c;
-  }
-  const unsigned long long below = (1ull << (threadIdx.x & 63)) - 1;
+// The wave's candidates for the `top` best of its logits: at least those (where
+// it has as many), at most kWaveBest, padded with zeros to a multiple of 4.
+// Logits at or above the top-th largest of the lanes' maxima are a superset,
+// most often of few more than `top`: one comparison a logit.  Where they are
+// too many (equal logits, one lane's), or there is NaN (`odd`), the top-th
+// largest key is found by its bits, and of the logits equal to it the first
+// are taken.
+template <class E>
+__device__ __forceinline__ int wave_best(const float (&v)[kChunks][8], const float (&cm)[kChunks],
+                                         const int (&col)[kChunks], int to, int top, bool odd,
+                                         u64* out) {
+  constexpr int SH = kLow<E>;
+  const int lane = threadIdx.x & 63;
+  const u64 below = (1ull << lane) - 1;
   int have = 0;
+  if (!odd) {
+    float lm = cm[0];
 #pragma unroll
-  for (int i = 0; i < kChunks; ++i) {
-    if (!__ballot(cm[i] >= tau)) continue;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const bool in = key[i][e] >= tau;
-      const unsigned long long b = __ballot(in);
-      const int at = have + __popcll(b & below);
-      if (in && at < kWaveBest) out[at] = {key[i][e], col[i] + e};
-      have += __popcll(b);
+    for (int i = 1; i < kChunks; ++i) lm = fmaxf(lm, cm[i]);
+    const unsigned lk = order_key<E>(lm);
+    unsigned t = 0;
+    for (int b = 31; b >= 16; --b) {               // (to within 2^-7: few more than needed)
+      const unsigned c = t | 1u << b;
+      if (__popcll(__ballot(lk >= c)) >= top) t = c;
     }
+    // (below the key of -infinity this is NaN, which nothing is below)
+    const float tau = order_value(t);
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+      if (!__ballot(!(cm[i] < tau))) continue;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const bool in = !(v[i][e] < tau);
+        const u64 b = __ballot(in);
+        if (!b) continue;
+        const int at = have + __popcll(b & below);
+        if (in && at < kWaveBest) out[at] = candidate(order_key<E>(v[i][e]), col[i] + e);
+        have += __popcll(b);
+      }
+    }
+    odd = have > kWaveBest;
   }
-  if (have <= kWaveBest) return have;
-  tau = 0;
-  for (int b = 31; b >= SH; --b) {
-    const unsigned c = tau | 1u << b;
-    int cnt = 0;
+  if (odd) {
+    auto key = [&](int i, int e) {
+      float x = v[i][e];
+      asm volatile("" : "+v"(x));      // (computed where it is used: 32 registers fewer)
+      return col[i] + e < to ? order_key<E>(x) : 0u;
+    };
+    unsigned t = 0;
+    for (int b = 31; b >= SH; --b) {
+      const unsigned c = t | 1u << b;
+      int cnt = 0;
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) cnt += __popcll(__ballot(key(i, e) >= c));
+      if (cnt >= top) t = c;
+    }
+    if (SH > 0 && t && !(t & 0x80000000u)) t |= (1u << SH) - 1;
+    have = 0;
 #pragma unroll
     for (int i = 0; i < kChunks; ++i)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) cnt += __popcll(__ballot(key[i][e] >= c));
-    if (cnt >= top) tau = c;
+      for (int e = 0; e < 8; ++e) {
+        const bool in = key(i, e) > t;
+        const u64 b = __ballot(in);
+        const int at = have + __popcll(b & below);
+        if (in && at < kWaveBest) out[at] = candidate(key(i, e), col[i] + e);
+        have += __popcll(b);
+      }
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {        // the columns' order: chunks, lanes, then e
+      int mine = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) mine += t && key(i, e) == t ? 1 : 0;
+      int at = have;
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const u64 w = __ballot(mine >> b & 1);
+        at += __popcll(w & below) << b;
+        have += __popcll(w) << b;
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (t && key(i, e) == t) {
+          if (at < top) out[at] = candidate(t, col[i] + e);
+          ++at;
+        }
+    }
+    have = min(have, top);
   }
-  if constexpr (SH > 0) {
-    if (tau && !(tau & 0x80000000u)) tau |= (1u << SH) - 1;
+  if (lane < 4 && have + lane < kWaveBest) out[have + lane] = 0;
+  return have;
+}
+
+// The 8 logits from column c on of a row that ends at `to`: -infinity behind it.
+template <class E>
+__device__ __forceinline__ void logits8(const Raw8<E>& raw, int c, int to, int n, float (&v)[8]) {
+  if (c < to) {
+    chunk8(raw, c, n, v);
+    if (c + 8 <= to) return;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (c + e >= to) v[e] = -__builtin_inff();
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = -__builtin_inff();
   }
-  have = 0;
+}
+__device__ __forceinline__ float max8(const float (&v)[8]) {
+  return fmaxf(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])), fmaxf(fmaxf(v[4], v[5]), fmaxf(v[6], v[7])));
+}
+// The sums of 32 logits relative to w.m; e with ENT only.
+template <bool ENT>
+__device__ __forceinline__ void add_logits(const float (&v)[kChunks][8], float scale, Part& w) {
 #pragma unroll
   for (int i = 0; i < kChunks; ++i)
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const bool in = key[i][e] > tau;
-      const unsigned long long b = __ballot(in);
-      const int at = have + __popcll(b & below);
-      if (in && at < kWaveBest) out[at] = {key[i][e], col[i] + e};
-      have += __popcll(b);
+      const float d = __builtin_fmaf(v[i][e], scale, -w.m);
+      const float q = exp_(d);
+      w.s += q;
+      if (ENT) w.e = __builtin_fmaf(q, fmaxf(d, -1e30f), w.e);
     }
-#pragma unroll
-  for (int i = 0; i < kChunks; ++i) {          // the columns' order: chunks, lanes, then e
-    int mine = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) mine += key[i][e] == tau ? 1 : 0;
-    int at = have;
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      const unsigned long long w = __ballot(mine >> b & 1);
-      at += __popcll(w & below) << b;
-      have += __popcll(w) << b;
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (key[i][e] == tau) {
-        if (at < top) out[at] = {tau, col[i] + e};
-        ++at;
-      }
-  }
-  return top;
 }
 
-template <class E, bool TOP>
-__global__ __launch_bounds__(1024) void k_logp_piece(LogpP p) {
-  extern __shared__ Best cand[];                    // TOP: kWaveBest a wave
+// (TOP at 8 waves a SIMD, which it would miss by a few registers: 1000 x 50257
+// fp32 with 5 alternatives 41.5 us, 44 at 6)
+template <class E, bool TOP, bool ENT>
+__global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(TOP ? 8 : 1)))
+void k_logp_piece(LogpP p) {
+  extern __shared__ __attribute__((aligned(16))) u64 cand[];     // TOP: kWaveBest a wave
   __shared__ Part sh[16];
-  __shared__ int count[17];
+  __shared__ int count[16];
   const long long block = flat_block();
   if (block >= p.T * p.S) return;
   const int nt = blockDim.x, wave = threadIdx.x >> 6, nw = nt >> 6;
   const long long t = block / p.S;
-  const int from = (int)(block - t * p.S) * p.len;
-  const int to = min(from + p.len, p.n);            // (a piece of a short row may be empty)
+  const int from = (int)(block - t * p.S) * p.len, to = min(from + p.len, p.n);
   const E* row = (const E*)p.x + t * p.ldx;
-  float v[kChunks][8];
+  float v[kChunks][8], cm[kChunks];
   int col[kChunks];
   {
     Raw8<E> raw[kChunks];
@@ -201,50 +256,23 @@ __global__ __launch_bounds__(1024) void k_logp_piece(LogpP p) {
       if (col[i] < to) raw[i] = fetch8(row, col[i], p.n);
     }
 #pragma unroll
-    for (int i = 0; i < kChunks; ++i) {
-      if (col[i] < to) {
-        chunk8(raw[i], col[i], p.n, v[i]);
-        if (col[i] + 8 > to) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (col[i] + e >= to) v[i][e] = -__builtin_inff();
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[i][e] = -__builtin_inff();
-      }
-    }
+    for (int i = 0; i < kChunks; ++i) logits8(raw[i], col[i], to, p.n, v[i]);
   }
   float mx = -__builtin_inff();
 #pragma unroll
-  for (int i = 0; i < kChunks; ++i)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) mx = fmaxf(mx, v[i][e]);
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) mx = fmaxf(mx, __shfl_xor(mx, o, 64));
-  Part w = {fmaxf(mx * p.scale, kLowest), 0.0f, 0.0f, 0.0f};
-#pragma unroll
-  for (int i = 0; i < kChunks; ++i)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float d = __builtin_fmaf(v[i][e], p.scale, -w.m);
-      const float q = exp_(d);
-      w.s += q;
-      w.e = __builtin_fmaf(q, fmaxf(d, -1e30f), w.e);
-    }
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    w.s += __shfl_xor(w.s, o, 64);
-    w.e += __shfl_xor(w.e, o, 64);
+  for (int i = 0; i < kChunks; ++i) {
+    cm[i] = max8(v[i]);
+    mx = fmaxf(mx, cm[i]);
   }
+  mx = wave_max(mx);
+  Part w = {fmaxf(mx * p.scale, kLowest), 0.0f, 0.0f, 0.0f};
+  add_logits<ENT>(v, p.scale, w);
+  w.s = wave_add(w.s);
+  if (ENT) w.e = wave_add(w.e);
   if ((threadIdx.x & 63) == 0) sh[wave] = w;
   if constexpr (TOP) {
-    unsigned key[kChunks][8];
-#pragma unroll
-    for (int i = 0; i < kChunks; ++i)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) key[i][e] = col[i] + e < to ? order_key<E>(v[i][e]) : 0u;
-    const int c = wave_best<kLow<E>>(key, col, p.top, cand + wave * kWaveBest);
+    const bool odd = __builtin_amdgcn_readfirstlane(w.s != w.s ? 1 : 0);    // the wave's sum is NaN
+    const int c = wave_best<E>(v, cm, col, to, p.top, odd, cand + wave * kWaveBest);
     if ((threadIdx.x & 63) == 0) count[wave] = c;
   }
   __syncthreads();
@@ -254,16 +282,16 @@ __global__ __launch_bounds__(1024) void k_logp_piece(LogpP p) {
     p.part[block] = a;
   }
   if constexpr (TOP) {
-    // every candidate against all waves' candidates
-    const int nc = nw * kWaveBest;
-    for (int i = threadIdx.x; i < nc; i += nt) {
-      if ((i & (kWaveBest - 1)) >= count[i / kWaveBest]) continue;
-      const Best mine = cand[i];
+    // every candidate of the wave against all waves' candidates
+    int all = 0;
+    for (int u = 0; u < nw; ++u) all += count[u];
+    for (int i = threadIdx.x & 63; i < count[wave]; i += 64) {
+      const u64 mine = cand[wave * kWaveBest + i];
       int rank = 0;
-      for (int u = 0; u < nw; ++u)
-        for (int j = 0; j < count[u]; ++j) rank += before(cand[u * kWaveBest + j], mine) ? 1 : 0;
+      for (int u = 0; u < nw; ++u) rank += count_before(cand + u * kWaveBest, 0, count[u], 4, mine);
       if (rank < p.top) p.best[block * p.top + rank] = mine;
     }
+    for (int i = all + threadIdx.x; i < p.top; i += nt) p.best[block * p.top + i] = 0;
   }
 }
 
@@ -271,45 +299,77 @@ __device__ __forceinline__ long long target_of(const void* target, int is64, lon
   return is64 ? ((const long long*)target)[t] : (long long)((const int*)target)[t];
 }
 
-// Rows from their pieces: a wave a row for the sums, and with TOP a workgroup a
-// row, whose threads rank the pieces' candidates.
-template <class E, bool TOP>
-__global__ __launch_bounds__(256) void k_logp_join(LogpP p) {
-  extern __shared__ Best cand[];
-  const int lane = threadIdx.x & 63;
-  const long long t = TOP ? flat_block() : flat_block() * 4 + (threadIdx.x >> 6);
-  if (t >= p.T) return;
-  Part a = {kLowest, 0.0f, 0.0f, 0.0f};
-  for (int s = lane; s < p.S; s += 64) a = merge(a, p.part[t * p.S + s]);
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1)
-    a = merge(a, {__shfl_xor(a.m, o, 64), __shfl_xor(a.s, o, 64), __shfl_xor(a.e, o, 64), 0.0f});
-  const bool none = a.s == 0.0f && a.m < 0.0f;         // every logit is -infinity
+// What a row's log probabilities, x scale - m - l, take.
+struct RowSums {
+  float m, l;
+  bool none;                                           // every logit is -infinity
+};
+// The target's logit, asked for before the pieces are joined.
+template <class E>
+__device__ __forceinline__ float target_logit(const LogpP& p, long long t, bool& token) {
+  token = false;
+  if (!p.target) return 0.0f;
+  const long long j = target_of(p.target, p.target64, t);
+  token = j >= 0 && j < p.n;
+  return token ? to_f32(((const E*)p.x)[t * p.ldx + j]) : 0.0f;
+}
+// A row from its joined pieces, its outputs written by one thread.
+__device__ __forceinline__ RowSums row_sums(const LogpP& p, long long t, const Part& a, bool write,
+                                            float x, bool token) {
+  RowSums r;
+  r.none = a.s == 0.0f && a.m < 0.0f;
   // (an infinite maximum, of a logit or of its product with scale, has no log)
-  const float l = none ? 0.0f : a.m > -kLowest ? __builtin_nanf("") : logf(a.s);
-  if (none) a.m = -__builtin_inff();
-  if (lane == 0 && (!TOP || threadIdx.x == 0)) {
-    p.stats[2 * t] = a.m;
-    p.stats[2 * t + 1] = l;
-    if (p.entropy) p.entropy[t] = none ? 0.0f : l - a.e / a.s;
-    if (p.target) {
-      const long long j = target_of(p.target, p.target64, t);
-      float v = 0.0f;                                  // no token: nothing
-      if (j >= 0 && j < p.n)
-        v = none ? -__builtin_inff()
-                 : __builtin_fmaf(to_f32(((const E*)p.x)[t * p.ldx + j]), p.scale, -a.m) - l;
-      p.logp[t] = v;
-    }
-  }
+  r.l = r.none ? 0.0f : a.m > -kLowest ? __builtin_nanf("") : logf(a.s);
+  r.m = r.none ? -__builtin_inff() : a.m;
+  if (!write) return r;
+  p.stats[2 * t] = r.m;
+  p.stats[2 * t + 1] = r.l;
+  if (p.entropy) p.entropy[t] = r.none ? 0.0f : r.l - a.e / a.s;
+  if (p.target)
+    p.logp[t] = !token ? 0.0f : r.none ? -__builtin_inff() : __builtin_fmaf(x, p.scale, -r.m) - r.l;
+  return r;
+}
+
+// Rows from their pieces: a thread a row, or with TOP a workgroup a row, whose
+// threads rank the pieces' candidates, several threads a candidate where there
+// are few.
+constexpr int kJoinTop = 512;
+template <class E, bool TOP>
+__global__ __launch_bounds__(TOP ? kJoinTop : 64) void k_logp_join(LogpP p) {
+  extern __shared__ __attribute__((aligned(16))) u64 cand[];
+  const long long t = TOP ? flat_block() : flat_block() * 64 + threadIdx.x;
+  if (t >= p.T) return;
+  const int nc = TOP ? p.S * p.top : 0;
+  Part a = {kLowest, 0.0f, 0.0f, 0.0f};
+  const bool write = !TOP || threadIdx.x == 0;
+  bool token = false;
+  const float x = write ? target_logit<E>(p, t, token) : 0.0f;
   if constexpr (TOP) {
-    const int nc = p.S * p.top;
-    for (int i = threadIdx.x; i < nc; i += 256) cand[i] = p.best[t * nc + i];
+    for (int i = threadIdx.x; i < (nc + 3) / 4 * 4; i += kJoinTop) cand[i] = i < nc ? p.best[t * nc + i] : 0;
+    const int lane = threadIdx.x & 63;
+    if (lane < p.S) a = p.part[t * p.S + lane];        // (S is at most 32)
+    a = wave_merge(a);
+  } else {
+#pragma unroll 4
+    for (int s = 0; s < p.S; ++s) a = merge(a, p.part[t * p.S + s]);
+  }
+  const RowSums r = row_sums(p, t, a, write, x, token);
+  if constexpr (TOP) {
     __syncthreads();
-    pick(cand, nc, p.top, [&](int rank, const Best& b) {
-      p.top_logp[t * p.top + rank] =
-          none ? -__builtin_inff() : __builtin_fmaf(order_value(b.key), p.scale, -a.m) - l;
-      p.top_index[t * p.top + rank] = b.at;
-    });
+    int q = 1;                                         // threads a candidate
+    while (q < 16 && nc * q * 2 <= kJoinTop) q *= 2;
+    const int sub = threadIdx.x & (q - 1);
+    for (int i = threadIdx.x / q; i < (nc + 63) / 64 * 64; i += kJoinTop / q) {
+      const u64 mine = i < nc ? cand[i] : 0;
+      int rank = count_before(cand, sub * 4, nc, q * 4, mine);
+      for (int o = 1; o < q; o <<= 1) rank += __shfl_xor(rank, o, 64);
+      if (mine && sub == 0 && rank < p.top) {
+        p.top_logp[t * p.top + rank] =
+            r.none ? -__builtin_inff()
+                   : __builtin_fmaf(order_value((unsigned)(mine >> 32)), p.scale, -r.m) - r.l;
+        p.top_index[t * p.top + rank] = 0xffffffffu - (unsigned)mine;
+      }
+    }
   }
 }
 
@@ -385,23 +445,27 @@ Pieces pieces_of(int n) {
 
 size_t logp_scratch(long long T, int n, int top) {
   const Pieces q = pieces_of(n);
-  return (size_t)T * q.S * (sizeof(Part) + (size_t)top * sizeof(Best));
+  return (size_t)T * q.S * (sizeof(Part) + (size_t)top * sizeof(u64));
 }
 
-template <class E>
-hipError_t launch_logp(const LogpP& p, const Pieces& q, hipStream_t s) {
+template <class E, bool ENT>
+hipError_t launch_logp_t(const LogpP& p, const Pieces& q, hipStream_t s) {
   const dim3 grid = blocks_grid(p.T * q.S), block(q.threads);
-  const size_t lds = (size_t)(q.threads / 64) * kWaveBest * sizeof(Best);
-  if (p.top) hipLaunchKernelGGL((k_logp_piece<E, true>), grid, block, lds, s, p);
-  else hipLaunchKernelGGL((k_logp_piece<E, false>), grid, block, 0, s, p);
+  const size_t lds = (size_t)(q.threads / 64) * kWaveBest * sizeof(u64);
+  if (p.top) hipLaunchKernelGGL((k_logp_piece<E, true, ENT>), grid, block, lds, s, p);
+  else hipLaunchKernelGGL((k_logp_piece<E, false, ENT>), grid, block, 0, s, p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (p.top)
-    hipLaunchKernelGGL((k_logp_join<E, true>), blocks_grid(p.T), dim3(256),
-                       (size_t)q.S * p.top * sizeof(Best), s, p);
+    hipLaunchKernelGGL((k_logp_join<E, true>), blocks_grid(p.T), dim3(kJoinTop),
+                       (size_t)pad_to((long long)q.S * p.top, 4) * sizeof(u64), s, p);
   else
-    hipLaunchKernelGGL((k_logp_join<E, false>), blocks_grid((p.T + 3) / 4), dim3(256), 0, s, p);
+    hipLaunchKernelGGL((k_logp_join<E, false>), blocks_grid((p.T + 63) / 64), dim3(64), 0, s, p);
   return hipGetLastError();
+}
+template <class E>
+hipError_t launch_logp(const LogpP& p, const Pieces& q, hipStream_t s) {
+  return p.entropy ? launch_logp_t<E, true>(p, q, s) : launch_logp_t<E, false>(p, q, s);
 }
 
 template <class E>
@@ -459,7 +523,7 @@ dion3_status dion3_log_probs(const void* X, int64_t ldx, const void* target, int
   p.x = X; p.ldx = ldx; p.target = target; p.target64 = target_bits == 64;
   p.logp = logp; p.stats = stats; p.entropy = entropy;
   p.top_logp = top_logp; p.top_index = (long long*)top_index;
-  p.part = (Part*)ws; p.best = (Best*)(p.part + T * q.S);
+  p.part = (Part*)ws; p.best = (u64*)(p.part + T * q.S);
   p.T = T; p.n = (int)n; p.top = top; p.S = q.S; p.len = q.len; p.scale = scale;
   hipStream_t s = (hipStream_t)stream;
   TraceScope ts("log_probs", 0.0, (double)T * n * size_of(dtype), s);
