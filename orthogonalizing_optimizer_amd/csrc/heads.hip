@@ -25,7 +25,8 @@ struct Side {
   const void* x; const void* w; const void* dy;
   void* y;
   long long ldx, hsx, lddy, hsdy, ldy, hsy;
-  int heads, batches, parts, units;   // batches of 64 / G heads; waves that share a token's; workgroups
+  int heads, batches, units;       // batches of 64 / G heads; workgroups
+  long long each;                  // batches of a wave
 };
 struct HeadsP {
   Side s[2];                      // queries, keys
@@ -110,21 +111,23 @@ struct Angles {
   }
 };
 
-// The batches of heads that a wave takes, token by token.
+// The batches of heads that a wave takes: a stretch of all of its side's, token
+// by token, as long as every other wave's.
 struct Walk {
-  long long task, t;
+  long long left, t;
   int b;
-  __device__ Walk(const HeadsP& p, const Side& s, long long first) : task(first) { place(p, s); }
-  __device__ void place(const HeadsP& p, const Side& s) {
-    t = task / s.parts;
-    b = (int)(task - t * s.parts);
+  __device__ Walk(const HeadsP& p, const Side& s, long long wave) {
+    const long long all = p.T * s.batches, first = wave * s.each;
+    left = all - first < s.each ? all - first : s.each;
+    t = first / s.batches;
+    b = (int)(first - t * s.batches);
   }
-  __device__ bool more(const HeadsP& p) const { return t < p.T; }
-  __device__ void next(const HeadsP& p, const Side& s, long long step) {
-    b += s.parts;
-    if (b < s.batches) return;
-    task += step;
-    place(p, s);
+  __device__ bool more() const { return left > 0; }
+  __device__ void next(const Side& s) {
+    --left;
+    if (++b < s.batches) return;
+    b = 0;
+    ++t;
   }
 };
 
@@ -160,21 +163,26 @@ __device__ __forceinline__ float head_sum(float v, int G) {
 }
 
 // The lane's 16 columns of head h of token t, asked for and as floats (zeros
-// where the lane has none).
-template <class E>
+// where the lane has none).  WHOLE: the turned columns and the others fill all
+// pieces, so no chunk ends early (the checks take 30 registers).
+template <bool WHOLE, class E>
 __device__ __forceinline__ void ask(const void* x, long long ld, long long hs, long long t, int h,
                                     const Item& it, bool mine, Raw8<E> (&raw)[2]) {
   if (!mine) return;
   const E* row = (const E*)x + t * ld + h * hs;
 #pragma unroll
-  for (int k = 0; k < 2; ++k) raw[k] = fetch8(row + it.base[k], it.c[k], it.lim[k]);
+  for (int k = 0; k < 2; ++k)
+    raw[k] = fetch8(row + it.base[k], it.c[k], WHOLE ? it.c[k] + 8 : it.lim[k]);
 }
-template <class E>
+template <bool WHOLE, class E>
 __device__ __forceinline__ void take(const Raw8<E> (&raw)[2], const Item& it, bool mine,
                                      float (&v)[2][8]) {
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    if (mine) {
+    if (WHOLE) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[k][e] = mine ? to_f32((E)raw[k].v[e]) : 0.0f;
+    } else if (mine) {
       chunk8(raw[k], it.c[k], it.lim[k], v[k]);
     } else {
 #pragma unroll
@@ -182,13 +190,14 @@ __device__ __forceinline__ void take(const Raw8<E> (&raw)[2], const Item& it, bo
     }
   }
 }
-template <class E>
+template <bool WHOLE, class E>
 __device__ __forceinline__ void put(void* y, long long ld, long long hs, long long t, int h,
                                     const Item& it, const float (&v)[2][8]) {
   E* row = (E*)y + t * ld + h * hs;
 #pragma unroll
   for (int k = 0; k < 2; ++k)
-    if (it.c[k] < it.lim[k]) store8(row + it.base[k], it.c[k], it.lim[k], v[k]);
+    if (WHOLE || it.c[k] < it.lim[k])
+      store8(row + it.base[k], it.c[k], WHOLE ? it.c[k] + 8 : it.lim[k], v[k]);
 }
 __device__ __forceinline__ float head_rstd(const float (&v)[2][8], int G, int D, float eps) {
   float ss = 0.0f;
@@ -197,20 +206,19 @@ __device__ __forceinline__ float head_rstd(const float (&v)[2][8], int G, int D,
   return 1.0f / sqrtf(head_sum(ss, G) / (float)D + eps);
 }
 
-template <class E, bool IL>
+template <class E, bool IL, bool WHOLE>
 __global__ __launch_bounds__(256) void k_heads(HeadsP p) {
   extern __shared__ __attribute__((aligned(16))) float2 turns[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int G = p.G, per = 64 / G, j = lane & (G - 1), slot = lane / G;
   const bool isk = (int)blockIdx.x >= p.s[0].units;
   const Side& s = p.s[isk];
-  const long long step = s.units * 4LL;
   Walk at(p, s, ((int)blockIdx.x - (isk ? p.s[0].units : 0)) * 4LL + wave);
-  if (!at.more(p)) return;
+  if (!at.more()) return;
   const Item it = my_item<IL>(j, p.D, p.r);
   Raw8<E> raw[2];
   bool mine = it.on && at.b * per + slot < s.heads;
-  ask(s.x, s.ldx, s.hsx, at.t, at.b * per + slot, it, mine, raw);
+  ask<WHOLE>(s.x, s.ldx, s.hsx, at.t, at.b * per + slot, it, mine, raw);
   double pos = position(p, at.t);
   float w[2][8], co[8], si[8];
   load_weight<E>(p, s, it, w);
@@ -218,15 +226,15 @@ __global__ __launch_bounds__(256) void k_heads(HeadsP p) {
   for (bool fresh = true;;) {
     if (fresh) ang.set(p, pos, it.rot ? 8 * j : 0, 1.0f, co, si);
     float v[2][8];
-    take(raw, it, mine, v);
+    take<WHOLE>(raw, it, mine, v);
     // the next batch's columns, and the next token's position, on their way
     const Walk now = at;
     const bool own = mine;
-    at.next(p, s, step);
-    const bool go = at.more(p);
+    at.next(s);
+    const bool go = at.more();
     if (go) {
       mine = it.on && at.b * per + slot < s.heads;
-      ask(s.x, s.ldx, s.hsx, at.t, at.b * per + slot, it, mine, raw);
+      ask<WHOLE>(s.x, s.ldx, s.hsx, at.t, at.b * per + slot, it, mine, raw);
       fresh = at.t != now.t;
       if (fresh) pos = position(p, at.t);
     }
@@ -234,7 +242,7 @@ __global__ __launch_bounds__(256) void k_heads(HeadsP p) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i / 8][i % 8] *= rs * w[i / 8][i % 8];
     rotate<IL>(v, co, si, it.rot);
-    if (own) put<E>(s.y, s.ldy, s.hsy, now.t, now.b * per + slot, it, v);
+    if (own) put<WHOLE, E>(s.y, s.ldy, s.hsy, now.t, now.b * per + slot, it, v);
     if (!go) return;
   }
 }
@@ -242,7 +250,7 @@ __global__ __launch_bounds__(256) void k_heads(HeadsP p) {
 // The weights' gradients: a lane adds up its columns over its tokens and
 // heads, the lanes of equal columns and the workgroup's waves are joined at
 // the end, and the workgroups' rows by k_heads_join, each in a fixed order.
-template <class E, bool IL>
+template <class E, bool IL, bool WHOLE>
 __global__ __launch_bounds__(256) void k_heads_grad(HeadsP p) {
   extern __shared__ __attribute__((aligned(16))) float2 turns[];
   float* sh = (float*)turns + 8 * p.pitch;             // 3 waves x D
@@ -250,17 +258,16 @@ __global__ __launch_bounds__(256) void k_heads_grad(HeadsP p) {
   const int G = p.G, per = 64 / G, j = lane & (G - 1), slot = lane / G;
   const bool isk = (int)blockIdx.x >= p.s[0].units;
   const Side& s = p.s[isk];
-  const long long step = s.units * 4LL;
   Walk at(p, s, ((int)blockIdx.x - (isk ? p.s[0].units : 0)) * 4LL + wave);
   const Item it = my_item<IL>(j, p.D, p.r);
   float dw[2][8];
 #pragma unroll
   for (int i = 0; i < 16; ++i) dw[i / 8][i % 8] = 0.0f;
-  if (at.more(p)) {
+  if (at.more()) {
     Raw8<E> rx[2], ry[2];
     bool mine = it.on && at.b * per + slot < s.heads;
-    ask(s.x, s.ldx, s.hsx, at.t, at.b * per + slot, it, mine, rx);
-    ask(s.dy, s.lddy, s.hsdy, at.t, at.b * per + slot, it, mine, ry);
+    ask<WHOLE>(s.x, s.ldx, s.hsx, at.t, at.b * per + slot, it, mine, rx);
+    ask<WHOLE>(s.dy, s.lddy, s.hsdy, at.t, at.b * per + slot, it, mine, ry);
     double pos = position(p, at.t);
     float w[2][8], co[8], si[8];
     load_weight<E>(p, s, it, w);
@@ -268,16 +275,16 @@ __global__ __launch_bounds__(256) void k_heads_grad(HeadsP p) {
     for (bool fresh = true;;) {
       if (fresh) ang.set(p, pos, it.rot ? 8 * j : 0, -1.0f, co, si);
       float x[2][8], u[2][8];
-      take(rx, it, mine, x);
-      take(ry, it, mine, u);
+      take<WHOLE>(rx, it, mine, x);
+      take<WHOLE>(ry, it, mine, u);
       const Walk now = at;
       const bool own = mine;
-      at.next(p, s, step);
-      const bool go = at.more(p);
+      at.next(s);
+      const bool go = at.more();
       if (go) {
         mine = it.on && at.b * per + slot < s.heads;
-        ask(s.x, s.ldx, s.hsx, at.t, at.b * per + slot, it, mine, rx);
-        ask(s.dy, s.lddy, s.hsdy, at.t, at.b * per + slot, it, mine, ry);
+        ask<WHOLE>(s.x, s.ldx, s.hsx, at.t, at.b * per + slot, it, mine, rx);
+        ask<WHOLE>(s.dy, s.lddy, s.hsdy, at.t, at.b * per + slot, it, mine, ry);
         fresh = at.t != now.t;
         if (fresh) pos = position(p, at.t);
       }
@@ -298,7 +305,7 @@ __global__ __launch_bounds__(256) void k_heads_grad(HeadsP p) {
 #pragma unroll
         for (int i = 0; i < 16; ++i)
           u[i / 8][i % 8] = rs * __builtin_fmaf(-x[i / 8][i % 8], c, u[i / 8][i % 8]);
-        put<E>(s.y, s.ldy, s.hsy, now.t, now.b * per + slot, it, u);
+        put<WHOLE, E>(s.y, s.ldy, s.hsy, now.t, now.b * per + slot, it, u);
       }
       if (!go) break;
     }
@@ -331,7 +338,7 @@ __global__ __launch_bounds__(256) void k_heads_grad(HeadsP p) {
 }
 
 // dw[side][c] = the sum over the side's workgroups: 16 columns a workgroup, 64
-// slices of the rows, added in slice order.
+// slices of the rows.
 __global__ __launch_bounds__(1024) void k_heads_join(const float* __restrict__ part, int qunits,
                                                      int kunits, int D, float* __restrict__ dw) {
   __shared__ float sh[64][17];
@@ -345,11 +352,9 @@ __global__ __launch_bounds__(1024) void k_heads_join(const float* __restrict__ p
     if (c < D) a += rows[(long long)u * D + c];
   sh[slice][col] = a;
   __syncthreads();
-  if (slice == 0 && c < D) {
-    a = 0.0f;
-    for (int i = 0; i < 64; ++i) a += sh[i][col];
-    dw[blockIdx.y * D + c] = a;
-  }
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, mine = blockIdx.x * 16 + wave;
+  a = wave_add(sh[lane][wave]);                        // a wave a column
+  if (lane == 0 && mine < D) dw[blockIdx.y * D + mine] = a;
 }
 
 // ------------------------------------------------------------------ the calls
@@ -362,30 +367,31 @@ int pieces(int D, int r, bool il) {
   return (il ? (r + 15) / 16 : (r / 2 + 7) / 8) + (D - r + 15) / 16;
 }
 // A head takes the power of two of lanes that holds its columns, 16 a lane.
-// kWaves waves are shared out between queries and keys by their batches; a
-// token's batches between waves where there are few tokens.
-constexpr int kWaves = 4096;
+// As many waves as stay resident (a few more would run after all others) are
+// shared out between queries and keys by their batches, and each takes equally
+// many of them: 8192 tokens of 32 + 8 heads of 128 take 34 us (5 TB/s; twice
+// the resident waves, 35 with as many) and 59 backwards (4.3 TB/s; 65 by whole
+// tokens, 57 with 4 waves a SIMD that read their weight from LDS: not kept).
 struct Split {
-  int G, batches[2], parts[2], units[2];
+  int G, batches[2], units[2];
+  long long each[2];
 };
-Split split_heads(long long T, int hq, int hk, int D, int r, bool il, int waves) {
-  Split q;
+Split split_heads(long long T, int hq, int hk, int D, int r, bool il, bool grad) {
+  Split q = {};
   q.G = 1;
   while (q.G < pieces(D, r, il)) q.G *= 2;
   const int per = 64 / q.G, heads[2] = {hq, hk};
+  const bool whole = r % 16 == 0 && D % 16 == 0;
+  const int units = 256 * (grad ? 3 : whole ? 10 : 4);
   for (int i = 0; i < 2; ++i) q.batches[i] = (heads[i] + per - 1) / per;
-  const int nb = q.batches[0] + q.batches[1];
   for (int i = 0; i < 2; ++i) {
-    if (q.batches[i] == 0) {
-      q.parts[i] = 1;
-      q.units[i] = 0;
-      continue;
-    }
-    const long long share = (long long)waves * q.batches[i] / nb + 1;
-    const long long parts = T > 0 ? (share + T - 1) / T : 1;
-    q.parts[i] = (int)(parts < q.batches[i] ? parts : q.batches[i]);
-    const long long tasks = T * q.parts[i], most = (share + 3) / 4;
-    q.units[i] = (int)((tasks + 3) / 4 < most ? (tasks + 3) / 4 : most);
+    const long long all = T * q.batches[i];
+    if (all == 0) continue;
+    const long long share = (long long)units * q.batches[i] / (q.batches[0] + q.batches[1]);
+    const long long waves = share < 1 ? 4 : share * 4;
+    q.each[i] = (all + waves - 1) / waves;
+    const long long used = (all + q.each[i] - 1) / q.each[i];
+    q.units[i] = (int)((used + 3) / 4);
   }
   return q;
 }
@@ -435,12 +441,29 @@ HeadsP describe(const dion3_heads* q, const dion3_heads* k, const Split& sp, con
     if (both[i]) {
       const dion3_heads& s = *both[i];
       p.s[i] = {s.X, s.w, s.dY, s.Y, s.ldx, s.hsx, s.lddy, s.hsdy, s.ldy, s.hsy, s.heads,
-                sp.batches[i], sp.parts[i], sp.units[i]};
+                sp.batches[i], sp.units[i], sp.each[i]};
     }
   p.freqs = freqs; p.pos = pos; p.T = T;
   p.D = D; p.r = r; p.G = sp.G; p.pitch = r ? (r / 2 + 7) / 8 * 8 : 8;
   p.pos64 = pos_bits == 64; p.wtype = wtype; p.eps = eps;
   return p;
+}
+
+template <class E, bool GRAD, bool IL, bool WHOLE>
+void launch_heads_t(const HeadsP& p, int units, size_t lds, hipStream_t s) {
+  if (GRAD) hipLaunchKernelGGL((k_heads_grad<E, IL, WHOLE>), dim3(units), dim3(256), lds, s, p);
+  else hipLaunchKernelGGL((k_heads<E, IL, WHOLE>), dim3(units), dim3(256), lds, s, p);
+}
+template <class E, bool GRAD>
+void launch_heads(const HeadsP& p, int units, size_t lds, int interleaved, hipStream_t s) {
+  const bool whole = p.r % 16 == 0 && p.D % 16 == 0;
+  if (interleaved) {
+    if (whole) launch_heads_t<E, GRAD, true, true>(p, units, lds, s);
+    else launch_heads_t<E, GRAD, true, false>(p, units, lds, s);
+  } else {
+    if (whole) launch_heads_t<E, GRAD, false, true>(p, units, lds, s);
+    else launch_heads_t<E, GRAD, false, false>(p, units, lds, s);
+  }
 }
 
 }  // namespace
@@ -459,18 +482,12 @@ dion3_status dion3_qk_norm_rope(const dion3_heads* q, const dion3_heads* k, cons
   TRY(check_heads(q, k, freqs, pos, pos_bits, T, D, r, interleaved, eps, wtype, dtype, false));
   if (T == 0) return DION3_OK;
   hipStream_t s = (hipStream_t)stream;
-  const Split sp = split_heads(T, q->heads, k ? k->heads : 0, D, r, interleaved, kWaves);
+  const Split sp = split_heads(T, q->heads, k ? k->heads : 0, D, r, interleaved, false);
   const HeadsP p = describe(q, k, sp, freqs, pos, pos_bits, T, D, r, eps, wtype);
   TraceScope ts("qk_norm_rope", 0.0, 4.0 * T * D * (q->heads + (k ? k->heads : 0)), s);
-  const dim3 grid((unsigned)units_of(sp)), block(256);
   const size_t lds = (size_t)p.pitch * 4 * 8;
-  if (dtype == DION3_BF16) {
-    if (interleaved) hipLaunchKernelGGL((k_heads<bf16, true>), grid, block, lds, s, p);
-    else hipLaunchKernelGGL((k_heads<bf16, false>), grid, block, lds, s, p);
-  } else {
-    if (interleaved) hipLaunchKernelGGL((k_heads<f16, true>), grid, block, lds, s, p);
-    else hipLaunchKernelGGL((k_heads<f16, false>), grid, block, lds, s, p);
-  }
+  if (dtype == DION3_BF16) launch_heads<bf16, false>(p, units_of(sp), lds, interleaved, s);
+  else launch_heads<f16, false>(p, units_of(sp), lds, interleaved, s);
   HIP_TRY(hipGetLastError());
   return DION3_OK;
 }
@@ -482,7 +499,7 @@ dion3_status dion3_qk_norm_rope_grad_workspace_size(int64_t T, int32_t hq, int32
   if (T > DION3_MAX_TOKENS || D > kMaxHeadDim || hq > kMaxHeads || hk > kMaxHeads ||
       pieces(D, r, interleaved) > 64)
     return DION3_ERR_UNSUPPORTED;
-  *bytes = (size_t)units_of(split_heads(T, hq, hk, D, r, interleaved, kWaves)) * D * 4;
+  *bytes = (size_t)units_of(split_heads(T, hq, hk, D, r, interleaved, true)) * D * 4;
   return DION3_OK;
 }
 
@@ -495,21 +512,15 @@ dion3_status dion3_qk_norm_rope_grad(const dion3_heads* q, const dion3_heads* k,
   if (!elem_aligned(dw, 4)) return DION3_ERR_ARG;
   if (T > 0 && !dw && !q->Y && !(k && k->Y)) return DION3_ERR_ARG;
   hipStream_t s = (hipStream_t)stream;
-  const Split sp = split_heads(T, q->heads, k ? k->heads : 0, D, r, interleaved, kWaves);
+  const Split sp = split_heads(T, q->heads, k ? k->heads : 0, D, r, interleaved, true);
   if (dw) TRY(check_scratch(ws, ws_bytes, (size_t)units_of(sp) * D * 4));
   if (T > 0) {
     HeadsP p = describe(q, k, sp, freqs, pos, pos_bits, T, D, r, eps, wtype);
     p.part = dw ? (float*)ws : nullptr;
     TraceScope ts("qk_norm_rope_grad", 0.0, 6.0 * T * D * (q->heads + (k ? k->heads : 0)), s);
-    const dim3 grid((unsigned)units_of(sp)), block(256);
     const size_t lds = (size_t)p.pitch * 4 * 8 + (dw ? (size_t)3 * D * 4 : 0);
-    if (dtype == DION3_BF16) {
-      if (interleaved) hipLaunchKernelGGL((k_heads_grad<bf16, true>), grid, block, lds, s, p);
-      else hipLaunchKernelGGL((k_heads_grad<bf16, false>), grid, block, lds, s, p);
-    } else {
-      if (interleaved) hipLaunchKernelGGL((k_heads_grad<f16, true>), grid, block, lds, s, p);
-      else hipLaunchKernelGGL((k_heads_grad<f16, false>), grid, block, lds, s, p);
-    }
+    if (dtype == DION3_BF16) launch_heads<bf16, true>(p, units_of(sp), lds, interleaved, s);
+    else launch_heads<f16, true>(p, units_of(sp), lds, interleaved, s);
     HIP_TRY(hipGetLastError());
   }
   if (dw) {
