@@ -137,13 +137,11 @@ def _declare(lib):
         "dion3_embedding_grad": (c.c_int, [vp, i32, vp, i64, vp, i64, i32, i64, i64, i64, f32, i32,
                                            vp, sz, vp]),
         "dion3_heads_size": (sz, []),
-        "dion3_qk_norm_rope": (c.c_int, [c.POINTER(HeadsDesc), c.POINTER(HeadsDesc), vp, vp, i32,
-                                         i64, i32, i32, i32, f32, i32, i32, vp]),
+        "dion3_qk_norm_rope": (c.c_int, [vp, vp, vp, vp, i32, i64, i32, i32, i32, f32, i32, i32, vp]),
         "dion3_qk_norm_rope_grad_workspace_size": (c.c_int, [i64, i32, i32, i32, i32, i32,
                                                              c.POINTER(sz)]),
-        "dion3_qk_norm_rope_grad": (c.c_int, [c.POINTER(HeadsDesc), c.POINTER(HeadsDesc), vp, vp,
-                                              i32, vp, i64, i32, i32, i32, f32, i32, i32, vp, sz,
-                                              vp]),
+        "dion3_qk_norm_rope_grad": (c.c_int, [vp, vp, vp, vp, i32, vp, i64, i32, i32, i32, f32, i32, i32,
+                                              vp, sz, vp]),
         "dion3_log_probs_workspace_size": (c.c_int, [i64, i64, i32, c.POINTER(sz)]),
         "dion3_log_probs": (c.c_int, [vp, i64, vp, i32, vp, vp, vp, vp, vp, i64, i64, i32, f32,
                                       i32, vp, sz, vp]),

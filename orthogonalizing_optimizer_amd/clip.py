@@ -50,12 +50,13 @@ def _table(grads, into, written):
         into = list(into)
         if len(into) != len(grads):
             raise ValueError("need one sum per gradient")
-    table, device, seen = array.array("q"), None, set()
+    table, device, seen = [], None, set()
+    strided, none = torch.strided, (0,) * 7
     for i, g in enumerate(grads):
         if g is None:
-            table.extend((0, 0, 0, 0, 0, 0, 0))
+            table += none
             continue
-        if not isinstance(g, torch.Tensor) or g.device.type != "cuda" or g.layout != torch.strided:
+        if not isinstance(g, torch.Tensor) or not g.is_cuda or g.layout is not strided:
             raise TypeError(f"gradient {i} must be a dense CUDA (HIP) tensor")
         if g.requires_grad:
             raise TypeError(f"gradient {i} requires a gradient itself: pass p.grad, not p")
@@ -66,26 +67,27 @@ def _table(grads, into, written):
             device = g.device
         elif g.device != device:
             raise ValueError("all gradients must be on one device")
-        m = into[i] if into is not None else None
-        if m is not None:
-            if not isinstance(m, torch.Tensor) or m.device != device or m.dtype != torch.float32:
+        m = None
+        if into is not None:
+            m = into[i]
+            if not isinstance(m, torch.Tensor) or m.device != device or m.dtype is not torch.float32:
                 raise TypeError(f"sum {i} must be a float32 tensor on {device}")
             if m.shape != g.shape:
                 raise ValueError(f"sum {i} must have shape {tuple(g.shape)}")
-        elif into is not None:
-            raise TypeError(f"sum {i} is missing")
         n = g.numel()
         if n == 0:
-            table.extend((0, 0, 0, 0, 0, 0, code))
+            table += none
             continue
-        gp, mp = g.data_ptr(), m.data_ptr() if m is not None else 0
+        gp, mp = g.data_ptr(), 0 if m is None else m.data_ptr()
+        if g.is_contiguous() and (m is None or m.is_contiguous()):
+            table += (gp, mp, 1, n, n, n, code)
+        else:
+            table += (gp, mp, *_layout(g, m, i), code)
         if written:
-            if (mp or gp) in seen:
-                raise ValueError(f"{'sum' if mp else 'gradient'} {i} is listed twice")
             seen.add(mp or gp)
-        rows, cols, ldg, ldm = _layout(g, m, i)
-        table.extend((gp, mp, rows, cols, ldg, ldm, code))
-    return table, len(grads), device
+    if written and len(seen) != sum(1 for n in table[3::7] if n):
+        raise ValueError("a gradient or a sum is listed twice")
+    return array.array("q", table), len(grads), device
 
 
 def grad_norm(grads, scale: float = 1.0, per_tensor: bool = False,

@@ -11,7 +11,7 @@ differentiable forms.
 """
 from __future__ import annotations
 
-import ctypes
+import array
 from typing import Optional
 
 import torch
@@ -123,15 +123,19 @@ def embedding_layer(tokens, w, scale: float = 1.0, dtype=None):
 
 def _heads(t, name):
     """(tokens, token stride, heads, head stride, columns) of [..., heads, columns]."""
-    if t.dim() < 2:
+    shape = t.shape
+    if len(shape) < 2:
         raise ValueError(f"{name} must be [..., heads, columns]")
-    h, D = t.shape[-2:]
+    h, D = shape[-2:]
     if h < 1 or D < 1:
         raise ValueError(f"{name} needs at least one head and one column")
-    if D > 1 and t.stride(-1) != 1:
+    if t.is_contiguous():
+        return t.numel() // (h * D), h * D, h, D, D
+    strides = t.stride()
+    if D > 1 and strides[-1] != 1:
         raise ValueError(f"{name} must have contiguous columns")
-    T, ld = _lead(t.shape[:-2], t.stride()[:-2], name)
-    hs = t.stride(-2) if h > 1 else D
+    T, ld = _lead(shape[:-2], strides[:-2], name)
+    hs = strides[-2] if h > 1 else D
     ld = h * D if ld is None else ld
     if (T > 1 and ld < D) or hs < D:
         raise ValueError(f"{name}: its heads overlap")
@@ -141,11 +145,11 @@ def _heads(t, name):
 def _positions(positions, lead, device):
     if not isinstance(positions, torch.Tensor) or positions.device != device:
         raise TypeError(f"positions must be a tensor on {device}")
-    if positions.dtype not in (torch.int64, torch.int32):
+    if positions.dtype is not torch.int64 and positions.dtype is not torch.int32:
         raise TypeError("positions must be int64 or int32")
     if positions.shape != lead:
-        positions = positions.expand(lead)           # (ValueError in torch's own words)
-    return positions.contiguous()
+        positions = positions.expand(lead)           # (torch's own error where it does not)
+    return positions if positions.is_contiguous() else positions.contiguous()
 
 
 def _freqs(freqs, D, device):
@@ -159,41 +163,49 @@ def _freqs(freqs, D, device):
 
 
 class _Sides:
-    """The checked queries and keys of a call, as the library takes them."""
+    """The checked queries and keys of a call, as the library takes them: a
+    dion3_heads each (its members in order, all of 8 bytes)."""
+
+    __slots__ = ("q", "k", "T", "D", "r", "pos", "bits", "desc", "wtype", "dtype", "keep")
 
     def __init__(self, q, k, q_weight, k_weight, positions, freqs):
         _t16(q, "q")
         self.q, self.k = q, k
-        self.T, ld, hq, hs, self.D = _heads(q, "q")
-        self.lead = q.shape[:-2]
-        _vector(q_weight, self.D, q, "q_weight")
-        self.desc = [_lib.HeadsDesc(X=_ptr(q), ldx=ld, hsx=hs, w=q_weight.data_ptr(), heads=hq), None]
+        self.T, ld, hq, hs, D = _heads(q, "q")
+        self.D = D
+        lead = q.shape[:-2]
+        _vector(q_weight, D, q, "q_weight")
+        # X, ldx, hsx, w, dY, lddy, hsdy, Y, ldy, hsy, heads
+        self.desc = [[q.data_ptr(), ld, hs, q_weight.data_ptr(), 0, 0, 0, 0, 0, 0, hq], None]
         if (k is None) != (k_weight is None):
             raise ValueError("k and k_weight belong together")
         if k is not None:
             _same(k, q, "k")
-            T, ld, hk, hs, D = _heads(k, "k")
-            if k.shape[:-2] != self.lead or D != self.D:
-                raise ValueError(f"k must have q's tokens and {self.D} columns a head")
+            _, ld, hk, hs, Dk = _heads(k, "k")
+            if k.shape[:-2] != lead or Dk != D:
+                raise ValueError(f"k must have q's tokens and {D} columns a head")
             _vector(k_weight, D, q, "k_weight")
             if k_weight.dtype != q_weight.dtype:
                 raise TypeError("q_weight and k_weight must have one type")
-            self.desc[1] = _lib.HeadsDesc(X=_ptr(k), ldx=ld, hsx=hs, w=k_weight.data_ptr(), heads=hk)
-        self.pos = _positions(positions, self.lead, q.device)
-        self.r = _freqs(freqs, self.D, q.device)
+            self.desc[1] = [k.data_ptr(), ld, hs, k_weight.data_ptr(), 0, 0, 0, 0, 0, 0, hk]
+        self.pos = _positions(positions, lead, q.device)
+        self.r = _freqs(freqs, D, q.device)
         self.wtype, self.dtype = _DTYPES[q_weight.dtype], _DTYPES[q.dtype]
-        self.freqs = freqs
-        self.bits = 64 if self.pos.dtype == torch.int64 else 32
+        self.bits = 64 if self.pos.dtype is torch.int64 else 32
 
     def output(self, i):
         """A contiguous output of side i, put into its description."""
-        t = (self.q, self.k)[i]
+        t = self.k if i else self.q
         y = t.new_empty(t.shape)
-        self.desc[i].Y, self.desc[i].ldy, self.desc[i].hsy = _ptr(y), t.shape[-2] * self.D, self.D
+        d = self.desc[i]
+        d[7], d[8], d[9] = y.data_ptr(), d[10] * self.D, self.D
         return y
 
     def refs(self):
-        return tuple(ctypes.byref(s) if s is not None else None for s in self.desc)
+        q, k = self.desc
+        self.keep = a = array.array("q", q if k is None else q + k)
+        p = a.buffer_info()[0]
+        return p, None if k is None else p + 88
 
 
 def qk_norm_rope(q, k, q_weight, k_weight, positions, freqs, eps: float = 1e-6,
@@ -230,7 +242,7 @@ def qk_norm_rope_grad(dyq, dyk, q, k, q_weight, k_weight, positions, freqs, eps:
         if t is not None:
             _same(dy, t, "dyq" if i == 0 else "dyk", t.shape)
             _, ld, _, hs, _ = _heads(dy, "dyq" if i == 0 else "dyk")
-            s.desc[i].dY, s.desc[i].lddy, s.desc[i].hsdy = _ptr(dy), ld, hs
+            s.desc[i][4:7] = dy.data_ptr(), ld, hs
     if not need_dx and not need_dw:
         return None, None, None, None
     dq = s.output(0) if need_dx else None
