@@ -21,7 +21,7 @@ namespace dion3 {
 namespace {
 
 constexpr int kMaxChunk = 32;         // places of one wave at most
-constexpr int kZeroRows = 8;          // rows of dW that one workgroup clears
+constexpr int kMaxZeroRows = 256;     // rows of dW that one workgroup clears at most (its threads)
 constexpr int kCountMax = 8192;       // tokens up to which places are counted, not sorted by digits
 constexpr int kTile = 4096;           // tokens of a workgroup of the sort by digits
 
@@ -229,7 +229,7 @@ struct EmbedGradP {
   float* dw; long long ldw;
   float* part;                        // [chunks][2][m]: a run from before, one that goes on
   long long T, sum_blocks;
-  int n, m, slices, len;              // slices of 512 columns, places of a chunk
+  int n, m, slices, len, zero_rows;   // slices of 512 columns, places of a chunk, rows to clear
   float scale;
   int accumulate;
 };
@@ -320,36 +320,54 @@ __global__ __launch_bounds__(256) void k_embed_grad(EmbedGradP p) {
     return;
   }
   __shared__ long long ends[2];
-  __shared__ int there[kZeroRows];
-  const long long v0 = (block - p.sum_blocks) * kZeroRows;
+  __shared__ unsigned char there[kMaxZeroRows];
+  const long long v0 = (block - p.sum_blocks) * p.zero_rows;
   if (v0 >= p.n || ACC) return;                     // (a grid may hold more blocks than asked for)
-  const int rows = (int)(p.n - v0 < kZeroRows ? p.n - v0 : kZeroRows);
+  const int rows = (int)(p.n - v0 < p.zero_rows ? p.n - v0 : p.zero_rows);
   if (wave < 2) {
     const long long at = first_at(p.key, p.T, (int)v0 + (wave ? rows : 0));
     if ((threadIdx.x & 63) == 0) ends[wave] = at;
   }
   __syncthreads();
-  if ((int)threadIdx.x < rows) {
-    long long lo = ends[0], hi = ends[1];
+  const long long lo = ends[0], hi = ends[1];
+  const int any = hi > lo;                          // tokens among these rows
+  if (any && (int)threadIdx.x < rows) {
+    long long a = lo, b = hi;
     const int v = (int)v0 + threadIdx.x;
-    const long long end = hi;
-    while (lo < hi) {
-      const long long mid = (lo + hi) / 2;
-      if (p.key[mid] < v) lo = mid + 1;
-      else hi = mid;
+    while (a < b) {
+      const long long mid = (a + b) / 2;
+      if (p.key[mid] < v) a = mid + 1;
+      else b = mid;
     }
-    there[threadIdx.x] = lo < end && p.key[lo] == v;
+    there[threadIdx.x] = a < hi && p.key[a] == v;
   }
   __syncthreads();
   // (nontemporal: 32000 x 4096 of 8192 tokens 100 us, 116 with plain stores,
   // which push dy's rows and the sums out of the cache)
   typedef float f4 __attribute__((ext_vector_type(4), aligned(4)));
-  for (int r = 0; r < rows; ++r) {
-    if (there[r]) continue;
-    float* row = p.dw + (v0 + r) * p.ldw;
-    for (int c = threadIdx.x * 4; c < p.m; c += 1024) {
+  const f4 zero = {0, 0, 0, 0};
+  float* base = p.dw + v0 * p.ldw;
+  if (p.ldw == p.m && p.m > 1 && p.m <= 4096) {       // short rows: one stretch
+    const unsigned n = (unsigned)rows * p.m, inv = (unsigned)((0x100000000ull + p.m - 1) / p.m);
+    for (unsigned i = threadIdx.x * 4; i < n; i += 1024) {
+      const bool whole = i + 4 <= n;
+      // i / m: exact for i m < 2^32
+      const int r0 = any ? __umulhi(i, inv) : 0, r1 = any && whole ? __umulhi(i + 3, inv) : r0;
+      if (whole && !(any && (there[r0] || there[r1]))) {
+        __builtin_nontemporal_store(zero, (f4*)(base + i));
+      } else {
+        for (unsigned e = i; e < i + 4 && e < n; ++e)
+          if (!any || !there[__umulhi(e, inv)]) base[e] = 0.0f;
+      }
+    }
+    return;
+  }
+  for (int r = wave; r < rows; r += 4) {
+    if (any && there[r]) continue;
+    float* row = base + r * p.ldw;
+    for (int c = (threadIdx.x & 63) * 4; c < p.m; c += 256) {
       if (c + 4 <= p.m) {
-        __builtin_nontemporal_store(f4{0, 0, 0, 0}, (f4*)(row + c));
+        __builtin_nontemporal_store(zero, (f4*)(row + c));
       } else {
         for (int e = c; e < p.m; ++e) row[e] = 0.0f;
       }
@@ -423,7 +441,8 @@ dim3 grid_of(long long blocks) {
 
 // The workspace: sorted keys and places (twice for the sort by digits, which
 // swaps them, and its histograms), then the partial rows.  A chunk is of
-// kMaxChunk places, of fewer where there would be too few waves.
+// kMaxChunk places, of fewer where there would be too few waves (but not where
+// one holds all tokens: that saves the joins' launch).
 struct EmbedPlan {
   int digits, tiles, len;
   long long chunks;
@@ -432,7 +451,7 @@ struct EmbedPlan {
 EmbedPlan plan_embed(long long T, int n, int m) {
   EmbedPlan q = {};
   q.len = kMaxChunk;
-  while (q.len > 8 && T / q.len * ((m + 511) / 512) < 2048) q.len /= 2;
+  while (T > kMaxChunk && q.len > 8 && T / q.len * ((m + 511) / 512) < 2048) q.len /= 2;
   q.chunks = (T + q.len - 1) / q.len;
   const size_t list = (size_t)pad_to(T, 64) * 4;
   size_t b = 2 * list;
@@ -565,7 +584,9 @@ dion3_status dion3_embedding_grad(const void* tokens, int32_t token_bits, const 
     HIP_TRY(sort_tokens(tokens, token_bits == 64, T, (int)n, q, (char*)ws, p.key, p.pos, s));
   }
   p.sum_blocks = (q.chunks * p.slices + 3) / 4;
-  const long long zero_blocks = accumulate ? 0 : (n + kZeroRows - 1) / kZeroRows;
+  // (about 128 KB a workgroup)
+  p.zero_rows = (int)(32768 / m < 8 ? 8 : 32768 / m > kMaxZeroRows ? kMaxZeroRows : 32768 / m);
+  const long long zero_blocks = accumulate ? 0 : (n + p.zero_rows - 1) / p.zero_rows;
   {
     TraceScope ts("embedding_grad", 0.0, (double)T * m * size_of(dtype) + 4.0 * (accumulate ? 0 : n) * m, s);
     const dim3 grid = grid_of(p.sum_blocks + zero_blocks);

@@ -84,7 +84,8 @@ KINDS = ["uniform", "frequent", "one", "falling", "none", "padded"]
 @pytest.mark.parametrize("T,n,m", [(1, 1, 1), (5, 3, 7), (31, 40, 64), (32, 7, 512), (33, 100, 520),
                                    (64, 1, 40), (517, 3000, 515), (1000, 70, 1030), (8192, 500, 40),
                                    (8193, 70, 36), (20000, 300, 20), (70000, 40000, 8),
-                                   (9000, 70001, 8)])
+                                   (9000, 70001, 8), (40, 5000, 1), (3, 9999, 2), (50, 3000, 3),
+                                   (700, 4000, 130), (100, 300, 4100)])
 def test_gradient(T, n, m, kind):
     g = torch.Generator().manual_seed(T + n + m)
     dtype = (BF, FP, F32)[(T + m) % 3]
