@@ -7,14 +7,14 @@
 // The gradient is summed without atomics, in an order fixed by the tokens:
 // their places are sorted by token, places of one token in order.  The sorted
 // list is cut into chunks of up to 32 places, a wave sums the rows of one chunk
-// for 512 columns, and writes a token's sum at the end of its run.  A run that
-// crosses chunks leaves one partial row a chunk, which a last launch adds up
-// in order, so that a token that fills the batch is split as well as others.
+// for 512 columns, and writes a token's sum at the end of its run.  A run
+// longer than two chunks leaves one partial row a chunk, which a last launch
+// adds up in order, so that a token that fills the batch is split as well.
 // Rows of dW without a token are cleared by further workgroups of the same
 // launch, which find the tokens of their rows in the sorted list.  Bound by
 // HBM: dW is written once (fp32, most of the bytes), dy read once (8192 tokens
-// of 32000 x 4096: 10 us for the places, 100 us, 5.9 TB/s, for the sums, 6 us
-// for the joins).
+// of 32000 x 4096: 9 us for the places, 85-90 us, 6.6 TB/s, for the sums and
+// zeros, 6 us for the joins; 65536 tokens by digits: 20 us a digit of 8 bits).
 #include "checks.h"
 
 namespace dion3 {
@@ -22,8 +22,9 @@ namespace {
 
 constexpr int kMaxChunk = 32;         // places of one wave at most
 constexpr int kMaxZeroRows = 256;     // rows of dW that one workgroup clears at most (its threads)
+constexpr int kShortRow = 1024;       // columns up to which rows are cleared as one stretch
 constexpr int kCountMax = 8192;       // tokens up to which places are counted, not sorted by digits
-constexpr int kTile = 4096;           // tokens of a workgroup of the sort by digits
+constexpr int kTile = 1024;           // tokens of a workgroup of the sort by digits
 
 __device__ __forceinline__ int token_key(const void* tokens, int is64, long long t, int n) {
   const long long v = is64 ? ((const long long*)tokens)[t] : (long long)((const int*)tokens)[t];
@@ -138,14 +139,15 @@ __global__ __launch_bounds__(1024) void k_embed_scan(int* __restrict__ hist, int
   __shared__ int sums[16];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   int carry = 0;
-  for (int from = 0; from < count; from += 4096) {          // 4 entries a thread
-    int v[4], s = 0;
-    const int at = from + (int)threadIdx.x * 4;
+  for (int from = 0; from < count; from += 16384) {         // 16 entries a thread
+    int4 v[4];
+    int s = 0;
+    const int at = from + (int)threadIdx.x * 16;            // (count is a multiple of 256)
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      v[k] = at + k < count ? hist[at + k] : 0;
-      s += v[k];
-    }
+    for (int k = 0; k < 4; ++k)
+      v[k] = at < count ? ((const int4*)(hist + at))[k] : make_int4(0, 0, 0, 0);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) s += v[k].x + v[k].y + v[k].z + v[k].w;
     int run = s;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
@@ -154,16 +156,21 @@ __global__ __launch_bounds__(1024) void k_embed_scan(int* __restrict__ hist, int
     }
     if (lane == 63) sums[wave] = run;
     __syncthreads();
-    int before = carry, all = 0;
+    int before = carry + run - s, all = 0;
+#pragma unroll
     for (int i = 0; i < 16; ++i) {
       if (i < wave) before += sums[i];
       all += sums[i];
     }
-    before += run - s;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      if (at + k < count) hist[at + k] = before;
-      before += v[k];
+      const int4 w = v[k];
+      v[k].x = before;
+      v[k].y = before + w.x;
+      v[k].z = v[k].y + w.y;
+      v[k].w = v[k].z + w.z;
+      before = v[k].w + w.w;
+      if (at < count) ((int4*)(hist + at))[k] = v[k];
     }
     carry += all;
     __syncthreads();
@@ -176,16 +183,20 @@ __global__ __launch_bounds__(256) void k_embed_place(DigitP p) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) count[i][threadIdx.x] = 0;
   __syncthreads();
-  // a wave takes 1024 tokens in order, 64 at a time
-  const long long from = (long long)blockIdx.x * kTile + wave * 1024;
+  // a wave takes a quarter of the tile in order, 64 tokens at a time
+  constexpr int R = kTile / 256;
+  const long long from = (long long)blockIdx.x * kTile + wave * (kTile / 4);
   const unsigned long long below = (1ull << lane) - 1;
-  int key[16], pos[16], at[16];
+  int key[R], pos[R], at[R];
 #pragma unroll
-  for (int r = 0; r < 16; ++r) {
+  for (int r = 0; r < R; ++r) {
     const long long i = from + r * 64 + lane;
-    const bool in = i < p.T;
-    key[r] = in ? digit_key(p, i) : 0;
-    pos[r] = in ? (p.tokens ? (int)i : p.pos[i]) : 0;
+    key[r] = i < p.T ? digit_key(p, i) : 0;
+    pos[r] = i < p.T ? (p.tokens ? (int)i : p.pos[i]) : 0;
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const bool in = from + r * 64 + lane < p.T;
     const int dig = key[r] >> p.shift & 255;
     unsigned long long same = __ballot(in);
 #pragma unroll
@@ -213,7 +224,7 @@ __global__ __launch_bounds__(256) void k_embed_place(DigitP p) {
   }
   __syncthreads();
 #pragma unroll
-  for (int r = 0; r < 16; ++r) {
+  for (int r = 0; r < R; ++r) {
     if (from + r * 64 + lane >= p.T) continue;
     const int to = count[wave][key[r] >> p.shift & 255] + at[r];
     p.okey[to] = key[r];
@@ -234,37 +245,57 @@ struct EmbedGradP {
   int accumulate;
 };
 
-// One wave: chunk x slice.  Rows are asked for U at a time, and with ACC the rows
-// of dW that their runs end in too (one by one, each waits for its own).
+// One wave: chunk x slice.  A run of up to two chunks' length that begins in the
+// chunk is finished by its wave (the next one leaves its first places out);
+// only longer ones leave partial rows.  Rows are asked for U at a time, and with
+// ACC the rows of dW that their runs end in too (one by one, each waits for its
+// own).
 template <class E, bool ACC>
 __device__ __forceinline__ void sum_chunk(const EmbedGradP& p, long long chunk, int slice) {
-  const int lane = threadIdx.x & 63, c = slice * 512 + lane * 8;
-  const long long from = chunk * p.len;
-  const int cnt = (int)(p.T - from < p.len ? p.T - from : p.len);
-  const int k = lane < cnt ? p.key[from + lane] : p.n;
-  const int at = lane < cnt ? p.pos[from + lane] : 0;
+  const int lane = threadIdx.x & 63, c = slice * 512 + lane * 8, len = p.len;
+  const long long from = chunk * len, rest = p.T - from;
+  const int cnt = rest < len ? (int)rest : len, known = rest < 2 * len ? (int)rest : 2 * len;
+  const int k = lane < known ? p.key[from + lane] : p.n;
+  const int at = lane < known ? p.pos[from + lane] : 0;
   const int before = from > 0 ? p.key[from - 1] : -1;
-  const int behind = from + p.len < p.T ? p.key[from + p.len] : -1;
+  const int back = from > 0 ? p.key[from - len] : -1, back1 = from > len ? p.key[from - len - 1] : -1;
+  const int beyond = rest > 2 * len ? p.key[from + 2 * len] : -1;
+  auto end_of = [&](int key, int i) {               // the first of the known places from i on of another key
+    const unsigned long long b = __ballot(k != key || lane >= known) >> i;
+    return b ? i + __builtin_ctzll(b) : known;
+  };
+  const int first = __builtin_amdgcn_readlane(k, 0), last = __builtin_amdgcn_readlane(k, cnt - 1);
+  int i0 = 0, stop = cnt;
+  bool head = false, tail = false;
+  if (first == before) {
+    const int e = end_of(first, 0);
+    if (e <= len && !(back == first && back1 == first)) i0 = e;     // finished by the wave before
+    else head = true;
+  }
+  if (i0 >= cnt) return;
+  if (known > cnt && __builtin_amdgcn_readlane(k, cnt) == last && !(head && last == first)) {
+    tail = beyond == last;
+    if (!tail) stop = end_of(last, cnt);
+  }
   float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  bool head = __builtin_amdgcn_readlane(k, 0) == before;
   constexpr int U = ACC ? 4 : 8;
-  for (int i0 = 0; i0 < cnt; i0 += U) {
+  for (; i0 < stop; i0 += U) {
     Raw8<E> raw[U];
     float old[ACC ? U : 1][8];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int i = i0 + u;
-      if (i >= cnt) continue;
+      if (i >= stop) continue;
       const int key = __builtin_amdgcn_readlane(k, i);
       if (key == p.n || c >= p.m) continue;
       raw[u] = fetch8((const E*)p.dy + __builtin_amdgcn_readlane(at, i) * p.lddy, c, p.m);
-      if (ACC && (i + 1 == cnt || __builtin_amdgcn_readlane(k, i + 1) != key))
+      if (ACC && (i + 1 == stop || __builtin_amdgcn_readlane(k, i + 1) != key))
         load8(p.dw + key * p.ldw, c, p.m, old[u]);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int i = i0 + u;
-      if (i >= cnt) continue;
+      if (i >= stop) continue;
       const int key = __builtin_amdgcn_readlane(k, i);
       if (key == p.n) return;                       // no tokens from here on
       if (c < p.m) {
@@ -273,11 +304,9 @@ __device__ __forceinline__ void sum_chunk(const EmbedGradP& p, long long chunk, 
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[e] += v[e];
       }
-      const int next = i + 1 < cnt ? __builtin_amdgcn_readlane(k, i + 1) : -1;
-      if (next == key) continue;
-      const bool tail = i + 1 == cnt && behind == key;
+      if (i + 1 < stop && __builtin_amdgcn_readlane(k, i + 1) == key) continue;
       if (c < p.m) {
-        if (head || tail) {
+        if (head || (tail && i + 1 == stop)) {
           store8(p.part + (chunk * 2 + (head ? 0 : 1)) * p.m, c, p.m, acc);
         } else {
 #pragma unroll
@@ -347,7 +376,7 @@ __global__ __launch_bounds__(256) void k_embed_grad(EmbedGradP p) {
   typedef float f4 __attribute__((ext_vector_type(4), aligned(4)));
   const f4 zero = {0, 0, 0, 0};
   float* base = p.dw + v0 * p.ldw;
-  if (p.ldw == p.m && p.m > 1 && p.m <= 4096) {       // short rows: one stretch
+  if (p.ldw == p.m && p.m > 1 && p.m <= kShortRow) {  // short rows: one stretch
     const unsigned n = (unsigned)rows * p.m, inv = (unsigned)((0x100000000ull + p.m - 1) / p.m);
     for (unsigned i = threadIdx.x * 4; i < n; i += 1024) {
       const bool whole = i + 4 <= n;
@@ -375,60 +404,72 @@ __global__ __launch_bounds__(256) void k_embed_grad(EmbedGradP p) {
   }
 }
 
-// The runs that cross chunks: the workgroup of the chunk in which one begins
-// adds up its partial rows, 256 columns a wave across, the 4 waves a quarter
-// of the rows each.
+// The long runs: a workgroup looks through 16 chunks for those in which one
+// begins and adds up its partial rows in 256 columns, its 4 waves a quarter of
+// the rows each.
+constexpr int kJoinChunks = 16;
 __global__ __launch_bounds__(256) void k_embed_join(EmbedGradP p, long long chunks) {
   __shared__ float sh[3][64][4];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, len = p.len;
   const long long block = (long long)blockIdx.y * gridDim.x + blockIdx.x;
   const int cols = (p.m + 255) / 256;
-  const long long c0 = block / cols, from = c0 * p.len, last = from + p.len - 1;
-  if (c0 >= chunks || last + 1 >= p.T) return;                    // (the last chunk)
-  const int key = p.key[last], next = p.key[last + 1], first = p.key[from];
-  const int before = from > 0 ? p.key[from - 1] : -1;
-  if (key == p.n || next != key) return;                          // no run goes on
-  if (first == key && before == key) return;                      // begun before
-  long long c1 = c0 + 1;                                          // the run's last chunk:
-  for (;;) {                                                      // those it fills, 64 at a time
-    const long long i = (c1 + lane) * p.len + p.len - 1;
-    const unsigned long long not_full = ~__ballot(i + 1 < p.T && p.key[i] == key && p.key[i + 1] == key);
-    const int full = not_full ? __builtin_ctzll(not_full) : 64;
-    c1 += full;
-    if (full < 64) break;
-  }
-  const int c = (int)(block - c0 * cols) * 256 + lane * 4;
-  const long long count = c1 - c0 + 1, per = (count + 3) / 4;
-  const long long a = wave * per, b = a + per < count ? a + per : count;
-  float v[4] = {0, 0, 0, 0};
-  const bool vec = c + 4 <= p.m;
-  struct __attribute__((packed, aligned(4))) F4 { float x[4]; };
-#pragma unroll 8
-  for (long long i = a; i < b; ++i) {
-    const float* row = p.part + ((c0 + i) * 2 + (i == 0 ? 1 : 0)) * p.m;
-    if (vec) {
-      const F4 f = *(const F4*)(row + c);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] += f.x[e];
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (c + e < p.m) v[e] += row[c + e];
+  const long long group = block / cols;
+  if (group * kJoinChunks >= chunks) return;
+  const int c = (int)(block - group * cols) * 256 + lane * 4;
+  int key = p.n;
+  {
+    const long long from = (group * kJoinChunks + lane) * len;
+    if (lane < kJoinChunks && from + 2 * len < p.T) {
+      const int first = p.key[from], last = p.key[from + len - 1], beyond = p.key[from + 2 * len];
+      const int before = from > 0 ? p.key[from - 1] : -1;
+      if (last == beyond && !(first == last && before == last)) key = last;
     }
   }
-  if (wave > 0) {
+  for (unsigned long long todo = __ballot(key != p.n); todo; todo &= todo - 1) {
+    const int which = __builtin_ctzll(todo), row = __builtin_amdgcn_readlane(key, which);
+    const long long c0 = group * kJoinChunks + which;
+    long long c1 = c0 + 1;                            // the run's last chunk:
+    for (;;) {                                        // those it fills, 64 at a time
+      const long long i = (c1 + lane) * len + len - 1;
+      const unsigned long long not_full =
+          ~__ballot(i + 1 < p.T && p.key[i] == row && p.key[i + 1] == row);
+      const int full = not_full ? __builtin_ctzll(not_full) : 64;
+      c1 += full;
+      if (full < 64) break;
+    }
+    const long long count = c1 - c0 + 1, per = (count + 3) / 4;
+    const long long a = wave * per, b = a + per < count ? a + per : count;
+    float v[4] = {0, 0, 0, 0};
+    const bool vec = c + 4 <= p.m;
+    struct __attribute__((packed, aligned(4))) F4 { float x[4]; };
+#pragma unroll 8
+    for (long long i = a; i < b; ++i) {
+      const float* part = p.part + ((c0 + i) * 2 + (i == 0 ? 1 : 0)) * p.m;
+      if (vec) {
+        const F4 f = *(const F4*)(part + c);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) sh[wave - 1][lane][e] = v[e];
+        for (int e = 0; e < 4; ++e) v[e] += f.x[e];
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (c + e < p.m) v[e] += part[c + e];
+      }
+    }
+    __syncthreads();                                  // (the run before has been read)
+    if (wave > 0) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sh[wave - 1][lane][e] = v[e];
+    }
+    __syncthreads();
+    if (wave > 0) continue;
+    for (int w = 0; w < 3; ++w)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] += sh[w][lane][e];
+    float* d = p.dw + row * p.ldw;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (c + e < p.m) d[c + e] = p.accumulate ? d[c + e] + p.scale * v[e] : p.scale * v[e];
   }
-  __syncthreads();
-  if (wave > 0) return;
-  for (int w = 0; w < 3; ++w)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] += sh[w][lane][e];
-  float* d = p.dw + key * p.ldw;
-#pragma unroll
-  for (int e = 0; e < 4; ++e)
-    if (c + e < p.m) d[c + e] = p.accumulate ? d[c + e] + p.scale * v[e] : p.scale * v[e];
 }
 
 // --------------------------------------------------------------- the launches
@@ -441,8 +482,10 @@ dim3 grid_of(long long blocks) {
 
 // The workspace: sorted keys and places (twice for the sort by digits, which
 // swaps them, and its histograms), then the partial rows.  A chunk is of
-// kMaxChunk places, of fewer where there would be too few waves (but not where
-// one holds all tokens: that saves the joins' launch).
+// kMaxChunk places, of fewer where there would be too few waves: 2048, or 4096
+// where dW is no larger than dy's sums (8192 tokens of 1000 x 4096 49 -> 41 us;
+// of 32000 x 4096, where more of them hold up the zeros, 104 -> 109).  Two chunks
+// have no run to join: up to 64 tokens take two, and no launch for it.
 struct EmbedPlan {
   int digits, tiles, len;
   long long chunks;
@@ -451,7 +494,10 @@ struct EmbedPlan {
 EmbedPlan plan_embed(long long T, int n, int m) {
   EmbedPlan q = {};
   q.len = kMaxChunk;
-  while (T > kMaxChunk && q.len > 8 && T / q.len * ((m + 511) / 512) < 2048) q.len /= 2;
+  const long long waves = n > T ? 2048 : 4096;
+  while (q.len > 8 && T / q.len * ((m + 511) / 512) < waves) q.len /= 2;
+  if (T <= 2 * kMaxChunk) q.len = (int)(T + 1) / 2;
+  if (q.len < 1) q.len = 1;
   q.chunks = (T + q.len - 1) / q.len;
   const size_t list = (size_t)pad_to(T, 64) * 4;
   size_t b = 2 * list;
@@ -584,8 +630,8 @@ dion3_status dion3_embedding_grad(const void* tokens, int32_t token_bits, const 
     HIP_TRY(sort_tokens(tokens, token_bits == 64, T, (int)n, q, (char*)ws, p.key, p.pos, s));
   }
   p.sum_blocks = (q.chunks * p.slices + 3) / 4;
-  // (about 128 KB a workgroup)
-  p.zero_rows = (int)(32768 / m < 8 ? 8 : 32768 / m > kMaxZeroRows ? kMaxZeroRows : 32768 / m);
+  // (about 32 KB a workgroup: 50257 x 1024 61 -> 56 us against 128 KB)
+  p.zero_rows = (int)(8192 / m < 8 ? 8 : 8192 / m > kMaxZeroRows ? kMaxZeroRows : 8192 / m);
   const long long zero_blocks = accumulate ? 0 : (n + p.zero_rows - 1) / p.zero_rows;
   {
     TraceScope ts("embedding_grad", 0.0, (double)T * m * size_of(dtype) + 4.0 * (accumulate ? 0 : n) * m, s);
@@ -595,9 +641,9 @@ dion3_status dion3_embedding_grad(const void* tokens, int32_t token_bits, const 
     else launch_embed_grad<float>(p, grid, s);
     HIP_TRY(hipGetLastError());
   }
-  if (q.chunks > 1) {
+  if (T > 2 * q.len) {
     TraceScope ts("embedding_join", 0.0, 0.0, s);
-    hipLaunchKernelGGL(k_embed_join, grid_of(q.chunks * ((m + 255) / 256)), dim3(256), 0, s, p,
+    hipLaunchKernelGGL(k_embed_join, grid_of((q.chunks + kJoinChunks - 1) / kJoinChunks * ((m + 255) / 256)), dim3(256), 0, s, p,
                        q.chunks);
     HIP_TRY(hipGetLastError());
   }

@@ -31,6 +31,13 @@ def text(g, T, n, kind):
         return torch.full((T,), n - 1)
     if kind == "falling":
         return (torch.arange(T).flip(0) * n) // max(T, 1)
+    if kind == "runs":            # around the ends of chunks of 8, 16 and 32 places
+        out = []
+        while len(out) < T:
+            r = [1, 2, 7, 8, 9, 15, 16, 17, 31, 32, 33, 63, 64, 65, 66, 95, 97, 128, 129, 200][int(torch.randint(20, (1,), generator=g))]
+            out += [len(out)] * r
+        t = torch.unique(torch.tensor(out[:T]), return_inverse=True)[1] % n
+        return t[torch.randperm(T, generator=g)]
     if kind == "none":
         return torch.where(torch.arange(T) % 2 == 0, -100, n)
     t = torch.randint(0, n, (T,), generator=g)                # "padded"
@@ -77,7 +84,7 @@ def test_lookup(T, n, m, wtype, dtype):
     assert y.dtype == wtype and torch.equal(y.cpu(), d(y).to(wtype))
 
 
-KINDS = ["uniform", "frequent", "one", "falling", "none", "padded"]
+KINDS = ["uniform", "frequent", "one", "falling", "none", "padded", "runs"]
 
 
 @pytest.mark.parametrize("kind", KINDS)
@@ -85,7 +92,8 @@ KINDS = ["uniform", "frequent", "one", "falling", "none", "padded"]
                                    (64, 1, 40), (517, 3000, 515), (1000, 70, 1030), (8192, 500, 40),
                                    (8193, 70, 36), (20000, 300, 20), (70000, 40000, 8),
                                    (9000, 70001, 8), (40, 5000, 1), (3, 9999, 2), (50, 3000, 3),
-                                   (700, 4000, 130), (100, 300, 4100)])
+                                   (700, 4000, 130), (100, 300, 4100), (65, 50, 40), (128, 50, 40),
+                                   (6000, 3000, 2600), (30000, 3000, 1100), (64, 30, 520)])
 def test_gradient(T, n, m, kind):
     g = torch.Generator().manual_seed(T + n + m)
     dtype = (BF, FP, F32)[(T + m) % 3]
