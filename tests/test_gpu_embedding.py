@@ -93,7 +93,8 @@ KINDS = ["uniform", "frequent", "one", "falling", "none", "padded", "runs"]
                                    (8193, 70, 36), (20000, 300, 20), (70000, 40000, 8),
                                    (9000, 70001, 8), (40, 5000, 1), (3, 9999, 2), (50, 3000, 3),
                                    (700, 4000, 130), (100, 300, 4100), (65, 50, 40), (128, 50, 40),
-                                   (6000, 3000, 2600), (30000, 3000, 1100), (64, 30, 520)])
+                                   (6000, 3000, 2600), (30000, 3000, 1100), (64, 30, 520), (90, 20, 513), (300, 50, 1027),
+                                   (40, 9, 258), (33, 10, 5), (70, 6, 65026)])
 def test_gradient(T, n, m, kind):
     g = torch.Generator().manual_seed(T + n + m)
     dtype = (BF, FP, F32)[(T + m) % 3]
