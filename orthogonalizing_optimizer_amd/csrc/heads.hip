@@ -69,6 +69,7 @@ __device__ __forceinline__ Item my_item(int j, int D, int r) {
       it.c[k] = t + 8 * k;
       it.lim[k] = D - r;
     }
+    if (!it.on) it.base[0] = it.base[1] = it.c[0] = it.c[1] = 0;      // (a place inside the head)
   }
   return it;
 }
@@ -167,12 +168,17 @@ __device__ __forceinline__ float head_sum(float v, int G) {
 // pieces, so no chunk ends early (the checks take 30 registers).
 template <bool WHOLE, class E>
 __device__ __forceinline__ void ask(const void* x, long long ld, long long hs, long long t, int h,
-                                    const Item& it, bool mine, Raw8<E> (&raw)[2]) {
+                                    int heads, const Item& it, bool mine, Raw8<E> (&raw)[2]) {
+  if (WHOLE) {           // no branches between the loads: lanes without a head read the last one's
+    const E* row = (const E*)x + t * ld + min(h, heads - 1) * hs;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) raw[k].v = ((const typename Raw8<E>::Any*)(row + it.base[k] + it.c[k]))->v;
+    return;
+  }
   if (!mine) return;
   const E* row = (const E*)x + t * ld + h * hs;
 #pragma unroll
-  for (int k = 0; k < 2; ++k)
-    raw[k] = fetch8(row + it.base[k], it.c[k], WHOLE ? it.c[k] + 8 : it.lim[k]);
+  for (int k = 0; k < 2; ++k) raw[k] = fetch8(row + it.base[k], it.c[k], it.lim[k]);
 }
 template <bool WHOLE, class E>
 __device__ __forceinline__ void take(const Raw8<E> (&raw)[2], const Item& it, bool mine,
@@ -196,8 +202,14 @@ __device__ __forceinline__ void put(void* y, long long ld, long long hs, long lo
   E* row = (E*)y + t * ld + h * hs;
 #pragma unroll
   for (int k = 0; k < 2; ++k)
-    if (WHOLE || it.c[k] < it.lim[k])
-      store8(row + it.base[k], it.c[k], WHOLE ? it.c[k] + 8 : it.lim[k], v[k]);
+    if (WHOLE) {
+      Raw8<E> r;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) r.v[e] = (E)v[k][e];
+      ((typename Raw8<E>::Any*)(row + it.base[k] + it.c[k]))->v = r.v;
+    } else if (it.c[k] < it.lim[k]) {
+      store8(row + it.base[k], it.c[k], it.lim[k], v[k]);
+    }
 }
 __device__ __forceinline__ float head_rstd(const float (&v)[2][8], int G, int D, float eps) {
   float ss = 0.0f;
@@ -218,7 +230,7 @@ __global__ __launch_bounds__(256) void k_heads(HeadsP p) {
   const Item it = my_item<IL>(j, p.D, p.r);
   Raw8<E> raw[2];
   bool mine = it.on && at.b * per + slot < s.heads;
-  ask<WHOLE>(s.x, s.ldx, s.hsx, at.t, at.b * per + slot, it, mine, raw);
+  ask<WHOLE>(s.x, s.ldx, s.hsx, at.t, at.b * per + slot, s.heads, it, mine, raw);
   double pos = position(p, at.t);
   float w[2][8], co[8], si[8];
   load_weight<E>(p, s, it, w);
@@ -234,7 +246,7 @@ __global__ __launch_bounds__(256) void k_heads(HeadsP p) {
     const bool go = at.more();
     if (go) {
       mine = it.on && at.b * per + slot < s.heads;
-      ask<WHOLE>(s.x, s.ldx, s.hsx, at.t, at.b * per + slot, it, mine, raw);
+      ask<WHOLE>(s.x, s.ldx, s.hsx, at.t, at.b * per + slot, s.heads, it, mine, raw);
       fresh = at.t != now.t;
       if (fresh) pos = position(p, at.t);
     }
@@ -266,8 +278,8 @@ __global__ __launch_bounds__(256) void k_heads_grad(HeadsP p) {
   if (at.more()) {
     Raw8<E> rx[2], ry[2];
     bool mine = it.on && at.b * per + slot < s.heads;
-    ask<WHOLE>(s.x, s.ldx, s.hsx, at.t, at.b * per + slot, it, mine, rx);
-    ask<WHOLE>(s.dy, s.lddy, s.hsdy, at.t, at.b * per + slot, it, mine, ry);
+    ask<WHOLE>(s.x, s.ldx, s.hsx, at.t, at.b * per + slot, s.heads, it, mine, rx);
+    ask<WHOLE>(s.dy, s.lddy, s.hsdy, at.t, at.b * per + slot, s.heads, it, mine, ry);
     double pos = position(p, at.t);
     float w[2][8], co[8], si[8];
     load_weight<E>(p, s, it, w);
@@ -283,8 +295,8 @@ __global__ __launch_bounds__(256) void k_heads_grad(HeadsP p) {
       const bool go = at.more();
       if (go) {
         mine = it.on && at.b * per + slot < s.heads;
-        ask<WHOLE>(s.x, s.ldx, s.hsx, at.t, at.b * per + slot, it, mine, rx);
-        ask<WHOLE>(s.dy, s.lddy, s.hsdy, at.t, at.b * per + slot, it, mine, ry);
+        ask<WHOLE>(s.x, s.ldx, s.hsx, at.t, at.b * per + slot, s.heads, it, mine, rx);
+        ask<WHOLE>(s.dy, s.lddy, s.hsdy, at.t, at.b * per + slot, s.heads, it, mine, ry);
         fresh = at.t != now.t;
         if (fresh) pos = position(p, at.t);
       }
@@ -369,7 +381,7 @@ int pieces(int D, int r, bool il) {
 // A head takes the power of two of lanes that holds its columns, 16 a lane.
 // As many waves as stay resident (a few more would run after all others) are
 // shared out between queries and keys by their batches, and each takes equally
-// many of them: 8192 tokens of 32 + 8 heads of 128 take 34 us (5 TB/s; twice
+// many of them: 8192 tokens of 32 + 8 heads of 128 take 32 us (5.2 TB/s; twice
 // the resident waves, 35 with as many) and 59 backwards (4.3 TB/s; 65 by whole
 // tokens, 57 with 4 waves a SIMD that read their weight from LDS: not kept).
 struct Split {
