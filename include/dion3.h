@@ -604,8 +604,9 @@ DION3_API dion3_status dion3_grad_norm(const dion3_grad* grads, int32_t count, f
 /* With that norm and c = 1 where norm <= max_norm, else max_norm / norm (in 64
  * bits, like the products below, which are rounded to fp32 once): each
  * gradient with an M is summed into it, M <- M + c scale G (G is not written),
- * each other one is scaled in place, G <- c scale G rounded to its type.  An infinite norm gives
- * c = 0, a NaN c = NaN.  norm: one float, or NULL.  max_norm may be infinite. */
+ * each other one is scaled in place, G <- c scale G rounded to its type.  An
+ * infinite norm gives c = 0, a NaN c = NaN.  norm: one float, or NULL.
+ * max_norm may be infinite. */
 DION3_API dion3_status dion3_clip_grad_norm(const dion3_grad* grads, int32_t count, float max_norm,
                                             float scale, float* norm, void* ws, size_t ws_bytes,
                                             void* stream);

@@ -120,7 +120,8 @@ def clip_grad_norm(grads, max_norm: float, scale: float = 1.0, into=None,
     gradients are then added to them and the gradients stay as they are.
     ``[optimizer.accumulate_grad(p) for p in ps]`` are the momenta of a
     ``Dion3``, whose next ``step()`` steps these parameters (leave their
-    ``.grad`` None by then, or it is added again).
+    ``.grad`` None by then, or it is added again); for a captured call, name
+    them before each step that follows a replay.
 
     No tensor that is written may be listed twice or overlap another one.
     Pass gradients, not parameters; None stands for no gradient."""

@@ -9,15 +9,16 @@
 // list is cut into chunks of up to 32 places, a wave sums the rows of one chunk
 // for 512 columns, and writes a token's sum at the end of its run.  A run
 // longer than two chunks leaves one partial row a chunk, which a last launch
-// adds up in order, so that a token that fills the batch is split as well.
-// The rows
-// of dW without one are cleared last, by the flags that the others' waves have
-// set: cleared before, all of it, the rows with sums would be written twice, and
-// beside the sums the two hold up each other.  Bound by
-// HBM: dW is written once (fp32, most of the bytes), dy read once.  8192 tokens
-// of 32000 x 4096 (591 MB) take 127 us: 10 for the places, 32 to 44 for the sums
-// (rows of 8 KB at random; writes of the call before still drain), 81 for the
-// other rows and the joins.  More than kCountMax tokens take about 20 us a digit.
+// adds up in order, so that a token that fills the batch is split as well.  The
+// rows of dW without one are cleared last, by the flags that the others' waves
+// have set: cleared before, all of it, the rows with sums would be written
+// twice, and beside the sums the two hold up each other.
+//
+// Bound by HBM: dW is written once (fp32, most of the bytes), dy read once.
+// 8192 tokens of 32000 x 4096 (591 MB) take 127 us: 10 for the places, 32 to 44
+// for the sums (rows of 8 KB at random; writes of the call before still drain),
+// 81 for the other rows and the joins.  More than kCountMax tokens take about
+// 20 us a digit.
 #include "checks.h"
 
 namespace dion3 {
@@ -88,7 +89,6 @@ __device__ __forceinline__ void zero_block(const Zero& z, long long block) {
   }
 }
 __global__ __launch_bounds__(256) void k_embed_zero(Zero z) { zero_block<256>(z, grid_block()); }
-
 
 // Up to kCountMax tokens: the place of t in the order is the number of tokens
 // before it, counted by comparing all with all (two instructions a pair).  A

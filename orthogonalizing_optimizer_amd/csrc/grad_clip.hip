@@ -7,18 +7,19 @@
 //
 // Bound by HBM: the norm reads every gradient once (303 M bf16 elements 104 us,
 // 5.8 TB/s), the second pass reads it again (such sizes pass the 256 MB cache)
-// and writes it, or reads and writes the sums (both passes 675 us, 5.4 TB/s).  Squares are summed in 64 bits: no gradient of a 16- or
-// 32-bit type leaves their range, and a conversion and a 64-bit fma an element
-// take less than the element's time on HBM.  So do the products with c, whose
-// factor leaves fp32's normal range where gradients are huge.
+// and writes it, or reads and writes the sums (both passes 675 us, 5.4 TB/s).
+// Squares are summed in 64 bits: no gradient of a 16- or 32-bit type leaves
+// their range, and a conversion and a 64-bit fma an element take less than the
+// element's time on HBM.  So do the products with c, whose factor leaves fp32's
+// normal range where gradients are huge.
 //
 // A workgroup takes one chunk of one tensor and leaves one partial sum; the
 // second pass adds all partial sums up in every workgroup, in one order, so
 // that no launch stands between the two and no atomics are needed.  Where that
 // would be more than about 2048 (16 KB for each workgroup to read), one
-// workgroup adds them up in between.  The tensors' table
-// travels in the kernel's arguments, kBatch tensors a launch: nothing is
-// copied to the device, so a call can be captured.
+// workgroup adds them up in between.  The tensors' table travels in the
+// kernel's arguments, kBatch tensors a launch: nothing is copied to the device,
+// so a call can be captured.
 #include "checks.h"
 
 namespace dion3 {

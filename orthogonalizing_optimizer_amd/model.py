@@ -1,17 +1,22 @@
 """Operators around the layers in a model's training step.
 
 Tokens' rows of an embedding (``embedding``); queries and keys normed per head
-and rotated by their positions in one pass (``qk_norm_rope``); log probabilities of given tokens with the entropy and the
-best alternatives (``log_probs``); their gradients.  As in ``layer``, every
-function is one call of libdion3.so (include/dion3.h states the formulas), runs
-on torch's current stream of the tensors' device and takes its workspace from
-torch's allocator per call (or from ``ws``); there is no fallback.
+and rotated by their positions in one pass (``qk_norm_rope``); log
+probabilities of given tokens with the entropy and the best alternatives
+(``log_probs``); their gradients.  As in ``layer``, every function is one call
+of libdion3.so (include/dion3.h states the formulas), runs on torch's current
+stream of the tensors' device and takes its workspace from torch's allocator
+per call (or from ``ws``); there is no fallback.
+
 ``embedding_layer``, ``qk_norm_rope_layer`` and ``token_log_probs`` are the
-differentiable forms.
+differentiable forms.  torch's rule for a captured backward pass holds: let no
+graph of the same leaves recorded outside the capture live (an earlier loss or
+output kept in a variable).
 """
 from __future__ import annotations
 
 import array
+import functools
 from typing import Optional
 
 import torch
@@ -20,6 +25,8 @@ from . import _lib
 from .layer import _DTYPES, _as_rows, _call, _matrix, _ptr, _rows, _same, _scratch, _size, _t16, _vector
 
 _MAX_STRIDE = 1 << 38
+# (these depend on sizes alone; a call to ask for one takes 1.4 us)
+_bytes = functools.lru_cache(maxsize=1024)(_size)
 
 
 def _lead(shape, strides, name):
@@ -92,7 +99,7 @@ def embedding_grad(tokens, dy, n: int, scale: float = 1.0, out=None, accumulate:
     if tuple(out.shape) != (n, m):
         raise ValueError(f"out must have shape {(n, m)}")
     _, _, ldw = _rows(out, "out")
-    p, nb, keep = _scratch(ws, _size("dion3_embedding_grad_workspace_size", T, n, m), dy.device)
+    p, nb, keep = _scratch(ws, _bytes("dion3_embedding_grad_workspace_size", T, n, m), dy.device)
     _call("dion3_embedding_grad", dy.device, _ptr(tokens), bits, _ptr(dy), lddy, _ptr(out), ldw,
           int(bool(accumulate)), T, n, m, float(scale), _DTYPES[dy.dtype], p, nb)
     return out
@@ -248,9 +255,9 @@ def qk_norm_rope_grad(dyq, dyk, q, k, q_weight, k_weight, positions, freqs, eps:
     dq = s.output(0) if need_dx else None
     dk = s.output(1) if need_dx and k is not None else None
     dw = q.new_empty((2, s.D), dtype=torch.float32) if need_dw else None
-    p, nb, keep = _scratch(ws, _size("dion3_qk_norm_rope_grad_workspace_size", s.T, q.shape[-2],
-                                     k.shape[-2] if k is not None else 0, s.D, s.r,
-                                     int(bool(interleaved))) if need_dw else 0, q.device)
+    p, nb, keep = _scratch(ws, _bytes("dion3_qk_norm_rope_grad_workspace_size", s.T, q.shape[-2],
+                                      k.shape[-2] if k is not None else 0, s.D, s.r,
+                                      int(bool(interleaved))) if need_dw else 0, q.device)
     _call("dion3_qk_norm_rope_grad", q.device, *s.refs(), _ptr(freqs), _ptr(s.pos), s.bits, _ptr(dw),
           s.T, s.D, s.r, int(bool(interleaved)), float(eps), s.wtype, s.dtype, p, nb)
     return (dq, dk, dw[0] if need_dw else None,
@@ -355,7 +362,7 @@ def log_probs(logits, targets=None, scale: float = 1.0, entropy: bool = False, t
             raise ValueError(f"top must be between 0 and {n}")
         tl = logits.new_empty(lead + (top,), dtype=torch.float32)
         ti = logits.new_empty(lead + (top,), dtype=torch.int64)
-    p, nb, keep = _scratch(ws, _size("dion3_log_probs_workspace_size", T, n, top), device)
+    p, nb, keep = _scratch(ws, _bytes("dion3_log_probs_workspace_size", T, n, top), device)
     _call("dion3_log_probs", device, _ptr(logits), ld, _ptr(targets), bits, _ptr(logp), _ptr(stats),
           _ptr(H), _ptr(tl), _ptr(ti), T, n, top, float(scale), _DTYPES[logits.dtype], p, nb)
     return logp, stats, H, tl, ti

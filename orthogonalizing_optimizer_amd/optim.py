@@ -230,7 +230,8 @@ class Dion3(_optimizer_base()):
         """Clip the ``.grad`` of all parameters by their global norm, in place,
         and return the norm (``clip_grad_norm``).  RuntimeError if gradients
         have been summed straight into momenta since the last step: those are
-        no longer apart from earlier ones."""
+        no longer apart from earlier ones.  (Sums inside captured graphs name
+        no parameter, so they are not noticed here.)"""
         from .clip import clip_grad_norm
         if self._accumulated:
             raise RuntimeError("gradients summed into the momentum cannot be clipped")
