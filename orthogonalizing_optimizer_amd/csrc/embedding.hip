@@ -15,10 +15,9 @@
 // twice, and beside the sums the two hold up each other.
 //
 // Bound by HBM: dW is written once (fp32, most of the bytes), dy read once.
-// 8192 tokens of 32000 x 4096 (591 MB) take 127 us: 10 for the places, 32 to 44
-// for the sums (rows of 8 KB at random; writes of the call before still drain),
-// 81 for the other rows and the joins.  More than kCountMax tokens take about
-// 20 us a digit.
+// 8192 tokens of 32000 x 4096 (591 MB) take 100 us (5.9 TB/s): 9 for the places,
+// 23 for the sums (rows of 8 KB at random), 67 for the other rows and the joins.
+// More than kCountMax tokens take about 20 us a digit.
 #include "checks.h"
 
 namespace dion3 {
@@ -39,7 +38,7 @@ template <class WT, class E>
 __global__ __launch_bounds__(256) void k_embed(const void* __restrict__ tokens, int is64,
                                                const WT* __restrict__ w, long long ldw,
                                                E* __restrict__ y, long long ldy, long long chunks,
-                                               int n, int m, unsigned nch, float scale) {
+                                               int n, int m, unsigned nch, float scale, int once) {
   const long long base = flat_base();
   if (base + threadIdx.x >= chunks) return;
   const long long row0 = base / nch;
@@ -52,7 +51,8 @@ __global__ __launch_bounds__(256) void k_embed(const void* __restrict__ tokens, 
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] *= scale;
   }
-  store8(y + (row0 + dr) * ldy, c, m, v);
+  if (once) store8_once(y + (row0 + dr) * ldy, c, m, v);
+  else store8(y + (row0 + dr) * ldy, c, m, v);
 }
 
 // ------------------------------------------------------------ places by token
@@ -63,8 +63,10 @@ __device__ __forceinline__ long long grid_block() {
 
 // Clears the rows of dW whose flag is not set (all of them without flags), 16
 // bytes a thread and 4 KB a workgroup, the workgroups in the order of their
-// addresses: 524 MB take 77 us (6.8 TB/s), 97 with 16 stores a thread, whose
-// writes lie further apart at any time.
+// addresses: 410 MB take 66 us (6.2 TB/s); with 16 stores a thread, whose writes
+// lie further apart at any time, a fourth more.  They pass the cache, as the sums do
+// (8192 tokens of 32000 x 4096 132 -> 100 us; with a pass over dW 246 -> 186 at
+// 32000 rows, 71 either way at 8000, 29 at 1000).
 struct Zero {
   float* dw;
   const unsigned char* set;
@@ -74,7 +76,7 @@ struct Zero {
 };
 template <int THREADS>
 __device__ __forceinline__ void zero_block(const Zero& z, long long block) {
-  typedef float f4 __attribute__((ext_vector_type(4), aligned(4)));
+  typedef float f4 __attribute__((ext_vector_type(4)));
   const long long base = block * THREADS;
   if (base + threadIdx.x >= z.items) return;
   const long long row0 = base / z.nch;
@@ -83,7 +85,7 @@ __device__ __forceinline__ void zero_block(const Zero& z, long long block) {
   if (z.set && z.set[row0 + dr]) return;
   float* d = z.dw + (row0 + dr) * z.ldw + c;
   if (c + 4 <= z.m) {
-    *(f4*)d = f4{0, 0, 0, 0};
+    store_once(d, f4{0, 0, 0, 0});
   } else {
     for (int e = 0; c + e < z.m; ++e) d[e] = 0.0f;
   }
@@ -381,7 +383,10 @@ __device__ __forceinline__ void sum_chunk(const EmbedGradP& p, long long chunk, 
 #pragma unroll
         for (int e = 0; e < W; ++e)
           acc[h].v[e] = ACC && !part ? old[u][h].v[e] + scale * acc[h].v[e] : scale * acc[h].v[e];
-        if (on[h]) *(Sum*)(row + c[h]) = acc[h];
+        if (on[h]) {
+          if constexpr (ACC) *(Sum*)(row + c[h]) = acc[h];
+          else store_once(row + c[h], acc[h].v);
+        }
         acc[h] = Sum{};
       }
       head = false;
@@ -564,8 +569,11 @@ hipError_t launch_embed(const void* tokens, int is64, const void* W, long long l
                         long long ldy, long long T, int n, int m, float scale, hipStream_t s) {
   const unsigned nch = (unsigned)((m + 7) / 8);
   const long long chunks = T * nch;
+  // Rows longer than the cache keeps are written past it (with a pass over them:
+  // 349 -> 316 us at 512 MB, 90 -> 87 at 128, 45.7 -> 46.5 at 64).
+  const int once = (double)T * m * sizeof(E) > 96e6;
   hipLaunchKernelGGL((k_embed<WT, E>), flat_grid(chunks), dim3(256), 0, s, tokens, is64,
-                     (const WT*)W, ldw, (E*)Y, ldy, chunks, n, m, nch, scale);
+                     (const WT*)W, ldw, (E*)Y, ldy, chunks, n, m, nch, scale, once);
   return hipGetLastError();
 }
 

@@ -7,7 +7,7 @@
 //
 // Bound by HBM: the norm reads every gradient once (303 M bf16 elements 104 us,
 // 5.8 TB/s), the second pass reads it again (such sizes pass the 256 MB cache)
-// and writes it, or reads and writes the sums (both passes 675 us, 5.4 TB/s).
+// and writes it, or reads and writes the sums (both passes 689 us, 5.3 TB/s).
 // Squares are summed in 64 bits: no gradient of a 16- or 32-bit type leaves
 // their range, and a conversion and a 64-bit fma an element take less than the
 // element's time on HBM.  So do the products with c, whose factor leaves fp32's
@@ -158,7 +158,7 @@ __global__ __launch_bounds__(256) void k_grad_norm(Ranges r, const double* __res
   if (threadIdx.x == 0) out[blockIdx.x] = (float)v;
 }
 
-template <class E>
+template <class E, bool ONCE>
 __device__ __forceinline__ void scale_chunk(const Entry& e, long long lo, long long hi, double c) {
   constexpr int W = Vec<E>::W, U = 4;
   E* __restrict__ g = (E*)e.g;
@@ -175,14 +175,16 @@ __device__ __forceinline__ void scale_chunk(const Entry& e, long long lo, long l
     }
     return;
   }
-  // W sums.  They pass by once, and nontemporally leave the cache to the
-  // gradients (303 M elements from bf16: 675 us, 693 with plain accesses)
-  typedef float f4 __attribute__((ext_vector_type(4), aligned(4)));
+  // W sums.  ONCE: they pass the cache (the gradients as well: 279 us become 287
+  // at 134 M elements, 689 become 685 at 303 M: not kept).
+  typedef float f4 __attribute__((ext_vector_type(4)));
+  struct __attribute__((packed, aligned(4))) Any4 { f4 v; };
   struct Sums { f4 q[W / 4]; };
   auto load = [&](long long at) {
     Sums r;
 #pragma unroll
-    for (int k = 0; k < W / 4; ++k) r.q[k] = __builtin_nontemporal_load((const f4*)(m + at) + k);
+    for (int k = 0; k < W / 4; ++k)
+      r.q[k] = ONCE ? load_once<f4>(m + at + 4 * k) : ((const Any4*)(m + at + 4 * k))->v;
     return r;
   };
   constexpr int S = 256 * W;
@@ -195,7 +197,10 @@ __device__ __forceinline__ void scale_chunk(const Entry& e, long long lo, long l
         x = (float)__builtin_fma((double)to_f32((E)v[k]), c, (double)x);
       }
 #pragma unroll
-      for (int k = 0; k < W / 4; ++k) __builtin_nontemporal_store(s.q[k], (f4*)(m + at) + k);
+      for (int k = 0; k < W / 4; ++k) {
+        if (ONCE) store_once(m + at + 4 * k, s.q[k]);
+        else ((Any4*)(m + at + 4 * k))->v = s.q[k];
+      }
     } else {
       typename Vec<E>::type o;
 #pragma unroll
@@ -230,6 +235,7 @@ __device__ __forceinline__ void scale_chunk(const Entry& e, long long lo, long l
   }
 }
 
+template <bool ONCE>
 __global__ __launch_bounds__(256) void k_grad_clip(Table t, const double* __restrict__ part,
                                                    int parts, float max_norm, float scale,
                                                    float* __restrict__ norm) {
@@ -239,13 +245,13 @@ __global__ __launch_bounds__(256) void k_grad_clip(Table t, const double* __rest
   // (a norm that is NaN makes c NaN, an infinite one 0)
   const double c = (v <= (double)max_norm ? 1.0 : (double)max_norm / v) * (double)scale;
   long long lo, hi;
-  // (from the end: what the first pass read last is still in the cache; 693
-  // us at 303 M elements, 707 from the start)
+  // (from the end: what the first pass read last is still in the cache; 2 % of
+  // the call at 303 M elements)
   const Entry& e = my_entry(t, gridDim.x - 1 - blockIdx.x, lo, hi);
   if (c == 1.0 && !e.m) return;          // g <- 1 g
-  if (e.dtype == DION3_F32) scale_chunk<float>(e, lo, hi, c);
-  else if (e.dtype == DION3_BF16) scale_chunk<bf16>(e, lo, hi, c);
-  else scale_chunk<f16>(e, lo, hi, c);
+  if (e.dtype == DION3_F32) scale_chunk<float, ONCE>(e, lo, hi, c);
+  else if (e.dtype == DION3_BF16) scale_chunk<bf16, ONCE>(e, lo, hi, c);
+  else scale_chunk<f16, ONCE>(e, lo, hi, c);
 }
 
 long long elements(const dion3_grad& d) { return (long long)d.rows * d.cols; }
@@ -267,6 +273,16 @@ long long chunk_size(const dion3_grad* d, int count) {
 }
 int chunks_of(const dion3_grad& d, long long chunk) {
   return (int)((elements(d) + chunk - 1) / chunk);
+}
+
+// Whether the sums pass the 256 MB cache: sums of 512 MB from bf16 take 279 us
+// past it and 307 through it (381 and 397 with a pass over the sums), of 256 MB
+// 142 and 149, but of 128 MB 73 and 63, of 64 MB 39 and 36.
+bool sums_once(const dion3_grad* d, int count) {
+  double b = 0.0;
+  for (int i = 0; i < count; ++i)
+    if (d[i].M) b += (double)elements(d[i]) * (d[i].dtype == DION3_F32 ? 8.0 : 6.0);
+  return b > 288e6;
 }
 
 // Calls launch(table, chunks of the batch, first) for every batch.
@@ -424,10 +440,12 @@ dion3_status dion3_clip_grad_norm(const dion3_grad* grads, int32_t count, float 
     part += parts;
     terms = 1;
   }
+  const bool once = sums_once(grads, count);
   TraceScope ts("grad_clip", 0.0, grad_bytes(grads, count, 8.0), s);
   HIP_TRY(for_batches(grads, count, chunk, [&](const Table& t, int chunks, bool first) {
-    hipLaunchKernelGGL(k_grad_clip, dim3(chunks), dim3(256), 0, s, t, part, terms, max_norm, scale,
-                       first ? norm : nullptr);
+    float* out = first ? norm : nullptr;
+    if (once) hipLaunchKernelGGL(k_grad_clip<true>, dim3(chunks), dim3(256), 0, s, t, part, terms, max_norm, scale, out);
+    else hipLaunchKernelGGL(k_grad_clip<false>, dim3(chunks), dim3(256), 0, s, t, part, terms, max_norm, scale, out);
     return hipGetLastError();
   }));
   return DION3_OK;

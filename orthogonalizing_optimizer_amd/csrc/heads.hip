@@ -166,19 +166,28 @@ __device__ __forceinline__ float head_sum(float v, int G) {
 // The lane's 16 columns of head h of token t, asked for and as floats (zeros
 // where the lane has none).  WHOLE: the turned columns and the others fill all
 // pieces, so no chunk ends early (the checks take 30 registers).
-template <bool WHOLE, class E>
+// ONCE: past the cache (chosen at compile time: of a branch between two loads
+// that differ in this alone the compiler makes one load).
+template <bool WHOLE, bool ONCE, class E>
 __device__ __forceinline__ void ask(const void* x, long long ld, long long hs, long long t, int h,
                                     int heads, const Item& it, bool mine, Raw8<E> (&raw)[2]) {
   if (WHOLE) {           // no branches between the loads: lanes without a head read the last one's
     const E* row = (const E*)x + t * ld + min(h, heads - 1) * hs;
 #pragma unroll
-    for (int k = 0; k < 2; ++k) raw[k].v = ((const typename Raw8<E>::Any*)(row + it.base[k] + it.c[k]))->v;
+    for (int k = 0; k < 2; ++k) {
+      const E* at = row + it.base[k] + it.c[k];
+      if (ONCE) raw[k].v = load_once<typename Raw8<E>::type>(at);
+      else raw[k].v = ((const typename Raw8<E>::Any*)at)->v;
+    }
     return;
   }
   if (!mine) return;
   const E* row = (const E*)x + t * ld + h * hs;
 #pragma unroll
-  for (int k = 0; k < 2; ++k) raw[k] = fetch8(row + it.base[k], it.c[k], it.lim[k]);
+  for (int k = 0; k < 2; ++k) {
+    if (ONCE) raw[k] = fetch8_once(row + it.base[k], it.c[k], it.lim[k]);
+    else raw[k] = fetch8(row + it.base[k], it.c[k], it.lim[k]);
+  }
 }
 template <bool WHOLE, class E>
 __device__ __forceinline__ void take(const Raw8<E> (&raw)[2], const Item& it, bool mine,
@@ -218,7 +227,7 @@ __device__ __forceinline__ float head_rstd(const float (&v)[2][8], int G, int D,
   return 1.0f / sqrtf(head_sum(ss, G) / (float)D + eps);
 }
 
-template <class E, bool IL, bool WHOLE>
+template <class E, bool IL, bool WHOLE, bool ONCE>
 __global__ __launch_bounds__(256) void k_heads(HeadsP p) {
   extern __shared__ __attribute__((aligned(16))) float2 turns[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -230,7 +239,7 @@ __global__ __launch_bounds__(256) void k_heads(HeadsP p) {
   const Item it = my_item<IL>(j, p.D, p.r);
   Raw8<E> raw[2];
   bool mine = it.on && at.b * per + slot < s.heads;
-  ask<WHOLE>(s.x, s.ldx, s.hsx, at.t, at.b * per + slot, s.heads, it, mine, raw);
+  ask<WHOLE, ONCE>(s.x, s.ldx, s.hsx, at.t, at.b * per + slot, s.heads, it, mine, raw);
   double pos = position(p, at.t);
   float w[2][8], co[8], si[8];
   load_weight<E>(p, s, it, w);
@@ -246,7 +255,7 @@ __global__ __launch_bounds__(256) void k_heads(HeadsP p) {
     const bool go = at.more();
     if (go) {
       mine = it.on && at.b * per + slot < s.heads;
-      ask<WHOLE>(s.x, s.ldx, s.hsx, at.t, at.b * per + slot, s.heads, it, mine, raw);
+      ask<WHOLE, ONCE>(s.x, s.ldx, s.hsx, at.t, at.b * per + slot, s.heads, it, mine, raw);
       fresh = at.t != now.t;
       if (fresh) pos = position(p, at.t);
     }
@@ -262,7 +271,7 @@ __global__ __launch_bounds__(256) void k_heads(HeadsP p) {
 // The weights' gradients: a lane adds up its columns over its tokens and
 // heads, the lanes of equal columns and the workgroup's waves are joined at
 // the end, and the workgroups' rows by k_heads_join, each in a fixed order.
-template <class E, bool IL, bool WHOLE>
+template <class E, bool IL, bool WHOLE, bool ONCE>
 __global__ __launch_bounds__(256) void k_heads_grad(HeadsP p) {
   extern __shared__ __attribute__((aligned(16))) float2 turns[];
   float* sh = (float*)turns + 8 * p.pitch;             // 3 waves x D
@@ -278,8 +287,8 @@ __global__ __launch_bounds__(256) void k_heads_grad(HeadsP p) {
   if (at.more()) {
     Raw8<E> rx[2], ry[2];
     bool mine = it.on && at.b * per + slot < s.heads;
-    ask<WHOLE>(s.x, s.ldx, s.hsx, at.t, at.b * per + slot, s.heads, it, mine, rx);
-    ask<WHOLE>(s.dy, s.lddy, s.hsdy, at.t, at.b * per + slot, s.heads, it, mine, ry);
+    ask<WHOLE, ONCE>(s.x, s.ldx, s.hsx, at.t, at.b * per + slot, s.heads, it, mine, rx);
+    ask<WHOLE, ONCE>(s.dy, s.lddy, s.hsdy, at.t, at.b * per + slot, s.heads, it, mine, ry);
     double pos = position(p, at.t);
     float w[2][8], co[8], si[8];
     load_weight<E>(p, s, it, w);
@@ -295,8 +304,8 @@ __global__ __launch_bounds__(256) void k_heads_grad(HeadsP p) {
       const bool go = at.more();
       if (go) {
         mine = it.on && at.b * per + slot < s.heads;
-        ask<WHOLE>(s.x, s.ldx, s.hsx, at.t, at.b * per + slot, s.heads, it, mine, rx);
-        ask<WHOLE>(s.dy, s.lddy, s.hsdy, at.t, at.b * per + slot, s.heads, it, mine, ry);
+        ask<WHOLE, ONCE>(s.x, s.ldx, s.hsx, at.t, at.b * per + slot, s.heads, it, mine, rx);
+        ask<WHOLE, ONCE>(s.dy, s.lddy, s.hsdy, at.t, at.b * per + slot, s.heads, it, mine, ry);
         fresh = at.t != now.t;
         if (fresh) pos = position(p, at.t);
       }
@@ -382,8 +391,9 @@ int pieces(int D, int r, bool il) {
 // As many waves as stay resident (a few more would run after all others) are
 // shared out between queries and keys by their batches, and each takes equally
 // many of them: 8192 tokens of 32 + 8 heads of 128 take 32 us (5.2 TB/s; twice
-// the resident waves, 35 with as many) and 59 backwards (4.3 TB/s; 65 by whole
-// tokens, 57 with 4 waves a SIMD that read their weight from LDS: not kept).
+// the resident waves, 36 with as many) and 57 backwards (4.4 TB/s; a tenth more
+// by whole tokens; with 4 waves a SIMD that read their weight from LDS 3 % less:
+// not kept).
 struct Split {
   int G, batches[2], units[2];
   long long each[2];
@@ -461,20 +471,31 @@ HeadsP describe(const dion3_heads* q, const dion3_heads* k, const Split& sp, con
   return p;
 }
 
-template <class E, bool GRAD, bool IL, bool WHOLE>
+template <class E, bool GRAD, bool IL, bool WHOLE, bool ONCE>
 void launch_heads_t(const HeadsP& p, int units, size_t lds, hipStream_t s) {
-  if (GRAD) hipLaunchKernelGGL((k_heads_grad<E, IL, WHOLE>), dim3(units), dim3(256), lds, s, p);
-  else hipLaunchKernelGGL((k_heads<E, IL, WHOLE>), dim3(units), dim3(256), lds, s, p);
+  if (GRAD) hipLaunchKernelGGL((k_heads_grad<E, IL, WHOLE, ONCE>), dim3(units), dim3(256), lds, s, p);
+  else hipLaunchKernelGGL((k_heads<E, IL, WHOLE, ONCE>), dim3(units), dim3(256), lds, s, p);
+}
+template <class E, bool GRAD, bool IL, bool WHOLE>
+void launch_heads_w(const HeadsP& p, int units, size_t lds, hipStream_t s) {
+  // What is read, if it is much, passes the cache and leaves it to what is
+  // written, which the attention reads next: 32 + 8 heads of 128 with a pass over
+  // the outputs take 92 us at 16384 tokens (98 with plain loads, 101 with the
+  // outputs past the cache), backwards 139 (150, 156); at 8192 80 backwards (84)
+  // and 49 forwards either way; at 4096 (42 MB read) 32 instead of 29 forwards.
+  const double read = (GRAD ? 4.0 : 2.0) * p.T * p.D * (p.s[0].heads + p.s[1].heads);
+  if (read > 64e6) launch_heads_t<E, GRAD, IL, WHOLE, true>(p, units, lds, s);
+  else launch_heads_t<E, GRAD, IL, WHOLE, false>(p, units, lds, s);
 }
 template <class E, bool GRAD>
 void launch_heads(const HeadsP& p, int units, size_t lds, int interleaved, hipStream_t s) {
   const bool whole = p.r % 16 == 0 && p.D % 16 == 0;
   if (interleaved) {
-    if (whole) launch_heads_t<E, GRAD, true, true>(p, units, lds, s);
-    else launch_heads_t<E, GRAD, true, false>(p, units, lds, s);
+    if (whole) launch_heads_w<E, GRAD, true, true>(p, units, lds, s);
+    else launch_heads_w<E, GRAD, true, false>(p, units, lds, s);
   } else {
-    if (whole) launch_heads_t<E, GRAD, false, true>(p, units, lds, s);
-    else launch_heads_t<E, GRAD, false, false>(p, units, lds, s);
+    if (whole) launch_heads_w<E, GRAD, false, true>(p, units, lds, s);
+    else launch_heads_w<E, GRAD, false, false>(p, units, lds, s);
   }
 }
 

@@ -88,6 +88,36 @@ __device__ __forceinline__ void store8(E* __restrict__ row, int c, int m, const 
   }
 }
 
+// 16 bytes, or 8 elements, at any element alignment, past the 256 MB cache: for
+// what is not read again before as much has passed, or is too long to stay.
+template <class E, int N>
+struct Once {
+  typedef E type __attribute__((ext_vector_type(N), aligned(sizeof(E))));
+};
+template <class V, class E, int N = sizeof(V) / sizeof(E)>
+__device__ __forceinline__ V load_once(const E* p) {
+  return __builtin_nontemporal_load((const typename Once<E, N>::type*)p);
+}
+template <class E, class V, int N = sizeof(V) / sizeof(E)>
+__device__ __forceinline__ void store_once(E* p, V v) {
+  __builtin_nontemporal_store(v, (typename Once<E, N>::type*)p);
+}
+template <class E>
+__device__ __forceinline__ Raw8<E> fetch8_once(const E* row, int c, int m) {
+  if (c + 8 > m) return fetch8(row, c, m);
+  Raw8<E> r;
+  r.v = load_once<typename Raw8<E>::type>(row + c);
+  return r;
+}
+template <class E>
+__device__ __forceinline__ void store8_once(E* row, int c, int m, const float (&v)[8]) {
+  if (c + 8 > m) return store8(row, c, m, v);
+  Raw8<E> r;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) r.v[e] = (E)v[e];
+  store_once(row + c, r.v);
+}
+
 // -------------------------------------------------------------- activations
 //
 // An element of an activation costs as much VALU time as it does HBM time

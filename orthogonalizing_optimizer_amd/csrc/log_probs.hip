@@ -383,7 +383,12 @@ struct GradP {
 };
 
 // One read and one write of a logit; in place where dX is X (a thread reads
-// its logits before it writes them, and nobody else's).
+// its logits before it writes them, and nobody else's).  Both pass the cache:
+// the logits, which the forward pass may have left there, are not needed again,
+// and what they leave of it speeds up what follows at every size (8192 x 32000
+// alone 199 -> 178 us; forward, gradient and a pass over it: 402 -> 350, and
+// 56 -> 52 at 1000 x 32000; with the forward pass's loads past the cache too,
+// 360 and 59).
 template <class E, bool ENT>
 __global__ __launch_bounds__(256) void k_logp_grad(GradP p) {
   const long long block = flat_block();
@@ -395,7 +400,7 @@ __global__ __launch_bounds__(256) void k_logp_grad(GradP p) {
 #pragma unroll
   for (int i = 0; i < kChunks; ++i) {
     const int c = from + (i * 256 + (int)threadIdx.x) * 8;
-    if (c < to) raw[i] = fetch8(row, c, p.n);
+    if (c < to) raw[i] = fetch8_once(row, c, p.n);
   }
   const float m = p.stats[2 * t], l = p.stats[2 * t + 1];
   long long j = p.target ? target_of(p.target, p.target64, t) : -1;
@@ -423,7 +428,7 @@ __global__ __launch_bounds__(256) void k_logp_grad(GradP p) {
       v[e] = none ? 0.0f : pr * (ENT ? __builtin_fmaf(b, fmaxf(q, -1e30f), a) : a);
       if (c + e == j && !none) v[e] += g;
     }
-    store8((E*)p.dx + t * p.lddx, c, min(to, p.n), v);
+    store8_once((E*)p.dx + t * p.lddx, c, min(to, p.n), v);
   }
 }
 
