@@ -368,9 +368,9 @@ __global__ __launch_bounds__(1024) void k_heads_join(const float* __restrict__ p
   const float* rows = part + (blockIdx.y ? (long long)qunits * D : 0);
   const int u1 = min(units, (slice + 1) * per);
   float a = 0.0f;
+  const int at = min(c, D - 1);                        // (no branch between the loads: 6.1 -> 4.6 us)
 #pragma unroll 8
-  for (int u = slice * per; u < u1; ++u)
-    if (c < D) a += rows[(long long)u * D + c];
+  for (int u = slice * per; u < u1; ++u) a += rows[(long long)u * D + at];
   sh[slice][col] = a;
   __syncthreads();
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, mine = blockIdx.x * 16 + wave;
