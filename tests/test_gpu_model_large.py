@@ -1,0 +1,92 @@
+"""Calls whose reads or writes pass the 256 MB cache, against the same calls on
+parts that do not: bit for bit where a row stands for itself."""
+import pytest
+import torch
+
+import orthogonalizing_optimizer_amd as d3
+from tests.layer_ref import EPS32
+
+pytestmark = pytest.mark.gpu
+BF, FP, F32 = torch.bfloat16, torch.float16, torch.float32
+
+
+@pytest.fixture(autouse=True)
+def room():
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 8 << 30:
+        pytest.skip("not enough free GPU memory")
+    yield
+    torch.cuda.empty_cache()
+
+
+def rnd(g, *shape, dtype=F32):
+    return torch.randn(*shape, generator=g, device="cuda").to(dtype)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dtype,D,r,gap", [(BF, 128, 128, 0), (FP, 96, 32, 8), (BF, 80, 20, 0), (FP, 100, 36, 3)])
+def test_heads(dtype, D, r, gap, interleaved):
+    g = torch.Generator(device="cuda").manual_seed(D + r)
+    hq, hk = 48, 5
+    h = hq + hk
+    T = int(70e6) // (2 * h * D) + 1
+    x, dy = rnd(g, T, h, D + gap, dtype=dtype)[..., :D], rnd(g, T, h, D + gap, dtype=dtype)[..., :D]
+    assert 2 * T * h * D > 64e6
+    w, v = rnd(g, D), rnd(g, D)
+    pos = torch.randint(0, 100000, (T,), generator=g, device="cuda")
+    fr = (10000.0 ** (-torch.arange(0, r, 2, dtype=torch.float64) / r)).cuda()
+
+    def both(a, b):
+        q, k = x[a:b, :hq], x[a:b, hq:]
+        y = d3.qk_norm_rope(q, k, w, v, pos[a:b], fr, interleaved=interleaved)
+        return y + d3.qk_norm_rope_grad(dy[a:b, :hq], dy[a:b, hq:], q, k, w, v, pos[a:b], fr,
+                                        interleaved=interleaved)
+
+    whole = both(0, T)
+    dw = [torch.zeros(D, dtype=torch.float64, device="cuda") for _ in range(2)]
+    for a in range(0, T, 1000):
+        b = min(T, a + 1000)
+        part = both(a, b)
+        for i in range(4):
+            assert torch.equal(whole[i][a:b], part[i]), (i, a)
+        for i in range(2):
+            dw[i] += part[4 + i].double()
+    # The terms are the same numbers in both; a term goes through at most 100
+    # additions (of a lane at most 40: the tokens' batches over 3000 waves; of
+    # the lanes 6, the waves 3, the workgroups 18), and is du hat with du at
+    # most sqrt(2) times the head's largest |dy|.
+    xd, top = x.double(), dy.double().abs().amax(-1, keepdim=True)
+    terms = 2 ** 0.5 * top * xd.abs() / torch.sqrt((xd * xd).mean(-1, keepdim=True) + 1e-6)
+    for i, part in enumerate((terms[:, :hq], terms[:, hq:])):
+        assert ((whole[4 + i].double() - dw[i]).abs() <= 2 * 100 * EPS32 * part.sum((0, 1))).all()
+
+
+def test_embedding():
+    g = torch.Generator(device="cuda").manual_seed(1)
+    for dtype, m in ((BF, 4096), (F32, 2050), (FP, 4099)):
+        w = rnd(g, 5000, m, dtype=dtype)
+        T = int(96e6) // (m * w.element_size()) + 77
+        t = torch.randint(-1, 5001, (T,), generator=g, device="cuda")
+        ok = (t >= 0) & (t < 5000)
+        want = w[t.clamp(0, 4999)] * ok[:, None]
+        assert torch.equal(d3.embedding(t, w), want), dtype
+
+
+@pytest.mark.parametrize("dtype", [F32, BF, FP])
+def test_clip_into_sums(dtype):
+    g = torch.Generator(device="cuda").manual_seed(2)
+    shapes = [(5001, 4099), (3, 7), (2500, 8000), (33,)]
+    grads, sums = [rnd(g, *s, dtype=dtype) for s in shapes], [rnd(g, *s) for s in shapes]
+    n = sum(v.numel() for v in grads)
+    while n * (4 + grads[0].element_size()) <= 288e6:
+        grads.append(rnd(g, 4000, 4001, dtype=dtype))
+        sums.append(rnd(g, 4000, 4001))
+        n += grads[-1].numel()
+    before = [m.clone() for m in sums]
+    norm = d3.clip_grad_norm(grads, 100.0, into=sums)
+    exact = sum(float(v.double().square().sum()) for v in grads) ** 0.5
+    assert abs(float(norm) - exact) <= exact * EPS32 * 1.001
+    c = 100.0 / exact
+    for v, b, m in zip(grads, before, sums):
+        want = b.double() + c * v.double()
+        assert ((m.double() - want).abs() <= want.abs() * EPS32 * 1.0001 + 1e-45).all()
