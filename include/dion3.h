@@ -463,7 +463,8 @@ DION3_API dion3_status dion3_linear_grad_weight(const void* dZ, int64_t lddz, co
  * = v (fp32, n x m; zeros for a row without tokens), or with accumulate != 0
  * that is added to dW, and rows without tokens are neither read nor written.
  * Sums are held in fp32, without atomics, in an order fixed by the tokens.
- * Errors: as for the layers' operators; scale must be finite. */
+ * Errors: as for the layers' operators, but row strides up to 2^38; scale must
+ * be finite. */
 DION3_API dion3_status dion3_embedding(const void* token, int32_t token_bits, const void* W,
                                        int64_t ldw, int32_t wtype, void* Y, int64_t ldy, int64_t T,
                                        int64_t n, int64_t m, float scale, int32_t dtype,
@@ -550,7 +551,8 @@ DION3_API dion3_status dion3_qk_norm_rope_grad(const dion3_heads* q, const dion3
  * gH = dentropy[t] (or NULL) and H = entropy[t] (read with dentropy only).
  * dX may be X.
  * Sums are held in fp32 in an order fixed by n.  Errors: as for the layers'
- * operators (sides: n); top negative or above n is an argument error, above
+ * operators (sides: n), but row strides up to 2^38 (the last tokens' rows of
+ * long sequences, say); top negative or above n is an argument error, above
  * DION3_MAX_TOP unsupported. */
 #define DION3_MAX_TOP 64
 DION3_API dion3_status dion3_log_probs_workspace_size(int64_t T, int64_t n, int32_t top,

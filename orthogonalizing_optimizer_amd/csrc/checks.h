@@ -37,6 +37,12 @@ dion3_status check_ld(long long ld, long long cols) {
   return ld > kMaxLd ? DION3_ERR_UNSUPPORTED : DION3_OK;
 }
 
+// Rows that are addressed in 64 bits.
+dion3_status check_far_ld(long long ld, long long cols) {
+  if (ld < cols) return DION3_ERR_ARG;
+  return ld > 1LL << 38 ? DION3_ERR_UNSUPPORTED : DION3_OK;
+}
+
 // 16-bit (and fp32) elements must be aligned to their own size.
 bool elem_aligned(const void* p, int size) { return ((uintptr_t)p & (size - 1)) == 0; }
 

@@ -610,8 +610,8 @@ dion3_status dion3_embedding(const void* tokens, int32_t token_bits, const void*
   if (!any_type(dtype) || (wtype != DION3_F32 && wtype != dtype) || !isfinite(scale))
     return DION3_ERR_ARG;
   TRY(check_sizes(T, n, m));
-  TRY(check_ld(ldw, m));
-  TRY(check_ld(ldy, m));
+  TRY(check_far_ld(ldw, m));
+  TRY(check_far_ld(ldy, m));
   TRY(check_tokens(tokens, token_bits, T));
   if (T == 0) return DION3_OK;
   if (!W || !Y || !elem_aligned(W, size_of(wtype)) || !elem_aligned(Y, size_of(dtype)))
@@ -644,8 +644,8 @@ dion3_status dion3_embedding_grad(const void* tokens, int32_t token_bits, const 
                                   void* ws, size_t ws_bytes, void* stream) {
   if (!any_type(dtype) || !isfinite(scale)) return DION3_ERR_ARG;
   TRY(check_sizes(T, n, m));
-  TRY(check_ld(lddy, m));
-  TRY(check_ld(ldw, m));
+  TRY(check_far_ld(lddy, m));
+  TRY(check_far_ld(ldw, m));
   TRY(check_tokens(tokens, token_bits, T));
   if (!dW || !elem_aligned(dW, 4)) return DION3_ERR_ARG;
   if (T > 0 && (!dY || !elem_aligned(dY, size_of(dtype)))) return DION3_ERR_ARG;

@@ -514,7 +514,7 @@ dion3_status dion3_log_probs(const void* X, int64_t ldx, const void* target, int
   TRY(check_sizes(T, n, 1));
   if (top < 0 || top > n) return DION3_ERR_ARG;
   if (top > kMaxTop) return DION3_ERR_UNSUPPORTED;
-  TRY(check_ld(ldx, n));
+  TRY(check_far_ld(ldx, n));
   TRY(check_targets(target, target_bits));
   if (T == 0) return DION3_OK;
   if (!X || !stats || (target != nullptr) != (logp != nullptr)) return DION3_ERR_ARG;
@@ -545,8 +545,8 @@ dion3_status dion3_log_probs_grad(const float* dlogp, const void* X, int64_t ldx
                                   void* stream) {
   if (!any_type(dtype) || !(scale > 0.0f) || !isfinite(scale)) return DION3_ERR_ARG;
   TRY(check_sizes(T, n, 1));
-  TRY(check_ld(ldx, n));
-  TRY(check_ld(lddx, n));
+  TRY(check_far_ld(ldx, n));
+  TRY(check_far_ld(lddx, n));
   TRY(check_targets(target, target_bits));
   if ((target != nullptr) != (dlogp != nullptr) && T > 0) return DION3_ERR_ARG;
   if (T == 0) return DION3_OK;

@@ -90,3 +90,27 @@ def test_clip_into_sums(dtype):
     for v, b, m in zip(grads, before, sums):
         want = b.double() + c * v.double()
         assert ((m.double() - want).abs() <= want.abs() * EPS32 * 1.0001 + 1e-45).all()
+
+
+def test_rows_far_apart():
+    """The last token's row of each sequence, and tables with such rows."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    n, S = 32001, 70
+    far = rnd(g, 5, S, n, dtype=BF)
+    assert S * n > 1 << 21
+    x = far[:, -1]
+    near = x.contiguous()
+    t = torch.randint(0, n, (5,), generator=g, device="cuda")
+    a, b = (d3.log_probs(v, t, entropy=True, top=7) for v in (x, near))
+    assert all(torch.equal(p, q) for p, q in zip(a, b))
+    ones, keep = torch.ones(5, device="cuda"), far[:, :-1].clone()
+    want = d3.log_probs_grad(ones, near, t, b[1], entropy=b[2], dentropy=ones)
+    d3.log_probs_grad(ones, x, t, a[1], entropy=a[2], dentropy=ones, out=x)
+    assert torch.equal(x, want) and torch.equal(far[:, :-1], keep)
+    w = rnd(g, 6, S, n)[:, 3]
+    tokens = torch.tensor([5, 0, 5, 7, 1], device="cuda")
+    y = d3.embedding(tokens, w)
+    assert torch.equal(y, d3.embedding(tokens, w.contiguous()))
+    dy = rnd(g, 5, S, n, dtype=BF)[:, 0]
+    grad = d3.embedding_grad(tokens, dy.contiguous(), 6)
+    assert torch.equal(d3.embedding_grad(tokens, dy, 6, out=w), grad)

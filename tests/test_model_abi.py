@@ -13,7 +13,7 @@ OK, ERR_ARG, ERR_WS, ERR_UNSUP = 0, -1, -2, -3
 P = 1 << 20              # a non-null, 256-aligned address that is never dereferenced
 F32, BF16, F16 = 0, 1, 2
 T, N, M = 40, 24, 16
-BIG, LD, TOK = (1 << 20) + 1, (1 << 21) + 8, (1 << 24) + 1
+BIG, LD, TOK = (1 << 20) + 1, (1 << 38) + 8, (1 << 24) + 1
 NAN, INF = float("nan"), float("inf")
 
 
