@@ -87,6 +87,8 @@ def _table(grads, into, written):
             seen.add(mp or gp)
     if written and len(seen) != sum(1 for n in table[3::7] if n):
         raise ValueError("a gradient or a sum is listed twice")
+    if into is not None and not seen.isdisjoint(table[0::7]):
+        raise ValueError("a sum is one of the gradients")
     return array.array("q", table), len(grads), device
 
 

@@ -226,6 +226,9 @@ def test_refusals():
         d3.clip_grad_norm([a, b, a], 1.0)
     with pytest.raises(ValueError):
         d3.clip_grad_norm([a, b], 1.0, into=[a, a])
+    for into in ([b, a], [a, torch.ones(4, 4, device="cuda")]):     # sums that are gradients
+        with pytest.raises(ValueError):
+            d3.clip_grad_norm([a, b], 1.0, into=into)
     with pytest.raises(ValueError):
         d3.clip_grad_norm([a], 1.0, into=[a, b])
     with pytest.raises(ValueError):
