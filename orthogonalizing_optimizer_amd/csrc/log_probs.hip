@@ -110,61 +110,95 @@ constexpr int kWaveBest = 128;     // candidates a wave leaves at most (at least
 // it has as many), at most kWaveBest, padded with zeros to a multiple of 4.
 // Logits at or above the top-th largest of the lanes' maxima are a superset,
 // most often of few more than `top`: one comparison a logit.  Where they are
-// too many (equal logits, one lane's), or there is NaN (`odd`), the top-th
-// largest key is found by its bits, and of the logits equal to it the first
-// are taken.
+// too many, a threshold above that one is looked for by halves, until it
+// leaves few enough.  Where none does (equal logits), or there are fewer than
+// `top` above -infinity, the logits above the threshold and the first of those
+// equal to it are taken; where there is NaN (`odd`), that threshold is found by
+// the keys' bits.  mx: the wave's maximum.
 template <class E>
 __device__ __forceinline__ int wave_best(const float (&v)[kChunks][8], const float (&cm)[kChunks],
-                                         const int (&col)[kChunks], int to, int top, bool odd,
-                                         u64* out) {
+                                         const int (&col)[kChunks], int to, int top, float mx,
+                                         bool odd, u64* out) {
   constexpr int SH = kLow<E>;
+  constexpr unsigned kNone = 0x007fffffu;              // the key of -infinity (and of what is no column)
   const int lane = threadIdx.x & 63;
   const u64 below = (1ull << lane) - 1;
   int have = 0;
+  unsigned t = 0;
+  bool equal = odd;                                    // candidates equal to a threshold
   if (!odd) {
     float lm = cm[0];
 #pragma unroll
     for (int i = 1; i < kChunks; ++i) lm = fmaxf(lm, cm[i]);
     const unsigned lk = order_key<E>(lm);
-    unsigned t = 0;
     for (int b = 31; b >= 16; --b) {               // (to within 2^-7: few more than needed)
       const unsigned c = t | 1u << b;
       if (__popcll(__ballot(lk >= c)) >= top) t = c;
     }
-    // (below the key of -infinity this is NaN, which nothing is below)
-    const float tau = order_value(t);
+    t = max(t, kNone + 1);
+    unsigned hi = (unsigned)__builtin_amdgcn_readfirstlane((int)order_key<E>(mx)) + 1;
+    for (;;) {
+      const float tau = order_value(t);
+      have = 0;
 #pragma unroll
-    for (int i = 0; i < kChunks; ++i) {
-      if (!__ballot(!(cm[i] < tau))) continue;
+      for (int i = 0; i < kChunks; ++i) {
+        if (!__ballot(cm[i] >= tau)) continue;
+        int from = col[i];
+        asm volatile("" : "+v"(from));   // (nothing computed ahead for a second time around)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const bool in = !(v[i][e] < tau);
-        const u64 b = __ballot(in);
-        if (!b) continue;
-        const int at = have + __popcll(b & below);
-        if (in && at < kWaveBest) out[at] = candidate(order_key<E>(v[i][e]), col[i] + e);
-        have += __popcll(b);
+        for (int e = 0; e < 8; ++e) {
+          float x = v[i][e];
+          const bool in = x >= tau;
+          const u64 b = __ballot(in);
+          if (!b) continue;
+          asm volatile("" : "+v"(x));
+          const int at = have + __popcll(b & below);
+          if (in && at < kWaveBest) out[at] = candidate(order_key<E>(x), from + e);
+          have += __popcll(b);
+        }
+      }
+      if (have <= kWaveBest) break;
+      bool found = false;
+      while (hi - t > 1 && !found) {
+        const unsigned c = t + (hi - t) / 2;
+        const float x = order_value(c);
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) n += __popcll(__ballot(v[i][e] >= x));
+        if (n >= top) t = c;
+        else hi = c;
+        found = n >= top && n <= kWaveBest;
+      }
+      if (!found) {
+        equal = true;
+        break;
       }
     }
-    odd = have > kWaveBest;
+    if (have < top) {
+      equal = true;
+      t = kNone;
+    }
   }
-  if (odd) {
+  if (equal) {
     auto key = [&](int i, int e) {
       float x = v[i][e];
       asm volatile("" : "+v"(x));      // (computed where it is used: 32 registers fewer)
       return col[i] + e < to ? order_key<E>(x) : 0u;
     };
-    unsigned t = 0;
-    for (int b = 31; b >= SH; --b) {
-      const unsigned c = t | 1u << b;
-      int cnt = 0;
+    if (odd) {
+      for (int b = 31; b >= SH; --b) {
+        const unsigned c = t | 1u << b;
+        int cnt = 0;
 #pragma unroll
-      for (int i = 0; i < kChunks; ++i)
+        for (int i = 0; i < kChunks; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) cnt += __popcll(__ballot(key(i, e) >= c));
-      if (cnt >= top) t = c;
+          for (int e = 0; e < 8; ++e) cnt += __popcll(__ballot(key(i, e) >= c));
+        if (cnt >= top) t = c;
+      }
+      if (SH > 0 && t && !(t & 0x80000000u)) t |= (1u << SH) - 1;
     }
-    if (SH > 0 && t && !(t & 0x80000000u)) t |= (1u << SH) - 1;
     have = 0;
 #pragma unroll
     for (int i = 0; i < kChunks; ++i)
@@ -272,7 +306,7 @@ void k_logp_piece(LogpP p) {
   if ((threadIdx.x & 63) == 0) sh[wave] = w;
   if constexpr (TOP) {
     const bool odd = __builtin_amdgcn_readfirstlane(w.s != w.s ? 1 : 0);    // the wave's sum is NaN
-    const int c = wave_best<E>(v, cm, col, to, p.top, odd, cand + wave * kWaveBest);
+    const int c = wave_best<E>(v, cm, col, to, p.top, mx, odd, cand + wave * kWaveBest);
     if ((threadIdx.x & 63) == 0) count[wave] = c;
   }
   __syncthreads();
@@ -435,13 +469,14 @@ __global__ __launch_bounds__(256) void k_logp_grad(GradP p) {
 // --------------------------------------------------------------- the launches
 
 // Pieces of at most 8192 logits (4 waves), of 32768 (16 waves) where a row
-// would have more than 16, of equal length.
+// would have more than 16, of equal length; one or two waves for rows that fill
+// no more.
 struct Pieces {
   int S, len, threads;
 };
 Pieces pieces_of(int n) {
   Pieces q;
-  q.threads = n > 16 * 8192 ? 1024 : 256;
+  q.threads = n > 16 * 8192 ? 1024 : n > 4096 ? 256 : n > 2048 ? 128 : 64;
   const int most = q.threads * 8 * kChunks;
   q.S = (n + most - 1) / most;
   q.len = ((n + q.S - 1) / q.S + 7) / 8 * 8;
