@@ -235,6 +235,65 @@ __device__ __forceinline__ int wave_best(const float (&v)[kChunks][8], const flo
   return have;
 }
 
+// Up to this many candidates of a workgroup are ranked by comparing all with
+// all; of more, one wave takes the `top` largest, in no order (the join ranks
+// them): 1000 x 32000 with 64 best takes 67 us, 100 ranked; 424 x 53616 with 20,
+// where there are fewer, 35 ranked and 39 not.
+constexpr int kRanked = 128;
+template <class E>
+__device__ __forceinline__ void best_of(const u64* cand, const int* count, int nw, int from,
+                                        int top, u64* best) {
+  constexpr int SH = kLow<E>, PL = 15;                 // (a piece's columns: 15 bits)
+  const int lane = threadIdx.x & 63;
+  auto each = [&](auto f) {
+#pragma unroll 2
+    for (int u = 0; u < nw; ++u) {
+      const int n = count[u];
+      const u64 a = lane < n ? cand[u * kWaveBest + lane] : 0;
+      const u64 b = lane + 64 < n ? cand[u * kWaveBest + 64 + lane] : 0;
+      f(a);
+      f(b);
+    }
+  };
+  // Thresholds by halves of (key without its constant bits, column from the
+  // end): the largest that `top` candidates reach.
+  auto at = [&](u64 c) {
+    const unsigned k = (unsigned)(c >> PL) << SH;
+    return candidate(k & 0x80000000u ? k : k | ((1u << SH) - 1),
+                     from + (1 << PL) - 1 - (int)(c & ((1u << PL) - 1)));
+  };
+  unsigned k0 = ~0u, k1 = 0;
+  each([&](u64 c) {
+    const unsigned k = (unsigned)(c >> 32);
+    k0 = c ? min(k0, k) : k0;
+    k1 = max(k1, k);
+  });
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    k0 = min(k0, (unsigned)__shfl_xor((int)k0, o, 64));
+    k1 = max(k1, (unsigned)__shfl_xor((int)k1, o, 64));
+  }
+  k0 = (unsigned)__builtin_amdgcn_readfirstlane((int)k0);
+  k1 = (unsigned)__builtin_amdgcn_readfirstlane((int)k1);
+  u64 lo = (u64)(k0 >> SH) << PL, hi = ((u64)(k1 >> SH) + 1 << PL) - 1;
+  for (int n = 0; lo < hi && n != top;) {
+    const u64 mid = lo + (hi - lo + 1) / 2, c = at(mid);
+    n = 0;
+    each([&](u64 a) { n += __popcll(__ballot(a >= c)); });
+    if (n >= top) lo = mid;
+    else hi = mid - 1;
+  }
+  const u64 least = at(lo), below = (1ull << lane) - 1;
+  int have = 0;
+  each([&](u64 c) {
+    const bool in = c >= least;
+    const u64 b = __ballot(in);
+    const int i = have + __popcll(b & below);
+    if (in && i < top) best[i] = c;
+    have += __popcll(b);
+  });
+}
+
 // The 8 logits from column c on of a row that ends at `to`: -infinity behind it.
 template <class E>
 __device__ __forceinline__ void logits8(const Raw8<E>& raw, int c, int to, int n, float (&v)[8]) {
@@ -316,9 +375,13 @@ void k_logp_piece(LogpP p) {
     p.part[block] = a;
   }
   if constexpr (TOP) {
-    // every candidate of the wave against all waves' candidates
     int all = 0;
     for (int u = 0; u < nw; ++u) all += count[u];
+    if (all > kRanked) {
+      if (wave == 0) best_of<E>(cand, count, nw, from, p.top, p.best + block * p.top);
+      return;
+    }
+    // every candidate of the wave against all waves' candidates
     for (int i = threadIdx.x & 63; i < count[wave]; i += 64) {
       const u64 mine = cand[wave * kWaveBest + i];
       int rank = 0;
@@ -366,20 +429,20 @@ __device__ __forceinline__ RowSums row_sums(const LogpP& p, long long t, const P
 
 // Rows from their pieces: a thread a row, or with TOP a workgroup a row, whose
 // threads rank the pieces' candidates, several threads a candidate where there
-// are few.
+// are fewer of them.
 constexpr int kJoinTop = 512;
 template <class E, bool TOP>
 __global__ __launch_bounds__(TOP ? kJoinTop : 64) void k_logp_join(LogpP p) {
   extern __shared__ __attribute__((aligned(16))) u64 cand[];
   const long long t = TOP ? flat_block() : flat_block() * 64 + threadIdx.x;
   if (t >= p.T) return;
-  const int nc = TOP ? p.S * p.top : 0;
+  const int nc = TOP ? p.S * p.top : 0, nt = blockDim.x;
   Part a = {kLowest, 0.0f, 0.0f, 0.0f};
   const bool write = !TOP || threadIdx.x == 0;
   bool token = false;
   const float x = write ? target_logit<E>(p, t, token) : 0.0f;
   if constexpr (TOP) {
-    for (int i = threadIdx.x; i < (nc + 3) / 4 * 4; i += kJoinTop) cand[i] = i < nc ? p.best[t * nc + i] : 0;
+    for (int i = threadIdx.x; i < (nc + 3) / 4 * 4; i += nt) cand[i] = i < nc ? p.best[t * nc + i] : 0;
     const int lane = threadIdx.x & 63;
     if (lane < p.S) a = p.part[t * p.S + lane];        // (S is at most 32)
     a = wave_merge(a);
@@ -391,9 +454,9 @@ __global__ __launch_bounds__(TOP ? kJoinTop : 64) void k_logp_join(LogpP p) {
   if constexpr (TOP) {
     __syncthreads();
     int q = 1;                                         // threads a candidate
-    while (q < 16 && nc * q * 2 <= kJoinTop) q *= 2;
+    while (q < 16 && nc * q * 2 <= nt) q *= 2;
     const int sub = threadIdx.x & (q - 1);
-    for (int i = threadIdx.x / q; i < (nc + 63) / 64 * 64; i += kJoinTop / q) {
+    for (int i = threadIdx.x / q; i < (nc + 63) / 64 * 64; i += nt / q) {
       const u64 mine = i < nc ? cand[i] : 0;
       int rank = count_before(cand, sub * 4, nc, q * 4, mine);
       for (int o = 1; o < q; o <<= 1) rank += __shfl_xor(rank, o, 64);
@@ -496,11 +559,16 @@ hipError_t launch_logp_t(const LogpP& p, const Pieces& q, hipStream_t s) {
   else hipLaunchKernelGGL((k_logp_piece<E, false, ENT>), grid, block, 0, s, p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  if (p.top)
-    hipLaunchKernelGGL((k_logp_join<E, true>), blocks_grid(p.T), dim3(kJoinTop),
-                       (size_t)pad_to((long long)q.S * p.top, 4) * sizeof(u64), s, p);
-  else
+  if (p.top) {
+    // (few rows: as many threads as help one; many: one a candidate)
+    const int nc = q.S * p.top;
+    int nt = kJoinTop;
+    while (p.T > 512 && nt > 64 && nt >= 2 * nc) nt /= 2;
+    hipLaunchKernelGGL((k_logp_join<E, true>), blocks_grid(p.T), dim3(nt),
+                       (size_t)pad_to(nc, 4) * sizeof(u64), s, p);
+  } else {
     hipLaunchKernelGGL((k_logp_join<E, false>), blocks_grid((p.T + 63) / 64), dim3(64), 0, s, p);
+  }
   return hipGetLastError();
 }
 template <class E>
