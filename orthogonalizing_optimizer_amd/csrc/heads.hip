@@ -25,7 +25,8 @@ struct Side {
   const void* x; const void* w; const void* dy;
   void* y;
   long long ldx, hsx, lddy, hsdy, ldy, hsy;
-  int heads, batches, units;       // batches of 64 / G heads; workgroups
+  int heads, batches, units;       // batches of a token's heads; workgroups
+  int tb, hb;                      // tokens and heads of a batch (powers of two, tb hb = 64 / G)
   long long each;                  // batches of a wave
 };
 struct HeadsP {
@@ -34,7 +35,8 @@ struct HeadsP {
   const void* pos;
   float* part;                    // gradient: one row of D floats a workgroup, or null
   long long T;
-  int D, r, G, pitch;             // pitch: angles of a wave in LDS (r / 2 rounded up to 8)
+  int D, r, G, pitch;             // pitch: angles of a token in LDS (r / 2 rounded up to 8)
+  int angles;                     // of a wave
   int pos64, wtype;
   float eps;
 };
@@ -84,27 +86,42 @@ __device__ __forceinline__ double position(const HeadsP& p, long long t) {
 // columns from LDS.  Nobody else touches the wave's part of it.
 struct Angles {
   float2* at;
-  double first;                   // the lane's frequency in turns
+  double first;                   // the frequency in turns of the lane's first pair
   __device__ Angles(const HeadsP& p, float2* lds, int wave) {
-    at = lds + wave * p.pitch;
-    first = frequency(p, threadIdx.x & 63);
+    at = lds + wave * p.angles;
+    first = frequency(p, (int)(threadIdx.x & 63) % p.pitch);
   }
   __device__ static double frequency(const HeadsP& p, int i) {
     return i < p.r / 2 ? p.freqs[i] * 0.15915494309189533577 : 0.0;
   }
-  __device__ void set(const HeadsP& p, double pos, int pair, float sign, float (&co)[8],
-                      float (&si)[8]) {
+  // tb tokens (MULTI; one otherwise), whose positions lanes 0 .. tb - 1 hold; the
+  // lane's is dt.
+  template <bool MULTI>
+  __device__ void set(const HeadsP& p, double pos, int tb, int dt, int pair, float sign,
+                      float (&co)[8], float (&si)[8]) {
     __builtin_amdgcn_wave_barrier();
-    for (int i = threadIdx.x & 63; i < p.pitch; i += 64) {
-      const double t = pos * (i < 64 ? first : frequency(p, i));
-      float2 v;
-      sincospif(2.0f * (float)(t - rint(t)), &v.y, &v.x);
-      at[i] = v;
+    const int n = (MULTI ? tb : 1) * p.pitch, lane = threadIdx.x & 63;
+    for (int i0 = 0; i0 < n; i0 += 64) {
+      const int i = i0 + lane;
+      int k = i;
+      double ps = pos;
+      if (MULTI) {
+        const int tok = min(i / p.pitch, tb - 1);
+        k = i - tok * p.pitch;
+        ps = __shfl(pos, tok, 64);
+      }
+      if (i < n) {
+        const double t = ps * (i0 == 0 ? first : frequency(p, k));
+        float2 v;
+        sincospif(2.0f * (float)(t - rint(t)), &v.y, &v.x);
+        at[i] = v;
+      }
     }
     __builtin_amdgcn_wave_barrier();
+    const float2* mine = at + (MULTI ? dt * p.pitch : 0) + pair;
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
-      const float4 v = *(const float4*)(at + pair + i);
+      const float4 v = *(const float4*)(mine + i);
       co[i] = v.x; si[i] = sign * v.y;
       co[i + 1] = v.z; si[i + 1] = sign * v.w;
     }
@@ -113,24 +130,45 @@ struct Angles {
 };
 
 // The batches of heads that a wave takes: a stretch of all of its side's, token
-// by token, as long as every other wave's.
+// by token (tb tokens by tb tokens), as long as every other wave's.
 struct Walk {
   long long left, t;
   int b;
   __device__ Walk(const HeadsP& p, const Side& s, long long wave) {
-    const long long all = p.T * s.batches, first = wave * s.each;
+    const long long all = (p.T + s.tb - 1) / s.tb * s.batches, first = wave * s.each;
     left = all - first < s.each ? all - first : s.each;
     t = first / s.batches;
     b = (int)(first - t * s.batches);
+    t *= s.tb;
   }
   __device__ bool more() const { return left > 0; }
   __device__ void next(const Side& s) {
     --left;
     if (++b < s.batches) return;
     b = 0;
-    ++t;
+    t += s.tb;
   }
 };
+
+// The lane's token and head within a batch, and whether there are such.  MULTI:
+// batches may be of several tokens (a variant of its own, because it costs the
+// others 2 to 8 %).
+template <bool MULTI>
+struct Slot {
+  int dt, h;
+  __device__ Slot(const Side& s, int slot)
+      : dt(MULTI ? slot / s.hb : 0), h(MULTI ? slot % s.hb : slot) {}
+  __device__ int head(const Side& s, const Walk& at) const { return at.b * s.hb + h; }
+  __device__ bool in(const HeadsP& p, const Side& s, const Walk& at) const {
+    return head(s, at) < s.heads && (!MULTI || at.t + dt < p.T);
+  }
+};
+template <bool MULTI>
+__device__ __forceinline__ double positions_of(const HeadsP& p, const Side& s, long long t) {
+  if (!MULTI) return position(p, t);
+  const long long u = t + ((int)(threadIdx.x & 63) & (s.tb - 1));
+  return position(p, u < p.T ? u : p.T - 1);
+}
 
 // Pairs (a, b) of the lane's columns: (v[0][i], v[1][i]), or neighbours.
 template <bool IL>
@@ -169,10 +207,10 @@ __device__ __forceinline__ float head_sum(float v, int G) {
 // ONCE: past the cache (chosen at compile time: of a branch between two loads
 // that differ in this alone the compiler makes one load).
 template <bool WHOLE, bool ONCE, class E>
-__device__ __forceinline__ void ask(const void* x, long long ld, long long hs, long long t, int h,
-                                    int heads, const Item& it, bool mine, Raw8<E> (&raw)[2]) {
-  if (WHOLE) {           // no branches between the loads: lanes without a head read the last one's
-    const E* row = (const E*)x + t * ld + min(h, heads - 1) * hs;
+__device__ __forceinline__ void ask(const void* x, long long ld, long long hs, long long t, int dt,
+                                    int h, const Item& it, bool mine, Raw8<E> (&raw)[2]) {
+  if (WHOLE) {           // no branches between the loads: lanes without a head read the first one's
+    const E* row = (const E*)x + t * ld + (mine ? dt * ld + h * hs : 0);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const E* at = row + it.base[k] + it.c[k];
@@ -182,7 +220,7 @@ __device__ __forceinline__ void ask(const void* x, long long ld, long long hs, l
     return;
   }
   if (!mine) return;
-  const E* row = (const E*)x + t * ld + h * hs;
+  const E* row = (const E*)x + t * ld + (dt * ld + h * hs);
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     if (ONCE) raw[k] = fetch8_once(row + it.base[k], it.c[k], it.lim[k]);
@@ -206,9 +244,9 @@ __device__ __forceinline__ void take(const Raw8<E> (&raw)[2], const Item& it, bo
   }
 }
 template <bool WHOLE, class E>
-__device__ __forceinline__ void put(void* y, long long ld, long long hs, long long t, int h,
-                                    const Item& it, const float (&v)[2][8]) {
-  E* row = (E*)y + t * ld + h * hs;
+__device__ __forceinline__ void put(void* y, long long ld, long long hs, long long t, int dt,
+                                    int h, const Item& it, const float (&v)[2][8]) {
+  E* row = (E*)y + t * ld + (dt * ld + h * hs);
 #pragma unroll
   for (int k = 0; k < 2; ++k)
     if (WHOLE) {
@@ -227,25 +265,26 @@ __device__ __forceinline__ float head_rstd(const float (&v)[2][8], int G, int D,
   return 1.0f / sqrtf(head_sum(ss, G) / (float)D + eps);
 }
 
-template <class E, bool IL, bool WHOLE, bool ONCE>
+template <class E, bool IL, bool WHOLE, bool ONCE, bool MULTI>
 __global__ __launch_bounds__(256) void k_heads(HeadsP p) {
   extern __shared__ __attribute__((aligned(16))) float2 turns[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int G = p.G, per = 64 / G, j = lane & (G - 1), slot = lane / G;
+  const int G = p.G, j = lane & (G - 1);
   const bool isk = (int)blockIdx.x >= p.s[0].units;
   const Side& s = p.s[isk];
+  const Slot<MULTI> slot(s, lane / G);
   Walk at(p, s, ((int)blockIdx.x - (isk ? p.s[0].units : 0)) * 4LL + wave);
   if (!at.more()) return;
   const Item it = my_item<IL>(j, p.D, p.r);
   Raw8<E> raw[2];
-  bool mine = it.on && at.b * per + slot < s.heads;
-  ask<WHOLE, ONCE>(s.x, s.ldx, s.hsx, at.t, at.b * per + slot, s.heads, it, mine, raw);
-  double pos = position(p, at.t);
+  bool mine = it.on && slot.in(p, s, at);
+  ask<WHOLE, ONCE>(s.x, s.ldx, s.hsx, at.t, slot.dt, slot.head(s, at), it, mine, raw);
+  double pos = positions_of<MULTI>(p, s, at.t);
   float w[2][8], co[8], si[8];
   load_weight<E>(p, s, it, w);
   Angles ang(p, turns, wave);
   for (bool fresh = true;;) {
-    if (fresh) ang.set(p, pos, it.rot ? 8 * j : 0, 1.0f, co, si);
+    if (fresh) ang.template set<MULTI>(p, pos, s.tb, slot.dt, it.rot ? 8 * j : 0, 1.0f, co, si);
     float v[2][8];
     take<WHOLE>(raw, it, mine, v);
     // the next batch's columns, and the next token's position, on their way
@@ -254,16 +293,16 @@ __global__ __launch_bounds__(256) void k_heads(HeadsP p) {
     at.next(s);
     const bool go = at.more();
     if (go) {
-      mine = it.on && at.b * per + slot < s.heads;
-      ask<WHOLE, ONCE>(s.x, s.ldx, s.hsx, at.t, at.b * per + slot, s.heads, it, mine, raw);
+      mine = it.on && slot.in(p, s, at);
+      ask<WHOLE, ONCE>(s.x, s.ldx, s.hsx, at.t, slot.dt, slot.head(s, at), it, mine, raw);
       fresh = at.t != now.t;
-      if (fresh) pos = position(p, at.t);
+      if (fresh) pos = positions_of<MULTI>(p, s, at.t);
     }
     const float rs = head_rstd(v, G, p.D, p.eps);
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i / 8][i % 8] *= rs * w[i / 8][i % 8];
     rotate<IL>(v, co, si, it.rot);
-    if (own) put<WHOLE, E>(s.y, s.ldy, s.hsy, now.t, now.b * per + slot, it, v);
+    if (own) put<WHOLE, E>(s.y, s.ldy, s.hsy, now.t, slot.dt, slot.head(s, now), it, v);
     if (!go) return;
   }
 }
@@ -271,14 +310,15 @@ __global__ __launch_bounds__(256) void k_heads(HeadsP p) {
 // The weights' gradients: a lane adds up its columns over its tokens and
 // heads, the lanes of equal columns and the workgroup's waves are joined at
 // the end, and the workgroups' rows by k_heads_join, each in a fixed order.
-template <class E, bool IL, bool WHOLE, bool ONCE>
+template <class E, bool IL, bool WHOLE, bool ONCE, bool MULTI>
 __global__ __launch_bounds__(256) void k_heads_grad(HeadsP p) {
   extern __shared__ __attribute__((aligned(16))) float2 turns[];
-  float* sh = (float*)turns + 8 * p.pitch;             // 3 waves x D
+  float* sh = (float*)turns + 8 * p.angles;             // 3 waves x D
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int G = p.G, per = 64 / G, j = lane & (G - 1), slot = lane / G;
+  const int G = p.G, j = lane & (G - 1);
   const bool isk = (int)blockIdx.x >= p.s[0].units;
   const Side& s = p.s[isk];
+  const Slot<MULTI> slot(s, lane / G);
   Walk at(p, s, ((int)blockIdx.x - (isk ? p.s[0].units : 0)) * 4LL + wave);
   const Item it = my_item<IL>(j, p.D, p.r);
   float dw[2][8];
@@ -286,15 +326,15 @@ __global__ __launch_bounds__(256) void k_heads_grad(HeadsP p) {
   for (int i = 0; i < 16; ++i) dw[i / 8][i % 8] = 0.0f;
   if (at.more()) {
     Raw8<E> rx[2], ry[2];
-    bool mine = it.on && at.b * per + slot < s.heads;
-    ask<WHOLE, ONCE>(s.x, s.ldx, s.hsx, at.t, at.b * per + slot, s.heads, it, mine, rx);
-    ask<WHOLE, ONCE>(s.dy, s.lddy, s.hsdy, at.t, at.b * per + slot, s.heads, it, mine, ry);
-    double pos = position(p, at.t);
+    bool mine = it.on && slot.in(p, s, at);
+    ask<WHOLE, ONCE>(s.x, s.ldx, s.hsx, at.t, slot.dt, slot.head(s, at), it, mine, rx);
+    ask<WHOLE, ONCE>(s.dy, s.lddy, s.hsdy, at.t, slot.dt, slot.head(s, at), it, mine, ry);
+    double pos = positions_of<MULTI>(p, s, at.t);
     float w[2][8], co[8], si[8];
     load_weight<E>(p, s, it, w);
     Angles ang(p, turns, wave);
     for (bool fresh = true;;) {
-      if (fresh) ang.set(p, pos, it.rot ? 8 * j : 0, -1.0f, co, si);
+      if (fresh) ang.template set<MULTI>(p, pos, s.tb, slot.dt, it.rot ? 8 * j : 0, -1.0f, co, si);
       float x[2][8], u[2][8];
       take<WHOLE>(rx, it, mine, x);
       take<WHOLE>(ry, it, mine, u);
@@ -303,11 +343,11 @@ __global__ __launch_bounds__(256) void k_heads_grad(HeadsP p) {
       at.next(s);
       const bool go = at.more();
       if (go) {
-        mine = it.on && at.b * per + slot < s.heads;
-        ask<WHOLE, ONCE>(s.x, s.ldx, s.hsx, at.t, at.b * per + slot, s.heads, it, mine, rx);
-        ask<WHOLE, ONCE>(s.dy, s.lddy, s.hsdy, at.t, at.b * per + slot, s.heads, it, mine, ry);
+        mine = it.on && slot.in(p, s, at);
+        ask<WHOLE, ONCE>(s.x, s.ldx, s.hsx, at.t, slot.dt, slot.head(s, at), it, mine, rx);
+        ask<WHOLE, ONCE>(s.dy, s.lddy, s.hsdy, at.t, slot.dt, slot.head(s, at), it, mine, ry);
         fresh = at.t != now.t;
-        if (fresh) pos = position(p, at.t);
+        if (fresh) pos = positions_of<MULTI>(p, s, at.t);
       }
       const float rs = head_rstd(x, G, p.D, p.eps);
       rotate<IL>(u, co, si, it.rot);
@@ -326,7 +366,7 @@ __global__ __launch_bounds__(256) void k_heads_grad(HeadsP p) {
 #pragma unroll
         for (int i = 0; i < 16; ++i)
           u[i / 8][i % 8] = rs * __builtin_fmaf(-x[i / 8][i % 8], c, u[i / 8][i % 8]);
-        put<WHOLE, E>(s.y, s.ldy, s.hsy, now.t, now.b * per + slot, it, u);
+        put<WHOLE, E>(s.y, s.ldy, s.hsy, now.t, slot.dt, slot.head(s, now), it, u);
       }
       if (!go) break;
     }
@@ -394,8 +434,13 @@ int pieces(int D, int r, bool il) {
 // the resident waves, 36 with as many) and 57 backwards (4.4 TB/s; a tenth more
 // by whole tokens; with 4 waves a SIMD that read their weight from LDS 3 % less:
 // not kept).
+//
+// Where a token has at most half as many heads as a batch, a batch takes several
+// tokens: 100000 tokens of 4 + 1 heads of 64 take 39 us and 67 backwards, 95 and
+// 171 with a token a batch.
+constexpr int kAngles = 512;        // a wave's in LDS, at most (one token's may be 512)
 struct Split {
-  int G, batches[2], units[2];
+  int G, pitch, angles, batches[2], units[2], tb[2], hb[2];
   long long each[2];
 };
 Split split_heads(long long T, int hq, int hk, int D, int r, bool il, bool grad) {
@@ -405,14 +450,23 @@ Split split_heads(long long T, int hq, int hk, int D, int r, bool il, bool grad)
   const int per = 64 / q.G, heads[2] = {hq, hk};
   const bool whole = r % 16 == 0 && D % 16 == 0;
   const int units = 256 * (grad ? 3 : whole ? 10 : 4);
-  for (int i = 0; i < 2; ++i) q.batches[i] = (heads[i] + per - 1) / per;
+  q.pitch = r ? (r / 2 + 7) / 8 * 8 : 8;
+  q.angles = q.pitch;
+  long long all[2];
   for (int i = 0; i < 2; ++i) {
-    const long long all = T * q.batches[i];
-    if (all == 0) continue;
-    const long long share = (long long)units * q.batches[i] / (q.batches[0] + q.batches[1]);
+    q.tb[i] = 1;
+    while (heads[i] * q.tb[i] * 2 <= per && heads[i] > 0 && q.pitch * q.tb[i] * 2 <= kAngles) q.tb[i] *= 2;
+    q.hb[i] = per / q.tb[i];
+    q.batches[i] = (heads[i] + q.hb[i] - 1) / q.hb[i];
+    if (q.pitch * q.tb[i] > q.angles) q.angles = q.pitch * q.tb[i];
+    all[i] = (T + q.tb[i] - 1) / q.tb[i] * q.batches[i];
+  }
+  for (int i = 0; i < 2; ++i) {
+    if (all[i] == 0) continue;
+    const long long share = (long long)((double)units * all[i] / (all[0] + all[1]));
     const long long waves = share < 1 ? 4 : share * 4;
-    q.each[i] = (all + waves - 1) / waves;
-    const long long used = (all + q.each[i] - 1) / q.each[i];
+    q.each[i] = (all[i] + waves - 1) / waves;
+    const long long used = (all[i] + q.each[i] - 1) / q.each[i];
     q.units[i] = (int)((used + 3) / 4);
   }
   return q;
@@ -463,18 +517,27 @@ HeadsP describe(const dion3_heads* q, const dion3_heads* k, const Split& sp, con
     if (both[i]) {
       const dion3_heads& s = *both[i];
       p.s[i] = {s.X, s.w, s.dY, s.Y, s.ldx, s.hsx, s.lddy, s.hsdy, s.ldy, s.hsy, s.heads,
-                sp.batches[i], sp.units[i], sp.each[i]};
+                sp.batches[i], sp.units[i], sp.tb[i], sp.hb[i], sp.each[i]};
     }
   p.freqs = freqs; p.pos = pos; p.T = T;
-  p.D = D; p.r = r; p.G = sp.G; p.pitch = r ? (r / 2 + 7) / 8 * 8 : 8;
+  p.D = D; p.r = r; p.G = sp.G; p.pitch = sp.pitch; p.angles = sp.angles;
   p.pos64 = pos_bits == 64; p.wtype = wtype; p.eps = eps;
   return p;
 }
 
+template <class E, bool GRAD, bool IL, bool WHOLE, bool ONCE, bool MULTI>
+void launch_heads_m(const HeadsP& p, int units, size_t lds, hipStream_t s) {
+  if (GRAD)
+    hipLaunchKernelGGL((k_heads_grad<E, IL, WHOLE, ONCE, MULTI>), dim3(units), dim3(256), lds, s, p);
+  else
+    hipLaunchKernelGGL((k_heads<E, IL, WHOLE, ONCE, MULTI>), dim3(units), dim3(256), lds, s, p);
+}
 template <class E, bool GRAD, bool IL, bool WHOLE, bool ONCE>
 void launch_heads_t(const HeadsP& p, int units, size_t lds, hipStream_t s) {
-  if (GRAD) hipLaunchKernelGGL((k_heads_grad<E, IL, WHOLE, ONCE>), dim3(units), dim3(256), lds, s, p);
-  else hipLaunchKernelGGL((k_heads<E, IL, WHOLE, ONCE>), dim3(units), dim3(256), lds, s, p);
+  if (p.s[0].tb > 1 || p.s[1].tb > 1)
+    launch_heads_m<E, GRAD, IL, WHOLE, ONCE, true>(p, units, lds, s);
+  else
+    launch_heads_m<E, GRAD, IL, WHOLE, ONCE, false>(p, units, lds, s);
 }
 template <class E, bool GRAD, bool IL, bool WHOLE>
 void launch_heads_w(const HeadsP& p, int units, size_t lds, hipStream_t s) {
@@ -518,7 +581,7 @@ dion3_status dion3_qk_norm_rope(const dion3_heads* q, const dion3_heads* k, cons
   const Split sp = split_heads(T, q->heads, k ? k->heads : 0, D, r, interleaved, false);
   const HeadsP p = describe(q, k, sp, freqs, pos, pos_bits, T, D, r, eps, wtype);
   TraceScope ts("qk_norm_rope", 0.0, 4.0 * T * D * (q->heads + (k ? k->heads : 0)), s);
-  const size_t lds = (size_t)p.pitch * 4 * 8;
+  const size_t lds = (size_t)p.angles * 4 * 8;
   if (dtype == DION3_BF16) launch_heads<bf16, false>(p, units_of(sp), lds, interleaved, s);
   else launch_heads<f16, false>(p, units_of(sp), lds, interleaved, s);
   HIP_TRY(hipGetLastError());
@@ -551,7 +614,7 @@ dion3_status dion3_qk_norm_rope_grad(const dion3_heads* q, const dion3_heads* k,
     HeadsP p = describe(q, k, sp, freqs, pos, pos_bits, T, D, r, eps, wtype);
     p.part = dw ? (float*)ws : nullptr;
     TraceScope ts("qk_norm_rope_grad", 0.0, 6.0 * T * D * (q->heads + (k ? k->heads : 0)), s);
-    const size_t lds = (size_t)p.pitch * 4 * 8 + (dw ? (size_t)3 * D * 4 : 0);
+    const size_t lds = (size_t)p.angles * 4 * 8 + (dw ? (size_t)3 * D * 4 : 0);
     if (dtype == DION3_BF16) launch_heads<bf16, true>(p, units_of(sp), lds, interleaved, s);
     else launch_heads<f16, true>(p, units_of(sp), lds, interleaved, s);
     HIP_TRY(hipGetLastError());
