@@ -4,7 +4,8 @@ import pytest
 import torch
 
 import orthogonalizing_optimizer_amd as d3
-from tests.layer_ref import EPS32
+from tests import test_gpu_embedding as emb
+from tests.layer_ref import EPS32, close
 
 pytestmark = pytest.mark.gpu
 BF, FP, F32 = torch.bfloat16, torch.float16, torch.float32
@@ -114,3 +115,15 @@ def test_rows_far_apart():
     dy = rnd(g, 5, S, n, dtype=BF)[:, 0]
     grad = d3.embedding_grad(tokens, dy.contiguous(), 6)
     assert torch.equal(d3.embedding_grad(tokens, dy, 6, out=w), grad)
+
+
+@pytest.mark.parametrize("kind", ["uniform", "frequent", "padded", "runs"])
+@pytest.mark.parametrize("T,n,m", [(262144, 300, 4), (262145, 300, 4), (300001, 70001, 9)])
+def test_embedding_gradient_of_many_tokens(T, n, m, kind):
+    """Around the number of tokens from which the digits' scan is a launch."""
+    g = torch.Generator().manual_seed(T + n)
+    t, dy = emb.text(g, T, n, kind), emb.rnd(g, T, m, dtype=BF)
+    want, off = emb.grad(t, dy, n, 1.0)
+    got = d3.embedding_grad(t.cuda(), dy.cuda(), n)
+    close(got, want, off, kind)
+    assert torch.equal(d3.embedding_grad(t.int().cuda(), dy.cuda(), n), got)
