@@ -45,11 +45,20 @@ struct HeadsP {
 // it lies in (base, length) and its place there.  Runs: the two halves of the
 // rotated columns, or all of them where pairs are neighbours; the columns past
 // them.
+//
+// How chunks fit their runs.  WHOLE: no chunk ends early (the checks take 30
+// registers).  LAPPED: every run has at least 8 columns, and a chunk that would
+// end behind its run lies over the one before instead; what lies over is
+// computed and written twice, with the same bits, and left out of sums (8192
+// tokens of 16 + 16 heads of 96, 24 turned: 25 us, 34 with ragged chunks;
+// backwards 48 and 76).  RAGGED: chunks are cut off at the end of the run.
+enum Fit { RAGGED, LAPPED, WHOLE };
 struct Item {
   int base[2], c[2], lim[2];
+  int dup[2];                      // LAPPED: columns at its start that are not the chunk's own
   bool on, rot;
 };
-template <bool IL>
+template <bool IL, int FIT>
 __device__ __forceinline__ Item my_item(int j, int D, int r) {
   Item it;
   const int half = r / 2, nr = IL ? (r + 15) / 16 : (half + 7) / 8;
@@ -72,6 +81,16 @@ __device__ __forceinline__ Item my_item(int j, int D, int r) {
       it.lim[k] = D - r;
     }
     if (!it.on) it.base[0] = it.base[1] = it.c[0] = it.c[1] = 0;      // (a place inside the head)
+  }
+  if (FIT == LAPPED && it.on) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int c = min(it.c[k], it.lim[k] - 8);
+      it.dup[k] = min(it.c[k] - c, 8);
+      it.c[k] = c;
+    }
+  } else {
+    it.dup[0] = it.dup[1] = 0;
   }
   return it;
 }
@@ -96,8 +115,9 @@ struct Angles {
   }
   // tb tokens (MULTI; one otherwise), whose positions lanes 0 .. tb - 1 hold; the
   // lane's is dt.
-  template <bool MULTI>
-  __device__ void set(const HeadsP& p, double pos, int tb, int dt, int pair, float sign,
+  // pair: of the lane's first four pairs, and of the others.
+  template <bool MULTI, int FIT>
+  __device__ void set(const HeadsP& p, double pos, int tb, int dt, int pair, int pair4, float sign,
                       float (&co)[8], float (&si)[8]) {
     __builtin_amdgcn_wave_barrier();
     const int n = (MULTI ? tb : 1) * p.pitch, lane = threadIdx.x & 63;
@@ -118,12 +138,20 @@ struct Angles {
       }
     }
     __builtin_amdgcn_wave_barrier();
-    const float2* mine = at + (MULTI ? dt * p.pitch : 0) + pair;
+    const float2* mine = at + (MULTI ? dt * p.pitch : 0);
+    if (FIT == LAPPED) {
 #pragma unroll
-    for (int i = 0; i < 8; i += 2) {
-      const float4 v = *(const float4*)(mine + i);
-      co[i] = v.x; si[i] = sign * v.y;
-      co[i + 1] = v.z; si[i + 1] = sign * v.w;
+      for (int i = 0; i < 8; ++i) {
+        const float2 v = mine[i < 4 ? pair + i : pair4 + i - 4];
+        co[i] = v.x; si[i] = sign * v.y;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) {
+        const float4 v = *(const float4*)(mine + pair + i);
+        co[i] = v.x; si[i] = sign * v.y;
+        co[i + 1] = v.z; si[i + 1] = sign * v.w;
+      }
     }
     __builtin_amdgcn_wave_barrier();
   }
@@ -202,14 +230,13 @@ __device__ __forceinline__ float head_sum(float v, int G) {
 }
 
 // The lane's 16 columns of head h of token t, asked for and as floats (zeros
-// where the lane has none).  WHOLE: the turned columns and the others fill all
-// pieces, so no chunk ends early (the checks take 30 registers).
+// where the lane has none).
 // ONCE: past the cache (chosen at compile time: of a branch between two loads
 // that differ in this alone the compiler makes one load).
-template <bool WHOLE, bool ONCE, class E>
+template <int FIT, bool ONCE, class E>
 __device__ __forceinline__ void ask(const void* x, long long ld, long long hs, long long t, int dt,
                                     int h, const Item& it, bool mine, Raw8<E> (&raw)[2]) {
-  if (WHOLE) {           // no branches between the loads: lanes without a head read the first one's
+  if (FIT != RAGGED) {   // no branches between the loads: lanes without a head read the first one's
     const E* row = (const E*)x + t * ld + (mine ? dt * ld + h * hs : 0);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -222,17 +249,14 @@ __device__ __forceinline__ void ask(const void* x, long long ld, long long hs, l
   if (!mine) return;
   const E* row = (const E*)x + t * ld + (dt * ld + h * hs);
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    if (ONCE) raw[k] = fetch8_once(row + it.base[k], it.c[k], it.lim[k]);
-    else raw[k] = fetch8(row + it.base[k], it.c[k], it.lim[k]);
-  }
+  for (int k = 0; k < 2; ++k) raw[k] = fetch8(row + it.base[k], it.c[k], it.lim[k]);
 }
-template <bool WHOLE, class E>
+template <int FIT, class E>
 __device__ __forceinline__ void take(const Raw8<E> (&raw)[2], const Item& it, bool mine,
                                      float (&v)[2][8]) {
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    if (WHOLE) {
+    if (FIT != RAGGED) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[k][e] = mine ? to_f32((E)raw[k].v[e]) : 0.0f;
     } else if (mine) {
@@ -243,13 +267,13 @@ __device__ __forceinline__ void take(const Raw8<E> (&raw)[2], const Item& it, bo
     }
   }
 }
-template <bool WHOLE, class E>
+template <int FIT, class E>
 __device__ __forceinline__ void put(void* y, long long ld, long long hs, long long t, int dt,
                                     int h, const Item& it, const float (&v)[2][8]) {
   E* row = (E*)y + t * ld + (dt * ld + h * hs);
 #pragma unroll
   for (int k = 0; k < 2; ++k)
-    if (WHOLE) {
+    if (FIT != RAGGED) {
       Raw8<E> r;
 #pragma unroll
       for (int e = 0; e < 8; ++e) r.v[e] = (E)v[k][e];
@@ -258,14 +282,24 @@ __device__ __forceinline__ void put(void* y, long long ld, long long hs, long lo
       store8(row + it.base[k], it.c[k], it.lim[k], v[k]);
     }
 }
-__device__ __forceinline__ float head_rstd(const float (&v)[2][8], int G, int D, float eps) {
+// v as far as it is the lane's own column.
+template <int FIT>
+__device__ __forceinline__ float own_column(const Item& it, int k, int e, float v) {
+  return FIT != LAPPED || e >= it.dup[k] ? v : 0.0f;
+}
+template <int FIT>
+__device__ __forceinline__ float head_rstd(const Item& it, const float (&v)[2][8], int G, int D,
+                                           float eps) {
   float ss = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) ss = __builtin_fmaf(v[i / 8][i % 8], v[i / 8][i % 8], ss);
+  for (int i = 0; i < 16; ++i) {
+    const float x = own_column<FIT>(it, i / 8, i % 8, v[i / 8][i % 8]);
+    ss = __builtin_fmaf(x, x, ss);
+  }
   return 1.0f / sqrtf(head_sum(ss, G) / (float)D + eps);
 }
 
-template <class E, bool IL, bool WHOLE, bool ONCE, bool MULTI>
+template <class E, bool IL, int FIT, bool ONCE, bool MULTI>
 __global__ __launch_bounds__(256) void k_heads(HeadsP p) {
   extern __shared__ __attribute__((aligned(16))) float2 turns[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -275,18 +309,20 @@ __global__ __launch_bounds__(256) void k_heads(HeadsP p) {
   const Slot<MULTI> slot(s, lane / G);
   Walk at(p, s, ((int)blockIdx.x - (isk ? p.s[0].units : 0)) * 4LL + wave);
   if (!at.more()) return;
-  const Item it = my_item<IL>(j, p.D, p.r);
+  const Item it = my_item<IL, FIT>(j, p.D, p.r);
+  const int pair = !it.rot ? 0 : FIT != LAPPED ? 8 * j : IL ? it.c[0] / 2 : it.c[0];
+  const int pair4 = !it.rot ? 0 : IL ? it.c[1] / 2 : it.c[0] + 4;      // (LAPPED)
   Raw8<E> raw[2];
   bool mine = it.on && slot.in(p, s, at);
-  ask<WHOLE, ONCE>(s.x, s.ldx, s.hsx, at.t, slot.dt, slot.head(s, at), it, mine, raw);
+  ask<FIT, ONCE>(s.x, s.ldx, s.hsx, at.t, slot.dt, slot.head(s, at), it, mine, raw);
   double pos = positions_of<MULTI>(p, s, at.t);
   float w[2][8], co[8], si[8];
   load_weight<E>(p, s, it, w);
   Angles ang(p, turns, wave);
   for (bool fresh = true;;) {
-    if (fresh) ang.template set<MULTI>(p, pos, s.tb, slot.dt, it.rot ? 8 * j : 0, 1.0f, co, si);
+    if (fresh) ang.template set<MULTI, FIT>(p, pos, s.tb, slot.dt, pair, pair4, 1.0f, co, si);
     float v[2][8];
-    take<WHOLE>(raw, it, mine, v);
+    take<FIT>(raw, it, mine, v);
     // the next batch's columns, and the next token's position, on their way
     const Walk now = at;
     const bool own = mine;
@@ -294,15 +330,15 @@ __global__ __launch_bounds__(256) void k_heads(HeadsP p) {
     const bool go = at.more();
     if (go) {
       mine = it.on && slot.in(p, s, at);
-      ask<WHOLE, ONCE>(s.x, s.ldx, s.hsx, at.t, slot.dt, slot.head(s, at), it, mine, raw);
+      ask<FIT, ONCE>(s.x, s.ldx, s.hsx, at.t, slot.dt, slot.head(s, at), it, mine, raw);
       fresh = at.t != now.t;
       if (fresh) pos = positions_of<MULTI>(p, s, at.t);
     }
-    const float rs = head_rstd(v, G, p.D, p.eps);
+    const float rs = head_rstd<FIT>(it, v, G, p.D, p.eps);
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i / 8][i % 8] *= rs * w[i / 8][i % 8];
     rotate<IL>(v, co, si, it.rot);
-    if (own) put<WHOLE, E>(s.y, s.ldy, s.hsy, now.t, slot.dt, slot.head(s, now), it, v);
+    if (own) put<FIT, E>(s.y, s.ldy, s.hsy, now.t, slot.dt, slot.head(s, now), it, v);
     if (!go) return;
   }
 }
@@ -310,7 +346,7 @@ __global__ __launch_bounds__(256) void k_heads(HeadsP p) {
 // The weights' gradients: a lane adds up its columns over its tokens and
 // heads, the lanes of equal columns and the workgroup's waves are joined at
 // the end, and the workgroups' rows by k_heads_join, each in a fixed order.
-template <class E, bool IL, bool WHOLE, bool ONCE, bool MULTI>
+template <class E, bool IL, int FIT, bool ONCE, bool MULTI>
 __global__ __launch_bounds__(256) void k_heads_grad(HeadsP p) {
   extern __shared__ __attribute__((aligned(16))) float2 turns[];
   float* sh = (float*)turns + 8 * p.angles;             // 3 waves x D
@@ -320,36 +356,38 @@ __global__ __launch_bounds__(256) void k_heads_grad(HeadsP p) {
   const Side& s = p.s[isk];
   const Slot<MULTI> slot(s, lane / G);
   Walk at(p, s, ((int)blockIdx.x - (isk ? p.s[0].units : 0)) * 4LL + wave);
-  const Item it = my_item<IL>(j, p.D, p.r);
+  const Item it = my_item<IL, FIT>(j, p.D, p.r);
+  const int pair = !it.rot ? 0 : FIT != LAPPED ? 8 * j : IL ? it.c[0] / 2 : it.c[0];
+  const int pair4 = !it.rot ? 0 : IL ? it.c[1] / 2 : it.c[0] + 4;      // (LAPPED)
   float dw[2][8];
 #pragma unroll
   for (int i = 0; i < 16; ++i) dw[i / 8][i % 8] = 0.0f;
   if (at.more()) {
     Raw8<E> rx[2], ry[2];
     bool mine = it.on && slot.in(p, s, at);
-    ask<WHOLE, ONCE>(s.x, s.ldx, s.hsx, at.t, slot.dt, slot.head(s, at), it, mine, rx);
-    ask<WHOLE, ONCE>(s.dy, s.lddy, s.hsdy, at.t, slot.dt, slot.head(s, at), it, mine, ry);
+    ask<FIT, ONCE>(s.x, s.ldx, s.hsx, at.t, slot.dt, slot.head(s, at), it, mine, rx);
+    ask<FIT, ONCE>(s.dy, s.lddy, s.hsdy, at.t, slot.dt, slot.head(s, at), it, mine, ry);
     double pos = positions_of<MULTI>(p, s, at.t);
     float w[2][8], co[8], si[8];
     load_weight<E>(p, s, it, w);
     Angles ang(p, turns, wave);
     for (bool fresh = true;;) {
-      if (fresh) ang.template set<MULTI>(p, pos, s.tb, slot.dt, it.rot ? 8 * j : 0, -1.0f, co, si);
+      if (fresh) ang.template set<MULTI, FIT>(p, pos, s.tb, slot.dt, pair, pair4, -1.0f, co, si);
       float x[2][8], u[2][8];
-      take<WHOLE>(rx, it, mine, x);
-      take<WHOLE>(ry, it, mine, u);
+      take<FIT>(rx, it, mine, x);
+      take<FIT>(ry, it, mine, u);
       const Walk now = at;
       const bool own = mine;
       at.next(s);
       const bool go = at.more();
       if (go) {
         mine = it.on && slot.in(p, s, at);
-        ask<WHOLE, ONCE>(s.x, s.ldx, s.hsx, at.t, slot.dt, slot.head(s, at), it, mine, rx);
-        ask<WHOLE, ONCE>(s.dy, s.lddy, s.hsdy, at.t, slot.dt, slot.head(s, at), it, mine, ry);
+        ask<FIT, ONCE>(s.x, s.ldx, s.hsx, at.t, slot.dt, slot.head(s, at), it, mine, rx);
+        ask<FIT, ONCE>(s.dy, s.lddy, s.hsdy, at.t, slot.dt, slot.head(s, at), it, mine, ry);
         fresh = at.t != now.t;
         if (fresh) pos = positions_of<MULTI>(p, s, at.t);
       }
-      const float rs = head_rstd(x, G, p.D, p.eps);
+      const float rs = head_rstd<FIT>(it, x, G, p.D, p.eps);
       rotate<IL>(u, co, si, it.rot);
       float c = 0.0f;
 #pragma unroll
@@ -359,14 +397,14 @@ __global__ __launch_bounds__(256) void k_heads_grad(HeadsP p) {
           x[k][e] *= rs;
           dw[k][e] = __builtin_fmaf(u[k][e], x[k][e], dw[k][e]);
           u[k][e] *= w[k][e];
-          c = __builtin_fmaf(u[k][e], x[k][e], c);
+          c = __builtin_fmaf(u[k][e], own_column<FIT>(it, k, e, x[k][e]), c);
         }
       c = head_sum(c, G) / (float)p.D;
       if (own && s.y) {
 #pragma unroll
         for (int i = 0; i < 16; ++i)
           u[i / 8][i % 8] = rs * __builtin_fmaf(-x[i / 8][i % 8], c, u[i / 8][i % 8]);
-        put<WHOLE, E>(s.y, s.ldy, s.hsy, now.t, slot.dt, slot.head(s, now), it, u);
+        put<FIT, E>(s.y, s.ldy, s.hsy, now.t, slot.dt, slot.head(s, now), it, u);
       }
       if (!go) break;
     }
@@ -376,12 +414,18 @@ __global__ __launch_bounds__(256) void k_heads_grad(HeadsP p) {
   for (int i = 0; i < 16; ++i)
     for (int o = G; o < 64; o <<= 1) dw[i / 8][i % 8] += __shfl_xor(dw[i / 8][i % 8], o, 64);
   const bool mine = it.on && lane < G;                 // one lane for each column
-  if (mine && wave > 0) {
+  auto put_sums = [&](float* row) {
 #pragma unroll
     for (int k = 0; k < 2; ++k)
-      if (it.c[k] < it.lim[k])
-        store8(sh + (wave - 1) * p.D + it.base[k], it.c[k], it.lim[k], dw[k]);
-  }
+      if (FIT == LAPPED) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (e >= it.dup[k]) row[it.base[k] + it.c[k] + e] = dw[k][e];
+      } else if (it.c[k] < it.lim[k]) {
+        store8(row + it.base[k], it.c[k], it.lim[k], dw[k]);
+      }
+  };
+  if (mine && wave > 0) put_sums(sh + (wave - 1) * p.D);
   __syncthreads();
   if (wave > 0 || !mine) return;
   for (int o = 0; o < 3; ++o)
@@ -392,10 +436,7 @@ __global__ __launch_bounds__(256) void k_heads_grad(HeadsP p) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) dw[k][e] += v[e];
     }
-#pragma unroll
-  for (int k = 0; k < 2; ++k)
-    if (it.c[k] < it.lim[k])
-      store8(p.part + (long long)blockIdx.x * p.D + it.base[k], it.c[k], it.lim[k], dw[k]);
+  put_sums(p.part + (long long)blockIdx.x * p.D);
 }
 
 // dw[side][c] = the sum over the side's workgroups: 16 columns a workgroup, 64
@@ -427,6 +468,11 @@ constexpr long long kMaxStride = 1LL << 38;
 int pieces(int D, int r, bool il) {
   return (il ? (r + 15) / 16 : (r / 2 + 7) / 8) + (D - r + 15) / 16;
 }
+Fit fit_of(int D, int r, bool il) {
+  if (r % 16 == 0 && D % 16 == 0) return WHOLE;
+  const int turned = il ? r : r / 2, rest = D - r;
+  return (turned == 0 || turned >= 8) && (rest == 0 || rest >= 8) ? LAPPED : RAGGED;
+}
 // A head takes the power of two of lanes that holds its columns, 16 a lane.
 // As many waves as stay resident (a few more would run after all others) are
 // shared out between queries and keys by their batches, and each takes equally
@@ -448,8 +494,7 @@ Split split_heads(long long T, int hq, int hk, int D, int r, bool il, bool grad)
   q.G = 1;
   while (q.G < pieces(D, r, il)) q.G *= 2;
   const int per = 64 / q.G, heads[2] = {hq, hk};
-  const bool whole = r % 16 == 0 && D % 16 == 0;
-  const int units = 256 * (grad ? 3 : whole ? 10 : 4);
+  const int units = 256 * (grad ? 3 : fit_of(D, r, il) != RAGGED ? 10 : 4);
   q.pitch = r ? (r / 2 + 7) / 8 * 8 : 8;
   q.angles = q.pitch;
   long long all[2];
@@ -525,21 +570,21 @@ HeadsP describe(const dion3_heads* q, const dion3_heads* k, const Split& sp, con
   return p;
 }
 
-template <class E, bool GRAD, bool IL, bool WHOLE, bool ONCE, bool MULTI>
+template <class E, bool GRAD, bool IL, int FIT, bool ONCE, bool MULTI>
 void launch_heads_m(const HeadsP& p, int units, size_t lds, hipStream_t s) {
   if (GRAD)
-    hipLaunchKernelGGL((k_heads_grad<E, IL, WHOLE, ONCE, MULTI>), dim3(units), dim3(256), lds, s, p);
+    hipLaunchKernelGGL((k_heads_grad<E, IL, FIT, ONCE, MULTI>), dim3(units), dim3(256), lds, s, p);
   else
-    hipLaunchKernelGGL((k_heads<E, IL, WHOLE, ONCE, MULTI>), dim3(units), dim3(256), lds, s, p);
+    hipLaunchKernelGGL((k_heads<E, IL, FIT, ONCE, MULTI>), dim3(units), dim3(256), lds, s, p);
 }
-template <class E, bool GRAD, bool IL, bool WHOLE, bool ONCE>
+template <class E, bool GRAD, bool IL, int FIT, bool ONCE>
 void launch_heads_t(const HeadsP& p, int units, size_t lds, hipStream_t s) {
   if (p.s[0].tb > 1 || p.s[1].tb > 1)
-    launch_heads_m<E, GRAD, IL, WHOLE, ONCE, true>(p, units, lds, s);
+    launch_heads_m<E, GRAD, IL, FIT, ONCE, true>(p, units, lds, s);
   else
-    launch_heads_m<E, GRAD, IL, WHOLE, ONCE, false>(p, units, lds, s);
+    launch_heads_m<E, GRAD, IL, FIT, ONCE, false>(p, units, lds, s);
 }
-template <class E, bool GRAD, bool IL, bool WHOLE>
+template <class E, bool GRAD, bool IL, int FIT>
 void launch_heads_w(const HeadsP& p, int units, size_t lds, hipStream_t s) {
   // What is read, if it is much, passes the cache and leaves it to what is
   // written, which the attention reads next: 32 + 8 heads of 128 with a pass over
@@ -547,19 +592,20 @@ void launch_heads_w(const HeadsP& p, int units, size_t lds, hipStream_t s) {
   // outputs past the cache), backwards 139 (150, 156); at 8192 80 backwards (84)
   // and 49 forwards either way; at 4096 (42 MB read) 32 instead of 29 forwards.
   const double read = (GRAD ? 4.0 : 2.0) * p.T * p.D * (p.s[0].heads + p.s[1].heads);
-  if (read > 64e6) launch_heads_t<E, GRAD, IL, WHOLE, true>(p, units, lds, s);
-  else launch_heads_t<E, GRAD, IL, WHOLE, false>(p, units, lds, s);
+  if (read > 64e6) launch_heads_t<E, GRAD, IL, FIT, true>(p, units, lds, s);
+  else launch_heads_t<E, GRAD, IL, FIT, false>(p, units, lds, s);
+}
+template <class E, bool GRAD, bool IL>
+void launch_heads_f(const HeadsP& p, int units, size_t lds, hipStream_t s) {
+  const Fit fit = fit_of(p.D, p.r, IL);
+  if (fit == WHOLE) launch_heads_w<E, GRAD, IL, WHOLE>(p, units, lds, s);
+  else if (fit == LAPPED) launch_heads_w<E, GRAD, IL, LAPPED>(p, units, lds, s);
+  else launch_heads_t<E, GRAD, IL, RAGGED, false>(p, units, lds, s);
 }
 template <class E, bool GRAD>
 void launch_heads(const HeadsP& p, int units, size_t lds, int interleaved, hipStream_t s) {
-  const bool whole = p.r % 16 == 0 && p.D % 16 == 0;
-  if (interleaved) {
-    if (whole) launch_heads_w<E, GRAD, true, true>(p, units, lds, s);
-    else launch_heads_w<E, GRAD, true, false>(p, units, lds, s);
-  } else {
-    if (whole) launch_heads_w<E, GRAD, false, true>(p, units, lds, s);
-    else launch_heads_w<E, GRAD, false, false>(p, units, lds, s);
-  }
+  if (interleaved) launch_heads_f<E, GRAD, true>(p, units, lds, s);
+  else launch_heads_f<E, GRAD, false>(p, units, lds, s);
 }
 
 }  // namespace

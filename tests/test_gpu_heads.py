@@ -274,6 +274,61 @@ def test_in_place_and_captured():
         assert torch.equal(grads[0], eager[0]) and torch.equal(grads[2], eager[2])
 
 
+@pytest.mark.parametrize("heads", [1, 2, 3, 20])
+@pytest.mark.parametrize("D,r,interleaved", [(80, 20, False), (96, 24, True), (9, 0, False), (17, 8, True),
+                                             (26, 18, False), (100, 50, False), (112, 112, False),
+                                             (23, 6, False), (8, 8, True), (16, 16, False), (64, 10, True),
+                                             (72, 16, False), (1000, 24, False), (130, 130, True)])
+def test_over_the_inputs(D, r, interleaved, heads):
+    """Y over X and dX over dY or X, where chunks of columns lie over each
+    other, end early or fit, and batches hold one token or several."""
+    import ctypes
+    from orthogonalizing_optimizer_amd import _lib
+    g = torch.Generator().manual_seed(D + r)
+    T, ld = 53, heads * D + 3
+    x, dy = (rnd(g, T, heads, D, dtype=BF).cuda() for _ in range(2))
+    w, fr = rnd(g, D).cuda(), freqs_of(r).cuda()
+    pos = torch.randint(0, 3000, (T,), generator=g).cuda()
+    y, _ = d3.qk_norm_rope(x, None, w, None, pos, fr, interleaved=interleaved)
+    want, _, wdw, _ = d3.qk_norm_rope_grad(dy, None, x, None, w, None, pos, fr, interleaved=interleaved)
+
+    def laid(t):
+        buf = torch.full((T * ld + 8,), 7.0, dtype=BF, device="cuda")
+        v = buf.as_strided((T, heads, D), (ld, D, 1), 1)
+        v.copy_(t)
+        return v, buf
+
+    def rest(v, buf):
+        mask = torch.ones_like(buf, dtype=torch.bool)
+        mask.as_strided(v.shape, v.stride(), v.storage_offset()).fill_(False)
+        return buf[mask]
+
+    def desc(x, dy, out):
+        return _lib.HeadsDesc(X=x.data_ptr(), ldx=ld, hsx=D, w=w.data_ptr(), dY=dy.data_ptr(), lddy=ld,
+                              hsdy=D, Y=out.data_ptr(), ldy=ld, hsy=D, heads=heads)
+
+    stream = torch.cuda.current_stream().cuda_stream
+    tail = (T, D, r, int(interleaved), 1e-6, 0, 1)
+    v, buf = laid(x)
+    assert d3.lib().dion3_qk_norm_rope(ctypes.byref(desc(v, v, v)), None, fr.data_ptr() or None,
+                                       pos.data_ptr(), 64, *tail, stream) == 0
+    assert torch.equal(v, y) and (rest(v, buf) == 7).all()
+    size = ctypes.c_size_t()
+    assert d3.lib().dion3_qk_norm_rope_grad_workspace_size(T, heads, 0, D, r, int(interleaved),
+                                                           ctypes.byref(size)) == 0
+    for over in (0, 1):
+        (v, vb), (u, ub) = laid(x), laid(dy)
+        out, ob = ((v, vb), (u, ub))[over]
+        dw = torch.empty(2, D, device="cuda")
+        ws = torch.full((size.value + 256,), 255, dtype=torch.uint8, device="cuda")
+        at = ws.data_ptr() + (-ws.data_ptr()) % 256
+        assert d3.lib().dion3_qk_norm_rope_grad(ctypes.byref(desc(v, u, out)), None, fr.data_ptr() or None,
+                                                pos.data_ptr(), 64, dw.data_ptr(), *tail, at,
+                                                size.value, stream) == 0
+        assert torch.equal(out, want) and (rest(out, ob) == 7).all()
+        assert torch.equal(dw[0], wdw) and not dw[1].any()
+
+
 def test_refusals():
     q, k = torch.ones(4, 3, 64, dtype=BF, device="cuda"), torch.ones(4, 2, 64, dtype=BF, device="cuda")
     w, pos, fr = torch.ones(64, device="cuda"), torch.arange(4, device="cuda"), freqs_of(64).cuda()
