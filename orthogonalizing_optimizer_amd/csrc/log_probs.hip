@@ -15,6 +15,9 @@
 // is joined by a second launch, so that few long rows fill the chip as many
 // rows do.  The pair (m, l) is kept apart up to the gradient: where logits are
 // large, down to the type's lowest value, m + l would have no bits left for l.
+//
+// 8192 x 32000 bf16 take 88 us and 5 for the join (5.9 TB/s), the gradient 175
+// (6.0 TB/s); 1000 x 50257 fp32 with the entropy and 5 alternatives 42 and 5.
 #include "checks.h"
 #include "wave.h"
 
@@ -429,7 +432,8 @@ __device__ __forceinline__ RowSums row_sums(const LogpP& p, long long t, const P
 
 // Rows from their pieces: a thread a row, or with TOP a workgroup a row, whose
 // threads rank the pieces' candidates, several threads a candidate where there
-// are fewer of them.
+// are fewer of them (taking the best first, as best_of does, is slower for few
+// rows: 12 us instead of 7 for 4 of 16 x 20 candidates).
 constexpr int kJoinTop = 512;
 template <class E, bool TOP>
 __global__ __launch_bounds__(TOP ? kJoinTop : 64) void k_logp_join(LogpP p) {
