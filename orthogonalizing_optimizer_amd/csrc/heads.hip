@@ -14,7 +14,7 @@
 // between lanes; a head takes G lanes (8 for 128 columns), a wave 64 / G heads
 // (a batch) at a time.  Waves stay and take batch after batch, of queries or of
 // keys (one weight and one sum of its gradient in registers), the next one's
-// columns on their way; a token's angles are computed once a wave.
+// columns on their way.  A wave computes the angles of its batch's token together.
 #include "checks.h"
 #include "wave.h"
 
@@ -27,7 +27,6 @@ struct Side {
   long long ldx, hsx, lddy, hsdy, ldy, hsy;
   int heads, batches, units;       // batches of a token's heads; workgroups
   int tb, hb;                      // tokens and heads of a batch (powers of two, tb hb = 64 / G)
-  long long each;                  // batches of a wave
 };
 struct HeadsP {
   Side s[2];                      // queries, keys
@@ -157,23 +156,32 @@ struct Angles {
   }
 };
 
-// The batches of heads that a wave takes: a stretch of all of its side's, token
-// by token (tb tokens by tb tokens), as long as every other wave's.
+// The batches of heads that a wave takes: every W-th of its side's, W its
+// waves, so that all waves read and write beside each other.  32 + 8 heads of
+// 128 backwards: 56 us at 8192 tokens and 104 at 16384, with a stretch of
+// neighbouring batches for each wave, which needs a token's angles less often,
+// 61 and 123, with runs of two 58 and 115; forwards at 16384 64, 74 and 72.
+// (Smaller heads backwards lose by it: 25 + 25 of 100 at 8192 86 us, 77 and 82.)
 struct Walk {
-  long long left, t;
-  int b;
+  long long left, t, dt;           // batches left; token, tokens of a step
+  int b, db;
   __device__ Walk(const HeadsP& p, const Side& s, long long wave) {
-    const long long all = (p.T + s.tb - 1) / s.tb * s.batches, first = wave * s.each;
-    left = all - first < s.each ? all - first : s.each;
-    t = first / s.batches;
-    b = (int)(first - t * s.batches);
+    const long long all = (p.T + s.tb - 1) / s.tb * s.batches;
+    const int W = 4 * s.units, q = W / s.batches;
+    left = (all - wave + W - 1) / W;
+    t = wave / s.batches;
+    b = (int)(wave - t * s.batches);
     t *= s.tb;
+    db = W - q * s.batches;
+    dt = (long long)q * s.tb;
   }
   __device__ bool more() const { return left > 0; }
   __device__ void next(const Side& s) {
     --left;
-    if (++b < s.batches) return;
-    b = 0;
+    t += dt;
+    b += db;
+    if (b < s.batches) return;
+    b -= s.batches;
     t += s.tb;
   }
 };
@@ -475,11 +483,12 @@ Fit fit_of(int D, int r, bool il) {
 }
 // A head takes the power of two of lanes that holds its columns, 16 a lane.
 // As many waves as stay resident (a few more would run after all others) are
-// shared out between queries and keys by their batches, and each takes equally
-// many of them: 8192 tokens of 32 + 8 heads of 128 take 32 us (5.2 TB/s; twice
-// the resident waves, 36 with as many) and 57 backwards (4.4 TB/s; a tenth more
-// by whole tokens; with 4 waves a SIMD that read their weight from LDS 3 % less:
-// not kept).
+// shared out between queries and keys by their batches: 8192 tokens of 32 + 8
+// heads of 128 take 32 us (5.2 TB/s; 36 with 7 workgroups a CU instead of 5) and
+// 56 backwards with the join (65 with 2 instead of 3, 72 with 4).  Not kept
+// backwards: two batches on their way (3 to 13 % slower at most sizes, spills),
+// 4 waves a SIMD that read their weight from LDS (3 % less at that size, when a
+// wave's batches were neighbours).
 //
 // Where a token has at most half as many heads as a batch, a batch takes several
 // tokens: 100000 tokens of 4 + 1 heads of 64 take 39 us and 67 backwards, 95 and
@@ -487,14 +496,13 @@ Fit fit_of(int D, int r, bool il) {
 constexpr int kAngles = 512;        // a wave's in LDS, at most (one token's may be 512)
 struct Split {
   int G, pitch, angles, batches[2], units[2], tb[2], hb[2];
-  long long each[2];
 };
 Split split_heads(long long T, int hq, int hk, int D, int r, bool il, bool grad) {
   Split q = {};
   q.G = 1;
   while (q.G < pieces(D, r, il)) q.G *= 2;
   const int per = 64 / q.G, heads[2] = {hq, hk};
-  const int units = 256 * (grad ? 3 : fit_of(D, r, il) != RAGGED ? 10 : 4);
+  const Fit fit = fit_of(D, r, il);
   q.pitch = r ? (r / 2 + 7) / 8 * 8 : 8;
   q.angles = q.pitch;
   long long all[2];
@@ -506,13 +514,13 @@ Split split_heads(long long T, int hq, int hk, int D, int r, bool il, bool grad)
     if (q.pitch * q.tb[i] > q.angles) q.angles = q.pitch * q.tb[i];
     all[i] = (T + q.tb[i] - 1) / q.tb[i] * q.batches[i];
   }
+  const bool multi = q.tb[0] > 1 || q.tb[1] > 1;
+  const int units = 256 * (grad ? 3 : fit == WHOLE || (fit == LAPPED && !multi) ? 5 : 4);
   for (int i = 0; i < 2; ++i) {
     if (all[i] == 0) continue;
     const long long share = (long long)((double)units * all[i] / (all[0] + all[1]));
     const long long waves = share < 1 ? 4 : share * 4;
-    q.each[i] = (all[i] + waves - 1) / waves;
-    const long long used = (all[i] + q.each[i] - 1) / q.each[i];
-    q.units[i] = (int)((used + 3) / 4);
+    q.units[i] = (int)(((all[i] < waves ? all[i] : waves) + 3) / 4);
   }
   return q;
 }
@@ -562,7 +570,7 @@ HeadsP describe(const dion3_heads* q, const dion3_heads* k, const Split& sp, con
     if (both[i]) {
       const dion3_heads& s = *both[i];
       p.s[i] = {s.X, s.w, s.dY, s.Y, s.ldx, s.hsx, s.lddy, s.hsdy, s.ldy, s.hsy, s.heads,
-                sp.batches[i], sp.units[i], sp.tb[i], sp.hb[i], sp.each[i]};
+                sp.batches[i], sp.units[i], sp.tb[i], sp.hb[i]};
     }
   p.freqs = freqs; p.pos = pos; p.T = T;
   p.D = D; p.r = r; p.G = sp.G; p.pitch = sp.pitch; p.angles = sp.angles;
