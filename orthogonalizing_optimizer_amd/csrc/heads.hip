@@ -50,7 +50,7 @@ struct HeadsP {
 // end behind its run lies over the one before instead; what lies over is
 // computed and written twice, with the same bits, and left out of sums (8192
 // tokens of 16 + 16 heads of 96, 24 turned: 25 us, 34 with ragged chunks;
-// backwards 48 and 76).  RAGGED: chunks are cut off at the end of the run.
+// backwards 52 and 76).  RAGGED: chunks are cut off at the end of the run.
 enum Fit { RAGGED, LAPPED, WHOLE };
 struct Item {
   int base[2], c[2], lim[2];
@@ -491,7 +491,7 @@ Fit fit_of(int D, int r, bool il) {
 // wave's batches were neighbours).
 //
 // Where a token has at most half as many heads as a batch, a batch takes several
-// tokens: 100000 tokens of 4 + 1 heads of 64 take 39 us and 67 backwards, 95 and
+// tokens: 100000 tokens of 4 + 1 heads of 64 take 37 us and 66 backwards, 95 and
 // 171 with a token a batch.
 constexpr int kAngles = 512;        // a wave's in LDS, at most (one token's may be 512)
 struct Split {
