@@ -537,7 +537,8 @@ __global__ __launch_bounds__(256) void k_logp_grad(GradP p) {
 
 // Pieces of at most 8192 logits (4 waves), of 32768 (16 waves) where a row
 // would have more than 16, of equal length; one or two waves for rows that fill
-// no more.
+// no more (20000 x 1500 without alternatives 22 us, 52 with four; 20000 x 4000
+// 40 and 59).
 struct Pieces {
   int S, len, threads;
 };

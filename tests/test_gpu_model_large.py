@@ -127,3 +127,51 @@ def test_embedding_gradient_of_many_tokens(T, n, m, kind):
     got = d3.embedding_grad(t.cuda(), dy.cuda(), n)
     close(got, want, off, kind)
     assert torch.equal(d3.embedding_grad(t.int().cuda(), dy.cuda(), n), got)
+
+
+def test_two_streams_and_threads():
+    """Calls at once, from two threads on two streams, each with its own results."""
+    import threading
+    g = torch.Generator(device="cuda").manual_seed(4)
+    n, T, D = 20001, 600, 128
+    fr = (10000.0 ** (-torch.arange(0, D, 2, dtype=torch.float64) / D)).cuda()
+
+    def inputs():
+        return dict(x=rnd(g, T, n, dtype=BF), t=torch.randint(-1, n, (T,), generator=g, device="cuda"),
+                    q=rnd(g, T, 12, D, dtype=BF), k=rnd(g, T, 2, D, dtype=BF), w=rnd(g, D),
+                    p=torch.randint(0, 9999, (T,), generator=g, device="cuda"), e=rnd(g, T, 300, dtype=BF),
+                    grads=[rnd(g, 500, 300, dtype=BF) for _ in range(70)])
+
+    def run(a):
+        lp = d3.log_probs(a["x"], a["t"], entropy=True, top=64)
+        dx = d3.log_probs_grad(lp[0], a["x"], a["t"], lp[1], entropy=lp[2], dentropy=lp[2])
+        y = d3.qk_norm_rope(a["q"], a["k"], a["w"], a["w"], a["p"], fr)
+        dy = d3.qk_norm_rope_grad(*y, a["q"], a["k"], a["w"], a["w"], a["p"], fr)
+        de = d3.embedding_grad(a["t"], a["e"], n)
+        sums = [torch.zeros(500, 300, device="cuda") for _ in a["grads"]]
+        norm = d3.clip_grad_norm(a["grads"], 1.0, into=sums)
+        return [*lp, dx, *y, *dy, de, norm, *sums]
+
+    both = [inputs(), inputs()]
+    want = [run(a) for a in both]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in both]
+    got, bad = [None, None], []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(streams[i]):
+                got[i] = [run(both[i]) for _ in range(8)]
+        except Exception as e:              # (a thread's own failure would not be the test's)
+            bad.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    torch.cuda.synchronize()
+    assert not bad
+    for i in range(2):
+        for outs in got[i]:
+            assert all(torch.equal(u, v) for u, v in zip(outs, want[i])), i
