@@ -533,9 +533,11 @@ DION3_API dion3_status dion3_qk_norm_rope_grad(const dion3_heads* q, const dion3
  * and the gradient.
  *
  * X holds T rows of n logits of dtype (DION3_F32, _BF16 or _F16) with row
- * stride ldx; z = scale X.  target: T integers of target_bits (32 or 64) bits,
- * or NULL; one outside [0, n) marks a row without a token (its logp is 0 and
- * it sends no gradient).
+ * stride ldx; z = scale X, held at -FLT_MAX where a finite logit's product
+ * passes it (and rounded to fp32 in rows whose maximum is 2^30 or more in
+ * magnitude).  target: T integers of target_bits (32 or 64) bits, or NULL; one
+ * outside [0, n) marks a row without a token (its logp is 0 and it sends no
+ * gradient).
  *   stats[t] = (m, l): m = max_j z_j, l = ln sum_j exp(z_j - m);
  *   logp[t] = (z_target - m) - l (given and NULL together with target);
  *   entropy[t] = -sum_j p_j ln p_j with p_j = exp((z_j - m) - l) (or NULL);

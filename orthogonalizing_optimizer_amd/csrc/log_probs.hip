@@ -1,7 +1,7 @@
 // Log probabilities of given tokens from rows of logits, with the entropy and
 // the best alternatives, and the gradient.
 //
-//   z = scale x,  m = max_j z_j,  l = ln sum_j exp(z_j - m)   per row of n,
+//   z = scale x,  m = max_j z_j (rounded),  l = ln sum_j exp(z_j - m)   per row of n,
 //   logp = (z_target - m) - l,  H = l - sum_j exp(z_j - m) (z_j - m) / exp(l),
 //   dx_j = scale (g (1[j = target] - p_j) - gH p_j (ln p_j + H)),
 //   p_j = exp((z_j - m) - l).
@@ -18,6 +18,8 @@
 //
 // 8192 x 32000 bf16 take 88 us and 5 for the join (5.9 TB/s), the gradient 175
 // (6.0 TB/s); 1000 x 50257 fp32 with the entropy and 5 alternatives 42 and 5.
+#include <type_traits>
+
 #include "checks.h"
 #include "wave.h"
 
@@ -30,6 +32,31 @@ constexpr float kLowest = -3.402823466e38f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float exp_(float d) { return __builtin_amdgcn_exp2f(d * kLog2e); }
+
+// A distance z - m, m the rounded maximum, takes its product with the scale
+// unrounded.  At the maximum it is then the product's rounding, at most 32 below
+// 2^30, which all distances of the row share and l takes back; m + l and p lose
+// nothing by it.  Where m is larger, that would leave exp's range (rows that a
+// mask has filled with the type's lowest value, at a temperature): there the
+// product is rounded first, the distance is 0 at the maximum, and exp of any
+// other one (128 at least) is 0.  A finite logit whose product passes the lowest
+// number of fp32 is held there: only rows of -infinity have no probabilities.
+constexpr float kLarge = 0x1p30f;
+__device__ __forceinline__ bool large(float m) { return fabsf(m) >= kLarge; }
+template <bool LARGE>
+__device__ __forceinline__ float distance(float x, float scale, float m) {
+#pragma clang fp contract(off)
+  if (!LARGE) return __builtin_fmaf(x, scale, -m);
+  float z = x * scale;
+  z = z == -__builtin_inff() && x != z ? kLowest : z;
+  return z - m;
+}
+// (an output's own: in sums and gradients exp of a held product is 0 all the same)
+__device__ __forceinline__ float distance(float x, float scale, float m) {
+  if (large(m)) return distance<true>(x, scale, m);
+  const float d = distance<false>(x, scale, m);
+  return d == -__builtin_inff() && x != d ? kLowest : d;
+}
 
 // The sums of a set of logits relative to m (kLowest for an empty set or one
 // of -infinity): s = sum exp(z - m), e = sum exp(z - m) (z - m).
@@ -315,13 +342,13 @@ __device__ __forceinline__ float max8(const float (&v)[8]) {
   return fmaxf(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])), fmaxf(fmaxf(v[4], v[5]), fmaxf(v[6], v[7])));
 }
 // The sums of 32 logits relative to w.m; e with ENT only.
-template <bool ENT>
+template <bool ENT, bool LARGE>
 __device__ __forceinline__ void add_logits(const float (&v)[kChunks][8], float scale, Part& w) {
 #pragma unroll
   for (int i = 0; i < kChunks; ++i)
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float d = __builtin_fmaf(v[i][e], scale, -w.m);
+      const float d = distance<LARGE>(v[i][e], scale, w.m);
       const float q = exp_(d);
       w.s += q;
       if (ENT) w.e = __builtin_fmaf(q, fmaxf(d, -1e30f), w.e);
@@ -362,7 +389,8 @@ void k_logp_piece(LogpP p) {
   }
   mx = wave_max(mx);
   Part w = {fmaxf(mx * p.scale, kLowest), 0.0f, 0.0f, 0.0f};
-  add_logits<ENT>(v, p.scale, w);
+  if (__builtin_amdgcn_readfirstlane(large(w.m))) add_logits<ENT, true>(v, p.scale, w);
+  else add_logits<ENT, false>(v, p.scale, w);
   w.s = wave_add(w.s);
   if (ENT) w.e = wave_add(w.e);
   if ((threadIdx.x & 63) == 0) sh[wave] = w;
@@ -417,7 +445,7 @@ __device__ __forceinline__ float target_logit(const LogpP& p, long long t, bool&
 __device__ __forceinline__ RowSums row_sums(const LogpP& p, long long t, const Part& a, bool write,
                                             float x, bool token) {
   RowSums r;
-  r.none = a.s == 0.0f && a.m < 0.0f;
+  r.none = a.s == 0.0f && a.m < 0.0f;      // (the largest logit's exp is at least exp(-32))
   // (an infinite maximum, of a logit or of its product with scale, has no log)
   r.l = r.none ? 0.0f : a.m > -kLowest ? __builtin_nanf("") : logf(a.s);
   r.m = r.none ? -__builtin_inff() : a.m;
@@ -426,7 +454,7 @@ __device__ __forceinline__ RowSums row_sums(const LogpP& p, long long t, const P
   p.stats[2 * t + 1] = r.l;
   if (p.entropy) p.entropy[t] = r.none ? 0.0f : r.l - a.e / a.s;
   if (p.target)
-    p.logp[t] = !token ? 0.0f : r.none ? -__builtin_inff() : __builtin_fmaf(x, p.scale, -r.m) - r.l;
+    p.logp[t] = !token ? 0.0f : r.none ? -__builtin_inff() : distance(x, p.scale, r.m) - r.l;
   return r;
 }
 
@@ -467,7 +495,7 @@ __global__ __launch_bounds__(TOP ? kJoinTop : 64) void k_logp_join(LogpP p) {
       if (mine && sub == 0 && rank < p.top) {
         p.top_logp[t * p.top + rank] =
             r.none ? -__builtin_inff()
-                   : __builtin_fmaf(order_value((unsigned)(mine >> 32)), p.scale, -r.m) - r.l;
+                   : distance(order_value((unsigned)(mine >> 32)), p.scale, r.m) - r.l;
         p.top_index[t * p.top + rank] = 0xffffffffu - (unsigned)mine;
       }
     }
@@ -515,22 +543,26 @@ __global__ __launch_bounds__(256) void k_logp_grad(GradP p) {
     b = -p.scale * p.gh[t];
     a = __builtin_fmaf(b, p.entropy[t], a);
   }
+  auto write = [&](auto is_large) {
 #pragma unroll
-  for (int i = 0; i < kChunks; ++i) {
-    const int c = from + (i * 256 + (int)threadIdx.x) * 8;
-    if (c >= to) continue;
-    float v[8];
-    chunk8(raw[i], c, p.n, v);
+    for (int i = 0; i < kChunks; ++i) {
+      const int c = from + (i * 256 + (int)threadIdx.x) * 8;
+      if (c >= to) continue;
+      float v[8];
+      chunk8(raw[i], c, p.n, v);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float q = __builtin_fmaf(v[e], p.scale, -m) - l;
-      const float pr = exp_(q);
-      // (bounded: 0 times an infinite ln p would be NaN)
-      v[e] = none ? 0.0f : pr * (ENT ? __builtin_fmaf(b, fmaxf(q, -1e30f), a) : a);
-      if (c + e == j && !none) v[e] += g;
+      for (int e = 0; e < 8; ++e) {
+        const float q = distance<decltype(is_large)::value>(v[e], p.scale, m) - l;
+        const float pr = exp_(q);
+        // (bounded: 0 times an infinite ln p would be NaN)
+        v[e] = none ? 0.0f : pr * (ENT ? __builtin_fmaf(b, fmaxf(q, -1e30f), a) : a);
+        if (c + e == j && !none) v[e] += g;
+      }
+      store8_once((E*)p.dx + t * p.lddx, c, min(to, p.n), v);
     }
-    store8_once((E*)p.dx + t * p.lddx, c, min(to, p.n), v);
-  }
+  };
+  if (__builtin_amdgcn_readfirstlane(large(m))) write(std::true_type());
+  else write(std::false_type());
 }
 
 // --------------------------------------------------------------- the launches
