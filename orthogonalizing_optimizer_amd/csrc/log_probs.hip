@@ -31,6 +31,10 @@ constexpr int kMaxTop = DION3_MAX_TOP;
 constexpr float kLowest = -3.402823466e38f;
 constexpr float kLn2 = 0.6931471805599453f;
 
+// Distances count as no farther where they are multiplied: exp is 0 from -104 on,
+// and 0 times what a sum or a gradient makes of an infinite or a huge distance
+// would be NaN.
+constexpr float kFar = -200.0f;
 __device__ __forceinline__ float exp_(float d) { return __builtin_amdgcn_exp2f(d * kLog2e); }
 
 // A distance z - m, m the rounded maximum, takes its product with the scale
@@ -65,8 +69,7 @@ struct Part {
 };
 __device__ __forceinline__ Part merge(const Part& a, const Part& b) {
   const float m = fmaxf(a.m, b.m);
-  // (bounded: 0 times an infinite distance would be NaN)
-  const float da = fmaxf(a.m - m, -1e30f), db = fmaxf(b.m - m, -1e30f);
+  const float da = fmaxf(a.m - m, kFar), db = fmaxf(b.m - m, kFar);
   const float fa = exp_(a.m - m), fb = exp_(b.m - m);      // infinities less themselves: NaN
   return {m, __builtin_fmaf(a.s, fa, b.s * fb),
           __builtin_fmaf(__builtin_fmaf(a.s, da, a.e), fa, __builtin_fmaf(b.s, db, b.e) * fb), 0.0f};
@@ -351,7 +354,7 @@ __device__ __forceinline__ void add_logits(const float (&v)[kChunks][8], float s
       const float d = distance<LARGE>(v[i][e], scale, w.m);
       const float q = exp_(d);
       w.s += q;
-      if (ENT) w.e = __builtin_fmaf(q, fmaxf(d, -1e30f), w.e);
+      if (ENT) w.e = __builtin_fmaf(q, fmaxf(d, kFar), w.e);
     }
 }
 
@@ -554,8 +557,7 @@ __global__ __launch_bounds__(256) void k_logp_grad(GradP p) {
       for (int e = 0; e < 8; ++e) {
         const float q = distance<decltype(is_large)::value>(v[e], p.scale, m) - l;
         const float pr = exp_(q);
-        // (bounded: 0 times an infinite ln p would be NaN)
-        v[e] = none ? 0.0f : pr * (ENT ? __builtin_fmaf(b, fmaxf(q, -1e30f), a) : a);
+        v[e] = none ? 0.0f : pr * (ENT ? __builtin_fmaf(b, fmaxf(q, kFar), a) : a);
         if (c + e == j && !none) v[e] += g;
       }
       store8_once((E*)p.dx + t * p.lddx, c, min(to, p.n), v);
