@@ -395,7 +395,8 @@ __global__ __launch_bounds__(256) void k_heads_grad(HeadsP p) {
         fresh = at.t != now.t;
         if (fresh) pos = positions_of<MULTI>(p, s, at.t);
       }
-      const float rs = head_rstd<FIT>(it, x, G, p.D, p.eps);
+      // (no head: nothing in the sums, also where eps is 0 and its statistic infinite)
+      const float stat = head_rstd<FIT>(it, x, G, p.D, p.eps), rs = own ? stat : 0.0f;
       rotate<IL>(u, co, si, it.rot);
       float c = 0.0f;
 #pragma unroll
