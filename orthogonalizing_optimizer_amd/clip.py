@@ -162,11 +162,9 @@ def clip_grad_norm(grads, max_norm: float, scale: float = 1.0, into=None,
     gradients, one that is NaN makes all of them NaN.
 
     ``into``: fp32 tensors, one for each gradient and of its shape; the scaled
-    gradients are then added to them and the gradients stay as they are.
-    ``[optimizer.accumulate_grad(p) for p in ps]`` are the momenta of a
-    ``Dion3``, whose next ``step()`` steps these parameters (leave their
-    ``.grad`` None by then, or it is added again); for a captured call, name
-    them before each step that follows a replay.
+    gradients are then added to them and the gradients stay as they are.  For
+    the momenta of a ``Dion3`` use its ``accumulate_clipped``, which steps the
+    parameters that have a gradient here and no others.
 
     No tensor that is written may be listed twice or overlap another one.
     Pass gradients, not parameters; None stands for no gradient."""

@@ -226,6 +226,30 @@ class Dion3(_optimizer_base()):
         if not captured:
             self._accumulated.add(p)
 
+    def accumulate_clipped(self, params, grads, max_norm, scale: float = 1.0):
+        """Sum ``grads`` (fp32, bf16 or fp16; one for each of ``params``, None
+        where there is none), clipped by their global norm, into the momenta of
+        ``params``, and return the norm (``clip_grad_norm(grads, max_norm,
+        scale, into=...)``).  The next ``step()`` steps the parameters with a
+        gradient whether or not they have a ``.grad`` (a ``.grad`` is added as
+        well).  One without is left alone, and so are all of them where the
+        call is refused.  Inside a capture no parameter is named: call
+        ``accumulate_grad(p)`` for each before a replay."""
+        from .clip import clip_grad_norm
+        params, grads = list(params), list(grads)
+        if len(params) != len(grads):
+            raise ValueError("need one gradient per parameter")
+        if len(set(params)) != len(params):
+            raise ValueError("a parameter is listed twice")
+        for p in params:
+            self.check_parameter(p)
+        uses = [None if g is None else self._use(p) for p, g in zip(params, grads)]
+        norm = clip_grad_norm(grads, max_norm, scale, into=[u and u[0] for u in uses])
+        for p, use in zip(params, uses):
+            if use is not None:
+                self._name(p, use[1])
+        return norm
+
     def clip_grad_norm(self, max_norm, scale: float = 1.0):
         """Clip the ``.grad`` of all parameters by their global norm, in place,
         and return the norm (``clip_grad_norm``).  RuntimeError if gradients
