@@ -462,7 +462,8 @@ DION3_API dion3_status dion3_linear_grad_weight(const void* dZ, int64_t lddz, co
  * The gradient: dW[v] = scale times the sum of dY[t] over the t with token[t]
  * = v (fp32, n x m; zeros for a row without tokens), or with accumulate != 0
  * that is added to dW, and rows without tokens are neither read nor written.
- * Sums are held in fp32, without atomics, in an order fixed by the tokens.
+ * Sums are held in fp32, those of a token with more than 64 rows in parts that
+ * are added up in 64 bits, without atomics, in an order fixed by the tokens.
  * Errors: as for the layers' operators, but row strides up to 2^38; scale must
  * be finite. */
 DION3_API dion3_status dion3_embedding(const void* token, int32_t token_bits, const void* W,

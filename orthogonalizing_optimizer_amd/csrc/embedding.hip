@@ -9,10 +9,11 @@
 // list is cut into chunks of up to 32 places, a wave sums the rows of one chunk
 // for 512 columns, and writes a token's sum at the end of its run.  A run
 // longer than two chunks leaves one partial row a chunk, which a last launch
-// adds up in order, so that a token that fills the batch is split as well.  The
-// rows of dW without one are cleared last, by the flags that the others' waves
-// have set: cleared before, all of it, the rows with sums would be written
-// twice, and beside the sums the two hold up each other.
+// adds up in order, and in 64 bits: a token that fills the batch has up to 2^19
+// of them (equal rows added in fp32 are off by 6e-5 at 2^20 places, by 1e-3 at
+// 2^24).  The rows of dW without one are cleared last, by the flags that the
+// others' waves have set: cleared before, all of it, the rows with sums would be
+// written twice, and beside the sums the two hold up each other.
 //
 // Bound by HBM: dW is written once (fp32, most of the bytes), dy read once.
 // 8192 tokens of 32000 x 4096 (591 MB) take 100 us (5.9 TB/s): 9 for the places,
@@ -435,7 +436,7 @@ __global__ __launch_bounds__(256) void k_embed_grad(EmbedGradP p) {
 constexpr int kJoinChunks = 16;
 __global__ __launch_bounds__(256) void k_embed_join(EmbedGradP p, long long chunks, long long joins,
                                                     Zero z) {
-  __shared__ float sh[3][64][4];
+  __shared__ double sh[3][64][4];
   if (grid_block() >= joins) {
     zero_block<256>(z, grid_block() - joins);
     return;
@@ -469,7 +470,7 @@ __global__ __launch_bounds__(256) void k_embed_join(EmbedGradP p, long long chun
     }
     const long long count = c1 - c0 + 1, per = (count + 3) / 4;
     const long long a = wave * per, b = a + per < count ? a + per : count;
-    float v[4] = {0, 0, 0, 0};
+    double v[4] = {0, 0, 0, 0};
     const bool vec = c + 4 <= p.m;
     struct __attribute__((packed, aligned(4))) F4 { float x[4]; };
 #pragma unroll 8
@@ -478,11 +479,11 @@ __global__ __launch_bounds__(256) void k_embed_join(EmbedGradP p, long long chun
       if (vec) {
         const F4 f = *(const F4*)(part + c);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] += f.x[e];
+        for (int e = 0; e < 4; ++e) v[e] += (double)f.x[e];
       } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (c + e < p.m) v[e] += part[c + e];
+          if (c + e < p.m) v[e] += (double)part[c + e];
       }
     }
     __syncthreads();                                  // (the run before has been read)
@@ -498,7 +499,7 @@ __global__ __launch_bounds__(256) void k_embed_join(EmbedGradP p, long long chun
     float* d = p.dw + row * p.ldw;
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      if (c + e < p.m) d[c + e] = p.accumulate ? d[c + e] + p.scale * v[e] : p.scale * v[e];
+      if (c + e < p.m) d[c + e] = (float)((p.accumulate ? (double)d[c + e] : 0.0) + p.scale * v[e]);
   }
 }
 
