@@ -25,7 +25,11 @@ namespace dion3 {
 namespace {
 
 constexpr int kMaxChunk = 32;         // places of one wave at most
-constexpr int kCountMax = 8192;       // tokens up to which places are counted, not sorted by digits
+// Tokens up to which places are counted, not sorted by digits.  Counting grows
+// with their square: 4100 tokens of 50257 x 768 take 37 us counted and 49
+// sorted, 8192 41 and 51; 8193 would take 46 and take 51, 10240 50 and 52, 12288
+// (48 KB of LDS) the same, added to a buffer 46 and 44.
+constexpr int kCountMax = 8192;
 constexpr int kTile = 1024;           // tokens of a workgroup of the sort by digits
 
 __device__ __forceinline__ int token_key(const void* tokens, int is64, long long t, int n) {

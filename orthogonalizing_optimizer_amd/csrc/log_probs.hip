@@ -35,6 +35,8 @@ constexpr float kLn2 = 0.6931471805599453f;
 // and 0 times what a sum or a gradient makes of an infinite or a huge distance
 // would be NaN.
 constexpr float kFar = -200.0f;
+// (d log2 e is rounded and the exponential the hardware's: a term is off by up to
+// 3 |d| + 2 units of 2^-24 of itself, for fp32 logits too; below 2^-126 it is 0)
 __device__ __forceinline__ float exp_(float d) { return __builtin_amdgcn_exp2f(d * kLog2e); }
 
 // A distance z - m, m the rounded maximum, takes its product with the scale
@@ -514,8 +516,9 @@ struct GradP {
   float scale;
 };
 
-// One read and one write of a logit; in place where dX is X (a thread reads
-// its logits before it writes them, and nobody else's).  Both pass the cache:
+// One read and one write of a logit; in place where dX is X (a thread reads its
+// logits before it writes them; at the end of a row it also reads up to 7 of
+// its neighbour's, which it drops).  Both pass the cache:
 // the logits, which the forward pass may have left there, are not needed again,
 // and what they leave of it speeds up what follows at every size (8192 x 32000
 // alone 199 -> 178 us; forward, gradient and a pass over it: 402 -> 350, and
@@ -572,7 +575,11 @@ __global__ __launch_bounds__(256) void k_logp_grad(GradP p) {
 // Pieces of at most 8192 logits (4 waves), of 32768 (16 waves) where a row
 // would have more than 16, of equal length; one or two waves for rows that fill
 // no more (20000 x 1500 without alternatives 22 us, 52 with four; 20000 x 4000
-// 40 and 59).
+// 40 and 59).  16 waves keep the longest rows at 32 pieces (the join's wave
+// holds 64), at a price, and from earlier on than that needs: with the entropy
+// and 20 alternatives of bf16, 4 and 16 waves take 26 and 47 us at 100 x 131072,
+// 224 and 283 at 2000 x 131072; past the border 26 and 50 at 100 x 131073, 243 and
+// 341 at 2000 x 131073, 450 and 520 at 2000 x 256000 (188 and 202 without).
 struct Pieces {
   int S, len, threads;
 };

@@ -226,7 +226,7 @@ def qk_norm_rope(q, k, q_weight, k_weight, positions, freqs, eps: float = 1e-6,
     and tokens (views of one product's output, say; leading dimensions share a
     stride); outputs are contiguous.  Weights [D] are fp32 or of q's type.
     ``positions``: int64 or int32, one a token (or of a shape that expands to
-    the tokens').  ``freqs``: float64, radians a position, for instance
+    the tokens', which is copied to one a token).  ``freqs``: float64, radians a position, for instance
     base ** (-torch.arange(0, r, 2, dtype=torch.float64) / r).  k and k_weight
     may be None (queries alone; yk is None)."""
     s = _Sides(q, k, q_weight, k_weight, positions, freqs)
@@ -344,7 +344,9 @@ def log_probs(logits, targets=None, scale: float = 1.0, entropy: bool = False, t
     ``targets`` [...] (int64 or int32): logp is their log probability; one
     outside [0, n) (a padded place's -100) gets 0.  stats [..., 2] holds the
     maximum m and l = ln sum exp(z - m): their sum is the log of the sum of
-    exponentials, and ``log_probs_grad`` reads them.  ``top`` (up to 64): the
+    exponentials, and ``log_probs_grad`` reads them.  A finite logit whose
+    product with ``scale`` passes fp32's lowest number counts as that number:
+    only a row of -infinity has no probabilities.  ``top`` (up to 64): the
     best alternatives' log probabilities and indices [..., top], best first,
     equal logits by their index."""
     T, n, ld = _logits(logits)

@@ -252,7 +252,10 @@ class Dion3(_optimizer_base()):
 
     def clip_grad_norm(self, max_norm, scale: float = 1.0):
         """Clip the ``.grad`` of all parameters by their global norm, in place,
-        and return the norm (``clip_grad_norm``).  RuntimeError if gradients
+        and return the norm (``clip_grad_norm``).  The norm is that of this
+        optimizer's parameters alone, which must be on one device; for a norm
+        over others' too, give all gradients to one call of
+        ``clip_grad_norm``.  RuntimeError if gradients
         have been summed straight into momenta since the last step: those are
         no longer apart from earlier ones.  (Sums inside captured graphs name
         no parameter, so they are not noticed here.)"""
