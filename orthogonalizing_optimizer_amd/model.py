@@ -226,9 +226,9 @@ def qk_norm_rope(q, k, q_weight, k_weight, positions, freqs, eps: float = 1e-6,
     and tokens (views of one product's output, say; leading dimensions share a
     stride); outputs are contiguous.  Weights [D] are fp32 or of q's type.
     ``positions``: int64 or int32, one a token (or of a shape that expands to
-    the tokens', which is copied to one a token).  ``freqs``: float64, radians a position, for instance
-    base ** (-torch.arange(0, r, 2, dtype=torch.float64) / r).  k and k_weight
-    may be None (queries alone; yk is None)."""
+    the tokens', which is copied to one a token).  ``freqs``: float64, radians a
+    position, for instance base ** (-torch.arange(0, r, 2, dtype=torch.float64)
+    / r).  k and k_weight may be None (queries alone; yk is None)."""
     s = _Sides(q, k, q_weight, k_weight, positions, freqs)
     yq = s.output(0)
     yk = s.output(1) if k is not None else None

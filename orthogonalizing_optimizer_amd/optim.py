@@ -241,8 +241,9 @@ class Dion3(_optimizer_base()):
             raise ValueError("need one gradient per parameter")
         if len(set(params)) != len(params):
             raise ValueError("a parameter is listed twice")
-        for p in params:
-            self.check_parameter(p)
+        for p, g in zip(params, grads):
+            if g is not None:
+                self.check_parameter(p)
         uses = [None if g is None else self._use(p) for p, g in zip(params, grads)]
         norm = clip_grad_norm(grads, max_norm, scale, into=[u and u[0] for u in uses])
         for p, use in zip(params, uses):

@@ -115,20 +115,23 @@ def test_refused_call_leaves_the_parameters():
 @pytest.mark.gpu
 def test_captured_and_replayed():
     ps, grads, opt = setting("cuda")
-    for p in ps:
+    ps.append(torch.randn(5, 7, device="cuda").requires_grad_(True))    # never a gradient, no momentum
+    opt.add_param_group({"params": [ps[3]]})
+    grads.append(None)
+    for p in ps[:3]:
         opt.momentum(p)
-    opt.accumulate_clipped(ps, [grads[0], None, grads[2]], 1.0)
+    opt.accumulate_clipped(ps, [grads[0], None, grads[2], None], 1.0)
     opt.step()
     graph, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
     with torch.cuda.graph(graph, stream=s):
-        norm = opt.accumulate_clipped(ps, [grads[0], None, grads[2]], 1.0)
+        norm = opt.accumulate_clipped(ps, [grads[0], None, grads[2], None], 1.0)
     assert not opt._accumulated
     for k in range(4):
         for i in (0, 2):
             grads[i].mul_(1.0 + k)
             opt.accumulate_grad(ps[i])
-        before = [(p.detach().clone(), opt.momentum(p).clone()) for p in ps]
+        before = [(p.detach().clone(), opt.momentum(p).clone()) for p in ps[:3]]
         graph.replay()
         torch.cuda.synchronize()
         want = float((d(grads[0]).square().sum() + d(grads[2]).square().sum()).sqrt())
@@ -139,3 +142,4 @@ def test_captured_and_replayed():
         opt.step()
         assert torch.equal(ps[1], before[1][0]) and torch.equal(opt.momentum(ps[1]), before[1][1])
         assert not torch.equal(ps[0], before[0][0])
+    assert "momentum" not in opt.state.get(ps[3], ())
